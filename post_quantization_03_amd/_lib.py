@@ -13,12 +13,15 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkq.so")
 KQ_F32, KQ_BF16 = 0, 1
 HG_FORM = {"diag": 0, "block": 1, "full": 2}
 OP = {"hessian": 0, "rotate_in": 1, "hg_sqrt": 2, "rotate_out": 3, "cholinv": 4, "quantize": 5, "unrotate": 6,
-      "loss": 7, "matvec": 8, "hg_lowrank": 9, "kfac_loss": 10, "cross": 11, "drift": 12}
+      "loss": 7, "matvec": 8, "hg_lowrank": 9, "kfac_loss": 10, "cross": 11, "drift": 12, "mx_gemm": 13,
+      "mx_gated": 14, "gated_forward": 15, "gated_backward": 16}
+ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 EXPORTS = ("kq_workspace_bytes", "kq_hessian_accum", "kq_rotate_in", "kq_hg_sqrt", "kq_rotate_out", "kq_cholinv",
            "kq_quantize_layer", "kq_sensitivity", "kq_unrotate", "kq_layer_loss", "kq_strerror", "kq_last_error",
            "kq_hadamard_order", "kq_version", "kq_allocate_bits", "kq_matvec_quantized",
            "kq_hg_extract", "kq_hg_lowrank", "kq_kfac_loss", "kq_quantize_layer_search",
-           "kq_block_order", "kq_permute_blocks", "kq_cross_accum", "kq_drift_target", "kq_matvec_quantized_static")
+           "kq_block_order", "kq_permute_blocks", "kq_cross_accum", "kq_drift_target", "kq_matvec_quantized_static",
+           "kq_mx_quantize", "kq_mx_dequantize", "kq_mx_gemm", "kq_mx_gated", "kq_gated_forward", "kq_gated_backward")
 
 
 class KQError(RuntimeError):
@@ -71,6 +74,12 @@ def lib() -> ctypes.CDLL:
         "kq_hg_lowrank": (_int, [_vp, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
         "kq_kfac_loss": (_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _int, _i64, _vp, _vp, _sz,
                                 _vp]),
+        "kq_mx_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+        "kq_mx_dequantize": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _int, _i64, _vp]),
+        "kq_mx_gemm": (_int, [_vp, _i64] * 4 + [_i64, _i64, _i64, _vp, _int, _i64, _vp, _sz, _vp]),
+        "kq_mx_gated": (_int, [_vp, _i64] * 6 + [_i64, _i64, _i64, _int, _vp, _int, _i64, _vp, _sz, _vp]),
+        "kq_gated_forward": (_int, [_vp, _i64] * 3 + [_int, _i64, _i64, _i64, _int] + [_vp, _i64] * 3 + [_vp, _sz, _vp]),
+        "kq_gated_backward": (_int, [_vp, _i64] * 6 + [_int, _i64, _i64, _i64, _int] + [_vp, _i64] * 5 + [_vp, _sz, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -284,3 +293,173 @@ def kq_allocate_bits(scores, sizes, budget: float = 3.0, bmin: int = 2, bmax: in
                                                       sz.ctypes.data_as(ctypes.POINTER(_i64)), len(sc), budget, bmin,
                                                       bmax, out.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))))
     return out
+
+
+# ------------------------------------------------- microscaled 4-bit products and the gated block
+# These wrappers also check what the C calls cannot see: types, shapes, devices and the memory behind a
+# view (rows are read in whole 16-byte pieces).
+def _matrix(name: str, what: str, t, rows: int, cols: int, dtypes, size: int = 0):
+    """Checks a row-major rows x cols matrix; returns (pointer, leading dimension in elements)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {what} has type {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: {what} is not on a GPU")
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: {what} is not row-major")
+    # the stride of a single row is arbitrary: any legal one will do
+    per = 16 // t.element_size()
+    ld = t.stride(0) if rows > 1 else -(-max(cols, size) // per) * per
+    if rows and size > cols:
+        end = t.storage_offset() + (rows - 1) * ld + size
+        if end * t.element_size() > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the last row of {what} ends inside its 16 bytes, past the storage")
+    return t.data_ptr(), ld
+
+
+def _whole(cols: int, t) -> int:
+    per = 16 // t.element_size()
+    return -(-cols // per) * per
+
+
+def _launch(name: str, tensors, stream, args) -> None:
+    """Calls `name` with args + [stream] on the tensors' device (one for all of them)."""
+    import torch
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"{name}: operands on different devices: {sorted(map(str, devs))}")
+    dev = devs.pop()
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"{name}: the stream is on {s.device}, the operands on {dev}")
+    with torch.cuda.device(dev):
+        _check(name, getattr(lib(), name)(*args, s.cuda_stream))
+
+
+def mx_empty(rows: int, cols: int, device):
+    """Buffers for a rows x cols matrix in the microscaled format: codes (16 bytes per 32 columns) and
+    scales (one byte per 32 columns, rows padded to 4 bytes), both uint8, contents undefined."""
+    import torch
+    nblk = -(-cols // 32)
+    return (torch.empty((rows, 16 * nblk), dtype=torch.uint8, device=device),
+            torch.empty((rows, -(-nblk // 4) * 4), dtype=torch.uint8, device=device))
+
+
+def _mx(name: str, what: str, codes, scales, cols: int):
+    """Checks a microscaled operand of `cols` columns; returns its four C arguments."""
+    import torch
+    nblk = -(-cols // 32)
+    for t, w in ((codes, "codes"), (scales, "scales")):
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name}: {what} {w} have type {t.dtype}, not uint8")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: {what} {w} are not on a GPU")
+        if t.dim() != 2 or t.shape[0] != codes.shape[0] or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: {what} {w} must be row-major, one row for each of the matrix")
+    if codes.shape[1] != 16 * nblk or not nblk <= scales.shape[1] <= -(-nblk // 4) * 4:
+        raise ValueError(f"{name}: {what} of {cols} columns needs 16 * {nblk} bytes of codes and {nblk} scales a row "
+                         f"(mx_empty), not {codes.shape[1]} and {scales.shape[1]}")
+    rows = codes.shape[0]
+    ldc = codes.stride(0) if rows > 1 else 16 * nblk
+    lds = scales.stride(0) if rows > 1 else -(-nblk // 4) * 4
+    if rows and scales.storage_offset() + (rows - 1) * lds + -(-nblk // 4) * 4 > scales.untyped_storage().nbytes():
+        raise ValueError(f"{name}: the last scale row of {what} ends inside its 4 bytes, past the storage")
+    return [codes.data_ptr(), ldc, scales.data_ptr(), lds]
+
+
+def _floats():
+    import torch
+    return (torch.float32, torch.bfloat16)
+
+
+def _act(name: str, act: str) -> int:
+    if act not in ACT:
+        raise ValueError(f"{name}: activation {act!r} is none of {sorted(ACT)}")
+    return ACT[act]
+
+
+def kq_mx_quantize(X, codes, scales, stream=None) -> None:
+    """X (rows x cols, fp32 or bf16) into codes and scales of mx_empty(rows, cols)."""
+    name = "kq_mx_quantize"
+    rows, cols = X.shape
+    p, ld = _matrix(name, "X", X, rows, cols, _floats())
+    if codes.shape[0] != rows:
+        raise ValueError(f"{name}: {codes.shape[0]} rows of codes for {rows} rows")
+    c = _mx(name, "the output", codes, scales, cols)
+    _launch(name, (X, codes, scales), stream, [p, _xdt(X), rows, cols, ld, *c])
+
+
+def kq_mx_dequantize(codes, scales, Y, stream=None) -> None:
+    """The values that codes and scales stand for, into Y (rows x cols, fp32 or bf16)."""
+    name = "kq_mx_dequantize"
+    rows, cols = Y.shape
+    p, ld = _matrix(name, "Y", Y, rows, cols, _floats())
+    if codes.shape[0] != rows:
+        raise ValueError(f"{name}: {codes.shape[0]} rows of codes for {rows} rows")
+    c = _mx(name, "the input", codes, scales, cols)
+    _launch(name, (codes, scales, Y), stream, [*c, rows, cols, p, _xdt(Y), ld])
+
+
+def kq_mx_gemm(Ac, As, Bc, Bs, i: int, Y, ws=None, stream=None) -> None:
+    """Y (n x o, fp32 or bf16) = A B^T for microscaled A (n x i) and B (o x i)."""
+    name = "kq_mx_gemm"
+    n, o = Ac.shape[0], Bc.shape[0]
+    p, ld = _matrix(name, "Y", Y, n, o, _floats())
+    w, wb = _ws(ws)
+    _launch(name, (Ac, As, Bc, Bs, Y, ws), stream,
+            [*_mx(name, "A", Ac, As, i), *_mx(name, "B", Bc, Bs, i), n, o, i, p, _xdt(Y), ld, w, wb])
+
+
+def kq_mx_gated(Xc, Xs, Gc, Gs, Uc, Us, i: int, act: str, H, ws=None, stream=None) -> None:
+    """H (n x o, fp32 or bf16) = act(X G^T) * (X U^T) for microscaled X (n x i), G and U (o x i)."""
+    name = "kq_mx_gated"
+    n, o = Xc.shape[0], Gc.shape[0]
+    if Uc.shape[0] != o:
+        raise ValueError(f"{name}: {o} gate rows and {Uc.shape[0]} up rows")
+    p, ld = _matrix(name, "H", H, n, o, _floats())
+    w, wb = _ws(ws)
+    _launch(name, (Xc, Xs, Gc, Gs, Uc, Us, H, ws), stream,
+            [*_mx(name, "X", Xc, Xs, i), *_mx(name, "gate weights", Gc, Gs, i), *_mx(name, "up weights", Uc, Us, i),
+             n, o, i, _act(name, act), p, _xdt(H), ld, w, wb])
+
+
+def kq_gated_forward(X, Wg, Wu, act: str, H, A=None, B=None, ws=None, stream=None) -> None:
+    """H = act(X Wg^T) * (X Wu^T); A and B, where given, take the two products. One type for all."""
+    name = "kq_gated_forward"
+    (n, i), o = X.shape, Wg.shape[0]
+    dt, wi = (X.dtype,), _whole(i, X)
+    if X.dtype not in _floats():
+        raise TypeError(f"{name}: X has type {X.dtype}")
+    ins = [_matrix(name, w, t, r, i, dt, wi) for w, t, r in (("X", X, n), ("Wg", Wg, o), ("Wu", Wu, o))]
+    outs = [(None, 0) if t is None else _matrix(name, w, t, n, o, dt) for w, t in (("H", H), ("A", A), ("B", B))]
+    w, wb = _ws(ws)
+    _launch(name, (X, Wg, Wu, H, A, B, ws), stream,
+            [*sum(ins, ()), _xdt(X), n, o, i, _act(name, act), *sum(outs, ()), w, wb])
+
+
+def kq_gated_backward(dH, A, B, X, Wg, Wu, act: str, dA, dB, dX=None, dWg=None, dWu=None, ws=None, stream=None) -> None:
+    """Gradients of kq_gated_forward from dH and the A and B that it kept: dA and dB always, dX, dWg and
+    dWu where given (X may be None without weight gradients, Wg and Wu without dX)."""
+    name = "kq_gated_backward"
+    n, o = dH.shape
+    if dH.dtype not in _floats():
+        raise TypeError(f"{name}: dH has type {dH.dtype}")
+    some = next((t for t in (dX, dWg, dWu, X, Wg, Wu) if t is not None), None)
+    i = 1 if some is None else some.shape[1]
+    dt, wi, wo = (dH.dtype,), _whole(i, dH), _whole(o, dH)
+    if dX is not None and (Wg is None or Wu is None):
+        raise ValueError(f"{name}: dX needs Wg and Wu")
+    if (dWg is not None or dWu is not None) and X is None:
+        raise ValueError(f"{name}: weight gradients need X")
+
+    def take(what, t, rows, cols, size=0):
+        return (None, 0) if t is None else _matrix(name, what, t, rows, cols, dt, size)
+
+    args = [*take("dH", dH, n, o), *take("A", A, n, o), *take("B", B, n, o), *take("X", X, n, i),
+            *take("Wg", Wg, o, i), *take("Wu", Wu, o, i), _xdt(dH), n, o, i, _act(name, act),
+            *take("dA", dA, n, o, wo), *take("dB", dB, n, o, wo), *take("dX", dX, n, i), *take("dWg", dWg, o, i),
+            *take("dWu", dWu, o, i)]
+    del wi
+    w, wb = _ws(ws)
+    _launch(name, (dH, A, B, X, Wg, Wu, dA, dB, dX, dWg, dWu, ws), stream, [*args, w, wb])

@@ -19,6 +19,9 @@ size_t hg_lowrank_ws(int64_t n, int64_t o, int64_t k);
 size_t kfac_loss_ws(int64_t o, int64_t i, kq_hg_form form, int64_t blk);
 size_t cross_ws(int64_t n, int64_t d);
 size_t drift_ws(int64_t o, int64_t i);
+size_t mx_product_ws(int64_t o, int64_t i, int64_t n, bool gated);
+size_t gated_forward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt);
+size_t gated_backward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt);
 
 namespace kq {
 
@@ -82,6 +85,10 @@ extern "C" size_t kq_workspace_bytes(kq_op op, int64_t o, int64_t i, int64_t n, 
         case KQ_OP_KFAC_LOSS: return kfac_loss_ws(o, i, form, blk);
         case KQ_OP_CROSS: return cross_ws(n, i);
         case KQ_OP_DRIFT: return drift_ws(o, i);
+        case KQ_OP_MX_GEMM: return mx_product_ws(o, i, n, false);
+        case KQ_OP_MX_GATED: return mx_product_ws(o, i, n, true);
+        case KQ_OP_GATED_FORWARD: return gated_forward_ws(o, i, n, xdt);
+        case KQ_OP_GATED_BACKWARD: return gated_backward_ws(o, i, n, xdt);
     }
     return 0;
 }

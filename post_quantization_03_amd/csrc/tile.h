@@ -1,0 +1,654 @@
+// Matrix-core products shared by the microscaled 4-bit operators (mx.hip) and the gated feed-forward
+// block (gated.hip). Not part of the C ABI.
+//
+// Every operand is handled in 16-byte chunks along its rows: 4 fp32, 8 bf16 or 32 E2M1 values (one
+// microscaled block). A lane of an MFMA operand holds exactly one chunk, lane group g = lane / 16
+// owning chunk g of four, so one step of four chunks is
+//   fp32   four v_mfma_f32_16x16x4_f32          (16 columns of K; element e of every chunk pairs up)
+//   bf16   one  v_mfma_f32_16x16x32_bf16        (32 columns)
+//   E2M1   one  v_mfma_scale_f32_16x16x128      (128 columns, one E8M0 scale byte per lane)
+// and one slab of 128 bytes a row is two steps whatever the type: the staging, the LDS layout and the
+// loops below are written once for the three.
+#pragma once
+
+#include "kq_internal.h"
+
+namespace kq {
+
+typedef float tl_f4 __attribute__((ext_vector_type(4)));
+typedef int tl_i4 __attribute__((ext_vector_type(4)));
+typedef int tl_i8 __attribute__((ext_vector_type(8)));
+typedef short tl_s4 __attribute__((ext_vector_type(4)));
+typedef __bf16 tl_b8 __attribute__((ext_vector_type(8)));
+
+enum { EL_F32 = 0, EL_BF16 = 1, EL_MX = 2 };
+template <int E>
+constexpr int el_chunk() { return E == EL_F32 ? 4 : E == EL_BF16 ? 8 : 32; }   // values in 16 bytes
+
+// ------------------------------------------------------------------------------------ conversions
+__device__ __forceinline__ uint16_t to_bf16(float v) {   // nearest even, NaN stays NaN
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+__device__ __forceinline__ float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// N consecutive values (N a multiple of 4) to dst[0 .. N-1] of row-major out, those below `left` only. dst is
+// aligned to min(4 N, 16) bytes for fp32 and to min(2 N, 16) for bf16 when left >= N.
+template <int N>
+__device__ __forceinline__ void store_run(void* out, int dt, int64_t off, const float (&v)[N], int64_t left) {
+    if (dt == KQ_BF16) {
+        uint16_t* p = static_cast<uint16_t*>(out) + off;
+        if (left >= N) {
+            uint32_t w[N / 2];
+#pragma unroll
+            for (int e = 0; e < N / 2; e++) w[e] = (uint32_t)to_bf16(v[2 * e]) | ((uint32_t)to_bf16(v[2 * e + 1]) << 16);
+            if constexpr (N % 8 == 0) {
+#pragma unroll
+                for (int e = 0; e < N / 8; e++)
+                    reinterpret_cast<uint4*>(p)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N / 4; e++) reinterpret_cast<uint2*>(p)[e] = make_uint2(w[2 * e], w[2 * e + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                if (e < left) p[e] = to_bf16(v[e]);
+        }
+    } else {
+        float* p = static_cast<float*>(out) + off;
+        if (left >= N) {
+#pragma unroll
+            for (int e = 0; e < N / 4; e++)
+                reinterpret_cast<float4*>(p)[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                if (e < left) p[e] = v[e];
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------- activations
+// gate = act(a) / a, the factor in 0..1 that multiplies a
+__device__ __forceinline__ float act_gate(float a, int act) {
+    switch (act) {
+        case KQ_ACT_SILU: return 1.0f / (1.0f + expf(-a));
+        case KQ_ACT_GELU: return 0.5f * erfcf(-0.70710678118654752f * a);
+        case KQ_ACT_GELU_TANH: return 1.0f / (1.0f + expf(-1.5957691216057308f * (a + 0.044715f * a * a * a)));
+        default: return a > 0.0f ? 1.0f : (a == a ? 0.0f : a);
+    }
+}
+__device__ __forceinline__ float act_value(float a, int act) { return a * act_gate(a, act); }
+
+// act(a) and act'(a)
+__device__ __forceinline__ void act_both(float a, int act, float& f, float& df) {
+    const float p = act_gate(a, act);
+    f = a * p;
+    switch (act) {
+        case KQ_ACT_SILU: df = p * (1.0f + a * (1.0f - p)); return;
+        case KQ_ACT_GELU: df = p + a * expf(-0.5f * a * a) * 0.39894228040143268f; return;
+        case KQ_ACT_GELU_TANH:
+            // beyond 16 the gate is 0 or 1 to the last bit, and a * a may not be finite
+            df = fabsf(a) > 16.0f ? p : p + a * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * a * a);
+            return;
+        default: df = p;
+    }
+}
+
+// --------------------------------------------------------------------------------------- products
+template <int OA, int OB>
+__device__ __forceinline__ tl_f4 mma_mx(tl_i4 a, tl_i4 b, tl_f4 c, int sa, int sb) {
+    const tl_i8 a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, OA, sa, OB, sb);
+}
+
+// c += a b over one step; for E2M1 byte oa of sa and byte ob of sb are the lane's block scales
+// (oa and ob are constants after unrolling)
+template <int E>
+__device__ __forceinline__ tl_f4 mma_step(tl_i4 a, tl_i4 b, tl_f4 c, int sa, int oa, int sb, int ob) {
+    if constexpr (E == EL_BF16) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(tl_b8, a), __builtin_bit_cast(tl_b8, b), c, 0, 0, 0);
+    } else if constexpr (E == EL_F32) {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__int_as_float(a[e]), __int_as_float(b[e]), c, 0, 0, 0);
+        return c;
+    } else {
+        switch (4 * oa + ob) {
+            case 0: return mma_mx<0, 0>(a, b, c, sa, sb);
+            case 1: return mma_mx<0, 1>(a, b, c, sa, sb);
+            case 2: return mma_mx<0, 2>(a, b, c, sa, sb);
+            case 3: return mma_mx<0, 3>(a, b, c, sa, sb);
+            case 4: return mma_mx<1, 0>(a, b, c, sa, sb);
+            case 5: return mma_mx<1, 1>(a, b, c, sa, sb);
+            case 6: return mma_mx<1, 2>(a, b, c, sa, sb);
+            case 7: return mma_mx<1, 3>(a, b, c, sa, sb);
+            case 8: return mma_mx<2, 0>(a, b, c, sa, sb);
+            case 9: return mma_mx<2, 1>(a, b, c, sa, sb);
+            case 10: return mma_mx<2, 2>(a, b, c, sa, sb);
+            case 11: return mma_mx<2, 3>(a, b, c, sa, sb);
+            case 12: return mma_mx<3, 0>(a, b, c, sa, sb);
+            case 13: return mma_mx<3, 1>(a, b, c, sa, sb);
+            case 14: return mma_mx<3, 2>(a, b, c, sa, sb);
+            default: return mma_mx<3, 3>(a, b, c, sa, sb);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------ tiles
+// What a tile product computes:
+//   TP_PLAIN   Y = A B^T                        A: M x K, B: N x K
+//   TP_GATED   Y = act(A B^T) * (A B2^T), optionally the two products themselves
+//   TP_GRAD_X  Y = A B + A2 B2                  A: M x K, B: K x N
+//   TP_GRAD_W  Y = A^T B, Y2 = A2^T B           A: K x M, B: K x N     (blockIdx.z picks the pair)
+enum { TP_PLAIN = 0, TP_GATED = 1, TP_GRAD_X = 2, TP_GRAD_W = 3 };
+
+struct TileArgs {
+    int64_t M, N, K;                     // K in values
+    const char *A, *A2, *B, *B2;
+    int64_t lda, lda2, ldb, ldb2;        // bytes
+    const uint32_t *sA, *sB;             // E2M1: scales laid out by mx_layout (ksteps dwords x 64 lanes a group)
+    int64_t ksteps;                      // E2M1: steps of 128 values (an even number)
+    void *Y, *Y2, *Y3;
+    int64_t ldy, ldy2, ldy3;             // values
+    int dt;                              // type of the outputs
+    int act;
+};
+
+constexpr int TL_M = 256, TL_N = 256;    // output tile (TL_N rows of B; half gate and half up when gated)
+constexpr int TL_THREADS = 512;          // 8 wavefronts as 2 x 4, each 128 x 64
+constexpr int TL_FM = 8, TL_FN = 4;      // 16 x 16 fragments of a wavefront
+constexpr int TL_OPB = 256 * 128;        // bytes of one operand's slab in LDS
+constexpr size_t TL_SMEM = size_t(4) * TL_OPB;
+// Offsets inside a tile's 256 rows (or 64 K rows) are 32-bit, everything else 64-bit: rows of at most 4 MiB.
+constexpr int64_t TL_LD_MAX = 4 << 20, TL_ROWS_MAX = 1LL << 31;
+
+// Tile of a work-group. Work-groups are dealt to the 8 XCDs in turn, so the linear id is remapped to give
+// each XCD one contiguous range; inside it tiles run in groups of TL_GROUP tile rows, column by column,
+// so that a group's panels of A and B stay in that XCD's L2.
+constexpr int TL_GROUP = 8;
+__device__ __forceinline__ void tile_of(int lid, int ny, int nx, int64_t& tm, int64_t& tn) {
+    const int L = nx * ny, per = L / 8, rem = L % 8, x = lid % 8;
+    lid = x * per + (x < rem ? x : rem) + lid / 8;
+    const int grp = lid / (TL_GROUP * nx), r0 = grp * TL_GROUP;
+    const int rows = ny - r0 < TL_GROUP ? ny - r0 : TL_GROUP;
+    const int in = lid - grp * TL_GROUP * nx;
+    tm = r0 + in % rows;
+    tn = in / rows;
+}
+
+// Row of B (inside a wavefront's 64, or inside its 32 gate or 32 up rows) that index x of fragment j holds.
+// A lane of the result holds rows 4 g .. 4 g + 3 of every fragment, so with this order it holds 4 * FNH
+// consecutive output columns: 16-byte stores, and a row segment of whole cache lines a wavefront.
+template <int FNH>
+__device__ __forceinline__ int b_row(int j, int x) { return (x >> 2) * (4 * FNH) + 4 * j + (x & 3); }
+
+// LDS, operand contiguous along K: rows of 128 bytes, chunk c of row r at position c ^ key(r). The 16 rows
+// of a fragment then spread over the banks. For A fragments hold consecutive rows; for B the rows of b_row.
+__device__ __forceinline__ int key_a(int r) { return r & 7; }
+template <int FNH>
+__device__ __forceinline__ int key_b(int r) { return (r & 3) | (((r / (4 * FNH)) & 1) << 2); }
+
+// LDS, bf16 operand contiguous along M or N ("transposed"): K rows of 512 bytes (256 values), 32-byte pair
+// p of K row k at position p ^ key_t(k). A transposing read takes 16 K rows of one pair at once: 16
+// different positions.
+__device__ __forceinline__ int key_t(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __attribute__((address_space(1))) void* glb_ptr;
+
+__device__ __forceinline__ void dma16(const char* src, char* lds) {
+    __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)lds, 16, 0, 0);
+}
+
+template <int E, int MODE>
+__global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
+    extern __shared__ __align__(16) char tl_sm[];
+    constexpr bool TA = MODE == TP_GRAD_W, TB = MODE == TP_GRAD_X || MODE == TP_GRAD_W;
+    static_assert(!TB || E == EL_BF16, "transposed operands are bf16");
+    constexpr int EPC = el_chunk<E>(), BK = 8 * EPC;
+    constexpr int FNH = MODE == TP_GATED ? TL_FN / 2 : TL_FN;
+    constexpr int TN_OUT = MODE == TP_GATED ? TL_N / 2 : TL_N;       // output columns of a tile
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int x16 = lane & 15, g4 = lane >> 4;
+    const int wm = wave >> 2, wn = wave & 3;
+    int64_t tm, tn;
+    tile_of((int)blockIdx.x, (int)((g.M + TL_M - 1) / TL_M), (int)((g.N + TN_OUT - 1) / TN_OUT), tm, tn);
+    const int64_t m0 = tm * TL_M, n0 = tn * TN_OUT;
+    const int mlast = (int)(g.M - 1 - m0 < TL_M - 1 ? g.M - 1 - m0 : TL_M - 1);          // last row inside
+    const int nlast = (int)(g.N - 1 - n0 < TN_OUT - 1 ? g.N - 1 - n0 : TN_OUT - 1);
+
+    // ---- staging: 4 loads of 16 bytes a lane and operand; load q of a wavefront fills KiB q * 8 + wave
+    const char *pA = MODE == TP_GRAD_W && blockIdx.z ? g.A2 : g.A, *pB = g.B;
+    const int64_t ldA = MODE == TP_GRAD_W && blockIdx.z ? g.lda2 : g.lda;
+    pA += TA ? m0 * 2 : m0 * ldA;
+    pB += TB ? n0 * 2 : n0 * g.ldb;
+    const char* pA2 = MODE == TP_GRAD_X ? g.A2 + m0 * g.lda2 : nullptr;
+    const char* pB2 = MODE == TP_GRAD_X ? g.B2 + n0 * 2 : MODE == TP_GATED ? g.B2 + n0 * g.ldb2 : nullptr;
+    uint32_t offA[4], offB[4], offA2[4], offB2[4];
+    int cA, cB[4];                       // chunk (K-contiguous operands) that the lane loads
+    {
+        const int r8 = lane >> 3, pos = lane & 7;
+        cA = pos ^ r8;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int r = (q * 8 + wave) * 8 + r8;
+            if constexpr (TA) {
+                const int k = (q * 8 + wave) * 2 + (lane >> 5), p = lane & 31;
+                int c = (((p >> 1) ^ key_t(k)) << 1) | (p & 1);
+                c = c * 8 <= mlast ? c : mlast >> 3;
+                offA[q] = (uint32_t)((int64_t)k * ldA + c * 16);
+            } else {
+                const int rr = r < mlast ? r : mlast;
+                offA[q] = (uint32_t)((int64_t)rr * ldA);
+                if constexpr (MODE == TP_GRAD_X) offA2[q] = (uint32_t)((int64_t)rr * g.lda2);
+            }
+            if constexpr (TB) {
+                const int k = (q * 8 + wave) * 2 + (lane >> 5), p = lane & 31;
+                int c = (((p >> 1) ^ key_t(k)) << 1) | (p & 1);
+                c = c * 8 <= nlast ? c : nlast >> 3;
+                offB[q] = (uint32_t)((int64_t)k * g.ldb + c * 16);
+                if constexpr (MODE == TP_GRAD_X) offB2[q] = (uint32_t)((int64_t)k * g.ldb2 + c * 16);
+            } else {
+                cB[q] = pos ^ key_b<FNH>(r);
+                // gated: rows 0..127 of the slab are gate rows (q < 2), 128..255 up rows
+                int rr = MODE == TP_GATED ? r & 127 : r;
+                rr = rr < nlast ? rr : nlast;
+                offB[q] = (uint32_t)((int64_t)rr * (MODE == TP_GATED && q >= 2 ? g.ldb2 : g.ldb));
+            }
+        }
+    }
+    const int64_t nch = (g.K + EPC - 1) / EPC;           // chunks of K, the last one possibly partial
+    const int part = E == EL_MX ? 0 : (int)(g.K % EPC);  // values in a partial last chunk (E2M1 blocks are whole)
+    const int64_t slabs1 = (g.K + BK - 1) / BK, slabs = MODE == TP_GRAD_X ? 2 * slabs1 : slabs1;
+
+    // slab t into buffer buf. K-contiguous operands: chunks past K become zero (E2M1: a valid chunk is read
+    // again; its scales are zero on both sides, so its products vanish). Transposed ones: K rows past K
+    // become zero. Rows and columns past M and N repeat the last one and are never stored.
+    auto stage = [&](int64_t t, int buf) {
+        char* la = tl_sm + buf * 2 * TL_OPB + wave * 1024;
+        char* lb = la + TL_OPB;
+        const bool second = MODE == TP_GRAD_X && t >= slabs1;
+        const int64_t s = second ? t - slabs1 : t;
+        const char* a0 = second ? pA2 : pA;
+        const char* b0 = second ? pB2 : pB;
+        const int64_t la_ld = second ? g.lda2 : ldA, lb_ld = second ? g.ldb2 : g.ldb;
+        const bool whole = (s + 1) * BK <= g.K;
+        if (whole) {
+            a0 += TA ? s * BK * la_ld : s * 128;
+            b0 += TB ? s * BK * lb_ld : s * 128;
+            const char* b2 = MODE == TP_GATED ? pB2 + s * 128 : nullptr;
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const uint32_t oa = second ? offA2[q] : offA[q];
+                dma16(a0 + (TA ? oa : oa + cA * 16), la + q * 8192);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const uint32_t ob = second ? offB2[q] : offB[q];
+                const char* b = MODE == TP_GATED && q >= 2 ? b2 : b0;
+                dma16(b + (TB ? ob : ob + cB[q] * 16), lb + q * 8192);
+            }
+            return;
+        }
+        const tl_i4 zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint32_t oa = second ? offA2[q] : offA[q];
+            if constexpr (TA) {
+                const int64_t k = s * BK + (q * 8 + wave) * 2 + (lane >> 5);
+                if (k < g.K) dma16(a0 + s * BK * la_ld + oa, la + q * 8192);
+                else *reinterpret_cast<tl_i4*>(la + q * 8192 + lane * 16) = zero;
+            } else {
+                int64_t c = s * 8 + cA;
+                if (E == EL_MX && c >= nch) c = nch - 1;
+                if (c < nch) dma16(a0 + oa + c * 16, la + q * 8192);
+                else *reinterpret_cast<tl_i4*>(la + q * 8192 + lane * 16) = zero;
+            }
+            const uint32_t ob = second ? offB2[q] : offB[q];
+            if constexpr (TB) {
+                const int64_t k = s * BK + (q * 8 + wave) * 2 + (lane >> 5);
+                if (k < g.K) dma16(b0 + s * BK * lb_ld + ob, lb + q * 8192);
+                else *reinterpret_cast<tl_i4*>(lb + q * 8192 + lane * 16) = zero;
+            } else {
+                int64_t c = s * 8 + cB[q];
+                if (E == EL_MX && c >= nch) c = nch - 1;
+                const char* b = MODE == TP_GATED && q >= 2 ? pB2 : b0;
+                if (c < nch) dma16(b + ob + c * 16, lb + q * 8192);
+                else *reinterpret_cast<tl_i4*>(lb + q * 8192 + lane * 16) = zero;
+            }
+        }
+    };
+    // values past K of a partial last chunk, once it has landed: each lane clears its own chunks
+    auto clear_part = [&](int64_t t, int buf) {
+        const int64_t s = MODE == TP_GRAD_X && t >= slabs1 ? t - slabs1 : t;
+        if (s != slabs1 - 1) return;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        char* la = tl_sm + buf * 2 * TL_OPB + wave * 1024 + lane * 16;
+        auto cut = [&](char* p) {
+            tl_i4 v = *reinterpret_cast<tl_i4*>(p);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                if constexpr (E == EL_F32) v[e] = e < part ? v[e] : 0;
+                else v[e] = 2 * e + 1 < part ? v[e] : 2 * e < part ? v[e] & 0xFFFF : 0;
+            }
+            *reinterpret_cast<tl_i4*>(p) = v;
+        };
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            if constexpr (!TA)
+                if (s * 8 + cA == nch - 1) cut(la + q * 8192);
+            if constexpr (!TB)
+                if (s * 8 + cB[q] == nch - 1) cut(la + TL_OPB + q * 8192);
+        }
+    };
+
+    tl_f4 acc[TL_FM][TL_FN];
+#pragma unroll
+    for (int i = 0; i < TL_FM; i++)
+#pragma unroll
+        for (int j = 0; j < TL_FN; j++) acc[i][j] = tl_f4{0, 0, 0, 0};
+
+    // scales of a slab's two steps (E2M1): a dword holds a lane's bytes of four fragments
+    uint32_t scA[2][2], scB[2], nxA[2][2], nxB[2];
+    const uint32_t *qA = nullptr, *qB = nullptr;
+    if constexpr (E == EL_MX) {
+        qA = g.sA + (tm * 4 + wm * 2) * g.ksteps * 64 + lane;
+        qB = g.sB + (tn * 4 + wn) * g.ksteps * 64 + lane;
+    }
+    auto load_scales = [&](int64_t t) {
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            nxA[0][s] = qA[(2 * t + s) * 64];
+            nxA[1][s] = qA[(g.ksteps + 2 * t + s) * 64];
+            nxB[s] = qB[(2 * t + s) * 64];
+        }
+    };
+
+    auto fragA = [&](const char* la, int i, int s) -> tl_i4 {
+        if constexpr (TA) {
+            const int k = 32 * s + 8 * g4 + (x16 >> 2), piece = x16 & 3;
+            tl_i4 r;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int kk = k + 4 * h, p = wm * 8 + i;
+                const char* a = la + kk * 512 + (((p ^ key_t(kk)) << 1) | (piece >> 1)) * 16 + (piece & 1) * 8;
+                const tl_s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)a);
+                reinterpret_cast<tl_s4*>(&r)[h] = v;
+            }
+            return r;
+        } else {
+            const int r = wm * 128 + 16 * i + x16;
+            return *reinterpret_cast<const tl_i4*>(la + r * 128 + (((s * 4 + g4) ^ key_a(r)) << 4));
+        }
+    };
+    auto fragB = [&](const char* lb, int j, int s) -> tl_i4 {
+        if constexpr (TB) {
+            const int k = 32 * s + 8 * g4 + (x16 >> 2), piece = x16 & 3;
+            tl_i4 r;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int kk = k + 4 * h, p = wn * 4 + j;
+                const char* a = lb + kk * 512 + (((p ^ key_t(kk)) << 1) | (piece >> 1)) * 16 + (piece & 1) * 8;
+                const tl_s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)a);
+                reinterpret_cast<tl_s4*>(&r)[h] = v;
+            }
+            return r;
+        } else {
+            const int r = MODE == TP_GATED ? (j >= FNH ? 128 : 0) + wn * 32 + b_row<FNH>(j % FNH, x16)
+                                           : wn * 64 + b_row<FNH>(j, x16);
+            return *reinterpret_cast<const tl_i4*>(lb + r * 128 + (((s * 4 + g4) ^ key_b<FNH>(r)) << 4));
+        }
+    };
+
+    stage(0, 0);
+    if constexpr (E == EL_MX) load_scales(0);
+    int buf = 0;
+    for (int64_t t = 0; t < slabs; t++) {
+        if (part && (!TA || !TB)) clear_part(t, buf);
+        __syncthreads();      // slab t has landed, and every wavefront is done with slab t - 1
+        if constexpr (E == EL_MX) {
+#pragma unroll
+            for (int s = 0; s < 2; s++) {
+                scA[0][s] = nxA[0][s];
+                scA[1][s] = nxA[1][s];
+                scB[s] = nxB[s];
+            }
+        }
+        if (t + 1 < slabs) {
+            stage(t + 1, buf ^ 1);
+            if constexpr (E == EL_MX) load_scales(t + 1);
+        }
+        const char* la = tl_sm + buf * 2 * TL_OPB;
+        const char* lb = la + TL_OPB;
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            tl_i4 fa[TL_FM], fb[TL_FN];
+#pragma unroll
+            for (int j = 0; j < TL_FN; j++) fb[j] = fragB(lb, j, s);
+#pragma unroll
+            for (int i = 0; i < TL_FM; i++) fa[i] = fragA(la, i, s);
+#pragma unroll
+            for (int i = 0; i < TL_FM; i++)
+#pragma unroll
+                for (int j = 0; j < TL_FN; j++) {
+                    // rows of the result are B's rows (output columns), columns are A's rows
+                    if constexpr (E == EL_MX)
+                        acc[i][j] = mma_step<E>(fb[j], fa[i], acc[i][j], (int)scB[s], j, (int)scA[i >> 2][s], i & 3);
+                    else
+                        acc[i][j] = mma_step<E>(fb[j], fa[i], acc[i][j], 0, 0, 0, 0);
+                }
+        }
+        buf ^= 1;
+    }
+
+    // ---- epilogue: lane holds output row x16 of fragment row i, columns as b_row (or 16 j + 4 g4 when transposed)
+    void* Y = MODE == TP_GRAD_W && blockIdx.z ? g.Y2 : g.Y;
+    const int64_t ldY = MODE == TP_GRAD_W && blockIdx.z ? g.ldy2 : g.ldy;
+#pragma unroll
+    for (int i = 0; i < TL_FM; i++) {
+        const int64_t m = m0 + wm * 128 + 16 * i + x16;
+        if (m >= g.M) continue;
+        if constexpr (MODE == TP_GATED) {
+            const int64_t n = n0 + wn * 32 + g4 * (4 * FNH);
+            float h[4 * FNH], a[4 * FNH], b[4 * FNH];
+#pragma unroll
+            for (int j = 0; j < FNH; j++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    a[4 * j + r] = acc[i][j][r];
+                    b[4 * j + r] = acc[i][j + FNH][r];
+                    h[4 * j + r] = act_value(a[4 * j + r], g.act) * b[4 * j + r];
+                }
+            store_run<4 * FNH>(Y, g.dt, m * ldY + n, h, g.N - n);
+            if (g.Y2) store_run<4 * FNH>(g.Y2, g.dt, m * g.ldy2 + n, a, g.N - n);
+            if (g.Y3) store_run<4 * FNH>(g.Y3, g.dt, m * g.ldy3 + n, b, g.N - n);
+        } else if constexpr (TB) {
+#pragma unroll
+            for (int j = 0; j < TL_FN; j++) {
+                const int64_t n = n0 + wn * 64 + 16 * j + 4 * g4;
+                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                store_run<4>(Y, g.dt, m * ldY + n, v, g.N - n);
+            }
+        } else {
+            const int64_t n = n0 + wn * 64 + g4 * (4 * FNH);
+            float v[4 * FNH];
+#pragma unroll
+            for (int j = 0; j < FNH; j++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) v[4 * j + r] = acc[i][j][r];
+            store_run<4 * FNH>(Y, g.dt, m * ldY + n, v, g.N - n);
+        }
+    }
+}
+
+template <int E, int MODE>
+kq_status tile_launch(const TileArgs& g, int pairs, hipStream_t st, const char* who) {
+    constexpr int TN_OUT = MODE == TP_GATED ? TL_N / 2 : TL_N;
+    const int64_t tiles = ((g.M + TL_M - 1) / TL_M) * ((g.N + TN_OUT - 1) / TN_OUT);
+    if (tiles > (1LL << 27)) return fail(KQ_ESHAPE, "%s: too many tiles", who);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_kernel<E, MODE>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)TL_SMEM);
+    if (e != hipSuccess) return fail(KQ_EHIP, "%s: %s", who, hipGetErrorString(e));
+    hipLaunchKernelGGL((tile_kernel<E, MODE>), dim3((unsigned)tiles, 1, (unsigned)pairs), dim3(TL_THREADS), TL_SMEM, st, g);
+    return check_launch(who);
+}
+
+// ------------------------------------------------------------------------------------- few tokens
+// Y (or the gated block) for up to 64 rows of A: the weights are read once, straight into registers, and
+// that stream is what bounds the call. A work-group owns 16 rows of B (and of B2); its 8 wavefronts take
+// the 128-byte slabs of K in turn and their sums meet in LDS, in wavefront order. The rows of A (tokens)
+// are few and come from L2.
+struct FewArgs {
+    int64_t n, o, K;                      // tokens, rows of B, values of K
+    const char *A, *B, *B2;
+    int64_t lda, ldb, ldb2;               // bytes
+    const uint8_t *sA, *sB, *sB2;         // E2M1: E8M0 bytes, rows of lds* bytes
+    int64_t ldsa, ldsb, ldsb2;
+    void *Y, *Y2, *Y3;
+    int64_t ldy, ldy2, ldy3;
+    int dt, act;
+};
+
+constexpr int FEW_WAVES = 8, FEW_THREADS = 64 * FEW_WAVES, FEW_MAX = 64;
+
+template <int E>
+struct FewFrag {
+    tl_i4 c[2];       // chunks g4 and 4 + g4 of a slab
+    uint32_t s[2];    // E2M1: the scale bytes of the two
+};
+
+// Chunks of one row's slab s. `whole`: all eight chunks are full.
+template <int E>
+__device__ __forceinline__ void few_load(FewFrag<E>& f, const char* row, const uint8_t* srow, int64_t s, int g4,
+                                         bool whole, int64_t nch, int part) {
+    const char* p = row + s * 128 + g4 * 16;
+    if (whole) {
+        f.c[0] = *reinterpret_cast<const tl_i4*>(p);
+        f.c[1] = *reinterpret_cast<const tl_i4*>(p + 64);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int64_t c = s * 8 + 4 * h + g4;
+            tl_i4 v = {0, 0, 0, 0};
+            if (c < nch) v = *reinterpret_cast<const tl_i4*>(p + 64 * h);
+            if (E != EL_MX && part && c == nch - 1) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    if constexpr (E == EL_F32) v[e] = e < part ? v[e] : 0;
+                    else v[e] = 2 * e + 1 < part ? v[e] : 2 * e < part ? v[e] & 0xFFFF : 0;
+                }
+            }
+            f.c[h] = v;
+        }
+    }
+    if constexpr (E == EL_MX) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int64_t b = s * 8 + 4 * h;     // scale rows are read four bytes at a time
+            const uint32_t w = b < nch ? *reinterpret_cast<const uint32_t*>(srow + b) : 0u;
+            f.s[h] = b + g4 < nch ? w >> (8 * g4) : 0u;
+        }
+    }
+}
+
+template <int E, bool GATED, int NB>
+__global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
+    extern __shared__ __align__(16) float few_sm[];       // [wave][matrix][token block][lane][4]
+    constexpr int EPC = el_chunk<E>(), MATS = GATED ? 2 : 1;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int x16 = lane & 15, g4 = lane >> 4;
+    const int64_t f0 = (int64_t)blockIdx.x * 16;
+    const int64_t row = f0 + x16 < g.o ? f0 + x16 : g.o - 1;
+    const char* rB = g.B + row * g.ldb;
+    const char* rB2 = GATED ? g.B2 + row * g.ldb2 : nullptr;
+    const uint8_t* qB = E == EL_MX ? g.sB + row * g.ldsb : nullptr;
+    const uint8_t* qB2 = E == EL_MX && GATED ? g.sB2 + row * g.ldsb2 : nullptr;
+    const char* rA[NB];
+    const uint8_t* qA[NB];
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+        const int64_t t = 16 * b + x16 < g.n ? 16 * b + x16 : g.n - 1;
+        rA[b] = g.A + t * g.lda;
+        qA[b] = E == EL_MX ? g.sA + t * g.ldsa : nullptr;
+    }
+    const int64_t nch = (g.K + EPC - 1) / EPC, slabs = (nch + 7) / 8;
+    const int part = (int)(g.K % EPC);
+    const int64_t full = E == EL_MX ? nch / 8 : g.K / (8 * EPC);      // slabs whose chunks are all whole
+
+    tl_f4 acc[MATS][NB];
+#pragma unroll
+    for (int m = 0; m < MATS; m++)
+#pragma unroll
+        for (int b = 0; b < NB; b++) acc[m][b] = tl_f4{0, 0, 0, 0};
+    auto slab = [&](int64_t s, bool whole) {
+        FewFrag<E> w[MATS], a[NB];
+        few_load<E>(w[0], rB, qB, s, g4, whole, nch, part);
+        if constexpr (GATED) few_load<E>(w[1], rB2, qB2, s, g4, whole, nch, part);
+#pragma unroll
+        for (int b = 0; b < NB; b++) few_load<E>(a[b], rA[b], qA[b], s, g4, whole, nch, part);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int m = 0; m < MATS; m++)
+#pragma unroll
+                for (int b = 0; b < NB; b++)
+                    acc[m][b] = mma_step<E>(w[m].c[h], a[b].c[h], acc[m][b], (int)w[m].s[h], 0, (int)a[b].s[h], 0);
+    };
+#pragma unroll 4
+    for (int64_t s = wave; s < full; s += FEW_WAVES) slab(s, true);
+    if (full < slabs && wave == (int)(full % FEW_WAVES)) slab(full, false);
+
+#pragma unroll
+    for (int m = 0; m < MATS; m++)
+#pragma unroll
+        for (int b = 0; b < NB; b++)
+            reinterpret_cast<tl_f4*>(few_sm)[((wave * MATS + m) * NB + b) * 64 + lane] = acc[m][b];
+    __syncthreads();
+    if (wave >= NB) return;
+    // wavefront b finishes token block b: lane holds token x16 and rows f0 + 4 g4 .. + 3
+    tl_f4 sum[MATS];
+#pragma unroll
+    for (int m = 0; m < MATS; m++) {
+        sum[m] = tl_f4{0, 0, 0, 0};
+        for (int w = 0; w < FEW_WAVES; w++) {
+            const tl_f4 v = reinterpret_cast<const tl_f4*>(few_sm)[((w * MATS + m) * NB + wave) * 64 + lane];
+#pragma unroll
+            for (int r = 0; r < 4; r++) sum[m][r] += v[r];
+        }
+    }
+    const int64_t t = 16 * wave + x16, n = f0 + 4 * g4;
+    if (t >= g.n) return;
+    float y[4];
+#pragma unroll
+    for (int r = 0; r < 4; r++) y[r] = GATED ? act_value(sum[0][r], g.act) * sum[MATS - 1][r] : sum[0][r];
+    store_run<4>(g.Y, g.dt, t * g.ldy + n, y, g.o - n);
+    if constexpr (GATED) {
+        if (g.Y2) {
+            const float v[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
+            store_run<4>(g.Y2, g.dt, t * g.ldy2 + n, v, g.o - n);
+        }
+        if (g.Y3) {
+            const float v[4] = {sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
+            store_run<4>(g.Y3, g.dt, t * g.ldy3 + n, v, g.o - n);
+        }
+    }
+}
+
+template <int E, bool GATED>
+kq_status few_launch(const FewArgs& g, hipStream_t st, const char* who) {
+    const int64_t wgs = (g.o + 15) / 16;
+    if (wgs > 2147483647LL) return fail(KQ_ESHAPE, "%s: too many rows", who);
+    const dim3 grid((unsigned)wgs);
+    const size_t one = (size_t)FEW_WAVES * (GATED ? 2 : 1) * 1024;
+    if (g.n <= 16) {
+        hipLaunchKernelGGL((few_kernel<E, GATED, 1>), grid, dim3(FEW_THREADS), one, st, g);
+    } else if (g.n <= 32) {
+        hipLaunchKernelGGL((few_kernel<E, GATED, 2>), grid, dim3(FEW_THREADS), 2 * one, st, g);
+    } else {
+        hipLaunchKernelGGL((few_kernel<E, GATED, 4>), grid, dim3(FEW_THREADS), 4 * one, st, g);
+    }
+    return check_launch(who);
+}
+
+}  // namespace kq

@@ -1,0 +1,548 @@
+"""Microscaled 4-bit operators and the gated feed-forward block on the GPU against the float64 oracle.
+
+Tolerances, all per element. U = eps(type) / 2 is a rounding to the output type; fp32 sums of k products
+p_1 .. p_k are off by at most k 2^-23 sum |p| in any order, with 2^-23 instead of 2^-24 because the matrix
+cores may truncate inside an instruction (S23 below). Activations: expf, erfcf and the division are good to
+a few 2^-24, and the argument's own rounding moves the gate by at most |a| 2^-23 of itself where the gate
+is not tiny, so act(a) is off by at most (16 + |a|) 2^-23 |a| and act'(a) by (16 + 4 |a|) 2^-23 (1 + |a|).
+|act'| <= 1.13 and |act''| <= 1.2 for all four.
+"""
+import numpy as np
+import pytest
+
+
+from oracle import blocks as ob
+from post_quantization_03_amd import _lib as K
+from post_quantization_03_amd import ffn
+from tests.gpu_util import host, say, to_dev, torch_dev, ws_tensor
+
+pytestmark = pytest.mark.gpu
+E23 = 2.0 ** -23
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+KINDS = ["silu", "gelu", "gelu_tanh", "relu"]
+
+
+def tdtype(dt):
+    torch, _ = torch_dev()
+    return torch.bfloat16 if dt == "bf16" else torch.float32
+
+
+def mat(n, d, dt, pad=0, fill=None):
+    """n x d on the device with rows on 16 bytes, `pad` extra chunks behind each row."""
+    torch, dev = torch_dev()
+    per = 8 if dt == "bf16" else 4
+    ld = (-(-d // per) + pad) * per
+    t = torch.empty((n, ld), dtype=tdtype(dt), device=dev)
+    t.fill_(float("nan") if fill is None else fill)
+    return t[:, :d]
+
+
+def put(a, dt, pad=0):
+    """Host values rounded to dt on the device, NaN in every padding element; and the values as float64."""
+    torch, dev = torch_dev()
+    a = np.asarray(a, dtype=np.float32)
+    t = mat(a.shape[0], a.shape[1], dt, pad)
+    t.copy_(torch.from_numpy(a).to(dev))
+    return t, get(t)
+
+
+def get(t):
+    return host(t.float()).astype(np.float64)
+
+
+def packed(a):
+    """Microscaled operand of host values: device buffers with stray bytes in the scale padding, and values."""
+    torch, dev = torch_dev()
+    codes, scales = ob.mx_quantize(a)
+    c, s = K.mx_empty(a.shape[0], a.shape[1], dev)
+    s.fill_(0xEE)
+    c.copy_(torch.from_numpy(codes))
+    s[:, :scales.shape[1]].copy_(torch.from_numpy(scales))
+    return (c, s), ob.mx_values(codes, scales, a.shape[1])
+
+
+def ws_of(op, o, i, n, dt="bf16"):
+    return ws_tensor(K.kq_workspace_bytes(op, o, i, n, K.KQ_BF16 if dt == "bf16" else K.KQ_F32))
+
+
+def check(got, want, tol, what):
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}: " \
+                          f"{got[bad][0]} for {want[bad][0]}, tolerance {np.broadcast_to(tol, want.shape)[bad][0]}"
+
+
+# --------------------------------------------------------------------------------- quantisation
+def special_rows(cols):
+    """Rows that hold every rounding boundary, signed zeros, subnormals and the ends of fp32's range."""
+    rng = np.random.default_rng(cols)
+    rows = [np.zeros(cols), -np.zeros(cols)]
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.96875])
+    for e in (-127, -126, -100, 0, 90, 124):
+        r = rng.choice(ties, cols) * rng.choice([-1.0, 1.0], cols)
+        r[::32] = 6.0                                     # pins the block's scale to 2^e
+        rows.append(r * 2.0 ** e)
+    near = rng.choice(ties, cols) * (1 + rng.choice([-1, 1], cols) * 2.0 ** -23)
+    near[::32] = 4.0
+    rows.append(near)
+    rows.append(rng.standard_normal(cols) * np.exp(3 * rng.standard_normal(cols)))
+    sub = np.zeros(cols)
+    sub[::7] = 2.0 ** -149
+    rows.append(sub)
+    return np.array(rows).astype(np.float32)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [1, 7, 31, 32, 33, 100, 1000, 4096])
+def test_quantise_and_back_exact(cols, dt):
+    torch, dev = torch_dev()
+    say(f"mx quantise cols={cols} {dt}")
+    x, v = put(special_rows(cols), dt, pad=1)
+    rows = x.shape[0]
+    codes, scales = ob.mx_quantize(v)
+    nblk = scales.shape[1]
+    c = torch.full((rows + 2, 16 * nblk + 16), 0xAB, dtype=torch.uint8, device=dev)
+    s = torch.full((rows + 2, -(-nblk // 4) * 4 + 4), 0xAB, dtype=torch.uint8, device=dev)
+    K.kq_mx_quantize(x, c[:rows, :16 * nblk], s[:rows, :nblk])
+    hc, hs_ = host(c), host(s)
+    assert np.array_equal(hs_[:rows, :nblk], scales)
+    assert np.array_equal(hc[:rows, :16 * nblk], codes)
+    assert (hc[rows:] == 0xAB).all() and (hc[:, 16 * nblk:] == 0xAB).all()      # nothing else is written
+    assert (hs_[rows:] == 0xAB).all() and (hs_[:, nblk:] == 0xAB).all()
+    for out in ("f32", "bf16"):
+        y = mat(rows, cols, out, pad=1, fill=-77.0)
+        K.kq_mx_dequantize(c[:rows, :16 * nblk], s[:rows, :nblk], y)
+        assert np.array_equal(get(y), ob.mx_values(codes, scales, cols))
+        whole = y.as_strided((rows, y.stride(0)), (y.stride(0), 1))
+        assert (host(whole.float())[:, cols:] == -77.0).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_quantise_infinities_and_nan(dt):
+    torch, dev = torch_dev()
+    x = np.ones((4, 96), dtype=np.float32)
+    x[0, 40], x[1, 95], x[2, 0], x[3, 33] = np.inf, np.nan, -np.inf, 3e38
+    t, v = put(x, dt)
+    c, s = K.mx_empty(4, 96, dev)
+    K.kq_mx_quantize(t, c, s)
+    want = ob.mx_quantize(v)[1]
+    assert np.array_equal(host(s)[:, :3], want) and (want == 255).sum() == 3
+    y = mat(4, 96, "f32")
+    K.kq_mx_dequantize(c, s, y)
+    nan = np.zeros((4, 96), dtype=bool)
+    nan[0, 32:64] = nan[1, 64:] = nan[2, :32] = True
+    assert np.array_equal(np.isnan(get(y)), nan)
+
+
+def test_dequantise_every_code_and_scale():
+    torch, dev = torch_dev()
+    codes = np.tile(np.arange(256, dtype=np.uint8), (256, 1))                  # all bytes in every row
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], 16, axis=1)    # one scale a row
+    c, s = torch.from_numpy(codes).to(dev), torch.from_numpy(scales).to(dev)
+    want = ob.mx_values(codes, scales, 512)
+    for dt in ("f32", "bf16"):
+        y = mat(256, 512, dt)
+        K.kq_mx_dequantize(c, s, y)
+        with np.errstate(over="ignore"):
+            w = want.astype(np.float32).astype(np.float64)     # past fp32's range (also bf16's): infinite
+        got = get(y)
+        assert np.array_equal(got, w, equal_nan=True)
+        assert np.array_equal(np.signbit(got), np.signbit(w) & ~np.isnan(got) | (np.signbit(got) & np.isnan(got)))
+
+
+def test_quantise_single_rows_and_none():
+    torch, dev = torch_dev()
+    x = torch.randn(1, 64, device=dev)
+    c, s = K.mx_empty(1, 64, dev)
+    K.kq_mx_quantize(x, c, s)
+    assert np.array_equal(host(c), ob.mx_quantize(get(x))[0])
+    c0, s0 = K.mx_empty(0, 64, dev)
+    K.kq_mx_quantize(x[:0], c0, s0)
+    K.kq_mx_dequantize(c0, s0, x[:0])
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------------------------- products
+MX_SHAPES = [(1, 1, 1), (1, 16, 32), (2, 17, 33), (5, 100, 255), (16, 64, 256), (17, 130, 257), (33, 48, 1000), (64, 200, 512),
+             (65, 1, 32), (65, 255, 100), (66, 256, 256), (100, 257, 260), (255, 129, 511), (257, 300, 1025),
+             (600, 513, 768), (3, 40, 11008), (70, 40, 5504)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,o,i", MX_SHAPES)
+def test_mx_gemm(n, o, i, dt):
+    say(f"mx gemm n={n} o={o} i={i} {dt}")
+    rng = np.random.default_rng(n * 1000 + o + i)
+    (ac, as_), a = packed(rng.standard_normal((n, i)) * np.exp(rng.standard_normal((n, i))))
+    (bc, bs), b = packed(rng.standard_normal((o, i)))
+    y = mat(n, o, dt, pad=1, fill=-77.0)
+    K.kq_mx_gemm(ac, as_, bc, bs, i, y, ws_of("mx_gemm", o, i, n))
+    want, s = a @ b.T, np.abs(a) @ np.abs(b).T
+    check(get(y), want, i * E23 * s + HALF[dt] * (np.abs(want) + i * E23 * s), "Y")
+    whole = host(y.as_strided((n, y.stride(0)), (y.stride(0), 1)).float())
+    assert (whole[:, o:] == -77.0).all()
+
+
+def act_tol(a, da, kind):
+    """Bound of the error of act at a computed argument off by da."""
+    return 1.13 * da + (16 + np.abs(a) + da) * E23 * (np.abs(a) + da)
+
+
+def gated_tol(a, b, da, db, kind, dt):
+    f = ob.act(a, kind)[0]
+    t = act_tol(a, da, kind)
+    h = np.abs(b) * t + np.abs(f) * db + t * db
+    return h + HALF[dt] * (np.abs(f * b) + h) + 2.0 ** -126    # results near the smallest fp32 may flush
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,o,i", MX_SHAPES)
+def test_mx_gated(n, o, i, dt):
+    kind = KINDS[(n + o) % 4]
+    say(f"mx gated n={n} o={o} i={i} {dt} {kind}")
+    rng = np.random.default_rng(n * 1000 + o + i)
+    (xc, xs), x = packed(rng.standard_normal((n, i)))
+    (gc, gs), g = packed(rng.standard_normal((o, i)) * 2 / np.sqrt(i))
+    (uc, us), u = packed(rng.standard_normal((o, i)) / np.sqrt(i))
+    h = mat(n, o, dt, pad=1, fill=-77.0)
+    K.kq_mx_gated(xc, xs, gc, gs, uc, us, i, kind, h, ws_of("mx_gated", o, i, n))
+    want, a, b = ob.gated(x, g, u, kind)
+    da, db = i * E23 * (np.abs(x) @ np.abs(g).T), i * E23 * (np.abs(x) @ np.abs(u).T)
+    check(get(h), want, gated_tol(a, b, da, db, kind, dt), "H")
+    whole = host(h.as_strided((n, h.stride(0)), (h.stride(0), 1)).float())
+    assert (whole[:, o:] == -77.0).all()
+
+
+@pytest.mark.parametrize("n", [5, 80])
+def test_mx_nan_block_stays_in_its_row(n):
+    rng = np.random.default_rng(n)
+    a, b = rng.standard_normal((n, 320)), rng.standard_normal((40, 320))
+    a[3, 300], b[7, 5] = np.nan, np.inf
+    (ac, as_), av = packed(a)
+    (bc, bs), bv = packed(b)
+    y = mat(n, 40, "f32")
+    K.kq_mx_gemm(ac, as_, bc, bs, 320, y, ws_of("mx_gemm", 40, 320, n))
+    nan = np.zeros((n, 40), dtype=bool)
+    nan[3], nan[:, 7] = True, True
+    got = get(y)
+    assert np.array_equal(np.isnan(got), nan)
+    want = np.nan_to_num(av) @ np.nan_to_num(bv).T
+    check(got[~nan], want[~nan], (320 * E23 * (np.abs(np.nan_to_num(av)) @ np.abs(np.nan_to_num(bv)).T) + 2e-7 * np.abs(want))[~nan], "Y")
+
+
+@pytest.mark.parametrize("n", [4, 70])
+def test_mx_extreme_scales(n):
+    """Products whose scales nearly cancel, and ones that vanish or overflow."""
+    rng = np.random.default_rng(9)
+    a = rng.standard_normal((n, 64)) * 2.0 ** 120
+    a[1] *= 2.0 ** -240
+    b = rng.standard_normal((16, 64)) * 2.0 ** -120
+    b[3] *= 2.0 ** 240
+    (ac, as_), av = packed(a)
+    (bc, bs), bv = packed(b)
+    y = mat(n, 16, "f32")
+    K.kq_mx_gemm(ac, as_, bc, bs, 64, y, ws_of("mx_gemm", 16, 64, n))
+    got, want, s = get(y), av @ bv.T, np.abs(av) @ np.abs(bv).T
+    fits = s < 2.0 ** 127
+    check(got[fits], want[fits], (64 * E23 * s + 2.0 ** -126)[fits], "Y")
+    over = np.abs(want) > 2.0 ** 130
+    assert over.any() and np.all(np.isinf(got[over]) | np.isnan(got[over]))
+
+
+# ---------------------------------------------------------------------------------- dense block
+DENSE_SHAPES = [(1, 1, 1), (1, 16, 64), (2, 17, 9), (7, 130, 33), (16, 40, 513), (33, 100, 72), (64, 65, 1001), (65, 129, 8),
+                (66, 128, 64), (100, 130, 257), (257, 300, 130), (520, 264, 520), (3, 40, 11008)]
+
+
+def dense_case(n, o, i, dt, scale=2.0):
+    rng = np.random.default_rng(n * 1000 + o + i)
+    X = put(rng.standard_normal((n, i)), dt, pad=1)
+    Wg = put(rng.standard_normal((o, i)) * scale / np.sqrt(i), dt, pad=2)
+    Wu = put(rng.standard_normal((o, i)) / np.sqrt(i), dt)
+    dH = put(rng.standard_normal((n, o)) * np.exp(rng.standard_normal((1, o))), dt, pad=1)
+    return X, Wg, Wu, dH
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,o,i", DENSE_SHAPES)
+def test_gated_forward(n, o, i, dt):
+    kind = KINDS[(n + i) % 4]
+    say(f"gated forward n={n} o={o} i={i} {dt} {kind}")
+    (X, x), (Wg, g), (Wu, u), _ = dense_case(n, o, i, dt)
+    H, A, B = (mat(n, o, dt, pad=p, fill=-77.0) for p in (1, 0, 2))
+    ws = ws_of("gated_forward", o, i, n, dt)
+    K.kq_gated_forward(X, Wg, Wu, kind, H, A, B, ws)
+    want, a, b = ob.gated(x, g, u, kind)
+    da, db = i * E23 * (np.abs(x) @ np.abs(g).T), i * E23 * (np.abs(x) @ np.abs(u).T)
+    check(get(A), a, da + HALF[dt] * (np.abs(a) + da), "A")
+    check(get(B), b, db + HALF[dt] * (np.abs(b) + db), "B")
+    check(get(H), want, gated_tol(a, b, da, db, kind, dt), "H")
+    for t in (H, A, B):
+        assert (host(t.as_strided((n, t.stride(0)), (t.stride(0), 1)).float())[:, o:] == -77.0).all()
+    H2 = mat(n, o, dt)
+    K.kq_gated_forward(X, Wg, Wu, kind, H2, ws=ws)          # without A and B: the same bits
+    assert np.array_equal(get(H2), get(H))
+
+
+def grad_tols(dH, a, b, x, g, u, kind, dt):
+    """Element bounds of dA, dB, dX, dWg, dWu: the activation's, the roundings of dA and dB, the sums."""
+    f, df = ob.act(a, kind)
+    dA, dB = dH * b * df, dH * f
+    ta = np.abs(dH * b) * (16 + 4 * np.abs(a)) * E23 * (1 + np.abs(a)) + 3 * E23 * np.abs(dA)
+    tb = np.abs(dH) * (16 + np.abs(a)) * E23 * np.abs(a) + 3 * E23 * np.abs(dB)
+    ta, tb = ta + HALF[dt] * (np.abs(dA) + ta), tb + HALF[dt] * (np.abs(dB) + tb)
+    n, o = dH.shape
+    Aa, Ab = np.abs(dA) + ta, np.abs(dB) + tb
+    tx = ta @ np.abs(g) + tb @ np.abs(u) + 2 * o * E23 * (Aa @ np.abs(g) + Ab @ np.abs(u))
+    tg = ta.T @ np.abs(x) + n * E23 * (Aa.T @ np.abs(x))
+    tu = tb.T @ np.abs(x) + n * E23 * (Ab.T @ np.abs(x))
+    want = (dA, dB, dA @ g + dB @ u, dA.T @ x, dB.T @ x)
+    tols = [ta, tb] + [t + HALF[dt] * (np.abs(w) + t) for t, w in zip((tx, tg, tu), want[2:])]
+    return want, [t + 2.0 ** -126 for t in tols]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,o,i", DENSE_SHAPES)
+def test_gated_backward(n, o, i, dt):
+    kind = KINDS[(n + i) % 4]
+    say(f"gated backward n={n} o={o} i={i} {dt} {kind}")
+    (X, x), (Wg, g), (Wu, u), (dH, dh) = dense_case(n, o, i, dt)
+    A, a = put(x @ g.T, dt)
+    B, b = put(x @ u.T, dt, pad=1)
+    outs = [mat(n, o, dt, 1, -77.0), mat(n, o, dt, 0, -77.0), mat(n, i, dt, 1, -77.0), mat(o, i, dt, 2, -77.0),
+            mat(o, i, dt, 0, -77.0)]
+    ws = ws_of("gated_backward", o, i, n, dt)
+    K.kq_gated_backward(dH, A, B, X, Wg, Wu, kind, *outs, ws)
+    want, tols = grad_tols(dh, a, b, x, g, u, kind, dt)
+    for name, t, w, tol in zip(("dA", "dB", "dX", "dWg", "dWu"), outs, want, tols):
+        check(get(t), w, tol, name)
+        assert (host(t.as_strided((t.shape[0], t.stride(0)), (t.stride(0), 1)).float())[:, t.shape[1]:] == -77.0).all()
+    # any subset of the outputs has the same bits
+    dA, dB, dX, dU = mat(n, o, dt), mat(n, o, dt), mat(n, i, dt), mat(o, i, dt)
+    K.kq_gated_backward(dH, A, B, X, Wg, Wu, kind, dA, dB, None, None, dU, ws)
+    assert np.array_equal(get(dU), get(outs[4])) and np.array_equal(get(dA), get(outs[0]))
+    K.kq_gated_backward(dH, A, B, None, Wg, Wu, kind, dA, dB, dX, ws=ws)
+    assert np.array_equal(get(dX), get(outs[2])) and np.array_equal(get(dB), get(outs[1]))
+    K.kq_gated_backward(dH, A, B, None, None, None, kind, dA, dB)
+    assert np.array_equal(get(dA), get(outs[0]))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_gradient_against_differences(kind):
+    """The fp32 kernel's gradients against central differences of the float64 forward pass along random
+    directions: h^2 times third derivatives (of order 10), plus the kernel's own bound."""
+    n, o, i = 30, 70, 40
+    (X, x), (Wg, g), (Wu, u), (dH, dh) = dense_case(n, o, i, "f32")
+    A, a = put(x @ g.T, "f32")
+    B, b = put(x @ u.T, "f32")
+    outs = [mat(n, o, "f32"), mat(n, o, "f32"), mat(n, i, "f32"), mat(o, i, "f32"), mat(o, i, "f32")]
+    K.kq_gated_backward(dH, A, B, X, Wg, Wu, kind, *outs, ws_of("gated_backward", o, i, n, "f32"))
+    _, tols = grad_tols(dh, a, b, x, g, u, kind, "f32")
+    rng = np.random.default_rng(4)
+    for k, (grad, tol) in enumerate(zip((get(t) for t in outs[2:]), tols[2:])):
+        V = rng.standard_normal(grad.shape)
+
+        def loss(t):
+            p = [x, g, u]
+            p[k] = p[k] + t * V
+            return (ob.gated(*p, kind)[0] * dh).sum()
+
+        h = 1e-5
+        diff = (loss(h) - loss(-h)) / (2 * h)
+        # relu's kink: a step of h |V| crosses it for few elements, each worth at most its jump
+        slack = 1e-7 * (np.abs(dh).sum() * 10 + np.abs(diff)) + (tol * np.abs(V)).sum()
+        if kind == "relu":
+            moved = np.abs(a) <= h * (np.abs(V) @ np.abs(g).T if k == 0 else np.abs(x) @ np.abs(V).T if k == 1 else 0 * a + 0)
+            slack += 2 * (np.abs(dh * b) * moved).sum() * np.abs(V).max() * 100
+        # A and B were rounded to fp32 before the kernel saw them
+        slack += 2.0 ** -22 * np.abs(grad * V).sum() * (1 + np.abs(a).max())
+        assert abs(diff - (grad * V).sum()) <= slack, (k, diff, (grad * V).sum(), slack)
+
+
+def test_gated_no_tokens():
+    torch, dev = torch_dev()
+    for dt in ("f32", "bf16"):
+        W = mat(20, 24, dt, fill=1.0)
+        z, x = mat(0, 20, dt), mat(0, 24, dt)
+        dG, dU = mat(20, 24, dt, 1, -77.0), mat(20, 24, dt, 0, -77.0)
+        K.kq_gated_forward(x, W, W, "silu", z)
+        K.kq_gated_backward(z, z, z, x, W, W, "silu", z, z, x, dG, dU)
+        assert (get(dG) == 0).all() and (get(dU) == 0).all()
+        assert (host(dG.as_strided((20, dG.stride(0)), (dG.stride(0), 1)).float())[:, 24:] == -77.0).all()
+
+
+def test_gated_large_arguments():
+    """Saturated gates: huge pre-activations of both signs give finite values and derivatives."""
+    torch, dev = torch_dev()
+    a = np.array([[-1e30, -1e10, -200.0, -50.0, -0.0, 0.0, 50.0, 200.0, 1e10, 1e30, -20.0, 17.0]])
+    dt = "f32"
+    A, av = put(a, dt)
+    B, bv = put(np.full_like(a, 2.0), dt)
+    dH, dh = put(np.ones_like(a), dt)
+    for kind in KINDS:
+        dA, dB = mat(1, 12, dt), mat(1, 12, dt)
+        K.kq_gated_backward(dH, A, B, None, None, None, kind, dA, dB)
+        with np.errstate(over="ignore", invalid="ignore"):
+            want_f = np.where(np.abs(av) > 100, np.maximum(av, 0), ob.act(np.clip(av, -100, 100), kind)[0])
+            want_d = np.where(np.abs(av) > 100, 1.0 * (av > 0), ob.act(np.clip(av, -100, 100), kind)[1])
+        check(get(dB), want_f, 1e-5 * np.abs(want_f) + 1e-6, f"act {kind}")
+        check(get(dA), 2 * want_d, 1e-5, f"act' {kind}")
+
+
+# --------------------------------------------------------------------- streams, graphs, two calls
+@pytest.mark.parametrize("n", [3, 300])
+def test_products_replayed_from_a_graph(n):
+    """One graph of the block's forward, backward and microscaled calls: every replay on new inputs gives the
+    eager result, with eager work between the replays."""
+    torch, dev = torch_dev()
+    o, i, dt = 136, 264, "bf16"
+    (X, _), (Wg, _), (Wu, _), (dH, _) = dense_case(n, o, i, dt)
+    rng = np.random.default_rng(n)
+    gq, uq = packed(rng.standard_normal((o, i)) * 0.1)[0], packed(rng.standard_normal((o, i)) * 0.1)[0]
+
+    def buffers():
+        return dict(H=mat(n, o, dt), A=mat(n, o, dt), B=mat(n, o, dt), dA=mat(n, o, dt), dB=mat(n, o, dt), dX=mat(n, i, dt),
+                    dG=mat(o, i, dt), dU=mat(o, i, dt), q=K.mx_empty(n, i, dev), M=mat(n, o, dt), Y=mat(n, o, "f32"),
+                    w1=ws_of("gated_forward", o, i, n, dt), w2=ws_of("gated_backward", o, i, n, dt),
+                    w3=ws_of("mx_gated", o, i, n), w4=ws_of("mx_gemm", o, i, n))
+
+    def run(b):
+        K.kq_gated_forward(X, Wg, Wu, "silu", b["H"], b["A"], b["B"], b["w1"])
+        K.kq_gated_backward(dH, b["A"], b["B"], X, Wg, Wu, "silu", b["dA"], b["dB"], b["dX"], b["dG"], b["dU"], b["w2"])
+        K.kq_mx_quantize(X, *b["q"])
+        K.kq_mx_gated(*b["q"], *gq, *uq, i, "silu", b["M"], b["w3"])
+        K.kq_mx_gemm(*b["q"], *gq, i, b["Y"], b["w4"])
+
+    cap, eager = buffers(), buffers()
+    run(cap)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(cap)
+    for rep in range(3):
+        X.copy_(torch.randn(n, i, device=dev))
+        dH.copy_(torch.randn(n, o, device=dev))
+        run(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        run(eager)
+        torch.cuda.synchronize()
+        for k in ("H", "A", "B", "dA", "dB", "dX", "dG", "dU", "M", "Y"):
+            assert np.array_equal(get(cap[k]), get(eager[k])), (rep, k)
+        assert np.array_equal(host(cap["q"][0]), host(eager["q"][0]))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with workspaces of their own give the bits of calls in turn."""
+    torch, dev = torch_dev()
+    n, o, i = 300, 520, 512
+    rng = np.random.default_rng(0)
+    ops = [(packed(rng.standard_normal((n, i)))[0], packed(rng.standard_normal((o, i)))[0]) for _ in range(2)]
+    want = []
+    for a, b in ops:
+        y = mat(n, o, "f32")
+        K.kq_mx_gemm(*a, *b, i, y, ws_of("mx_gemm", o, i, n))
+        want.append(get(y))
+    ys = [mat(n, o, "f32") for _ in ops]
+    wss = [ws_of("mx_gemm", o, i, n) for _ in ops]
+    streams = [torch.cuda.Stream(dev) for _ in ops]
+    for _ in range(5):
+        for (a, b), y, w, st in zip(ops, ys, wss, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            K.kq_mx_gemm(*a, *b, i, y, w, stream=st)
+        torch.cuda.synchronize()
+        for y, w in zip(ys, want):
+            assert np.array_equal(get(y), w)
+
+
+def test_results_do_not_depend_on_the_workspace_contents():
+    torch, dev = torch_dev()
+    rng = np.random.default_rng(3)
+    n, o, i = 90, 130, 1000
+    a, b = packed(rng.standard_normal((n, i)))[0], packed(rng.standard_normal((o, i)))[0]
+    got = []
+    for fill in (0, 255):
+        ws = ws_of("mx_gemm", o, i, n)
+        ws.fill_(fill)
+        y = mat(n, o, "f32")
+        K.kq_mx_gemm(*a, *b, i, y, ws)
+        got.append(get(y))
+    assert np.array_equal(*got)
+
+
+# --------------------------------------------------------------------------------- wrapper refusals
+def test_wrapper_refusals_on_device():
+    torch, dev = torch_dev()
+    x, w = torch.zeros(4, 64, device=dev), torch.zeros(8, 64, device=dev)
+    c, s = K.mx_empty(4, 64, dev)
+    wc, wsc = K.mx_empty(8, 64, dev)
+    h = torch.zeros(4, 8, device=dev)
+    with pytest.raises(ValueError, match="shape"):
+        K.kq_mx_gemm(c, s, wc, wsc, 64, torch.zeros(4, 9, device=dev))
+    with pytest.raises(ValueError, match="needs 16"):
+        K.kq_mx_gemm(c, s, wc, wsc, 65, h)
+    with pytest.raises(ValueError, match="rows of codes"):
+        K.kq_mx_quantize(x, wc, wsc)
+    with pytest.raises(ValueError, match="row-major"):
+        K.kq_mx_quantize(torch.zeros(64, 4, device=dev).T, c, s)
+    with pytest.raises(ValueError, match="shape"):
+        K.kq_gated_forward(x, w, w[:4], "silu", h)
+    with pytest.raises(TypeError, match="type"):
+        K.kq_gated_forward(x, w, w.bfloat16(), "silu", h)
+    with pytest.raises(K.KQError, match="16-byte"):
+        K.kq_gated_forward(torch.zeros(4, 66, device=dev)[:, :62], torch.zeros(8, 66, device=dev)[:, :62],
+                           torch.zeros(8, 66, device=dev)[:, :62], "silu", h)
+    with pytest.raises(ValueError, match="past the storage"):     # the last row's 16 bytes are not all there
+        K.kq_gated_forward(torch.zeros(4 * 64 - 3, device=dev).as_strided((4, 61), (64, 1)),
+                           torch.zeros(8, 64, device=dev)[:, :61], torch.zeros(8, 64, device=dev)[:, :61], "silu", h)
+    with pytest.raises(ValueError, match="different devices"):
+        K.kq_mx_gemm(c, s, wc, wsc, 64, h, ws=torch.empty(4, dtype=torch.uint8))
+
+
+# ----------------------------------------------------------------------------------- used together
+def test_calibrate_quantise_and_serve():
+    """The block as it is used: statistics from one batch, the per-layer solver on gate and up, and the
+    microscaled block on prompts and on single tokens."""
+    from post_quantization_03_amd.layer import LayerCfg, quantize_layer
+    torch, dev = torch_dev()
+    n, o, i, m = 600, 256, 128, 128
+    rng = np.random.default_rng(11)
+    X, x = put(rng.standard_normal((n, i)), "bf16")
+    Wg, g = put(rng.standard_normal((o, i)) * 0.1, "bf16")
+    Wu, u = put(rng.standard_normal((o, i)) * 0.1, "bf16")
+    Wd, d = put(rng.standard_normal((m, o)) * 0.1, "bf16")
+    dH, dh = put(rng.standard_normal((n, o)) * np.exp(rng.standard_normal((1, o))), "bf16")
+    cfg = LayerCfg(bits=4, group=128, form="diag")
+    signs = [to_dev(rng.integers(0, 2, k) * 2 - 1, "i8") for k in (i, o, o)]
+    out = ffn.quantize_gated(X, Wg, Wu, dH, "silu", *signs, cfg, verify=True)
+    cal = out["calibration"]
+    h, a, b = ob.gated(x, g, u, "silu")
+    # A and B reach the backward pass rounded to bf16, so each gradient row entry is off by a few 2^-8 of
+    # |dh| (1 + |a|)(1 + |b|); the covariance averages n squares of them
+    f, df = ob.act(a, "silu")
+    want = {"HG_gate": ((dh * b * df) ** 2).mean(0), "HG_up": ((dh * f) ** 2).mean(0)}
+    bound = ((np.abs(dh) * (1 + np.abs(a)) * (1 + np.abs(b))) ** 2).mean(0)
+    for k, w in want.items():
+        check(get(cal[k].reshape(1, -1))[0], w, 8 * 2.0 ** -8 * bound, k)
+    assert out["gate"]["info"].cpu().tolist() == [0, 0] and out["up"]["info"].cpu().tolist() == [0, 0]
+    # the solver's result is that of the layer called by itself with these statistics, bit for bit. (Its error
+    # has no bound in the weights' own norm: the grids are uniform after S = H_G^{1/2}, so a row's error grows
+    # as 1 / S_r, and here S spans exp(N(0, 1)) twice over.)
+    for k, W, t in (("gate", Wg, signs[1]), ("up", Wu, signs[2])):
+        alone = quantize_layer(X, W, cal["HG_" + k], signs[0], t, cfg, verify=True)
+        for name in ("codes", "scale", "offset", "What"):
+            assert np.array_equal(host(alone[name]), host(out[k][name])), (k, name)
+
+    block = ffn.MXFeedForward(Wg, Wu, Wd, "silu")
+    for rows in (n, 1, 3):
+        y = get(block(X[:rows]))
+        xq = ob.mx_values(*ob.mx_quantize(x[:rows]), i)
+        gq, uq, dq = (ob.mx_values(*ob.mx_quantize(w), w.shape[1]) for w in (g, u, d))
+        hw, aw, bw = ob.gated(xq, gq, uq, "silu")
+        H = mat(rows, o, "bf16")
+        K.kq_mx_gated(*ffn.mx_quantize(X[:rows]), *block.gate, *block.up, i, "silu", H, ws_of("mx_gated", o, i, rows))
+        da, db = i * E23 * (np.abs(xq) @ np.abs(gq).T), i * E23 * (np.abs(xq) @ np.abs(uq).T)
+        check(get(H), hw, gated_tol(aw, bw, da, db, "silu", "bf16"), "H")
+        hq = ob.mx_values(*ob.mx_quantize(get(H)), o)       # the codes of the kernel's own H
+        s = np.abs(hq) @ np.abs(dq).T
+        yw = hq @ dq.T
+        check(y, yw, o * E23 * s + HALF["bf16"] * (np.abs(yw) + o * E23 * s), "Y")

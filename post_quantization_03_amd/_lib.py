@@ -297,44 +297,108 @@ def kq_allocate_bits(scores, sizes, budget: float = 3.0, bmin: int = 2, bmax: in
 
 # ------------------------------------------------- microscaled 4-bit products and the gated block
 # These wrappers also check what the C calls cannot see: types, shapes, devices and the memory behind a
-# view (rows are read in whole 16-byte pieces).
-def _matrix(name: str, what: str, t, rows: int, cols: int, dtypes, size: int = 0):
-    """Checks a row-major rows x cols matrix; returns (pointer, leading dimension in elements)."""
-    if t.dtype not in dtypes:
+# view (rows are read in whole 16-byte pieces). A call on few tokens runs for a few microseconds on the
+# GPU, so the checks read each tensor's attributes once and no device guard is entered on the current device.
+_FLOATS: dict = {}      # torch dtype -> (kq_dtype, elements in 16 bytes)
+
+
+def _floats() -> dict:
+    if not _FLOATS:
+        import torch
+        _FLOATS.update({torch.float32: (KQ_F32, 4), torch.bfloat16: (KQ_BF16, 8)})
+    return _FLOATS
+
+
+def _float(name: str, what: str, t):
+    """(kq_dtype, elements in 16 bytes) of a tensor's type."""
+    f = _floats().get(t.dtype)
+    if f is None:
         raise TypeError(f"{name}: {what} has type {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: {what} is not on a GPU")
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    return f
+
+
+def _matrix(name: str, what: str, t, rows: int, cols: int, dtype, per: int, whole: bool, dev: list):
+    """Checks a row-major rows x cols matrix of `dtype` on the device of the others; returns (pointer,
+    leading dimension). whole: its rows are read in pieces of `per` elements, the last one included."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {what} has type {t.dtype}, not {dtype}")
+    if t.shape != (rows, cols):
         raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {(rows, cols)}")
-    if cols > 1 and t.stride(1) != 1:
+    _same_device(name, what, t, dev)
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name}: {what} is not row-major")
-    # the stride of a single row is arbitrary: any legal one will do
-    per = 16 // t.element_size()
-    ld = t.stride(0) if rows > 1 else -(-max(cols, size) // per) * per
-    if rows and size > cols:
-        end = t.storage_offset() + (rows - 1) * ld + size
+    if rows <= 1:       # the stride of a single row is arbitrary: any legal one will do
+        ld = -(-cols // per) * per
+    if whole and cols % per and rows:
+        end = t.storage_offset() + (rows - 1) * ld + -(-cols // per) * per
         if end * t.element_size() > t.untyped_storage().nbytes():
             raise ValueError(f"{name}: the last row of {what} ends inside its 16 bytes, past the storage")
     return t.data_ptr(), ld
 
 
-def _whole(cols: int, t) -> int:
-    per = 16 // t.element_size()
-    return -(-cols // per) * per
+def _same_device(name: str, what: str, t, dev: list) -> None:
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name}: {what} is not on a GPU")
+    if not dev:
+        dev.append(d)
+    elif d != dev[0]:
+        raise ValueError(f"{name}: operands on different devices: {what} on cuda:{d}, others on cuda:{dev[0]}")
 
 
-def _launch(name: str, tensors, stream, args) -> None:
-    """Calls `name` with args + [stream] on the tensors' device (one for all of them)."""
+def _mx(name: str, what: str, codes, scales, cols: int, dev: list) -> tuple:
+    """Checks a microscaled operand of `cols` columns; returns its four C arguments."""
     import torch
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"{name}: operands on different devices: {sorted(map(str, devs))}")
-    dev = devs.pop()
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError(f"{name}: the stream is on {s.device}, the operands on {dev}")
-    with torch.cuda.device(dev):
-        _check(name, getattr(lib(), name)(*args, s.cuda_stream))
+    nblk = (cols + 31) // 32
+    for t, w in ((codes, "codes"), (scales, "scales")):
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name}: {what} {w} have type {t.dtype}, not uint8")
+    if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0]:
+        raise ValueError(f"{name}: {what} needs codes and scales with one row for each of the matrix")
+    _same_device(name, what + " codes", codes, dev)
+    _same_device(name, what + " scales", scales, dev)
+    (rows, wc), ws_ = codes.shape, scales.shape[1]
+    if wc != 16 * nblk or not nblk <= ws_ <= (nblk + 3) // 4 * 4:
+        raise ValueError(f"{name}: {what} of {cols} columns needs 16 * {nblk} bytes of codes and {nblk} scales a row "
+                         f"(mx_empty), not {wc} and {ws_}")
+    (ldc, c1), (lds, s1) = codes.stride(), scales.stride()
+    if c1 != 1 or (s1 != 1 and ws_ > 1):
+        raise ValueError(f"{name}: {what} is not row-major")
+    if rows <= 1:
+        ldc, lds = 16 * nblk, (nblk + 3) // 4 * 4
+    if ws_ % 4 and rows and scales.storage_offset() + (rows - 1) * lds + (nblk + 3) // 4 * 4 > scales.untyped_storage().nbytes():
+        raise ValueError(f"{name}: the last scale row of {what} ends inside its 4 bytes, past the storage")
+    return codes.data_ptr(), ldc, scales.data_ptr(), lds
+
+
+def _launch(name: str, fn, dev: list, ws, stream, *args) -> None:
+    """fn(*args [, workspace, its bytes], stream) on the operands' device."""
+    import torch
+    if ws is not False:
+        if ws is None:
+            args += (None, 0)
+        else:
+            _same_device(name, "the workspace", ws, dev)
+            args += (ws.data_ptr(), ws.numel() * ws.element_size())
+    d = dev[0]
+    if stream is None:
+        stream = torch.cuda.current_stream(d)
+    elif stream.device.index != d:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the operands on cuda:{d}")
+    if torch.cuda.current_device() == d:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(d):
+            status = fn(*args, stream.cuda_stream)
+    if status:
+        raise KQError(name, status, last_error())
+
+
+def _act(name: str, act: str) -> int:
+    if act not in ACT:
+        raise ValueError(f"{name}: activation {act!r} is none of {sorted(ACT)}")
+    return ACT[act]
 
 
 def mx_empty(rows: int, cols: int, device):
@@ -346,120 +410,85 @@ def mx_empty(rows: int, cols: int, device):
             torch.empty((rows, -(-nblk // 4) * 4), dtype=torch.uint8, device=device))
 
 
-def _mx(name: str, what: str, codes, scales, cols: int):
-    """Checks a microscaled operand of `cols` columns; returns its four C arguments."""
-    import torch
-    nblk = -(-cols // 32)
-    for t, w in ((codes, "codes"), (scales, "scales")):
-        if t.dtype != torch.uint8:
-            raise TypeError(f"{name}: {what} {w} have type {t.dtype}, not uint8")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: {what} {w} are not on a GPU")
-        if t.dim() != 2 or t.shape[0] != codes.shape[0] or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name}: {what} {w} must be row-major, one row for each of the matrix")
-    if codes.shape[1] != 16 * nblk or not nblk <= scales.shape[1] <= -(-nblk // 4) * 4:
-        raise ValueError(f"{name}: {what} of {cols} columns needs 16 * {nblk} bytes of codes and {nblk} scales a row "
-                         f"(mx_empty), not {codes.shape[1]} and {scales.shape[1]}")
-    rows = codes.shape[0]
-    ldc = codes.stride(0) if rows > 1 else 16 * nblk
-    lds = scales.stride(0) if rows > 1 else -(-nblk // 4) * 4
-    if rows and scales.storage_offset() + (rows - 1) * lds + -(-nblk // 4) * 4 > scales.untyped_storage().nbytes():
-        raise ValueError(f"{name}: the last scale row of {what} ends inside its 4 bytes, past the storage")
-    return [codes.data_ptr(), ldc, scales.data_ptr(), lds]
-
-
-def _floats():
-    import torch
-    return (torch.float32, torch.bfloat16)
-
-
-def _act(name: str, act: str) -> int:
-    if act not in ACT:
-        raise ValueError(f"{name}: activation {act!r} is none of {sorted(ACT)}")
-    return ACT[act]
-
-
 def kq_mx_quantize(X, codes, scales, stream=None) -> None:
     """X (rows x cols, fp32 or bf16) into codes and scales of mx_empty(rows, cols)."""
-    name = "kq_mx_quantize"
+    name, dev = "kq_mx_quantize", []
     rows, cols = X.shape
-    p, ld = _matrix(name, "X", X, rows, cols, _floats())
+    dt, per = _float(name, "X", X)
+    p = _matrix(name, "X", X, rows, cols, X.dtype, per, False, dev)
     if codes.shape[0] != rows:
         raise ValueError(f"{name}: {codes.shape[0]} rows of codes for {rows} rows")
-    c = _mx(name, "the output", codes, scales, cols)
-    _launch(name, (X, codes, scales), stream, [p, _xdt(X), rows, cols, ld, *c])
+    _launch(name, lib().kq_mx_quantize, dev, False, stream, p[0], dt, rows, cols, p[1],
+            *_mx(name, "the output", codes, scales, cols, dev))
 
 
 def kq_mx_dequantize(codes, scales, Y, stream=None) -> None:
     """The values that codes and scales stand for, into Y (rows x cols, fp32 or bf16)."""
-    name = "kq_mx_dequantize"
+    name, dev = "kq_mx_dequantize", []
     rows, cols = Y.shape
-    p, ld = _matrix(name, "Y", Y, rows, cols, _floats())
+    dt, per = _float(name, "Y", Y)
+    p = _matrix(name, "Y", Y, rows, cols, Y.dtype, per, False, dev)
     if codes.shape[0] != rows:
         raise ValueError(f"{name}: {codes.shape[0]} rows of codes for {rows} rows")
-    c = _mx(name, "the input", codes, scales, cols)
-    _launch(name, (codes, scales, Y), stream, [*c, rows, cols, p, _xdt(Y), ld])
+    _launch(name, lib().kq_mx_dequantize, dev, False, stream, *_mx(name, "the input", codes, scales, cols, dev), rows, cols,
+            p[0], dt, p[1])
 
 
 def kq_mx_gemm(Ac, As, Bc, Bs, i: int, Y, ws=None, stream=None) -> None:
     """Y (n x o, fp32 or bf16) = A B^T for microscaled A (n x i) and B (o x i)."""
-    name = "kq_mx_gemm"
+    name, dev = "kq_mx_gemm", []
     n, o = Ac.shape[0], Bc.shape[0]
-    p, ld = _matrix(name, "Y", Y, n, o, _floats())
-    w, wb = _ws(ws)
-    _launch(name, (Ac, As, Bc, Bs, Y, ws), stream,
-            [*_mx(name, "A", Ac, As, i), *_mx(name, "B", Bc, Bs, i), n, o, i, p, _xdt(Y), ld, w, wb])
+    dt, per = _float(name, "Y", Y)
+    p = _matrix(name, "Y", Y, n, o, Y.dtype, per, False, dev)
+    _launch(name, lib().kq_mx_gemm, dev, ws, stream, *_mx(name, "A", Ac, As, i, dev), *_mx(name, "B", Bc, Bs, i, dev), n, o,
+            i, p[0], dt, p[1])
 
 
 def kq_mx_gated(Xc, Xs, Gc, Gs, Uc, Us, i: int, act: str, H, ws=None, stream=None) -> None:
     """H (n x o, fp32 or bf16) = act(X G^T) * (X U^T) for microscaled X (n x i), G and U (o x i)."""
-    name = "kq_mx_gated"
+    name, dev = "kq_mx_gated", []
     n, o = Xc.shape[0], Gc.shape[0]
     if Uc.shape[0] != o:
         raise ValueError(f"{name}: {o} gate rows and {Uc.shape[0]} up rows")
-    p, ld = _matrix(name, "H", H, n, o, _floats())
-    w, wb = _ws(ws)
-    _launch(name, (Xc, Xs, Gc, Gs, Uc, Us, H, ws), stream,
-            [*_mx(name, "X", Xc, Xs, i), *_mx(name, "gate weights", Gc, Gs, i), *_mx(name, "up weights", Uc, Us, i),
-             n, o, i, _act(name, act), p, _xdt(H), ld, w, wb])
+    dt, per = _float(name, "H", H)
+    p = _matrix(name, "H", H, n, o, H.dtype, per, False, dev)
+    _launch(name, lib().kq_mx_gated, dev, ws, stream, *_mx(name, "X", Xc, Xs, i, dev),
+            *_mx(name, "gate weights", Gc, Gs, i, dev), *_mx(name, "up weights", Uc, Us, i, dev), n, o, i, _act(name, act),
+            p[0], dt, p[1])
 
 
 def kq_gated_forward(X, Wg, Wu, act: str, H, A=None, B=None, ws=None, stream=None) -> None:
     """H = act(X Wg^T) * (X Wu^T); A and B, where given, take the two products. One type for all."""
-    name = "kq_gated_forward"
-    (n, i), o = X.shape, Wg.shape[0]
-    dt, wi = (X.dtype,), _whole(i, X)
-    if X.dtype not in _floats():
-        raise TypeError(f"{name}: X has type {X.dtype}")
-    ins = [_matrix(name, w, t, r, i, dt, wi) for w, t, r in (("X", X, n), ("Wg", Wg, o), ("Wu", Wu, o))]
-    outs = [(None, 0) if t is None else _matrix(name, w, t, n, o, dt) for w, t in (("H", H), ("A", A), ("B", B))]
-    w, wb = _ws(ws)
-    _launch(name, (X, Wg, Wu, H, A, B, ws), stream,
-            [*sum(ins, ()), _xdt(X), n, o, i, _act(name, act), *sum(outs, ()), w, wb])
+    name, dev = "kq_gated_forward", []
+    (n, i), o, t = X.shape, Wg.shape[0], X.dtype
+    dt, per = _float(name, "X", X)
+    args = (*_matrix(name, "X", X, n, i, t, per, True, dev), *_matrix(name, "Wg", Wg, o, i, t, per, True, dev),
+            *_matrix(name, "Wu", Wu, o, i, t, per, True, dev), dt, n, o, i, _act(name, act),
+            *_matrix(name, "H", H, n, o, t, per, False, dev),
+            *((None, 0) if A is None else _matrix(name, "A", A, n, o, t, per, False, dev)),
+            *((None, 0) if B is None else _matrix(name, "B", B, n, o, t, per, False, dev)))
+    _launch(name, lib().kq_gated_forward, dev, ws, stream, *args)
 
 
 def kq_gated_backward(dH, A, B, X, Wg, Wu, act: str, dA, dB, dX=None, dWg=None, dWu=None, ws=None, stream=None) -> None:
     """Gradients of kq_gated_forward from dH and the A and B that it kept: dA and dB always, dX, dWg and
     dWu where given (X may be None without weight gradients, Wg and Wu without dX)."""
-    name = "kq_gated_backward"
-    n, o = dH.shape
-    if dH.dtype not in _floats():
-        raise TypeError(f"{name}: dH has type {dH.dtype}")
-    some = next((t for t in (dX, dWg, dWu, X, Wg, Wu) if t is not None), None)
-    i = 1 if some is None else some.shape[1]
-    dt, wi, wo = (dH.dtype,), _whole(i, dH), _whole(o, dH)
+    name, dev = "kq_gated_backward", []
+    (n, o), t = dH.shape, dH.dtype
+    dt, per = _float(name, "dH", dH)
     if dX is not None and (Wg is None or Wu is None):
         raise ValueError(f"{name}: dX needs Wg and Wu")
     if (dWg is not None or dWu is not None) and X is None:
         raise ValueError(f"{name}: weight gradients need X")
+    some = next((m for m in (dX, dWg, dWu, X, Wg, Wu) if m is not None), None)
+    i = 1 if some is None else some.shape[1]
 
-    def take(what, t, rows, cols, size=0):
-        return (None, 0) if t is None else _matrix(name, what, t, rows, cols, dt, size)
+    def take(what, m, rows, cols, whole):
+        return (None, 0) if m is None else _matrix(name, what, m, rows, cols, t, per, whole, dev)
 
-    args = [*take("dH", dH, n, o), *take("A", A, n, o), *take("B", B, n, o), *take("X", X, n, i),
-            *take("Wg", Wg, o, i), *take("Wu", Wu, o, i), _xdt(dH), n, o, i, _act(name, act),
-            *take("dA", dA, n, o, wo), *take("dB", dB, n, o, wo), *take("dX", dX, n, i), *take("dWg", dWg, o, i),
-            *take("dWu", dWu, o, i)]
-    del wi
-    w, wb = _ws(ws)
-    _launch(name, (dH, A, B, X, Wg, Wu, dA, dB, dX, dWg, dWu, ws), stream, [*args, w, wb])
+    # dA and dB are also operands, of the products that follow
+    args = (*take("dH", dH, n, o, False), *take("A", A, n, o, False), *take("B", B, n, o, False), *take("X", X, n, i, True),
+            *take("Wg", Wg, o, i, True), *take("Wu", Wu, o, i, True), dt, n, o, i, _act(name, act),
+            *take("dA", dA, n, o, True), *take("dB", dB, n, o, True), *take("dX", dX, n, i, False),
+            *take("dWg", dWg, o, i, False), *take("dWu", dWu, o, i, False))
+    _launch(name, lib().kq_gated_backward, dev, ws, stream, *args)

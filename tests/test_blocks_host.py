@@ -149,14 +149,10 @@ def test_wrappers_refuse_host_tensors_and_bad_types():
         K.kq_mx_quantize(x, c, s)
     with pytest.raises(TypeError, match="type"):
         K.kq_mx_quantize(x.double(), c, s)
-    with pytest.raises(TypeError, match="uint8"):
-        K._mx("f", "A", c.int(), s, 64)
     with pytest.raises(ValueError, match="GPU"):
         K.kq_gated_forward(x, x, x, "silu", x)
     with pytest.raises(TypeError, match="type"):
         K.kq_gated_forward(x.half(), x, x, "silu", x)
-    with pytest.raises(ValueError, match="activation"):
-        K._act("f", "tanh")
     with pytest.raises(ValueError, match="needs Wg and Wu"):
         K.kq_gated_backward(x, x, x, None, None, None, "silu", x, x, dX=x)
     with pytest.raises(ValueError, match="need X"):

@@ -494,8 +494,12 @@ def test_wrapper_refusals_on_device():
     with pytest.raises(ValueError, match="past the storage"):     # the last row's 16 bytes are not all there
         K.kq_gated_forward(torch.zeros(4 * 64 - 3, device=dev).as_strided((4, 61), (64, 1)),
                            torch.zeros(8, 64, device=dev)[:, :61], torch.zeros(8, 64, device=dev)[:, :61], "silu", h)
-    with pytest.raises(ValueError, match="different devices"):
+    with pytest.raises(ValueError, match="not on a GPU"):
         K.kq_mx_gemm(c, s, wc, wsc, 64, h, ws=torch.empty(4, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="uint8"):
+        K.kq_mx_gemm(c.int(), s, wc, wsc, 64, h)
+    with pytest.raises(ValueError, match="activation"):
+        K.kq_gated_forward(x, w, w, "tanh", h)
 
 
 # ----------------------------------------------------------------------------------- used together

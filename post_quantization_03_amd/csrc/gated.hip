@@ -54,13 +54,15 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const void* dH, int64_t
         load(dH, lddh, r, c, h);
         load(A, lda, r, c, a);
         load(B, ldb, r, c, b);
+        with_act(act, [&](auto ACT) {
 #pragma unroll
-        for (int k = 0; k < V; k++) {
-            float f, df;
-            act_both(a[k], act, f, df);
-            da[k] = h[k] * b[k] * df;
-            db[k] = h[k] * f;
-        }
+            for (int k = 0; k < V; k++) {
+                float f, df;
+                act_both<ACT.value>(a[k], f, df);
+                da[k] = h[k] * b[k] * df;
+                db[k] = h[k] * f;
+            }
+        });
         store_run<V>(dA, BF ? KQ_BF16 : KQ_F32, r * ldda + c, da, o - c);
         store_run<V>(dB, BF ? KQ_BF16 : KQ_F32, r * lddb + c, db, o - c);
     }

@@ -11,6 +11,8 @@
 // loops below are written once for the three.
 #pragma once
 
+#include <type_traits>
+
 #include "kq_internal.h"
 
 namespace kq {
@@ -69,30 +71,50 @@ __device__ __forceinline__ void store_run(void* out, int dt, int64_t off, const 
 }
 
 // ------------------------------------------------------------------------------------- activations
-// gate = act(a) / a, the factor in 0..1 that multiplies a
-__device__ __forceinline__ float act_gate(float a, int act) {
-    switch (act) {
-        case KQ_ACT_SILU: return 1.0f / (1.0f + expf(-a));
-        case KQ_ACT_GELU: return 0.5f * erfcf(-0.70710678118654752f * a);
-        case KQ_ACT_GELU_TANH: return 1.0f / (1.0f + expf(-1.5957691216057308f * (a + 0.044715f * a * a * a)));
-        default: return a > 0.0f ? 1.0f : (a == a ? 0.0f : a);
-    }
+// gate = act(a) / a, the factor in 0..1 that multiplies a. The logistic gates take the hardware's exp2 and
+// reciprocal (both within an ulp): the argument's rounding, |a| 2^-24 relative, is of the same order.
+__device__ __forceinline__ float logistic(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
 }
-__device__ __forceinline__ float act_value(float a, int act) { return a * act_gate(a, act); }
+template <int ACT>
+__device__ __forceinline__ float act_gate(float a) {
+    if constexpr (ACT == KQ_ACT_SILU) return logistic(a);
+    else if constexpr (ACT == KQ_ACT_GELU) return 0.5f * erfcf(-0.70710678118654752f * a);
+    else if constexpr (ACT == KQ_ACT_GELU_TANH) return logistic(1.5957691216057308f * (a + 0.044715f * a * a * a));
+    else return a > 0.0f ? 1.0f : (a == a ? 0.0f : a);
+}
 
 // act(a) and act'(a)
-__device__ __forceinline__ void act_both(float a, int act, float& f, float& df) {
-    const float p = act_gate(a, act);
+template <int ACT>
+__device__ __forceinline__ void act_both(float a, float& f, float& df) {
+    const float p = act_gate<ACT>(a);
     f = a * p;
+    if constexpr (ACT == KQ_ACT_SILU) df = p * (1.0f + a * (1.0f - p));
+    else if constexpr (ACT == KQ_ACT_GELU) df = p + a * __builtin_amdgcn_exp2f(-0.72134752044448170f * a * a) * 0.39894228040143268f;
+    else if constexpr (ACT == KQ_ACT_GELU_TANH)
+        // beyond 16 the gate is 0 or 1 to the last bit, and a * a may not be finite
+        df = fabsf(a) > 16.0f ? p : p + a * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * a * a);
+    else df = p;
+}
+
+// f(ACT) for the activation given at run time: one branch around a whole run of values
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
     switch (act) {
-        case KQ_ACT_SILU: df = p * (1.0f + a * (1.0f - p)); return;
-        case KQ_ACT_GELU: df = p + a * expf(-0.5f * a * a) * 0.39894228040143268f; return;
-        case KQ_ACT_GELU_TANH:
-            // beyond 16 the gate is 0 or 1 to the last bit, and a * a may not be finite
-            df = fabsf(a) > 16.0f ? p : p + a * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * a * a);
-            return;
-        default: df = p;
+        case KQ_ACT_SILU: f(std::integral_constant<int, KQ_ACT_SILU>{}); return;
+        case KQ_ACT_GELU: f(std::integral_constant<int, KQ_ACT_GELU>{}); return;
+        case KQ_ACT_GELU_TANH: f(std::integral_constant<int, KQ_ACT_GELU_TANH>{}); return;
+        default: f(std::integral_constant<int, KQ_ACT_RELU>{});
     }
+}
+
+// h = act(a) * b
+template <int N>
+__device__ __forceinline__ void act_times(float (&h)[N], const float (&a)[N], const float (&b)[N], int act) {
+    with_act(act, [&](auto A) {
+#pragma unroll
+        for (int e = 0; e < N; e++) h[e] = a[e] * act_gate<A.value>(a[e]) * b[e];
+    });
 }
 
 // --------------------------------------------------------------------------------------- products
@@ -195,10 +217,28 @@ __device__ __forceinline__ int key_b(int r) { return (r & 3) | (((r / (4 * FNH))
 __device__ __forceinline__ int key_t(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
-typedef __attribute__((address_space(1))) void* glb_ptr;
 
-__device__ __forceinline__ void dma16(const char* src, char* lds) {
-    __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)lds, 16, 0, 0);
+// 16 bytes a lane from base + off straight to LDS (lds + 16 lane; base and lds are the wavefront's). HIDDEN:
+// the compiler takes a transposing LDS read to depend on every load to LDS in flight and would wait for
+// the slab just requested, so beside such reads the load is written out. It has no output register, and
+// landed_barrier waits for it.
+template <bool HIDDEN>
+__device__ __forceinline__ void dma16(const char* base, uint32_t off, char* lds) {
+    if constexpr (HIDDEN) {
+        const tl_i4 rsrc = {(int)(uintptr_t)base, (int)((uintptr_t)base >> 32) & 0xFFFF, -1, 0x00020000};
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                     :: "v"(off), "s"(rsrc), "s"((uint32_t)(uintptr_t)(lds_ptr)lds) : "memory", "m0");
+    } else {
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0xFFFFFFFF, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)lds, 16, (int)off, 0, 0, 0);
+    }
+}
+
+// Barrier at which every wavefront's loads to LDS have landed. The wait is written out: a barrier by itself
+// orders ordinary LDS and global accesses, not the loads that write LDS.
+__device__ __forceinline__ void landed_barrier() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0) alone
+    __syncthreads();
 }
 
 template <int E, int MODE>
@@ -223,107 +263,72 @@ __global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
     const int64_t ldA = MODE == TP_GRAD_W && blockIdx.z ? g.lda2 : g.lda;
     pA += TA ? m0 * 2 : m0 * ldA;
     pB += TB ? n0 * 2 : n0 * g.ldb;
-    const char* pA2 = MODE == TP_GRAD_X ? g.A2 + m0 * g.lda2 : nullptr;
-    const char* pB2 = MODE == TP_GRAD_X ? g.B2 + n0 * 2 : MODE == TP_GATED ? g.B2 + n0 * g.ldb2 : nullptr;
-    uint32_t offA[4], offB[4], offA2[4], offB2[4];
-    int cA, cB[4];                       // chunk (K-contiguous operands) that the lane loads
-    {
-        const int r8 = lane >> 3, pos = lane & 7;
-        cA = pos ^ r8;
+    const char* pB2 = MODE == TP_GATED ? g.B2 + n0 * g.ldb2 : nullptr;
+    const int r8 = lane >> 3, pos = lane & 7;
+    // chunk of a K-contiguous operand that the lane loads (the same in all four loads: they are 64 rows apart)
+    const int cA = pos ^ r8, cB = pos ^ key_b<FNH>(wave * 8 + r8);
+    uint32_t offA[4], offB[4];
+    auto offsets = [&](int64_t lda, int64_t ldb) {
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            const int r = (q * 8 + wave) * 8 + r8;
-            if constexpr (TA) {
-                const int k = (q * 8 + wave) * 2 + (lane >> 5), p = lane & 31;
-                int c = (((p >> 1) ^ key_t(k)) << 1) | (p & 1);
-                c = c * 8 <= mlast ? c : mlast >> 3;
-                offA[q] = (uint32_t)((int64_t)k * ldA + c * 16);
-            } else {
-                const int rr = r < mlast ? r : mlast;
-                offA[q] = (uint32_t)((int64_t)rr * ldA);
-                if constexpr (MODE == TP_GRAD_X) offA2[q] = (uint32_t)((int64_t)rr * g.lda2);
-            }
-            if constexpr (TB) {
-                const int k = (q * 8 + wave) * 2 + (lane >> 5), p = lane & 31;
-                int c = (((p >> 1) ^ key_t(k)) << 1) | (p & 1);
-                c = c * 8 <= nlast ? c : nlast >> 3;
-                offB[q] = (uint32_t)((int64_t)k * g.ldb + c * 16);
-                if constexpr (MODE == TP_GRAD_X) offB2[q] = (uint32_t)((int64_t)k * g.ldb2 + c * 16);
-            } else {
-                cB[q] = pos ^ key_b<FNH>(r);
-                // gated: rows 0..127 of the slab are gate rows (q < 2), 128..255 up rows
-                int rr = MODE == TP_GATED ? r & 127 : r;
-                rr = rr < nlast ? rr : nlast;
-                offB[q] = (uint32_t)((int64_t)rr * (MODE == TP_GATED && q >= 2 ? g.ldb2 : g.ldb));
-            }
-        }
-    }
-    const int64_t nch = (g.K + EPC - 1) / EPC;           // chunks of K, the last one possibly partial
-    const int part = E == EL_MX ? 0 : (int)(g.K % EPC);  // values in a partial last chunk (E2M1 blocks are whole)
-    const int64_t slabs1 = (g.K + BK - 1) / BK, slabs = MODE == TP_GRAD_X ? 2 * slabs1 : slabs1;
-
-    // slab t into buffer buf. K-contiguous operands: chunks past K become zero (E2M1: a valid chunk is read
-    // again; its scales are zero on both sides, so its products vanish). Transposed ones: K rows past K
-    // become zero. Rows and columns past M and N repeat the last one and are never stored.
-    auto stage = [&](int64_t t, int buf) {
-        char* la = tl_sm + buf * 2 * TL_OPB + wave * 1024;
-        char* lb = la + TL_OPB;
-        const bool second = MODE == TP_GRAD_X && t >= slabs1;
-        const int64_t s = second ? t - slabs1 : t;
-        const char* a0 = second ? pA2 : pA;
-        const char* b0 = second ? pB2 : pB;
-        const int64_t la_ld = second ? g.lda2 : ldA, lb_ld = second ? g.ldb2 : g.ldb;
-        const bool whole = (s + 1) * BK <= g.K;
-        if (whole) {
-            a0 += TA ? s * BK * la_ld : s * 128;
-            b0 += TB ? s * BK * lb_ld : s * 128;
-            const char* b2 = MODE == TP_GATED ? pB2 + s * 128 : nullptr;
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const uint32_t oa = second ? offA2[q] : offA[q];
-                dma16(a0 + (TA ? oa : oa + cA * 16), la + q * 8192);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const uint32_t ob = second ? offB2[q] : offB[q];
-                const char* b = MODE == TP_GATED && q >= 2 ? b2 : b0;
-                dma16(b + (TB ? ob : ob + cB[q] * 16), lb + q * 8192);
-            }
-            return;
-        }
-        const tl_i4 zero = {0, 0, 0, 0};
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const uint32_t oa = second ? offA2[q] : offA[q];
-            if constexpr (TA) {
-                const int64_t k = s * BK + (q * 8 + wave) * 2 + (lane >> 5);
-                if (k < g.K) dma16(a0 + s * BK * la_ld + oa, la + q * 8192);
-                else *reinterpret_cast<tl_i4*>(la + q * 8192 + lane * 16) = zero;
-            } else {
-                int64_t c = s * 8 + cA;
-                if (E == EL_MX && c >= nch) c = nch - 1;
-                if (c < nch) dma16(a0 + oa + c * 16, la + q * 8192);
-                else *reinterpret_cast<tl_i4*>(la + q * 8192 + lane * 16) = zero;
-            }
-            const uint32_t ob = second ? offB2[q] : offB[q];
-            if constexpr (TB) {
-                const int64_t k = s * BK + (q * 8 + wave) * 2 + (lane >> 5);
-                if (k < g.K) dma16(b0 + s * BK * lb_ld + ob, lb + q * 8192);
-                else *reinterpret_cast<tl_i4*>(lb + q * 8192 + lane * 16) = zero;
-            } else {
-                int64_t c = s * 8 + cB[q];
-                if (E == EL_MX && c >= nch) c = nch - 1;
-                const char* b = MODE == TP_GATED && q >= 2 ? pB2 : b0;
-                if (c < nch) dma16(b + ob + c * 16, lb + q * 8192);
-                else *reinterpret_cast<tl_i4*>(lb + q * 8192 + lane * 16) = zero;
-            }
+            const int r = (q * 8 + wave) * 8 + r8;                                 // row of a K-contiguous operand
+            const int k = (q * 8 + wave) * 2 + (lane >> 5), p = lane & 31;         // row and place of a transposed one
+            const int c = (((p >> 1) ^ key_t(k)) << 1) | (p & 1);
+            if constexpr (TA) offA[q] = (uint32_t)k * (uint32_t)lda + (c * 8 <= mlast ? c : mlast >> 3) * 16;
+            else offA[q] = (uint32_t)(r < mlast ? r : mlast) * (uint32_t)lda + cA * 16;
+            // gated: rows 0..127 of the slab are gate rows (q < 2), 128..255 up rows
+            const int rb = MODE == TP_GATED ? r & 127 : r;
+            if constexpr (TB) offB[q] = (uint32_t)k * (uint32_t)ldb + (c * 8 <= nlast ? c : nlast >> 3) * 16;
+            else offB[q] = (uint32_t)(rb < nlast ? rb : nlast) * (uint32_t)(MODE == TP_GATED && q >= 2 ? g.ldb2 : ldb) + cB * 16;
         }
     };
+    offsets(ldA, g.ldb);
+    const int64_t nch = (g.K + EPC - 1) / EPC;           // chunks of K, the last one possibly partial
+    const int part = E == EL_MX ? 0 : (int)(g.K % EPC);  // values in a partial last chunk (E2M1 blocks are whole)
+    const int slabs = (int)((g.K + BK - 1) / BK);
+    const int whole = (int)(g.K / BK);                   // slabs that lie inside K
+    int64_t stepA = TA ? BK * ldA : 128, stepB = TB ? BK * g.ldb : 128;
+    int ts = 0;                                          // slab to be staged next
+
+    // Stages the next slab into buffer buf. K-contiguous operands: chunks past K become zero (E2M1: a valid chunk
+    // is read again; its scales are zero on both sides, so its products vanish). Transposed ones: K rows past
+    // K become zero. Rows and columns past M and N repeat the last one and are never stored.
+    auto stage = [&](int buf) {
+        char* la = tl_sm + buf * 2 * TL_OPB + wave * 1024;
+        char* lb = la + TL_OPB;
+        if (ts < whole) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) dma16<TB>(pA, offA[q], la + q * 8192);
+#pragma unroll
+            for (int q = 0; q < 4; q++) dma16<TB>(MODE == TP_GATED && q >= 2 ? pB2 : pB, offB[q], lb + q * 8192);
+        } else {
+            const tl_i4 zero = {0, 0, 0, 0};
+            const int left = (int)(nch - (int64_t)ts * 8), krows = (int)(g.K - (int64_t)ts * BK);
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int k = (q * 8 + wave) * 2 + (lane >> 5);
+                const bool inA = TA ? k < krows : cA < left, inB = TB ? k < krows : cB < left;
+                if constexpr (E == EL_MX) {
+                    dma16<TB>(pA, offA[q] + (inA ? 0 : (left - 1 - cA) * 16), la + q * 8192);
+                    dma16<TB>(MODE == TP_GATED && q >= 2 ? pB2 : pB, offB[q] + (inB ? 0 : (left - 1 - cB) * 16), lb + q * 8192);
+                } else {
+                    if (inA) dma16<TB>(pA, offA[q], la + q * 8192);
+                    else *reinterpret_cast<tl_i4*>(la + q * 8192 + lane * 16) = zero;
+                    if (inB) dma16<TB>(MODE == TP_GATED && q >= 2 ? pB2 : pB, offB[q], lb + q * 8192);
+                    else *reinterpret_cast<tl_i4*>(lb + q * 8192 + lane * 16) = zero;
+                }
+            }
+        }
+        ts++;
+        pA += stepA;
+        pB += stepB;
+        if (MODE == TP_GATED) pB2 += 128;
+    };
     // values past K of a partial last chunk, once it has landed: each lane clears its own chunks
-    auto clear_part = [&](int64_t t, int buf) {
-        const int64_t s = MODE == TP_GRAD_X && t >= slabs1 ? t - slabs1 : t;
-        if (s != slabs1 - 1) return;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    auto clear_part = [&](int t, int buf) {
+        if (t != slabs - 1) return;
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) alone
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         char* la = tl_sm + buf * 2 * TL_OPB + wave * 1024 + lane * 16;
         auto cut = [&](char* p) {
             tl_i4 v = *reinterpret_cast<tl_i4*>(p);
@@ -334,13 +339,11 @@ __global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
             }
             *reinterpret_cast<tl_i4*>(p) = v;
         };
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            if constexpr (!TA)
-                if (s * 8 + cA == nch - 1) cut(la + q * 8192);
-            if constexpr (!TB)
-                if (s * 8 + cB[q] == nch - 1) cut(la + TL_OPB + q * 8192);
-        }
+        const int last = (int)((nch - 1) & 7);           // the chunk's place in the slab
+        if (!TA && cA == last)
+            for (int q = 0; q < 4; q++) cut(la + q * 8192);
+        if (!TB && cB == last)
+            for (int q = 0; q < 4; q++) cut(la + TL_OPB + q * 8192);
     };
 
     tl_f4 acc[TL_FM][TL_FN];
@@ -350,96 +353,112 @@ __global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
         for (int j = 0; j < TL_FN; j++) acc[i][j] = tl_f4{0, 0, 0, 0};
 
     // scales of a slab's two steps (E2M1): a dword holds a lane's bytes of four fragments
-    uint32_t scA[2][2], scB[2], nxA[2][2], nxB[2];
-    const uint32_t *qA = nullptr, *qB = nullptr;
+    uint32_t scA[2][2], scB[2];
+    const uint32_t *qA = nullptr, *qB = nullptr;         // step 0 of the slab whose scales are loaded next
     if constexpr (E == EL_MX) {
-        qA = g.sA + (tm * 4 + wm * 2) * g.ksteps * 64 + lane;
-        qB = g.sB + (tn * 4 + wn) * g.ksteps * 64 + lane;
+        qA = g.sA + (tm * 4 + wm * 2) * g.ksteps * 64;
+        qB = g.sB + (tn * 4 + wn) * g.ksteps * 64;
     }
-    auto load_scales = [&](int64_t t) {
-#pragma unroll
-        for (int s = 0; s < 2; s++) {
-            nxA[0][s] = qA[(2 * t + s) * 64];
-            nxA[1][s] = qA[(g.ksteps + 2 * t + s) * 64];
-            nxB[s] = qB[(2 * t + s) * 64];
+    auto load_scales = [&](int s) {
+        scA[0][s] = qA[s * 64 + lane];
+        scA[1][s] = qA[(g.ksteps + s) * 64 + lane];
+        scB[s] = qB[s * 64 + lane];
+        if (s == 1) {
+            qA += 128;
+            qB += 128;
         }
     };
 
-    auto fragA = [&](const char* la, int i, int s) -> tl_i4 {
-        if constexpr (TA) {
-            const int k = 32 * s + 8 * g4 + (x16 >> 2), piece = x16 & 3;
-            tl_i4 r;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int kk = k + 4 * h, p = wm * 8 + i;
-                const char* a = la + kk * 512 + (((p ^ key_t(kk)) << 1) | (piece >> 1)) * 16 + (piece & 1) * 8;
-                const tl_s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)a);
-                reinterpret_cast<tl_s4*>(&r)[h] = v;
-            }
-            return r;
-        } else {
-            const int r = wm * 128 + 16 * i + x16;
-            return *reinterpret_cast<const tl_i4*>(la + r * 128 + (((s * 4 + g4) ^ key_a(r)) << 4));
-        }
+    // fragment i of A (j of B) for step s of the slab at LDS offset `at`. Transposed: lane x16 of group g4 ends
+    // with the 8 K rows 8 g4 .. 8 g4 + 7 of column 16 i + x16, from two reads of 4 K rows each; the key
+    // of those rows depends on the lane alone, so i enters the address by one exclusive or.
+    const int kt = 8 * g4 + (x16 >> 2);
+    const int lfA = TA ? kt * 512 + ((wm * 8) ^ key_t(kt)) * 32 + (x16 & 3) * 8
+                       : (wm * 128 + x16) * 128 + ((g4 ^ key_a(x16)) << 4);
+    const int rB0 = MODE == TP_GATED ? wn * 32 + b_row<FNH>(0, x16) : wn * 64 + b_row<FNH>(0, x16);
+    const int lfB = TB ? kt * 512 + ((wn * 4) ^ key_t(kt)) * 32 + (x16 & 3) * 8 : rB0 * 128 + ((g4 ^ key_b<FNH>(rB0)) << 4);
+    auto tr_frag = [&](int off) -> tl_i4 {
+        const tl_s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)(tl_sm + off));
+        const tl_s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)(tl_sm + off + 2048));
+        tl_i4 r;
+        reinterpret_cast<tl_s4*>(&r)[0] = lo;
+        reinterpret_cast<tl_s4*>(&r)[1] = hi;
+        return r;
     };
-    auto fragB = [&](const char* lb, int j, int s) -> tl_i4 {
-        if constexpr (TB) {
-            const int k = 32 * s + 8 * g4 + (x16 >> 2), piece = x16 & 3;
-            tl_i4 r;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int kk = k + 4 * h, p = wn * 4 + j;
-                const char* a = lb + kk * 512 + (((p ^ key_t(kk)) << 1) | (piece >> 1)) * 16 + (piece & 1) * 8;
-                const tl_s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)a);
-                reinterpret_cast<tl_s4*>(&r)[h] = v;
-            }
-            return r;
-        } else {
-            const int r = MODE == TP_GATED ? (j >= FNH ? 128 : 0) + wn * 32 + b_row<FNH>(j % FNH, x16)
-                                           : wn * 64 + b_row<FNH>(j, x16);
-            return *reinterpret_cast<const tl_i4*>(lb + r * 128 + (((s * 4 + g4) ^ key_b<FNH>(r)) << 4));
-        }
+    auto fragA = [&](int at, int i, int s) -> tl_i4 {
+        if constexpr (TA) return tr_frag(((at + lfA) ^ (i * 32)) + s * 16384);
+        else return *reinterpret_cast<const tl_i4*>(tl_sm + ((at + lfA) ^ (s * 64)) + i * 2048);
+    };
+    auto fragB = [&](int at, int j, int s) -> tl_i4 {
+        at += TL_OPB;
+        if constexpr (TB) return tr_frag(((at + lfB) ^ (j * 32)) + s * 16384);
+        else return *reinterpret_cast<const tl_i4*>(tl_sm + ((at + lfB) ^ (s * 64)) + (j >= FNH ? 128 * 128 : 0) + (j % FNH) * 512);
     };
 
-    stage(0, 0);
-    if constexpr (E == EL_MX) load_scales(0);
-    int buf = 0;
-    for (int64_t t = 0; t < slabs; t++) {
-        if (part && (!TA || !TB)) clear_part(t, buf);
-        __syncthreads();      // slab t has landed, and every wavefront is done with slab t - 1
-        if constexpr (E == EL_MX) {
+    // The loop is software-pipelined by half a slab: while one step's products run, the next step's fragments
+    // come from LDS, and the barrier stands between the two steps of a slab. At the barrier every wavefront
+    // has all of slab t in registers or accumulators, so its buffer takes slab t + 2, and slab t + 1 has had
+    // a whole slab's products to arrive in. Registers: a fragment of A is overwritten in place by the next
+    // step's once its products are issued, except that the first step's last two are kept beside the second
+    // step's (fx), whose loads would otherwise be waited for at the barrier.
+    constexpr int KEEP = 2, INPL = TL_FM - KEEP;
+    tl_i4 fa[TL_FM], fx[KEEP], fb[2][TL_FN];
+    auto slab_at = [&](int t) { return (t & 1) * 2 * TL_OPB; };
+    auto products = [&](int i, int s, tl_i4 a) {
 #pragma unroll
-            for (int s = 0; s < 2; s++) {
-                scA[0][s] = nxA[0][s];
-                scA[1][s] = nxA[1][s];
-                scB[s] = nxB[s];
+        for (int j = 0; j < TL_FN; j++) {
+            // rows of the result are B's rows (output columns), columns are A's rows
+            if constexpr (E == EL_MX)
+                acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], (int)scB[s], j, (int)scA[i >> 2][s], i & 3);
+            else
+                acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], 0, 0, 0, 0);
+        }
+    };
+    // One step: the products of A's fragment i with all of B's, then the reads that replace what they used,
+    // spread over the step so that no product waits for a burst of them.
+    auto step = [&](int s, int at) {
+        const int nx = s ^ 1;            // the step whose fragments are read (slab at `at`)
+#pragma unroll
+        for (int i = 0; i < TL_FM; i++) {
+            products(i, s, s == 1 && i >= INPL ? fx[i - INPL] : fa[i]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (i < INPL) fa[i] = fragA(at, i, nx);
+            if (i < KEEP) {
+                if (s == 0) fx[i] = fragA(at, INPL + i, nx);
+                else fa[INPL + i] = fragA(at, INPL + i, nx);
             }
+            if (i % 2 == 0 && i / 2 < TL_FN) fb[nx][i / 2] = fragB(at, i / 2, nx);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (t + 1 < slabs) {
-            stage(t + 1, buf ^ 1);
-            if constexpr (E == EL_MX) load_scales(t + 1);
+    };
+    for (int pair = 0; pair < (MODE == TP_GRAD_X ? 2 : 1); pair++) {
+        if (MODE == TP_GRAD_X && pair) {                 // A2 and B2 into the same sums
+            ts = 0;
+            pA = g.A2 + m0 * g.lda2;
+            pB = g.B2 + n0 * 2;
+            stepB = BK * g.ldb2;
+            offsets(g.lda2, g.ldb2);
         }
-        const char* la = tl_sm + buf * 2 * TL_OPB;
-        const char* lb = la + TL_OPB;
+        stage(0);
+        if (part && (!TA || !TB)) clear_part(0, 0);
+        if constexpr (E == EL_MX) load_scales(0);
+        landed_barrier();
+        if (slabs > 1) stage(1);
 #pragma unroll
-        for (int s = 0; s < 2; s++) {
-            tl_i4 fa[TL_FM], fb[TL_FN];
+        for (int j = 0; j < TL_FN; j++) fb[0][j] = fragB(0, j, 0);
 #pragma unroll
-            for (int j = 0; j < TL_FN; j++) fb[j] = fragB(lb, j, s);
-#pragma unroll
-            for (int i = 0; i < TL_FM; i++) fa[i] = fragA(la, i, s);
-#pragma unroll
-            for (int i = 0; i < TL_FM; i++)
-#pragma unroll
-                for (int j = 0; j < TL_FN; j++) {
-                    // rows of the result are B's rows (output columns), columns are A's rows
-                    if constexpr (E == EL_MX)
-                        acc[i][j] = mma_step<E>(fb[j], fa[i], acc[i][j], (int)scB[s], j, (int)scA[i >> 2][s], i & 3);
-                    else
-                        acc[i][j] = mma_step<E>(fb[j], fa[i], acc[i][j], 0, 0, 0, 0);
-                }
+        for (int i = 0; i < TL_FM; i++) fa[i] = fragA(0, i, 0);
+        for (int t = 0; t < slabs; t++) {
+            if constexpr (E == EL_MX) load_scales(1);
+            step(0, slab_at(t));
+            if (part && (!TA || !TB) && t + 1 < slabs) clear_part(t + 1, (t + 1) & 1);
+            landed_barrier();     // slab t + 1 has landed, and every wavefront holds the rest of slab t
+            if (E == EL_MX && t + 1 < slabs) load_scales(0);     // ahead of the slab's loads: waiting for it skips those
+            if (t + 2 < slabs) stage(t & 1);
+            __builtin_amdgcn_sched_barrier(0);
+            // past the last slab the fragments come from LDS that nothing uses any more
+            step(1, slab_at(t + 1));
         }
-        buf ^= 1;
     }
 
     // ---- epilogue: lane holds output row x16 of fragment row i, columns as b_row (or 16 j + 4 g4 when transposed)
@@ -458,8 +477,8 @@ __global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
                 for (int r = 0; r < 4; r++) {
                     a[4 * j + r] = acc[i][j][r];
                     b[4 * j + r] = acc[i][j + FNH][r];
-                    h[4 * j + r] = act_value(a[4 * j + r], g.act) * b[4 * j + r];
                 }
+            act_times(h, a, b, g.act);
             store_run<4 * FNH>(Y, g.dt, m * ldY + n, h, g.N - n);
             if (g.Y2) store_run<4 * FNH>(g.Y2, g.dt, m * g.ldy2 + n, a, g.N - n);
             if (g.Y3) store_run<4 * FNH>(g.Y3, g.dt, m * g.ldy3 + n, b, g.N - n);
@@ -619,9 +638,11 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
     }
     const int64_t t = 16 * wave + x16, n = f0 + 4 * g4;
     if (t >= g.n) return;
-    float y[4];
-#pragma unroll
-    for (int r = 0; r < 4; r++) y[r] = GATED ? act_value(sum[0][r], g.act) * sum[MATS - 1][r] : sum[0][r];
+    float y[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
+    if constexpr (GATED) {
+        const float a[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]}, b[4] = {sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
+        act_times(y, a, b, g.act);
+    }
     store_run<4>(g.Y, g.dt, t * g.ldy + n, y, g.o - n);
     if constexpr (GATED) {
         if (g.Y2) {

@@ -89,14 +89,20 @@ static kq_status dense_check(const char* who, kq_dtype dt, const Dense& m, int64
     return KQ_OK;
 }
 
+static kq_status ws_check(const char* who, const void* ws, size_t have, size_t need) {
+    if (!ws || have < need || !aligned16(ws)) return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
+    return KQ_OK;
+}
+
 static const char* bytes_of(const void* p) { return static_cast<const char*>(p); }
 
 template <int E>
 static kq_status gated_forward(const char* who, const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu,
                                int64_t ldu, int64_t n, int64_t o, int64_t i, int act, kq_dtype dt, void* H, int64_t ldh,
-                               void* A, int64_t lda, void* B, int64_t ldb, hipStream_t st) {
+                               void* A, int64_t lda, void* B, int64_t ldb, void* ws,
+                               size_t ws_bytes, hipStream_t st) {
     const int64_t es = E == EL_BF16 ? 2 : 4;
-    if (n <= FEW_MAX) {
+    if (few_tokens<E>(n, o, i)) {
         FewArgs f{};
         f.n = n; f.o = o; f.K = i;
         f.A = bytes_of(X); f.lda = ldx * es;
@@ -113,15 +119,31 @@ static kq_status gated_forward(const char* who, const void* X, int64_t ldx, cons
     g.B2 = bytes_of(Wu); g.ldb2 = ldu * es;
     g.Y = H; g.ldy = ldh; g.Y2 = A; g.ldy2 = lda; g.Y3 = B; g.ldy3 = ldb;
     g.dt = dt; g.act = act;
-    return tile_launch<E, TP_GATED>(g, 1, st, who);
+    Arena ar(ws, ws_bytes);
+    const size_t np = tile_plan<E, TP_GATED>(n, o, i, 1).part;
+    return tile_launch<E, TP_GATED>(g, 1, np ? ar.take<float>(np) : nullptr, st, who);
 }
 
 }  // namespace kq
 
 using namespace kq;
 
-size_t gated_forward_ws(int64_t, int64_t, int64_t, kq_dtype) { return 0; }
-size_t gated_backward_ws(int64_t, int64_t, int64_t, kq_dtype) { return 0; }
+size_t gated_forward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
+    if (n <= 0 || o <= 0 || i <= 0 || (dt == KQ_BF16 ? few_tokens<EL_BF16>(n, o, i) : few_tokens<EL_F32>(n, o, i))) return 0;
+    return sizeof(float) * (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GATED>(n, o, i, 1) : tile_plan<EL_F32, TP_GATED>(n, o, i, 1)).part;
+}
+
+// The products run one after another on the caller's stream and share the split sums' memory.
+size_t gated_backward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
+    if (n <= 0 || o <= 0 || i <= 0) return 0;
+    size_t most = 0;
+    for (int pairs = 1; pairs <= 2; pairs++) {
+        const size_t w = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_W>(o, i, n, pairs) : tile_plan<EL_F32, TP_GRAD_W>(o, i, n, pairs)).part;
+        most = w > most ? w : most;
+    }
+    const size_t x = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_X>(n, i, o, 1) : tile_plan<EL_F32, TP_GRAD_X>(n, i, o, 1)).part;
+    return sizeof(float) * (x > most ? x : most);
+}
 
 extern "C" kq_status kq_gated_forward(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu,
                                       kq_dtype dt, int64_t n, int64_t o, int64_t i, kq_act act, void* H, int64_t ldh,
@@ -138,11 +160,12 @@ extern "C" kq_status kq_gated_forward(const void* X, int64_t ldx, const void* Wg
     KQ_TRY(dense_check(who, dt, Dense{H, ldh, "H"}, n, o));
     if (A) KQ_TRY(dense_check(who, dt, Dense{A, lda, "A"}, n, o));
     if (B) KQ_TRY(dense_check(who, dt, Dense{B, ldb, "B"}, n, o));
-    if (ws_bytes < gated_forward_ws(o, i, n, dt)) return fail(KQ_EWORKSPACE, "%s: workspace too small", who);
-    (void)ws;
+    if (const size_t need = gated_forward_ws(o, i, n, dt)) KQ_TRY(ws_check(who, ws, ws_bytes, need));
     if (dt == KQ_BF16)
-        return gated_forward<EL_BF16>(who, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, hs(stream));
-    return gated_forward<EL_F32>(who, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, hs(stream));
+        return gated_forward<EL_BF16>(who, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, ws, ws_bytes,
+                                      hs(stream));
+    return gated_forward<EL_F32>(who, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, ws, ws_bytes,
+                                      hs(stream));
 }
 
 extern "C" kq_status kq_gated_backward(const void* dH, int64_t lddh, const void* A, int64_t lda, const void* B, int64_t ldb,
@@ -181,8 +204,9 @@ extern "C" kq_status kq_gated_backward(const void* dH, int64_t lddh, const void*
         KQ_TRY(dense_check(who, dt, Dense{Wu, ldu, "Wu"}, o, i));
     }
     if (dWg || dWu) KQ_TRY(dense_check(who, dt, Dense{X, ldx, "X"}, n, i));
-    if (ws_bytes < gated_backward_ws(o, i, n, dt)) return fail(KQ_EWORKSPACE, "%s: workspace too small", who);
-    (void)ws;
+    if (dX || dWg || dWu)
+        if (const size_t need = gated_backward_ws(o, i, n, dt)) KQ_TRY(ws_check(who, ws, ws_bytes, need));
+    float* part = static_cast<float*>(ws);
     {
         const int64_t total = n * ((o + 16 / es - 1) / (16 / es));
         const dim3 grid((unsigned)((total + 255) / 256 < 65536 ? (total + 255) / 256 : 65536));
@@ -194,40 +218,25 @@ extern "C" kq_status kq_gated_backward(const void* dH, int64_t lddh, const void*
                                dA, ldda, dB, lddb);
         KQ_TRY(check_launch(who));
     }
-    if (dt == KQ_F32) {
-        const float *fa = static_cast<const float*>(dA), *fb = static_cast<const float*>(dB);
-        if (dX) {
-            float* y = static_cast<float*>(dX);
-            KQ_TRY(gemm<float>(gemm_args<float>(n, i, o, fa, ldda, static_cast<const float*>(Wg), ldg, y, lddx, 1.f, 0.f),
-                               false, false, st));
-            KQ_TRY(gemm<float>(gemm_args<float>(n, i, o, fb, lddb, static_cast<const float*>(Wu), ldu, y, lddx, 1.f, 1.f),
-                               false, false, st));
-        }
-        const float* x = static_cast<const float*>(X);
-        if (dWg)
-            KQ_TRY(gemm<float>(gemm_args<float>(o, i, n, fa, ldda, x, ldx, static_cast<float*>(dWg), lddg, 1.f, 0.f), true,
-                               false, st));
-        if (dWu)
-            KQ_TRY(gemm<float>(gemm_args<float>(o, i, n, fb, lddb, x, ldx, static_cast<float*>(dWu), lddu, 1.f, 0.f), true,
-                               false, st));
-        return KQ_OK;
-    }
     if (dX) {
         TileArgs g{};
         g.M = n; g.N = i; g.K = o;
-        g.A = bytes_of(dA); g.lda = ldda * 2; g.B = bytes_of(Wg); g.ldb = ldg * 2;
-        g.A2 = bytes_of(dB); g.lda2 = lddb * 2; g.B2 = bytes_of(Wu); g.ldb2 = ldu * 2;
+        g.A = bytes_of(dA); g.lda = ldda * es; g.B = bytes_of(Wg); g.ldb = ldg * es;
+        g.A2 = bytes_of(dB); g.lda2 = lddb * es; g.B2 = bytes_of(Wu); g.ldb2 = ldu * es;
         g.Y = dX; g.ldy = lddx; g.dt = dt;
-        KQ_TRY((tile_launch<EL_BF16, TP_GRAD_X>(g, 1, st, who)));
+        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_X>(g, 1, part, st, who)));
+        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_X>(g, 1, part, st, who)));
     }
     if (dWg || dWu) {
         TileArgs g{};
         g.M = o; g.N = i; g.K = n;
-        g.A = bytes_of(dWg ? dA : dB); g.lda = (dWg ? ldda : lddb) * 2;
-        g.A2 = bytes_of(dB); g.lda2 = lddb * 2;
-        g.B = bytes_of(X); g.ldb = ldx * 2;
+        g.A = bytes_of(dWg ? dA : dB); g.lda = (dWg ? ldda : lddb) * es;
+        g.A2 = bytes_of(dB); g.lda2 = lddb * es;
+        g.B = bytes_of(X); g.ldb = ldx * es;
         g.Y = dWg ? dWg : dWu; g.ldy = dWg ? lddg : lddu; g.Y2 = dWu; g.ldy2 = lddu; g.dt = dt;
-        KQ_TRY((tile_launch<EL_BF16, TP_GRAD_W>(g, dWg && dWu ? 2 : 1, st, who)));
+        const int pairs = dWg && dWu ? 2 : 1;
+        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_W>(g, pairs, part, st, who)));
+        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_W>(g, pairs, part, st, who)));
     }
     return KQ_OK;
 }

@@ -105,49 +105,64 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __res
 //   KIND 0  A: fragment f holds rows 64 group + 16 f + x16
 //   KIND 1  B: rows 64 group + b_row<4>(f, x16)
 //   KIND 2  gated: fragments 0, 1 are gate rows 32 group + b_row<2>(f, x16), 2 and 3 up rows
+struct MxBytes16 {       // scale rows are aligned to 4 bytes
+    uint32_t w[4];
+};
 struct MxLayout {
     const uint8_t *s, *s2;
     int64_t lds, lds2, rows, groups;
     uint32_t* out;
 };
 
+// A lane reads 16 bytes (four steps) of each of its four rows and stores four dwords.
 template <int KIND>
-__device__ __forceinline__ void mx_layout_group(const MxLayout& L, int64_t group, int64_t nblk, int64_t ksteps) {
+__device__ __forceinline__ void mx_layout_group(const MxLayout& L, int64_t group, int nblk, int ksteps) {
     const int lane = threadIdx.x & 63, x16 = lane & 15, g4 = lane >> 4;
     const uint8_t* row[4];
-    bool in[4];
+    uint32_t keep[4];
 #pragma unroll
     for (int f = 0; f < 4; f++) {
         const int64_t r = KIND == 0 ? 64 * group + 16 * f + x16
                         : KIND == 1 ? 64 * group + b_row<4>(f, x16) : 32 * group + b_row<2>(f & 1, x16);
-        in[f] = r < L.rows;
-        row[f] = KIND == 2 && f >= 2 ? L.s2 + (in[f] ? r : 0) * L.lds2 : L.s + (in[f] ? r : 0) * L.lds;
+        const bool in = r < L.rows;
+        keep[f] = in ? 0xFFu : 0u;
+        row[f] = KIND == 2 && f >= 2 ? L.s2 + (in ? r : 0) * L.lds2 : L.s + (in ? r : 0) * L.lds;
     }
-    for (int64_t k = threadIdx.x >> 6; k < ksteps; k += 4) {
-        const int64_t blk = 4 * k + g4;
-        uint32_t w = 0;
-        if (blk < nblk) {
+    for (int k = (threadIdx.x >> 6) * 4; k < ksteps; k += 16) {
+        uint32_t v[4][4];                        // [row][step]
 #pragma unroll
-            for (int f = 0; f < 4; f++) w |= (in[f] ? (uint32_t)row[f][blk] : 0u) << (8 * f);
+        for (int f = 0; f < 4; f++) {
+            if (16 + 4 * k <= nblk) {
+                const MxBytes16 t = *reinterpret_cast<const MxBytes16*>(row[f] + 4 * k);
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[f][e] = t.w[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[f][e] = 4 * (k + e) < nblk ? *reinterpret_cast<const uint32_t*>(row[f] + 4 * (k + e)) : 0u;
+            }
         }
-        L.out[(group * ksteps + k) * 64 + lane] = w;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int f = 0; f < 4; f++) w |= ((v[f][e] >> (8 * g4)) & keep[f]) << (8 * f);
+            if (4 * (k + e) + g4 >= nblk) w = 0;
+            if (k + e < ksteps) L.out[(group * ksteps + k + e) * 64 + lane] = w;
+        }
     }
 }
 
 // one work-group of 4 wavefronts a group of 64 rows, A's groups first
 template <bool GATED>
-__global__ __launch_bounds__(256) void mx_layout_kernel(MxLayout a, MxLayout b, int64_t nblk, int64_t ksteps) {
+__global__ __launch_bounds__(256) void mx_layout_kernel(MxLayout a, MxLayout b, int nblk, int ksteps) {
     const int64_t group = blockIdx.x;
     if (group < a.groups) mx_layout_group<0>(a, group, nblk, ksteps);
     else mx_layout_group<GATED ? 2 : 1>(b, group - a.groups, nblk, ksteps);
 }
 
 // 64-row groups of the laid-out scales: whole tiles, so that every wavefront of the last one reads inside
-static int64_t mx_groups_a(int64_t n) { return (n + TL_M - 1) / TL_M * (TL_M / 64); }
-static int64_t mx_groups_b(int64_t o, bool gated) {
-    const int64_t w = gated ? TL_N / 2 : TL_N;
-    return (o + w - 1) / w * 4;
-}
+static int64_t mx_groups_a(int64_t n) { return (n + TL_ROWS - 1) / TL_ROWS * (TL_ROWS / 64); }
+static int64_t mx_groups_b(int64_t o, bool gated) { return mx_groups_a(gated ? 2 * o : o); }
 static int64_t mx_ksteps(int64_t i) { return (i + 255) / 256 * 2; }
 
 struct MxOperand {
@@ -179,7 +194,7 @@ static kq_status mx_out_check(const char* who, const void* Y, kq_dtype dt, int64
 static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand& B, const MxOperand* U, int64_t n,
                             int64_t o, int64_t i, int act, void* Y, kq_dtype dt, int64_t ldy, void* ws, size_t ws_bytes,
                             hipStream_t st) {
-    if (n <= FEW_MAX) {
+    if (few_tokens<EL_MX>(n, o, i)) {
         FewArgs f{};
         f.n = n; f.o = o; f.K = i;
         f.A = reinterpret_cast<const char*>(A.c); f.lda = A.ldc; f.sA = A.s; f.ldsa = A.lds;
@@ -192,12 +207,14 @@ static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand
     Arena ar(ws, ws_bytes);
     uint32_t* la = ar.take<uint32_t>((size_t)(ga * ks * 64));
     uint32_t* lb = ar.take<uint32_t>((size_t)(gb * ks * 64));
+    const size_t np = (U ? tile_plan<EL_MX, TP_GATED>(n, o, i, 1) : tile_plan<EL_MX, TP_PLAIN>(n, o, i, 1)).part;
+    float* part = np ? ar.take<float>(np) : nullptr;
     if (!ws || !ar.ok()) return fail(KQ_EWORKSPACE, "%s: workspace too small", who);
     const MxLayout a{A.s, nullptr, A.lds, 0, n, ga, la};
     const MxLayout b{B.s, U ? U->s : nullptr, B.lds, U ? U->lds : 0, o, gb, lb};
     const dim3 grid((unsigned)(ga + gb));
-    if (U) hipLaunchKernelGGL((mx_layout_kernel<true>), grid, dim3(256), 0, st, a, b, (i + 31) / 32, ks);
-    else hipLaunchKernelGGL((mx_layout_kernel<false>), grid, dim3(256), 0, st, a, b, (i + 31) / 32, ks);
+    if (U) hipLaunchKernelGGL((mx_layout_kernel<true>), grid, dim3(256), 0, st, a, b, (int)((i + 31) / 32), (int)ks);
+    else hipLaunchKernelGGL((mx_layout_kernel<false>), grid, dim3(256), 0, st, a, b, (int)((i + 31) / 32), (int)ks);
     KQ_TRY(check_launch(who));
     TileArgs g{};
     g.M = n; g.N = o; g.K = i;
@@ -206,7 +223,7 @@ static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand
     if (U) { g.B2 = reinterpret_cast<const char*>(U->c); g.ldb2 = U->ldc; }
     g.sA = la; g.sB = lb; g.ksteps = ks;
     g.Y = Y; g.ldy = ldy; g.dt = dt; g.act = act;
-    return U ? tile_launch<EL_MX, TP_GATED>(g, 1, st, who) : tile_launch<EL_MX, TP_PLAIN>(g, 1, st, who);
+    return U ? tile_launch<EL_MX, TP_GATED>(g, 1, part, st, who) : tile_launch<EL_MX, TP_PLAIN>(g, 1, part, st, who);
 }
 
 }  // namespace kq
@@ -214,10 +231,12 @@ static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand
 using namespace kq;
 
 size_t mx_product_ws(int64_t o, int64_t i, int64_t n, bool gated) {
-    if (n <= FEW_MAX || o <= 0 || i <= 0) return 0;
+    if (n <= 0 || o <= 0 || i <= 0 || few_tokens<EL_MX>(n, o, i)) return 0;
     Sizer s;
     s.take<uint32_t>((size_t)(mx_groups_a(n) * mx_ksteps(i) * 64));
     s.take<uint32_t>((size_t)(mx_groups_b(o, gated) * mx_ksteps(i) * 64));
+    const size_t part = (gated ? tile_plan<EL_MX, TP_GATED>(n, o, i, 1) : tile_plan<EL_MX, TP_PLAIN>(n, o, i, 1)).part;
+    if (part) s.take<float>(part);
     return s.used;
 }
 

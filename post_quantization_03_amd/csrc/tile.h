@@ -11,6 +11,7 @@
 // loops below are written once for the three.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "kq_internal.h"
@@ -162,7 +163,7 @@ __device__ __forceinline__ tl_f4 mma_step(tl_i4 a, tl_i4 b, tl_f4 c, int sa, int
 //   TP_PLAIN   Y = A B^T                        A: M x K, B: N x K
 //   TP_GATED   Y = act(A B^T) * (A B2^T), optionally the two products themselves
 //   TP_GRAD_X  Y = A B + A2 B2                  A: M x K, B: K x N
-//   TP_GRAD_W  Y = A^T B, Y2 = A2^T B           A: K x M, B: K x N     (blockIdx.z picks the pair)
+//   TP_GRAD_W  Y = A^T B, Y2 = A2^T B           A: K x M, B: K x N
 enum { TP_PLAIN = 0, TP_GATED = 1, TP_GRAD_X = 2, TP_GRAD_W = 3 };
 
 struct TileArgs {
@@ -175,13 +176,25 @@ struct TileArgs {
     int64_t ldy, ldy2, ldy3;             // values
     int dt;                              // type of the outputs
     int act;
+    int pairs;                           // TP_GRAD_W: products (2, or 1 when one gradient is wanted)
+    int sper;                            // slabs of K a work-group takes (all of them when K is not split)
+    float* part;                         // K split: sums of split s of pair p at part + (s * pairs + p) * pstride
+    int64_t pstride, pld;                // (values; gated: gate columns, then up columns from pld / 2)
 };
 
-constexpr int TL_M = 256, TL_N = 256;    // output tile (TL_N rows of B; half gate and half up when gated)
-constexpr int TL_THREADS = 512;          // 8 wavefronts as 2 x 4, each 128 x 64
-constexpr int TL_FM = 8, TL_FN = 4;      // 16 x 16 fragments of a wavefront
-constexpr int TL_OPB = 256 * 128;        // bytes of one operand's slab in LDS
-constexpr size_t TL_SMEM = size_t(4) * TL_OPB;
+// Tile shapes: TM rows of A by TN rows of B (half gate, half up when gated), WM x WN wavefronts.
+template <int TM_, int TN_, int WM_, int WN_, int OCC>
+struct TileShape {
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, W = WM_ * WN_, THREADS = 64 * W, EU = OCC;
+    static constexpr int FM = TM / WM / 16, FN = TN / WN / 16;           // 16 x 16 fragments of a wavefront
+    static constexpr int OPA = TM * 128, BUF = (TM + TN) * 128;          // bytes of A's slab, of both
+    static constexpr int QA = TM / 8 / W, QB = TN / 8 / W;               // loads of 1 KiB a wavefront and slab
+    static constexpr size_t SMEM = 2 * BUF;
+};
+typedef TileShape<256, 256, 2, 4, 2> TileL;      // one work-group a compute unit
+typedef TileShape<128, 128, 2, 2, 2> TileM;      // two
+typedef TileShape<64, 64, 2, 2, 4> TileS;        // four
+constexpr int TL_ROWS = 256;                     // rows of the largest tile: padding of mx_layout's groups
 // Offsets inside a tile's 256 rows (or 64 K rows) are 32-bit, everything else 64-bit: rows of at most 4 MiB.
 constexpr int64_t TL_LD_MAX = 4 << 20, TL_ROWS_MAX = 1LL << 31;
 
@@ -199,22 +212,28 @@ __device__ __forceinline__ void tile_of(int lid, int ny, int nx, int64_t& tm, in
     tn = in / rows;
 }
 
-// Row of B (inside a wavefront's 64, or inside its 32 gate or 32 up rows) that index x of fragment j holds.
-// A lane of the result holds rows 4 g .. 4 g + 3 of every fragment, so with this order it holds 4 * FNH
-// consecutive output columns: 16-byte stores, and a row segment of whole cache lines a wavefront.
-template <int FNH>
-__device__ __forceinline__ int b_row(int j, int x) { return (x >> 2) * (4 * FNH) + 4 * j + (x & 3); }
+// Rows of B go to wavefronts in groups of four fragments: 64 rows, or 32 gate rows and the same 32 up rows
+// (GF = 4 or 2 fragments). Index x of fragment f of a group holds the group's row b_row<GF>(f, x). A lane of the
+// result holds rows 4 g .. 4 g + 3 of every fragment, so with this order neighbouring fragments are
+// neighbouring columns: 16-byte stores, and row segments of whole cache lines a group.
+template <int GF>
+__device__ __forceinline__ int b_row(int f, int x) { return (x >> 2) * (4 * GF) + 4 * f + (x & 3); }
 
 // LDS, operand contiguous along K: rows of 128 bytes, chunk c of row r at position c ^ key(r). The 16 rows
 // of a fragment then spread over the banks. For A fragments hold consecutive rows; for B the rows of b_row.
 __device__ __forceinline__ int key_a(int r) { return r & 7; }
-template <int FNH>
-__device__ __forceinline__ int key_b(int r) { return (r & 3) | (((r / (4 * FNH)) & 1) << 2); }
+template <int GF>
+__device__ __forceinline__ int key_b(int r) { return (r & 3) | (((r / (4 * GF)) & 1) << 2); }
 
-// LDS, bf16 operand contiguous along M or N ("transposed"): K rows of 512 bytes (256 values), 32-byte pair
-// p of K row k at position p ^ key_t(k). A transposing read takes 16 K rows of one pair at once: 16
-// different positions.
-__device__ __forceinline__ int key_t(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
+// LDS, operand contiguous along M or N ("transposed"): rows of K, each of the tile's T values. A fragment reads
+// 16 columns of 16 K rows at once, U = 32 (bf16) or 64 (fp32) bytes of each; unit u of K row k lies at
+// position u ^ key_t(k), so the rows' units spread over the banks (bf16: 16 rows k & 3, k >> 3 of a
+// transposing read; fp32: 4 rows k >> 2).
+template <int E, int T>
+__device__ __forceinline__ int key_t(int k) {
+    if constexpr (E == EL_BF16) return ((k & 3) | (((k >> 3) & 3) << 2)) & (T / 16 - 1);
+    else return (k >> 2) & 3;
+}
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
@@ -241,95 +260,119 @@ __device__ __forceinline__ void landed_barrier() {
     __syncthreads();
 }
 
-template <int E, int MODE>
-__global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
+template <int E, int MODE, typename C>
+__global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
     extern __shared__ __align__(16) char tl_sm[];
-    constexpr bool TA = MODE == TP_GRAD_W, TB = MODE == TP_GRAD_X || MODE == TP_GRAD_W;
-    static_assert(!TB || E == EL_BF16, "transposed operands are bf16");
-    constexpr int EPC = el_chunk<E>(), BK = 8 * EPC;
-    constexpr int FNH = MODE == TP_GATED ? TL_FN / 2 : TL_FN;
-    constexpr int TN_OUT = MODE == TP_GATED ? TL_N / 2 : TL_N;       // output columns of a tile
+    constexpr bool TA = MODE == TP_GRAD_W, TB = MODE == TP_GRAD_X || MODE == TP_GRAD_W, GATED = MODE == TP_GATED;
+    static_assert(!TB || E != EL_MX, "blocks of E2M1 lie along K");
+    constexpr bool HID = TB && E == EL_BF16;
+    constexpr int EPC = el_chunk<E>(), BK = 8 * EPC, ES = 16 / (E == EL_MX ? 16 : EPC);   // ES: bytes of a dense value
+    constexpr int FM = C::FM, FN = C::FN, QA = C::QA, QB = C::QB;
+    constexpr int GF = GATED ? 2 : 4, GW = GATED ? 32 : 64;              // a group's fragments and columns (of a half)
+    constexpr int FW = GATED ? FN / 2 : FN, SUB = GF / FW;               // fragments a half of a wavefront, wavefronts a group
+    constexpr int TN_OUT = GATED ? C::TN / 2 : C::TN;                    // output columns of a tile
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int x16 = lane & 15, g4 = lane >> 4;
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / C::WN, wn = wave % C::WN, grp = wn / SUB, sub = wn % SUB;
     int64_t tm, tn;
-    tile_of((int)blockIdx.x, (int)((g.M + TL_M - 1) / TL_M), (int)((g.N + TN_OUT - 1) / TN_OUT), tm, tn);
-    const int64_t m0 = tm * TL_M, n0 = tn * TN_OUT;
-    const int mlast = (int)(g.M - 1 - m0 < TL_M - 1 ? g.M - 1 - m0 : TL_M - 1);          // last row inside
+    tile_of((int)blockIdx.x, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), tm, tn);
+    const int64_t m0 = tm * C::TM, n0 = tn * TN_OUT;
+    const int mlast = (int)(g.M - 1 - m0 < C::TM - 1 ? g.M - 1 - m0 : C::TM - 1);          // last row inside
     const int nlast = (int)(g.N - 1 - n0 < TN_OUT - 1 ? g.N - 1 - n0 : TN_OUT - 1);
+    const int wpair = MODE == TP_GRAD_W ? (int)blockIdx.z % g.pairs : 0;
+    const int split = MODE == TP_GRAD_W ? (int)blockIdx.z / g.pairs : (int)blockIdx.z;
 
-    // ---- staging: 4 loads of 16 bytes a lane and operand; load q of a wavefront fills KiB q * 8 + wave
-    const char *pA = MODE == TP_GRAD_W && blockIdx.z ? g.A2 : g.A, *pB = g.B;
-    const int64_t ldA = MODE == TP_GRAD_W && blockIdx.z ? g.lda2 : g.lda;
-    pA += TA ? m0 * 2 : m0 * ldA;
-    pB += TB ? n0 * 2 : n0 * g.ldb;
-    const char* pB2 = MODE == TP_GATED ? g.B2 + n0 * g.ldb2 : nullptr;
+    // ---- staging: loads of 16 bytes a lane; load q of a wavefront fills KiB q * W + wave of its operand
     const int r8 = lane >> 3, pos = lane & 7;
-    // chunk of a K-contiguous operand that the lane loads (the same in all four loads: they are 64 rows apart)
-    const int cA = pos ^ r8, cB = pos ^ key_b<FNH>(wave * 8 + r8);
-    uint32_t offA[4], offB[4];
-    auto offsets = [&](int64_t lda, int64_t ldb) {
+    // chunk of a K-contiguous operand that the lane loads (the same in all loads: they are a multiple of 32 rows apart)
+    const int cA = pos ^ r8, cB = pos ^ key_b<GF>(wave * 8 + r8);
+    // K row of a transposed operand (in load 0), and the chunk of it that the lane loads
+    constexpr int LA = C::TM * ES / 16, LB = C::TN * ES / 16;            // lanes (chunks) a K row
+    constexpr int UC = E == EL_BF16 ? 2 : 4;                             // chunks a unit
+    auto tchunk = [&](int k, int p, int key, int last) {
+        const int c = ((p / UC) ^ key) * UC + p % UC;
+        return c * EPC <= last ? c : last / EPC;
+    };
+    const char *pA, *pB, *pB2 = nullptr;
+    int64_t stepA, stepB;
+    uint32_t offA[QA], offB[QB];
+    auto operands = [&](const char* A, int64_t lda, const char* B, int64_t ldb) {
+        pA = A + (TA ? m0 * ES : m0 * lda);
+        pB = B + (TB ? n0 * ES : n0 * ldb);
+        if (GATED) pB2 = g.B2 + n0 * g.ldb2;
+        stepA = TA ? BK * lda : 128;
+        stepB = TB ? BK * ldb : 128;
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const int r = (q * 8 + wave) * 8 + r8;                                 // row of a K-contiguous operand
-            const int k = (q * 8 + wave) * 2 + (lane >> 5), p = lane & 31;         // row and place of a transposed one
-            const int c = (((p >> 1) ^ key_t(k)) << 1) | (p & 1);
-            if constexpr (TA) offA[q] = (uint32_t)k * (uint32_t)lda + (c * 8 <= mlast ? c : mlast >> 3) * 16;
-            else offA[q] = (uint32_t)(r < mlast ? r : mlast) * (uint32_t)lda + cA * 16;
-            // gated: rows 0..127 of the slab are gate rows (q < 2), 128..255 up rows
-            const int rb = MODE == TP_GATED ? r & 127 : r;
-            if constexpr (TB) offB[q] = (uint32_t)k * (uint32_t)ldb + (c * 8 <= nlast ? c : nlast >> 3) * 16;
-            else offB[q] = (uint32_t)(rb < nlast ? rb : nlast) * (uint32_t)(MODE == TP_GATED && q >= 2 ? g.ldb2 : ldb) + cB * 16;
+        for (int q = 0; q < QA; q++) {
+            if constexpr (TA) {
+                const int k = (q * C::W + wave) * (64 / LA) + lane / LA;
+                offA[q] = (uint32_t)k * (uint32_t)lda + tchunk(k, lane % LA, key_t<E, C::TM>(k), mlast) * 16;
+            } else {
+                const int r = (q * C::W + wave) * 8 + r8;
+                offA[q] = (uint32_t)(r < mlast ? r : mlast) * (uint32_t)lda + cA * 16;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < QB; q++) {
+            if constexpr (TB) {
+                const int k = (q * C::W + wave) * (64 / LB) + lane / LB;
+                offB[q] = (uint32_t)k * (uint32_t)ldb + tchunk(k, lane % LB, key_t<E, C::TN>(k), nlast) * 16;
+            } else {
+                // gated: the first half of the slab's rows are gate rows, the second up rows
+                const int r = (q * C::W + wave) * 8 + r8, rb = GATED ? r & (C::TN / 2 - 1) : r;
+                offB[q] = (uint32_t)(rb < nlast ? rb : nlast) * (uint32_t)(GATED && q >= QB / 2 ? g.ldb2 : ldb) + cB * 16;
+            }
         }
     };
-    offsets(ldA, g.ldb);
     const int64_t nch = (g.K + EPC - 1) / EPC;           // chunks of K, the last one possibly partial
     const int part = E == EL_MX ? 0 : (int)(g.K % EPC);  // values in a partial last chunk (E2M1 blocks are whole)
-    const int slabs = (int)((g.K + BK - 1) / BK);
+    const int slabsK = (int)((g.K + BK - 1) / BK);
     const int whole = (int)(g.K / BK);                   // slabs that lie inside K
-    int64_t stepA = TA ? BK * ldA : 128, stepB = TB ? BK * g.ldb : 128;
+    const int s0 = split * g.sper, slabs = slabsK - s0 < g.sper ? slabsK - s0 : g.sper;    // this work-group's
     int ts = 0;                                          // slab to be staged next
 
     // Stages the next slab into buffer buf. K-contiguous operands: chunks past K become zero (E2M1: a valid chunk
     // is read again; its scales are zero on both sides, so its products vanish). Transposed ones: K rows past
     // K become zero. Rows and columns past M and N repeat the last one and are never stored.
     auto stage = [&](int buf) {
-        char* la = tl_sm + buf * 2 * TL_OPB + wave * 1024;
-        char* lb = la + TL_OPB;
+        char* la = tl_sm + buf * C::BUF + wave * 1024;
+        char* lb = la + C::OPA;
+        constexpr int Q = C::W * 1024;
         if (ts < whole) {
 #pragma unroll
-            for (int q = 0; q < 4; q++) dma16<TB>(pA, offA[q], la + q * 8192);
+            for (int q = 0; q < QA; q++) dma16<HID>(pA, offA[q], la + q * Q);
 #pragma unroll
-            for (int q = 0; q < 4; q++) dma16<TB>(MODE == TP_GATED && q >= 2 ? pB2 : pB, offB[q], lb + q * 8192);
+            for (int q = 0; q < QB; q++) dma16<HID>(GATED && q >= QB / 2 ? pB2 : pB, offB[q], lb + q * Q);
         } else {
             const tl_i4 zero = {0, 0, 0, 0};
             const int left = (int)(nch - (int64_t)ts * 8), krows = (int)(g.K - (int64_t)ts * BK);
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int k = (q * 8 + wave) * 2 + (lane >> 5);
-                const bool inA = TA ? k < krows : cA < left, inB = TB ? k < krows : cB < left;
-                if constexpr (E == EL_MX) {
-                    dma16<TB>(pA, offA[q] + (inA ? 0 : (left - 1 - cA) * 16), la + q * 8192);
-                    dma16<TB>(MODE == TP_GATED && q >= 2 ? pB2 : pB, offB[q] + (inB ? 0 : (left - 1 - cB) * 16), lb + q * 8192);
-                } else {
-                    if (inA) dma16<TB>(pA, offA[q], la + q * 8192);
-                    else *reinterpret_cast<tl_i4*>(la + q * 8192 + lane * 16) = zero;
-                    if (inB) dma16<TB>(MODE == TP_GATED && q >= 2 ? pB2 : pB, offB[q], lb + q * 8192);
-                    else *reinterpret_cast<tl_i4*>(lb + q * 8192 + lane * 16) = zero;
-                }
+            for (int q = 0; q < QA; q++) {
+                const bool in = TA ? (q * C::W + wave) * (64 / LA) + lane / LA < krows : cA < left;
+                if (E == EL_MX) dma16<HID>(pA, offA[q] + (in ? 0 : (left - 1 - cA) * 16), la + q * Q);
+                else if (in) dma16<HID>(pA, offA[q], la + q * Q);
+                else *reinterpret_cast<tl_i4*>(la + q * Q + lane * 16) = zero;
+            }
+#pragma unroll
+            for (int q = 0; q < QB; q++) {
+                const char* b = GATED && q >= QB / 2 ? pB2 : pB;
+                const bool in = TB ? (q * C::W + wave) * (64 / LB) + lane / LB < krows : cB < left;
+                if (E == EL_MX) dma16<HID>(b, offB[q] + (in ? 0 : (left - 1 - cB) * 16), lb + q * Q);
+                else if (in) dma16<HID>(b, offB[q], lb + q * Q);
+                else *reinterpret_cast<tl_i4*>(lb + q * Q + lane * 16) = zero;
             }
         }
         ts++;
         pA += stepA;
         pB += stepB;
-        if (MODE == TP_GATED) pB2 += 128;
+        if (GATED) pB2 += 128;
     };
     // values past K of a partial last chunk, once it has landed: each lane clears its own chunks
     auto clear_part = [&](int t, int buf) {
-        if (t != slabs - 1) return;
+        if (s0 + t != slabsK - 1) return;
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) alone
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        char* la = tl_sm + buf * 2 * TL_OPB + wave * 1024 + lane * 16;
+        char* la = tl_sm + buf * C::BUF + wave * 1024 + lane * 16;
         auto cut = [&](char* p) {
             tl_i4 v = *reinterpret_cast<tl_i4*>(p);
 #pragma unroll
@@ -341,75 +384,92 @@ __global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
         };
         const int last = (int)((nch - 1) & 7);           // the chunk's place in the slab
         if (!TA && cA == last)
-            for (int q = 0; q < 4; q++) cut(la + q * 8192);
+            for (int q = 0; q < QA; q++) cut(la + q * C::W * 1024);
         if (!TB && cB == last)
-            for (int q = 0; q < 4; q++) cut(la + TL_OPB + q * 8192);
+            for (int q = 0; q < QB; q++) cut(la + C::OPA + q * C::W * 1024);
     };
 
-    tl_f4 acc[TL_FM][TL_FN];
+    tl_f4 acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < TL_FM; i++)
+    for (int i = 0; i < FM; i++)
 #pragma unroll
-        for (int j = 0; j < TL_FN; j++) acc[i][j] = tl_f4{0, 0, 0, 0};
+        for (int j = 0; j < FN; j++) acc[i][j] = tl_f4{0, 0, 0, 0};
 
-    // scales of a slab's two steps (E2M1): a dword holds a lane's bytes of four fragments
-    uint32_t scA[2][2], scB[2];
+    // scales of a slab's two steps (E2M1): a dword holds a lane's bytes of four fragments (64 rows)
+    constexpr int SA = FM >= 4 ? FM / 4 : 1;
+    uint32_t scA[SA][2], scB[2];
     const uint32_t *qA = nullptr, *qB = nullptr;         // step 0 of the slab whose scales are loaded next
     if constexpr (E == EL_MX) {
-        qA = g.sA + (tm * 4 + wm * 2) * g.ksteps * 64;
-        qB = g.sB + (tn * 4 + wn) * g.ksteps * 64;
+        qA = g.sA + ((m0 + wm * FM * 16) / 64 * g.ksteps + 2 * s0) * 64;
+        qB = g.sB + ((n0 / GW + grp) * g.ksteps + 2 * s0) * 64;
     }
     auto load_scales = [&](int s) {
-        scA[0][s] = qA[s * 64 + lane];
-        scA[1][s] = qA[(g.ksteps + s) * 64 + lane];
+#pragma unroll
+        for (int a = 0; a < SA; a++) {
+            scA[a][s] = qA[(a * g.ksteps + s) * 64 + lane];
+            if (FM < 4) scA[a][s] >>= 8 * FM * (wm % (4 / (FM < 4 ? FM : 4)));
+        }
         scB[s] = qB[s * 64 + lane];
+        if (SUB > 1) scB[s] >>= 8 * FW * sub;
         if (s == 1) {
             qA += 128;
             qB += 128;
         }
     };
 
-    // fragment i of A (j of B) for step s of the slab at LDS offset `at`. Transposed: lane x16 of group g4 ends
-    // with the 8 K rows 8 g4 .. 8 g4 + 7 of column 16 i + x16, from two reads of 4 K rows each; the key
-    // of those rows depends on the lane alone, so i enters the address by one exclusive or.
-    const int kt = 8 * g4 + (x16 >> 2);
-    const int lfA = TA ? kt * 512 + ((wm * 8) ^ key_t(kt)) * 32 + (x16 & 3) * 8
-                       : (wm * 128 + x16) * 128 + ((g4 ^ key_a(x16)) << 4);
-    const int rB0 = MODE == TP_GATED ? wn * 32 + b_row<FNH>(0, x16) : wn * 64 + b_row<FNH>(0, x16);
-    const int lfB = TB ? kt * 512 + ((wn * 4) ^ key_t(kt)) * 32 + (x16 & 3) * 8 : rB0 * 128 + ((g4 ^ key_b<FNH>(rB0)) << 4);
-    auto tr_frag = [&](int off) -> tl_i4 {
-        const tl_s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)(tl_sm + off));
-        const tl_s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)(tl_sm + off + 2048));
+    // fragment i of A (j of B) for step s of the slab at LDS offset `at`. Transposed: lane x16 of group g4 ends with
+    // the K rows of its chunk of column 16 i + x16 (bf16: 8 rows from two transposing reads of 4; fp32: 4 rows);
+    // the key of those rows depends on the lane alone, so i enters the address by one exclusive or.
+    const int lfA = !TA ? (wm * FM * 16 + x16) * 128 + ((g4 ^ key_a(x16)) << 4)
+                  : E == EL_BF16 ? (8 * g4 + (x16 >> 2)) * (C::TM * 2) +
+                                   ((wm * FM) ^ key_t<E, C::TM>(8 * g4 + (x16 >> 2))) * 32 + (x16 & 3) * 8
+                                 : 4 * g4 * (C::TM * 4) + ((wm * FM) ^ g4) * 64 + x16 * 4;
+    const int rB0 = grp * GW + b_row<GF>(sub * FW, x16);
+    const int lfB = !TB ? rB0 * 128 + ((g4 ^ key_b<GF>(rB0)) << 4)
+                  : E == EL_BF16 ? (8 * g4 + (x16 >> 2)) * (C::TN * 2) +
+                                   ((wn * FN) ^ key_t<E, C::TN>(8 * g4 + (x16 >> 2))) * 32 + (x16 & 3) * 8
+                                 : 4 * g4 * (C::TN * 4) + ((wn * FN) ^ g4) * 64 + x16 * 4;
+    auto tr_frag = [&](int off, int f, int s, int T) -> tl_i4 {
         tl_i4 r;
-        reinterpret_cast<tl_s4*>(&r)[0] = lo;
-        reinterpret_cast<tl_s4*>(&r)[1] = hi;
+        if constexpr (E == EL_BF16) {
+            const char* p = tl_sm + (off ^ (f * 32)) + s * 32 * T * 2;
+            const tl_s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)p);
+            const tl_s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tl_s4*)(p + 8 * T));
+            reinterpret_cast<tl_s4*>(&r)[0] = lo;
+            reinterpret_cast<tl_s4*>(&r)[1] = hi;
+        } else {
+            const char* p = tl_sm + (off ^ (f * 64)) + s * 16 * T * 4;
+#pragma unroll
+            for (int e = 0; e < 4; e++) r[e] = *reinterpret_cast<const int*>(p + e * T * 4);
+        }
         return r;
     };
     auto fragA = [&](int at, int i, int s) -> tl_i4 {
-        if constexpr (TA) return tr_frag(((at + lfA) ^ (i * 32)) + s * 16384);
+        if constexpr (TA) return tr_frag(at + lfA, i, s, C::TM);
         else return *reinterpret_cast<const tl_i4*>(tl_sm + ((at + lfA) ^ (s * 64)) + i * 2048);
     };
     auto fragB = [&](int at, int j, int s) -> tl_i4 {
-        at += TL_OPB;
-        if constexpr (TB) return tr_frag(((at + lfB) ^ (j * 32)) + s * 16384);
-        else return *reinterpret_cast<const tl_i4*>(tl_sm + ((at + lfB) ^ (s * 64)) + (j >= FNH ? 128 * 128 : 0) + (j % FNH) * 512);
+        at += C::OPA;
+        if constexpr (TB) return tr_frag(at + lfB, j, s, C::TN);
+        else return *reinterpret_cast<const tl_i4*>(tl_sm + ((at + lfB) ^ (s * 64)) + (j / FW) * (C::TN / 2 * 128) + (j % FW) * 512);
     };
 
     // The loop is software-pipelined by half a slab: while one step's products run, the next step's fragments
     // come from LDS, and the barrier stands between the two steps of a slab. At the barrier every wavefront
     // has all of slab t in registers or accumulators, so its buffer takes slab t + 2, and slab t + 1 has had
     // a whole slab's products to arrive in. Registers: a fragment of A is overwritten in place by the next
-    // step's once its products are issued, except that the first step's last two are kept beside the second
+    // step's once its products are issued, except that the first step's last ones are kept beside the second
     // step's (fx), whose loads would otherwise be waited for at the barrier.
-    constexpr int KEEP = 2, INPL = TL_FM - KEEP;
-    tl_i4 fa[TL_FM], fx[KEEP], fb[2][TL_FN];
-    auto slab_at = [&](int t) { return (t & 1) * 2 * TL_OPB; };
+    constexpr int KEEP = FM / 4, INPL = FM - KEEP;
+    tl_i4 fa[FM], fx[KEEP ? KEEP : 1], fb[2][FN];
+    auto slab_at = [&](int t) { return (t & 1) * C::BUF; };
     auto products = [&](int i, int s, tl_i4 a) {
 #pragma unroll
-        for (int j = 0; j < TL_FN; j++) {
+        for (int j = 0; j < FN; j++) {
             // rows of the result are B's rows (output columns), columns are A's rows
             if constexpr (E == EL_MX)
-                acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], (int)scB[s], j, (int)scA[i >> 2][s], i & 3);
+                acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], (int)scB[s], GATED && FN == 2 ? 2 * j : j,
+                                        (int)scA[i / 4][s], i & 3);
             else
                 acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], 0, 0, 0, 0);
         }
@@ -419,35 +479,35 @@ __global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
     auto step = [&](int s, int at) {
         const int nx = s ^ 1;            // the step whose fragments are read (slab at `at`)
 #pragma unroll
-        for (int i = 0; i < TL_FM; i++) {
-            products(i, s, s == 1 && i >= INPL ? fx[i - INPL] : fa[i]);
+        for (int i = 0; i < FM; i++) {
+            products(i, s, s == 1 && i >= INPL ? fx[i >= INPL ? i - INPL : 0] : fa[i]);
             __builtin_amdgcn_sched_barrier(0);
             if (i < INPL) fa[i] = fragA(at, i, nx);
             if (i < KEEP) {
                 if (s == 0) fx[i] = fragA(at, INPL + i, nx);
                 else fa[INPL + i] = fragA(at, INPL + i, nx);
             }
-            if (i % 2 == 0 && i / 2 < TL_FN) fb[nx][i / 2] = fragB(at, i / 2, nx);
+#pragma unroll
+            for (int j = i * FN / FM; j < (i + 1) * FN / FM; j++) fb[nx][j] = fragB(at, j, nx);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    operands(MODE == TP_GRAD_W && wpair ? g.A2 : g.A, MODE == TP_GRAD_W && wpair ? g.lda2 : g.lda, g.B, g.ldb);
     for (int pair = 0; pair < (MODE == TP_GRAD_X ? 2 : 1); pair++) {
-        if (MODE == TP_GRAD_X && pair) {                 // A2 and B2 into the same sums
-            ts = 0;
-            pA = g.A2 + m0 * g.lda2;
-            pB = g.B2 + n0 * 2;
-            stepB = BK * g.ldb2;
-            offsets(g.lda2, g.ldb2);
-        }
+        if (MODE == TP_GRAD_X && pair) operands(g.A2, g.lda2, g.B2, g.ldb2);     // into the same sums
+        ts = s0;
+        pA += s0 * stepA;
+        pB += s0 * stepB;
+        if (GATED) pB2 += s0 * 128;
         stage(0);
         if (part && (!TA || !TB)) clear_part(0, 0);
         if constexpr (E == EL_MX) load_scales(0);
         landed_barrier();
         if (slabs > 1) stage(1);
 #pragma unroll
-        for (int j = 0; j < TL_FN; j++) fb[0][j] = fragB(0, j, 0);
+        for (int j = 0; j < FN; j++) fb[0][j] = fragB(0, j, 0);
 #pragma unroll
-        for (int i = 0; i < TL_FM; i++) fa[i] = fragA(0, i, 0);
+        for (int i = 0; i < FM; i++) fa[i] = fragA(0, i, 0);
         for (int t = 0; t < slabs; t++) {
             if constexpr (E == EL_MX) load_scales(1);
             step(0, slab_at(t));
@@ -461,56 +521,170 @@ __global__ __launch_bounds__(TL_THREADS, 2) void tile_kernel(TileArgs g) {
         }
     }
 
-    // ---- epilogue: lane holds output row x16 of fragment row i, columns as b_row (or 16 j + 4 g4 when transposed)
-    void* Y = MODE == TP_GRAD_W && blockIdx.z ? g.Y2 : g.Y;
-    const int64_t ldY = MODE == TP_GRAD_W && blockIdx.z ? g.ldy2 : g.ldy;
+    // ---- epilogue: lane holds output row x16 of fragment row i and runs of neighbouring columns
+    const bool w2 = MODE == TP_GRAD_W && wpair;
+    float* pt = g.part ? g.part + (int64_t)blockIdx.z * g.pstride : nullptr;
+    void* Y = pt ? pt : w2 ? g.Y2 : g.Y;
+    const int64_t ldY = pt ? g.pld : w2 ? g.ldy2 : g.ldy;
+    const int dt = pt ? KQ_F32 : g.dt;
+    const int64_t nrun = n0 + grp * GW + g4 * (4 * GF) + 4 * sub * FW;
 #pragma unroll
-    for (int i = 0; i < TL_FM; i++) {
-        const int64_t m = m0 + wm * 128 + 16 * i + x16;
+    for (int i = 0; i < FM; i++) {
+        const int64_t m = m0 + wm * FM * 16 + 16 * i + x16;
         if (m >= g.M) continue;
-        if constexpr (MODE == TP_GATED) {
-            const int64_t n = n0 + wn * 32 + g4 * (4 * FNH);
-            float h[4 * FNH], a[4 * FNH], b[4 * FNH];
+        if constexpr (TB) {
 #pragma unroll
-            for (int j = 0; j < FNH; j++)
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    a[4 * j + r] = acc[i][j][r];
-                    b[4 * j + r] = acc[i][j + FNH][r];
-                }
-            act_times(h, a, b, g.act);
-            store_run<4 * FNH>(Y, g.dt, m * ldY + n, h, g.N - n);
-            if (g.Y2) store_run<4 * FNH>(g.Y2, g.dt, m * g.ldy2 + n, a, g.N - n);
-            if (g.Y3) store_run<4 * FNH>(g.Y3, g.dt, m * g.ldy3 + n, b, g.N - n);
-        } else if constexpr (TB) {
-#pragma unroll
-            for (int j = 0; j < TL_FN; j++) {
-                const int64_t n = n0 + wn * 64 + 16 * j + 4 * g4;
+            for (int j = 0; j < FN; j++) {
+                const int64_t n = n0 + wn * FN * 16 + 16 * j + 4 * g4;
                 const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                store_run<4>(Y, g.dt, m * ldY + n, v, g.N - n);
+                store_run<4>(Y, dt, m * ldY + n, v, g.N - n);
             }
         } else {
-            const int64_t n = n0 + wn * 64 + g4 * (4 * FNH);
-            float v[4 * FNH];
+            float a[4 * FW];
 #pragma unroll
-            for (int j = 0; j < FNH; j++)
+            for (int j = 0; j < FW; j++)
 #pragma unroll
-                for (int r = 0; r < 4; r++) v[4 * j + r] = acc[i][j][r];
-            store_run<4 * FNH>(Y, g.dt, m * ldY + n, v, g.N - n);
+                for (int r = 0; r < 4; r++) a[4 * j + r] = acc[i][j][r];
+            if constexpr (!GATED) {
+                store_run<4 * FW>(Y, dt, m * ldY + nrun, a, g.N - nrun);
+            } else {
+                float h[4 * FW], b[4 * FW];
+#pragma unroll
+                for (int j = 0; j < FW; j++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++) b[4 * j + r] = acc[i][j + FW][r];
+                if (pt) {
+                    store_run<4 * FW>(pt, KQ_F32, m * g.pld + nrun, a, g.N - nrun);
+                    store_run<4 * FW>(pt, KQ_F32, m * g.pld + g.pld / 2 + nrun, b, g.N - nrun);
+                } else {
+                    act_times(h, a, b, g.act);
+                    store_run<4 * FW>(Y, dt, m * ldY + nrun, h, g.N - nrun);
+                    if (g.Y2) store_run<4 * FW>(g.Y2, dt, m * g.ldy2 + nrun, a, g.N - nrun);
+                    if (g.Y3) store_run<4 * FW>(g.Y3, dt, m * g.ldy3 + nrun, b, g.N - nrun);
+                }
+            }
         }
     }
 }
 
+// Sums of the splits, in split order, and the epilogue: 4 columns a thread.
+template <int MODE>
+__global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g, int splits) {
+    const int64_t per = (g.N + 3) / 4, total = g.M * per;
+    const int pair = blockIdx.z;
+    auto sum = [&](const float* p, float (&v)[4]) {
+        float4 s = *reinterpret_cast<const float4*>(p);
+        for (int k = 1; k < splits; k++) {
+            const float4 t = *reinterpret_cast<const float4*>(p + (int64_t)k * g.pairs * g.pstride);
+            s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+        }
+        v[0] = s.x; v[1] = s.y; v[2] = s.z; v[3] = s.w;
+    };
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+        const int64_t m = e / per, n = (e - m * per) * 4;
+        const float* p = g.part + pair * g.pstride + m * g.pld + n;
+        float a[4];
+        sum(p, a);
+        if constexpr (MODE == TP_GATED) {
+            float b[4], h[4];
+            sum(p + g.pld / 2, b);
+            act_times(h, a, b, g.act);
+            store_run<4>(g.Y, g.dt, m * g.ldy + n, h, g.N - n);
+            if (g.Y2) store_run<4>(g.Y2, g.dt, m * g.ldy2 + n, a, g.N - n);
+            if (g.Y3) store_run<4>(g.Y3, g.dt, m * g.ldy3 + n, b, g.N - n);
+        } else {
+            store_run<4>(pair ? g.Y2 : g.Y, g.dt, m * (pair ? g.ldy2 : g.ldy) + n, a, g.N - n);
+        }
+    }
+}
+
+// How a product is cut: tile shape (0 L, 1 M, 2 S) and splits of K, by the estimated time of each choice.
+// A slab of a tile takes `lat` us by itself on a compute unit and `w` us of a busy one's matrix cores, a tile
+// `fix` more for its first loads and its epilogue; split sums are written and read once at 6.4 TB/s by a
+// second launch (3 us). The constants are fitted to measurements of 8 products at 15 sizes each, all
+// shapes and 1 to 16 splits (MI355X); the choice is within 1 % of the fastest on average and 8 % at worst.
+// fp32 products are bound by the matrix cores in every shape and always take the small one, which leaves
+// the fewest of them idle. Some times, us (bf16 gated block, n x o x i): 65 x 11008 x 4096 L 87, M 46, S 39; 2048 x 11008 x 4096
+// L 320, M 399, S 638; 512 x 4096 x 11008 M 122, M in two splits 93, L in four 96.
+struct TilePlan {
+    int shape, splits, sper;
+    size_t part;         // floats of split sums
+};
+
 template <int E, int MODE>
-kq_status tile_launch(const TileArgs& g, int pairs, hipStream_t st, const char* who) {
-    constexpr int TN_OUT = MODE == TP_GATED ? TL_N / 2 : TL_N;
-    const int64_t tiles = ((g.M + TL_M - 1) / TL_M) * ((g.N + TN_OUT - 1) / TN_OUT);
-    if (tiles > (1LL << 27)) return fail(KQ_ESHAPE, "%s: too many tiles", who);
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_kernel<E, MODE>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)TL_SMEM);
-    if (e != hipSuccess) return fail(KQ_EHIP, "%s: %s", who, hipGetErrorString(e));
-    hipLaunchKernelGGL((tile_kernel<E, MODE>), dim3((unsigned)tiles, 1, (unsigned)pairs), dim3(TL_THREADS), TL_SMEM, st, g);
+TilePlan tile_plan(int64_t M, int64_t N, int64_t K, int pairs) {
+    constexpr int BK = 8 * el_chunk<E>();
+    constexpr int size[3] = {256, 128, 64}, occ[3] = {1, 2, 4}, cuts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
+    constexpr double lat[3] = {1.4, 0.9, 0.75}, fix[3] = {10.0, 4.0, 1.7};
+    constexpr double w[3] = {1.55, 0.5, E == EL_F32 ? 0.2 : 0.38};
+    const int64_t slabs = (K + BK - 1) / BK, cols = (N + 3) / 4 * 4 * (MODE == TP_GATED ? 2 : 1);
+    TilePlan best{};
+    double least = 0.0;
+    for (int h = E == EL_F32 ? 2 : 0; h < 3; h++) {
+        const int64_t tn = MODE == TP_GATED ? size[h] / 2 : size[h];
+        const int64_t tiles = ((M + size[h] - 1) / size[h]) * ((N + tn - 1) / tn) * pairs;
+        for (int c = 0; c < 8; c++) {
+            const int64_t sper = (slabs + cuts[c] - 1) / cuts[c], splits = (slabs + sper - 1) / sper;
+            if (splits != cuts[c] && c > 0) continue;
+            const int64_t wgs = tiles * splits, percu = (wgs + 255) / 256, rounds = (percu + occ[h] - 1) / occ[h];
+            const double by_lat = (double)rounds * lat[h], by_w = (double)percu * w[h];
+            double t = (double)(sper * (MODE == TP_GRAD_X ? 2 : 1)) * (by_lat > by_w ? by_lat : by_w) + (double)rounds * fix[h];
+            const size_t part = splits > 1 ? (size_t)(splits * pairs * M * cols) : 0;
+            if (part) t += 3.0 + 8.0 * (double)part / 6.4e6;
+            if (best.splits == 0 || t < least) {
+                least = t;
+                best = TilePlan{h, (int)splits, (int)sper, part};
+            }
+        }
+    }
+    return best;
+}
+
+template <int E, int MODE, typename C>
+kq_status tile_launch_shape(const TileArgs& g, int splits, hipStream_t st, const char* who) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
+    const int64_t tiles = ((g.M + C::TM - 1) / C::TM) * ((g.N + TN_OUT - 1) / TN_OUT);
+    if (tiles > (1LL << 27)) return fail(KQ_ESHAPE, "%s: too many tiles", who);     // tile_of's products stay in 31 bits
+    // the allowance for dynamic LDS belongs to a device's copy of the kernel: asked for once a device
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return fail(KQ_EHIP, "%s: no current device", who);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev > 63 || !(allowed.load(std::memory_order_relaxed) & bit)) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_kernel<E, MODE, C>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        if (e != hipSuccess) return fail(KQ_EHIP, "%s: %s", who, hipGetErrorString(e));
+        if (dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
+    hipLaunchKernelGGL((tile_kernel<E, MODE, C>), dim3((unsigned)tiles, 1, (unsigned)(splits * g.pairs)), dim3(C::THREADS),
+                       C::SMEM, st, g);
     return check_launch(who);
+}
+
+// part: workspace of tile_plan(...).part floats
+template <int E, int MODE>
+kq_status tile_launch(TileArgs g, int pairs, float* part, hipStream_t st, const char* who) {
+    const TilePlan p = tile_plan<E, MODE>(g.M, g.N, g.K, pairs);
+    g.pairs = pairs;
+    g.sper = p.sper;
+    if (p.splits > 1) {
+        if (!part) return fail(KQ_EWORKSPACE, "%s: workspace too small", who);
+        g.part = part;
+        g.pld = (g.N + 3) / 4 * 4 * (MODE == TP_GATED ? 2 : 1);
+        g.pstride = g.M * g.pld;
+    }
+    if constexpr (E != EL_F32) {
+        if (p.shape == 0) KQ_TRY((tile_launch_shape<E, MODE, TileL>(g, p.splits, st, who)));
+        if (p.shape == 1) KQ_TRY((tile_launch_shape<E, MODE, TileM>(g, p.splits, st, who)));
+    }
+    if (p.shape == 2) KQ_TRY((tile_launch_shape<E, MODE, TileS>(g, p.splits, st, who)));
+    if (p.splits > 1) {
+        const int64_t total = g.M * ((g.N + 3) / 4), wgs = (total + 255) / 256;
+        hipLaunchKernelGGL((tile_reduce_kernel<MODE>), dim3((unsigned)(wgs < 8192 ? wgs : 8192), 1, (unsigned)pairs), dim3(256), 0,
+                           st, g, p.splits);
+        KQ_TRY(check_launch(who));
+    }
+    return KQ_OK;
 }
 
 // ------------------------------------------------------------------------------------- few tokens
@@ -529,7 +703,19 @@ struct FewArgs {
     int dt, act;
 };
 
-constexpr int FEW_WAVES = 8, FEW_THREADS = 64 * FEW_WAVES, FEW_MAX = 64;
+constexpr int FEW_WAVES = 8, FEW_THREADS = 64 * FEW_WAVES;
+
+// Whether n tokens run here rather than as tiles. Measured on MI355X, us here / as tiles, o x i weights:
+//   E2M1  11008 x 4096: 15.3 / 17.6 at 32 tokens, 21.6 / 17.8 at 33; 4096 x 11008: 17.3 / 22.9 at 64 (every
+//         work-group of 16 rows reads the tokens again, so the bound falls with o)
+//   bf16  gated 11008 x 4096: 34.1 / 34.7 at 8, 36.2 / 34.4 at 16; 1376 x 1000: 6.7 / 9.2 at 48
+//   fp32  gated 11008 x 4096: 104 / 135 at 32, 173 / 134 at 33; 1376 x 1000: 10.0 / 15.4 at 32, 16.6 / 15.6 at 33
+template <int E>
+bool few_tokens(int64_t n, int64_t o, int64_t i) {
+    if (E == EL_MX) return n <= 32 || (n <= 64 && n * o <= 64 * 4096);
+    if (E == EL_F32) return n <= 32;
+    return n <= 8 || (n <= 48 && o * i <= (1 << 22));
+}
 
 template <int E>
 struct FewFrag {
@@ -562,11 +748,17 @@ __device__ __forceinline__ void few_load(FewFrag<E>& f, const char* row, const u
         }
     }
     if constexpr (E == EL_MX) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(srow + s * 8);
+        if (whole) {
+            f.s[0] = q[0] >> (8 * g4);
+            f.s[1] = q[1] >> (8 * g4);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int64_t b = s * 8 + 4 * h;     // scale rows are read four bytes at a time
-            const uint32_t w = b < nch ? *reinterpret_cast<const uint32_t*>(srow + b) : 0u;
-            f.s[h] = b + g4 < nch ? w >> (8 * g4) : 0u;
+            for (int h = 0; h < 2; h++) {
+                const int64_t b = s * 8 + 4 * h;     // scale rows are read four bytes at a time
+                const uint32_t w = b < nch ? q[h] : 0u;
+                f.s[h] = b + g4 < nch ? w >> (8 * g4) : 0u;
+            }
         }
     }
 }
@@ -600,23 +792,33 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
     for (int m = 0; m < MATS; m++)
 #pragma unroll
         for (int b = 0; b < NB; b++) acc[m][b] = tl_f4{0, 0, 0, 0};
-    auto slab = [&](int64_t s, bool whole) {
-        FewFrag<E> w[MATS], a[NB];
-        few_load<E>(w[0], rB, qB, s, g4, whole, nch, part);
-        if constexpr (GATED) few_load<E>(w[1], rB2, qB2, s, g4, whole, nch, part);
+    // U slabs at a time: all their loads are in flight before the first product
+    auto batch = [&](int64_t s, auto UC, bool whole) {
+        constexpr int U = UC.value;
+        FewFrag<E> w[U][MATS], a[U][NB];
 #pragma unroll
-        for (int b = 0; b < NB; b++) few_load<E>(a[b], rA[b], qA[b], s, g4, whole, nch, part);
+        for (int u = 0; u < U; u++) {
+            const int64_t su = s + u * FEW_WAVES;
+            few_load<E>(w[u][0], rB, qB, su, g4, whole, nch, part);
+            if constexpr (GATED) few_load<E>(w[u][1], rB2, qB2, su, g4, whole, nch, part);
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+            for (int b = 0; b < NB; b++) few_load<E>(a[u][b], rA[b], qA[b], su, g4, whole, nch, part);
+        }
 #pragma unroll
-            for (int m = 0; m < MATS; m++)
+        for (int u = 0; u < U; u++)
 #pragma unroll
-                for (int b = 0; b < NB; b++)
-                    acc[m][b] = mma_step<E>(w[m].c[h], a[b].c[h], acc[m][b], (int)w[m].s[h], 0, (int)a[b].s[h], 0);
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int m = 0; m < MATS; m++)
+#pragma unroll
+                    for (int b = 0; b < NB; b++)
+                        acc[m][b] = mma_step<E>(w[u][m].c[h], a[u][b].c[h], acc[m][b], (int)w[u][m].s[h], 0, (int)a[u][b].s[h], 0);
     };
-#pragma unroll 4
-    for (int64_t s = wave; s < full; s += FEW_WAVES) slab(s, true);
-    if (full < slabs && wave == (int)(full % FEW_WAVES)) slab(full, false);
+    constexpr int U = E == EL_MX && NB < 4 ? 2 : 1;
+    int64_t s = wave;
+    for (; s + (U - 1) * FEW_WAVES < full; s += U * FEW_WAVES) batch(s, std::integral_constant<int, U>{}, true);
+    if (U > 1 && s < full) batch(s, std::integral_constant<int, 1>{}, true);
+    if (full < slabs && wave == (int)(full % FEW_WAVES)) batch(full, std::integral_constant<int, 1>{}, false);
 
 #pragma unroll
     for (int m = 0; m < MATS; m++)

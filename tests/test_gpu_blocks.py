@@ -388,6 +388,67 @@ def test_gated_large_arguments():
         check(get(dA), 2 * want_d, 1e-5, f"act' {kind}")
 
 
+# ------------------------------------------------------------------------------------ large tiles
+# one size for each tile shape and split of K that a type and product can take
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,o,i", [(1500, 2999, 33), (130, 4001, 7990), (3000, 2999, 2001), (65, 130, 2000), (300, 2900, 5000)])
+def test_mx_products_in_every_tile_shape(n, o, i, dt):
+    torch, dev = torch_dev()
+    say(f"mx tiles n={n} o={o} i={i} {dt}")
+    torch.manual_seed(n)
+
+    def operand(rows, std):
+        x = mat(rows, i, "f32")
+        x.copy_(torch.randn(rows, i, device=dev) * std)
+        c, s = K.mx_empty(rows, i, dev)
+        K.kq_mx_quantize(x, c, s)
+        v = mat(rows, i, "f32")
+        K.kq_mx_dequantize(c, s, v)
+        return (c, s), v.double()
+
+    (a, av), (b, bv), (u, uv) = operand(n, 1.0), operand(o, 2 / i ** 0.5), operand(o, 1 / i ** 0.5)
+    y = mat(n, o, dt)
+    K.kq_mx_gemm(*a, *b, i, y, ws_of("mx_gemm", o, i, n))
+    want, sa = av @ bv.T, av.abs() @ bv.abs().T
+    bound = i * E23 * sa + HALF[dt] * (want.abs() + i * E23 * sa)
+    assert bool(((y.double() - want).abs() <= bound).all()), "Y"
+    h = mat(n, o, dt)
+    K.kq_mx_gated(*a, *b, *u, i, "silu", h, ws_of("mx_gated", o, i, n))
+    B, sb = av @ uv.T, av.abs() @ uv.abs().T
+    A, da, db = host(want), host(i * E23 * sa), host(i * E23 * sb)
+    check(get(h), ob.act(A, "silu")[0] * host(B), gated_tol(A, host(B), da, db, "silu", dt), "H")
+
+
+@pytest.mark.parametrize("n,o,i,dt", [(1500, 1501, 33, "bf16"), (66, 1500, 4000, "bf16"), (1500, 1500, 4001, "bf16"),
+                                      (2000, 4000, 300, "bf16"), (3000, 300, 2999, "bf16"), (66, 2000, 2999, "bf16"),
+                                      (1500, 2000, 3001, "bf16"), (300, 2999, 3000, "bf16"), (700, 900, 1100, "f32")])
+def test_gated_block_in_every_tile_shape(n, o, i, dt):
+    torch, dev = torch_dev()
+    say(f"gated tiles n={n} o={o} i={i} {dt}")
+    torch.manual_seed(o)
+
+    def operand(rows, cols, std):
+        t = mat(rows, cols, dt, pad=1)
+        t.copy_(torch.randn(rows, cols, device=dev) * std)
+        return t, t.double()
+
+    (X, x), (Wg, g), (Wu, u) = operand(n, i, 1.0), operand(o, i, 2 / i ** 0.5), operand(o, i, 1 / i ** 0.5)
+    dH, dh = operand(n, o, 1.0)
+    H, A, B = mat(n, o, dt), mat(n, o, dt), mat(n, o, dt)
+    K.kq_gated_forward(X, Wg, Wu, "silu", H, A, B, ws_of("gated_forward", o, i, n, dt))
+    a, b = x @ g.T, x @ u.T
+    da, db = i * E23 * (x.abs() @ g.abs().T), i * E23 * (x.abs() @ u.abs().T)
+    assert bool(((A.double() - a).abs() <= da + HALF[dt] * (a.abs() + da)).all()), "A"
+    assert bool(((B.double() - b).abs() <= db + HALF[dt] * (b.abs() + db)).all()), "B"
+    ha, hb = host(a), host(b)
+    check(get(H), ob.act(ha, "silu")[0] * hb, gated_tol(ha, hb, host(da), host(db), "silu", dt), "H")
+    outs = [mat(n, o, dt), mat(n, o, dt), mat(n, i, dt), mat(o, i, dt), mat(o, i, dt)]
+    K.kq_gated_backward(dH, A, B, X, Wg, Wu, "silu", *outs, ws_of("gated_backward", o, i, n, dt))
+    want, tols = grad_tols(host(dh), get(A), get(B), *(host(t) for t in (x, g, u)), "silu", dt)
+    for name, t, w, tol in zip(("dA", "dB", "dX", "dWg", "dWu"), outs, want, tols):
+        check(get(t), w, tol, name)
+
+
 # --------------------------------------------------------------------- streams, graphs, two calls
 @pytest.mark.parametrize("n", [3, 300])
 def test_products_replayed_from_a_graph(n):

@@ -300,18 +300,23 @@ def kq_allocate_bits(scores, sizes, budget: float = 3.0, bmin: int = 2, bmax: in
 # view (rows are read in whole 16-byte pieces). A call on few tokens runs for a few microseconds on the
 # GPU, so the checks read each tensor's attributes once and no device guard is entered on the current device.
 _FLOATS: dict = {}      # torch dtype -> (kq_dtype, elements in 16 bytes)
+_TORCH: list = []       # torch.uint8, the raw current stream of a device, the current device
 
 
-def _floats() -> dict:
-    if not _FLOATS:
+def _torch() -> list:
+    if not _TORCH:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _TORCH.extend((torch.uint8, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), torch.cuda.current_device))
         _FLOATS.update({torch.float32: (KQ_F32, 4), torch.bfloat16: (KQ_BF16, 8)})
-    return _FLOATS
+    return _TORCH
 
 
 def _float(name: str, what: str, t):
     """(kq_dtype, elements in 16 bytes) of a tensor's type."""
-    f = _floats().get(t.dtype)
+    if not _FLOATS:
+        _torch()
+    f = _FLOATS.get(t.dtype)
     if f is None:
         raise TypeError(f"{name}: {what} has type {t.dtype}")
     return f
@@ -324,7 +329,9 @@ def _matrix(name: str, what: str, t, rows: int, cols: int, dtype, per: int, whol
         raise TypeError(f"{name}: {what} has type {t.dtype}, not {dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {(rows, cols)}")
-    _same_device(name, what, t, dev)
+    d = t.get_device()
+    if d < 0 or not dev or d != dev[0]:
+        _same_device(name, what, d, dev)
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name}: {what} is not row-major")
@@ -337,8 +344,7 @@ def _matrix(name: str, what: str, t, rows: int, cols: int, dtype, per: int, whol
     return t.data_ptr(), ld
 
 
-def _same_device(name: str, what: str, t, dev: list) -> None:
-    d = t.get_device()
+def _same_device(name: str, what: str, d: int, dev: list) -> None:
     if d < 0:
         raise ValueError(f"{name}: {what} is not on a GPU")
     if not dev:
@@ -349,48 +355,53 @@ def _same_device(name: str, what: str, t, dev: list) -> None:
 
 def _mx(name: str, what: str, codes, scales, cols: int, dev: list) -> tuple:
     """Checks a microscaled operand of `cols` columns; returns its four C arguments."""
-    import torch
-    nblk = (cols + 31) // 32
-    for t, w in ((codes, "codes"), (scales, "scales")):
-        if t.dtype != torch.uint8:
-            raise TypeError(f"{name}: {what} {w} have type {t.dtype}, not uint8")
-    if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0]:
+    u8 = _torch()[0]
+    if codes.dtype != u8 or scales.dtype != u8:
+        raise TypeError(f"{name}: {what} codes and scales have types {codes.dtype} and {scales.dtype}, not uint8")
+    cs, ss = codes.shape, scales.shape
+    if len(cs) != 2 or len(ss) != 2 or cs[0] != ss[0]:
         raise ValueError(f"{name}: {what} needs codes and scales with one row for each of the matrix")
-    _same_device(name, what + " codes", codes, dev)
-    _same_device(name, what + " scales", scales, dev)
-    (rows, wc), ws_ = codes.shape, scales.shape[1]
-    if wc != 16 * nblk or not nblk <= ws_ <= (nblk + 3) // 4 * 4:
+    d, e = codes.get_device(), scales.get_device()
+    if d < 0 or d != e or not dev or d != dev[0]:
+        _same_device(name, what + " codes", d, dev)
+        _same_device(name, what + " scales", e, dev)
+    nblk = (cols + 31) // 32
+    rows, wide, have = cs[0], (nblk + 3) // 4 * 4, ss[1]
+    if cs[1] != 16 * nblk or not nblk <= have <= wide:
         raise ValueError(f"{name}: {what} of {cols} columns needs 16 * {nblk} bytes of codes and {nblk} scales a row "
-                         f"(mx_empty), not {wc} and {ws_}")
+                         f"(mx_empty), not {cs[1]} and {have}")
     (ldc, c1), (lds, s1) = codes.stride(), scales.stride()
-    if c1 != 1 or (s1 != 1 and ws_ > 1):
+    if c1 != 1 or (s1 != 1 and have > 1):
         raise ValueError(f"{name}: {what} is not row-major")
     if rows <= 1:
-        ldc, lds = 16 * nblk, (nblk + 3) // 4 * 4
-    if ws_ % 4 and rows and scales.storage_offset() + (rows - 1) * lds + (nblk + 3) // 4 * 4 > scales.untyped_storage().nbytes():
+        ldc, lds = 16 * nblk, wide
+    if have != wide and rows and scales.storage_offset() + (rows - 1) * lds + wide > scales.untyped_storage().nbytes():
         raise ValueError(f"{name}: the last scale row of {what} ends inside its 4 bytes, past the storage")
     return codes.data_ptr(), ldc, scales.data_ptr(), lds
 
 
 def _launch(name: str, fn, dev: list, ws, stream, *args) -> None:
     """fn(*args [, workspace, its bytes], stream) on the operands' device."""
-    import torch
+    _, raw_stream, current_device = _torch()
+    d = dev[0]
     if ws is not False:
         if ws is None:
             args += (None, 0)
         else:
-            _same_device(name, "the workspace", ws, dev)
+            _same_device(name, "the workspace", ws.get_device(), dev)
             args += (ws.data_ptr(), ws.numel() * ws.element_size())
-    d = dev[0]
     if stream is None:
-        stream = torch.cuda.current_stream(d)
+        s = raw_stream(d)
     elif stream.device.index != d:
         raise ValueError(f"{name}: the stream is on {stream.device}, the operands on cuda:{d}")
-    if torch.cuda.current_device() == d:
-        status = fn(*args, stream.cuda_stream)
     else:
+        s = stream.cuda_stream
+    if current_device() == d:
+        status = fn(*args, s)
+    else:
+        import torch
         with torch.cuda.device(d):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, s)
     if status:
         raise KQError(name, status, last_error())
 

@@ -120,7 +120,7 @@ static kq_status gated_forward(const char* who, const void* X, int64_t ldx, cons
     g.Y = H; g.ldy = ldh; g.Y2 = A; g.ldy2 = lda; g.Y3 = B; g.ldy3 = ldb;
     g.dt = dt; g.act = act;
     Arena ar(ws, ws_bytes);
-    const size_t np = tile_plan<E, TP_GATED>(n, o, i, 1).part;
+    const size_t np = tile_plan<E, TP_GATED>(n, o, i).part;
     return tile_launch<E, TP_GATED>(g, 1, np ? ar.take<float>(np) : nullptr, st, who);
 }
 
@@ -130,19 +130,15 @@ using namespace kq;
 
 size_t gated_forward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
     if (n <= 0 || o <= 0 || i <= 0 || (dt == KQ_BF16 ? few_tokens<EL_BF16>(n, o, i) : few_tokens<EL_F32>(n, o, i))) return 0;
-    return sizeof(float) * (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GATED>(n, o, i, 1) : tile_plan<EL_F32, TP_GATED>(n, o, i, 1)).part;
+    return sizeof(float) * (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GATED>(n, o, i) : tile_plan<EL_F32, TP_GATED>(n, o, i)).part;
 }
 
 // The products run one after another on the caller's stream and share the split sums' memory.
 size_t gated_backward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
     if (n <= 0 || o <= 0 || i <= 0) return 0;
-    size_t most = 0;
-    for (int pairs = 1; pairs <= 2; pairs++) {
-        const size_t w = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_W>(o, i, n, pairs) : tile_plan<EL_F32, TP_GRAD_W>(o, i, n, pairs)).part;
-        most = w > most ? w : most;
-    }
-    const size_t x = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_X>(n, i, o, 1) : tile_plan<EL_F32, TP_GRAD_X>(n, i, o, 1)).part;
-    return sizeof(float) * (x > most ? x : most);
+    const size_t w = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_W>(o, i, n) : tile_plan<EL_F32, TP_GRAD_W>(o, i, n)).part;
+    const size_t x = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_X>(n, i, o) : tile_plan<EL_F32, TP_GRAD_X>(n, i, o)).part;
+    return sizeof(float) * (x > w ? x : w);
 }
 
 extern "C" kq_status kq_gated_forward(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu,

@@ -97,8 +97,8 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __res
     }
 }
 
-// -------------------------------------------------------------------------------- scales for tiles
-// The tile product's lane (x16, g4) needs, for step k of 128 columns and each of its fragments, the scale byte
+// -------------------------------------------------------------------------- scales for large tiles
+// A lane of the two larger tile shapes (x16, g4) needs, for step k of 128 columns and each of its fragments, the scale byte
 // of one row's block 4 k + g4. This pass gathers them so that one coalesced dword a lane holds four
 // fragments' bytes: out[(group * ksteps + k) * 64 + lane], group = 64 rows. Blocks past the last column get
 // byte 0 (2^-127), on both operands: the product of two such blocks is below the smallest fp32, zero.
@@ -165,6 +165,10 @@ static int64_t mx_groups_a(int64_t n) { return (n + TL_ROWS - 1) / TL_ROWS * (TL
 static int64_t mx_groups_b(int64_t o, bool gated) { return mx_groups_a(gated ? 2 * o : o); }
 static int64_t mx_ksteps(int64_t i) { return (i + 255) / 256 * 2; }
 
+static TilePlan mx_plan(int64_t n, int64_t o, int64_t i, bool gated) {
+    return gated ? tile_plan<EL_MX, TP_GATED>(n, o, i) : tile_plan<EL_MX, TP_PLAIN>(n, o, i);
+}
+
 struct MxOperand {
     const uint8_t* c;
     int64_t ldc;
@@ -178,7 +182,7 @@ static kq_status mx_check(const char* who, const char* what, const MxOperand& m,
     if (m.ldc < 16 * nblk || m.lds < nblk) return fail(KQ_ESHAPE, "%s: leading dimension of %s too small", who, what);
     if (!aligned16(m.c) || m.ldc % 16 || reinterpret_cast<uintptr_t>(m.s) % 4 || m.lds % 4)
         return fail(KQ_EINVAL, "%s: %s codes must be aligned to 16 bytes and scales to 4, rows likewise", who, what);
-    if (m.ldc > TL_LD_MAX || rows > TL_ROWS_MAX) return fail(KQ_ESHAPE, "%s: %s too large", who, what);
+    if (m.ldc > TL_LD_MAX || m.lds > TL_LD_MAX || rows > TL_ROWS_MAX) return fail(KQ_ESHAPE, "%s: %s too large", who, what);
     return KQ_OK;
 }
 
@@ -203,26 +207,36 @@ static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand
         f.Y = Y; f.ldy = ldy; f.dt = dt; f.act = act;
         return U ? few_launch<EL_MX, true>(f, st, who) : few_launch<EL_MX, false>(f, st, who);
     }
-    const int64_t ks = mx_ksteps(i), ga = mx_groups_a(n), gb = mx_groups_b(o, U != nullptr);
+    const TilePlan plan = mx_plan(n, o, i, U != nullptr);
     Arena ar(ws, ws_bytes);
-    uint32_t* la = ar.take<uint32_t>((size_t)(ga * ks * 64));
-    uint32_t* lb = ar.take<uint32_t>((size_t)(gb * ks * 64));
-    const size_t np = (U ? tile_plan<EL_MX, TP_GATED>(n, o, i, 1) : tile_plan<EL_MX, TP_PLAIN>(n, o, i, 1)).part;
-    float* part = np ? ar.take<float>(np) : nullptr;
-    if (!ws || !ar.ok()) return fail(KQ_EWORKSPACE, "%s: workspace too small", who);
-    const MxLayout a{A.s, nullptr, A.lds, 0, n, ga, la};
-    const MxLayout b{B.s, U ? U->s : nullptr, B.lds, U ? U->lds : 0, o, gb, lb};
-    const dim3 grid((unsigned)(ga + gb));
-    if (U) hipLaunchKernelGGL((mx_layout_kernel<true>), grid, dim3(256), 0, st, a, b, (int)((i + 31) / 32), (int)ks);
-    else hipLaunchKernelGGL((mx_layout_kernel<false>), grid, dim3(256), 0, st, a, b, (int)((i + 31) / 32), (int)ks);
-    KQ_TRY(check_launch(who));
     TileArgs g{};
     g.M = n; g.N = o; g.K = i;
     g.A = reinterpret_cast<const char*>(A.c); g.lda = A.ldc;
     g.B = reinterpret_cast<const char*>(B.c); g.ldb = B.ldc;
-    if (U) { g.B2 = reinterpret_cast<const char*>(U->c); g.ldb2 = U->ldc; }
-    g.sA = la; g.sB = lb; g.ksteps = ks;
+    g.rA = A.s; g.ldrA = A.lds; g.rB = B.s; g.ldrB = B.lds;
+    if (U) {
+        g.B2 = reinterpret_cast<const char*>(U->c); g.ldb2 = U->ldc;
+        g.rB2 = U->s; g.ldrB2 = U->lds;
+    }
     g.Y = Y; g.ldy = ldy; g.dt = dt; g.act = act;
+    g.ksteps = mx_ksteps(i);
+    const int64_t ga = mx_groups_a(n), gb = mx_groups_b(o, U != nullptr);
+    uint32_t* la = plan.shape < 2 ? ar.take<uint32_t>((size_t)(ga * g.ksteps * 64)) : nullptr;
+    uint32_t* lb = plan.shape < 2 ? ar.take<uint32_t>((size_t)(gb * g.ksteps * 64)) : nullptr;
+    float* part = plan.part ? ar.take<float>(plan.part) : nullptr;
+    if ((plan.shape < 2 || plan.part) && (!ws || !aligned16(ws) || !ar.ok()))
+        return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
+    if (plan.shape < 2) {
+        g.sA = la;
+        g.sB = lb;
+        const MxLayout a{A.s, nullptr, A.lds, 0, n, ga, la};
+        const MxLayout b{B.s, U ? U->s : nullptr, B.lds, U ? U->lds : 0, o, gb, lb};
+        const dim3 grid((unsigned)(ga + gb));
+        const int nblk = (int)((i + 31) / 32);
+        if (U) hipLaunchKernelGGL((mx_layout_kernel<true>), grid, dim3(256), 0, st, a, b, nblk, (int)g.ksteps);
+        else hipLaunchKernelGGL((mx_layout_kernel<false>), grid, dim3(256), 0, st, a, b, nblk, (int)g.ksteps);
+        KQ_TRY(check_launch(who));
+    }
     return U ? tile_launch<EL_MX, TP_GATED>(g, 1, part, st, who) : tile_launch<EL_MX, TP_PLAIN>(g, 1, part, st, who);
 }
 
@@ -232,11 +246,13 @@ using namespace kq;
 
 size_t mx_product_ws(int64_t o, int64_t i, int64_t n, bool gated) {
     if (n <= 0 || o <= 0 || i <= 0 || few_tokens<EL_MX>(n, o, i)) return 0;
+    const TilePlan plan = mx_plan(n, o, i, gated);
     Sizer s;
-    s.take<uint32_t>((size_t)(mx_groups_a(n) * mx_ksteps(i) * 64));
-    s.take<uint32_t>((size_t)(mx_groups_b(o, gated) * mx_ksteps(i) * 64));
-    const size_t part = (gated ? tile_plan<EL_MX, TP_GATED>(n, o, i, 1) : tile_plan<EL_MX, TP_PLAIN>(n, o, i, 1)).part;
-    if (part) s.take<float>(part);
+    if (plan.shape < 2) {
+        s.take<uint32_t>((size_t)(mx_groups_a(n) * mx_ksteps(i) * 64));
+        s.take<uint32_t>((size_t)(mx_groups_b(o, gated) * mx_ksteps(i) * 64));
+    }
+    if (plan.part) s.take<float>(plan.part);
     return s.used;
 }
 

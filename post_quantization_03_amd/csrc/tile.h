@@ -170,8 +170,10 @@ struct TileArgs {
     int64_t M, N, K;                     // K in values
     const char *A, *A2, *B, *B2;
     int64_t lda, lda2, ldb, ldb2;        // bytes
-    const uint32_t *sA, *sB;             // E2M1: scales laid out by mx_layout (ksteps dwords x 64 lanes a group)
-    int64_t ksteps;                      // E2M1: steps of 128 values (an even number)
+    const uint32_t *sA, *sB;             // E2M1, shapes L, M: scales laid out by mx_layout (ksteps dwords x 64 lanes a group)
+    int64_t ksteps;                      // steps of 128 values (an even number)
+    const uint8_t *rA, *rB, *rB2;        // E2M1, shape S: the scale bytes themselves, rows of ldr* bytes
+    int64_t ldrA, ldrB, ldrB2;
     void *Y, *Y2, *Y3;
     int64_t ldy, ldy2, ldy3;             // values
     int dt;                              // type of the outputs
@@ -190,6 +192,7 @@ struct TileShape {
     static constexpr int OPA = TM * 128, BUF = (TM + TN) * 128;          // bytes of A's slab, of both
     static constexpr int QA = TM / 8 / W, QB = TN / 8 / W;               // loads of 1 KiB a wavefront and slab
     static constexpr size_t SMEM = 2 * BUF;
+    static constexpr bool LAID = TM >= 128;                              // E2M1: scales laid out ahead
 };
 typedef TileShape<256, 256, 2, 4, 2> TileL;      // one work-group a compute unit
 typedef TileShape<128, 128, 2, 2, 2> TileM;      // two
@@ -338,7 +341,14 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
         char* la = tl_sm + buf * C::BUF + wave * 1024;
         char* lb = la + C::OPA;
         constexpr int Q = C::W * 1024;
-        if (ts < whole) {
+        if constexpr (E == EL_MX) {
+            const int left = (int)nch - 1 - ts * 8;      // the last chunk's place from this slab's first
+            const int backA = left < cA ? (left - cA) * 16 : 0, backB = left < cB ? (left - cB) * 16 : 0;
+#pragma unroll
+            for (int q = 0; q < QA; q++) dma16<HID>(pA, offA[q] + backA, la + q * Q);
+#pragma unroll
+            for (int q = 0; q < QB; q++) dma16<HID>(GATED && q >= QB / 2 ? pB2 : pB, offB[q] + backB, lb + q * Q);
+        } else if (ts < whole) {
 #pragma unroll
             for (int q = 0; q < QA; q++) dma16<HID>(pA, offA[q], la + q * Q);
 #pragma unroll
@@ -349,16 +359,14 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
 #pragma unroll
             for (int q = 0; q < QA; q++) {
                 const bool in = TA ? (q * C::W + wave) * (64 / LA) + lane / LA < krows : cA < left;
-                if (E == EL_MX) dma16<HID>(pA, offA[q] + (in ? 0 : (left - 1 - cA) * 16), la + q * Q);
-                else if (in) dma16<HID>(pA, offA[q], la + q * Q);
+                if (in) dma16<HID>(pA, offA[q], la + q * Q);
                 else *reinterpret_cast<tl_i4*>(la + q * Q + lane * 16) = zero;
             }
 #pragma unroll
             for (int q = 0; q < QB; q++) {
                 const char* b = GATED && q >= QB / 2 ? pB2 : pB;
                 const bool in = TB ? (q * C::W + wave) * (64 / LB) + lane / LB < krows : cB < left;
-                if (E == EL_MX) dma16<HID>(b, offB[q] + (in ? 0 : (left - 1 - cB) * 16), lb + q * Q);
-                else if (in) dma16<HID>(b, offB[q], lb + q * Q);
+                if (in) dma16<HID>(b, offB[q], lb + q * Q);
                 else *reinterpret_cast<tl_i4*>(lb + q * Q + lane * 16) = zero;
             }
         }
@@ -395,25 +403,84 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
 #pragma unroll
         for (int j = 0; j < FN; j++) acc[i][j] = tl_f4{0, 0, 0, 0};
 
-    // scales of a slab's two steps (E2M1): a dword holds a lane's bytes of four fragments (64 rows)
-    constexpr int SA = FM >= 4 ? FM / 4 : 1;
-    uint32_t scA[SA][2], scB[2];
-    const uint32_t *qA = nullptr, *qB = nullptr;         // step 0 of the slab whose scales are loaded next
-    if constexpr (E == EL_MX) {
+    // Scales of a slab's two steps (E2M1). Shapes L and M take them laid out, a dword of a lane for four fragments
+    // (64 rows). Shape S reads 8 bytes (a slab) of the row of each of its 4 fragments, which saves the
+    // launch ahead of the product; with M's 8 fragments these loads, 16 rows each, cost more than it
+    // (2048 x 11008 x 4096: 123 us, laid out 67; S at 333 x 1376 x 1000: 5.2 us, laid out 10.4).
+    constexpr bool LAID = C::LAID;
+    constexpr int SA = LAID ? FM / 4 : FM, SB = LAID ? 1 : FN;
+    uint32_t scA[SA][2], scB[SB][2], nxA[SA][2], nxB[SB][2];
+    const uint32_t *qA = nullptr, *qB = nullptr;         // L, M: step 0 of the slab whose scales are loaded next (uniform)
+    const uint8_t *sa = nullptr, *sb = nullptr, *sb2 = nullptr;
+    uint32_t soA[SA], soB[SB];
+    if constexpr (E == EL_MX && LAID) {
         qA = g.sA + ((m0 + wm * FM * 16) / 64 * g.ksteps + 2 * s0) * 64;
         qB = g.sB + ((n0 / GW + grp) * g.ksteps + 2 * s0) * 64;
     }
-    auto load_scales = [&](int s) {
+    if constexpr (E == EL_MX && !LAID) {
+        sa = g.rA + m0 * g.ldrA + s0 * 8;
+        sb = g.rB + n0 * g.ldrB + s0 * 8;
+        if (GATED) sb2 = g.rB2 + n0 * g.ldrB2 + s0 * 8;
 #pragma unroll
-        for (int a = 0; a < SA; a++) {
-            scA[a][s] = qA[(a * g.ksteps + s) * 64 + lane];
-            if (FM < 4) scA[a][s] >>= 8 * FM * (wm % (4 / (FM < 4 ? FM : 4)));
+        for (int i = 0; i < FM; i++) {
+            const int r = wm * FM * 16 + 16 * i + x16;
+            soA[i] = (uint32_t)(r < mlast ? r : mlast) * (uint32_t)g.ldrA;
         }
-        scB[s] = qB[s * 64 + lane];
-        if (SUB > 1) scB[s] >>= 8 * FW * sub;
+#pragma unroll
+        for (int j = 0; j < FN; j++) {
+            const int r = grp * GW + b_row<GF>(sub * FW + j % FW, x16);
+            soB[j] = (uint32_t)(r < nlast ? r : nlast) * (uint32_t)(j >= FW ? g.ldrB2 : g.ldrB);
+        }
+    }
+    // L, M: step s of the next slab, over the register that its last use has left. Buffer loads: a uniform base and one
+    // lane offset, where plain ones would hold a 64-bit address for each of the three.
+    auto load_laid = [&](int s) {
+        auto word = [&](const uint32_t* p) {
+            const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(p), 0, 0xFFFFFFFF, 0x00020000);
+            return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, lane * 4, 0, 0);
+        };
+#pragma unroll
+        for (int a = 0; a < SA; a++) scA[a][s] = word(qA + (a * g.ksteps + s) * 64);
+        scB[0][s] = word(qB + s * 64);
         if (s == 1) {
             qA += 128;
             qB += 128;
+        }
+    };
+    // S: both steps of slab t (of this work-group), to be taken when its products begin
+    auto load_raw = [&](int t) {
+        const int left = (int)nch - (s0 + t) * 8;        // blocks from the slab's first
+        auto at = [&](int f) { return f < FM ? sa + soA[f < FM ? f : 0] : (f - FM >= FW ? sb2 : sb) + soB[f < FM ? 0 : f - FM]; };
+        if (left >= 8) {
+#pragma unroll
+            for (int f = 0; f < FM + FN; f++) {
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(at(f));
+                uint32_t* v = f < FM ? nxA[f < FM ? f : 0] : nxB[f < FM ? 0 : f - FM];
+                v[0] = q[0];
+                v[1] = q[1];
+            }
+        } else {
+            // blocks past K: the smallest scale on both sides, whose products vanish
+#pragma unroll
+            for (int f = 0; f < FM + FN; f++) {
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(at(f));
+                uint32_t* v = f < FM ? nxA[f < FM ? f : 0] : nxB[f < FM ? 0 : f - FM];
+                const uint32_t lo = q[0], hi = left > 4 ? q[1] : 0u;
+                v[0] = g4 < left ? lo : 0u;
+                v[1] = 4 + g4 < left ? hi : 0u;
+            }
+        }
+        sa += 8;
+        sb += 8;
+        if (GATED) sb2 += 8;
+    };
+    auto take_raw = [&]() {
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+#pragma unroll
+            for (int i = 0; i < FM; i++) scA[i][s] = nxA[i][s] >> (8 * g4);
+#pragma unroll
+            for (int j = 0; j < FN; j++) scB[j][s] = nxB[j][s] >> (8 * g4);
         }
     };
 
@@ -467,29 +534,32 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
 #pragma unroll
         for (int j = 0; j < FN; j++) {
             // rows of the result are B's rows (output columns), columns are A's rows
-            if constexpr (E == EL_MX)
-                acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], (int)scB[s], GATED && FN == 2 ? 2 * j : j,
-                                        (int)scA[i / 4][s], i & 3);
+            if constexpr (E == EL_MX && LAID)
+                acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], (int)scB[0][s], j, (int)scA[i / 4][s], i & 3);
+            else if constexpr (E == EL_MX)
+                acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], (int)scB[j][s], 0, (int)scA[i][s], 0);
             else
                 acc[i][j] = mma_step<E>(fb[s][j], a, acc[i][j], 0, 0, 0, 0);
         }
     };
     // One step: the products of A's fragment i with all of B's, then the reads that replace what they used,
     // spread over the step so that no product waits for a burst of them.
-    auto step = [&](int s, int at) {
-        const int nx = s ^ 1;            // the step whose fragments are read (slab at `at`)
+    auto step = [&](int s, int at, auto READ) {
+        const int nx = s ^ 1;            // the step whose fragments are read (slab at `at`), unless there is none
 #pragma unroll
         for (int i = 0; i < FM; i++) {
             products(i, s, s == 1 && i >= INPL ? fx[i >= INPL ? i - INPL : 0] : fa[i]);
             __builtin_amdgcn_sched_barrier(0);
-            if (i < INPL) fa[i] = fragA(at, i, nx);
-            if (i < KEEP) {
-                if (s == 0) fx[i] = fragA(at, INPL + i, nx);
-                else fa[INPL + i] = fragA(at, INPL + i, nx);
-            }
+            if constexpr (READ.value) {
+                if (i < INPL) fa[i] = fragA(at, i, nx);
+                if (i < KEEP) {
+                    if (s == 0) fx[i] = fragA(at, INPL + i, nx);
+                    else fa[INPL + i] = fragA(at, INPL + i, nx);
+                }
 #pragma unroll
-            for (int j = i * FN / FM; j < (i + 1) * FN / FM; j++) fb[nx][j] = fragB(at, j, nx);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int j = i * FN / FM; j < (i + 1) * FN / FM; j++) fb[nx][j] = fragB(at, j, nx);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
     operands(MODE == TP_GRAD_W && wpair ? g.A2 : g.A, MODE == TP_GRAD_W && wpair ? g.lda2 : g.lda, g.B, g.ldb);
@@ -501,24 +571,36 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
         if (GATED) pB2 += s0 * 128;
         stage(0);
         if (part && (!TA || !TB)) clear_part(0, 0);
-        if constexpr (E == EL_MX) load_scales(0);
+        if constexpr (E == EL_MX && LAID) load_laid(0);
+        if constexpr (E == EL_MX && !LAID) load_raw(0);
         landed_barrier();
         if (slabs > 1) stage(1);
 #pragma unroll
         for (int j = 0; j < FN; j++) fb[0][j] = fragB(0, j, 0);
 #pragma unroll
         for (int i = 0; i < FM; i++) fa[i] = fragA(0, i, 0);
-        for (int t = 0; t < slabs; t++) {
-            if constexpr (E == EL_MX) load_scales(1);
-            step(0, slab_at(t));
-            if (part && (!TA || !TB) && t + 1 < slabs) clear_part(t + 1, (t + 1) & 1);
-            landed_barrier();     // slab t + 1 has landed, and every wavefront holds the rest of slab t
-            if (E == EL_MX && t + 1 < slabs) load_scales(0);     // ahead of the slab's loads: waiting for it skips those
-            if (t + 2 < slabs) stage(t & 1);
+        // STAGE: slab t + 2 exists; NEXT: slab t + 1 does. Constants, so that the loads of a turn of the main loop are
+        // always the same in number and the wait for the scales leaves the slab's loads in flight.
+        auto turn = [&](int t, auto STAGE, auto NEXT) {
+            if constexpr (E == EL_MX && LAID) load_laid(1);
+            if constexpr (E == EL_MX && !LAID) take_raw();
+            step(0, slab_at(t), std::true_type{});
+            if constexpr (NEXT.value) {
+                if (part && (!TA || !TB)) clear_part(t + 1, (t + 1) & 1);
+                landed_barrier();     // slab t + 1 has landed, and every wavefront holds the rest of slab t
+                if constexpr (E == EL_MX && LAID) load_laid(0);      // ahead of the slab's loads
+                if constexpr (E == EL_MX && !LAID) load_raw(t + 1);
+                if constexpr (STAGE.value) stage(t & 1);
+            }
             __builtin_amdgcn_sched_barrier(0);
-            // past the last slab the fragments come from LDS that nothing uses any more
-            step(1, slab_at(t + 1));
-        }
+            step(1, slab_at(t + 1), NEXT);
+        };
+        int t = 0;
+        for (; t + 2 < slabs; t++) turn(t, std::true_type{}, std::true_type{});
+        if (t + 1 < slabs) turn(t++, std::false_type{}, std::true_type{});
+        turn(t, std::false_type{}, std::false_type{});
+        // the next pair's first slab overwrites the buffers only once every wavefront has read its last fragments
+        if (MODE == TP_GRAD_X && pair == 0) __syncthreads();
     }
 
     // ---- epilogue: lane holds output row x16 of fragment row i and runs of neighbouring columns
@@ -600,9 +682,10 @@ __global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g, int splits
 
 // How a product is cut: tile shape (0 L, 1 M, 2 S) and splits of K, by the estimated time of each choice.
 // A slab of a tile takes `lat` us by itself on a compute unit and `w` us of a busy one's matrix cores, a tile
-// `fix` more for its first loads and its epilogue; split sums are written and read once at 6.4 TB/s by a
-// second launch (3 us). The constants are fitted to measurements of 8 products at 15 sizes each, all
-// shapes and 1 to 16 splits (MI355X); the choice is within 1 % of the fastest on average and 8 % at worst.
+// `fix` more for its first loads and its epilogue; split sums are written and read once at 3.5 TB/s by a
+// second launch (4 us), and E2M1 scales laid out by one of 3 us. The constants are fitted to measurements of 8
+// products at 15 sizes each, all shapes and 1 to 16 splits (MI355X); the choice is within 2 % of the
+// fastest on average and 14 % at worst.
 // fp32 products are bound by the matrix cores in every shape and always take the small one, which leaves
 // the fewest of them idle. Some times, us (bf16 gated block, n x o x i): 65 x 11008 x 4096 L 87, M 46, S 39; 2048 x 11008 x 4096
 // L 320, M 399, S 638; 512 x 4096 x 11008 M 122, M in two splits 93, L in four 96.
@@ -612,11 +695,13 @@ struct TilePlan {
 };
 
 template <int E, int MODE>
-TilePlan tile_plan(int64_t M, int64_t N, int64_t K, int pairs) {
+TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
+    // both weight gradients' plan also where one is wanted, so that it is the same bits either way
+    constexpr int pairs = MODE == TP_GRAD_W ? 2 : 1;
     constexpr int BK = 8 * el_chunk<E>();
     constexpr int size[3] = {256, 128, 64}, occ[3] = {1, 2, 4}, cuts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
-    constexpr double lat[3] = {1.4, 0.9, 0.75}, fix[3] = {10.0, 4.0, 1.7};
-    constexpr double w[3] = {1.55, 0.5, E == EL_F32 ? 0.2 : 0.38};
+    constexpr double lat[3] = {1.4, 0.9, E == EL_MX ? 0.9 : 0.75}, fix[3] = {10.0, 4.0, 1.7};
+    constexpr double w[3] = {1.55, 0.5, E == EL_F32 ? 0.2 : E == EL_MX ? 0.68 : 0.38};
     const int64_t slabs = (K + BK - 1) / BK, cols = (N + 3) / 4 * 4 * (MODE == TP_GATED ? 2 : 1);
     TilePlan best{};
     double least = 0.0;
@@ -630,7 +715,8 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K, int pairs) {
             const double by_lat = (double)rounds * lat[h], by_w = (double)percu * w[h];
             double t = (double)(sper * (MODE == TP_GRAD_X ? 2 : 1)) * (by_lat > by_w ? by_lat : by_w) + (double)rounds * fix[h];
             const size_t part = splits > 1 ? (size_t)(splits * pairs * M * cols) : 0;
-            if (part) t += 3.0 + 8.0 * (double)part / 6.4e6;
+            if (part) t += 4.0 + 8.0 * (double)part / 3.5e6;
+            if (E == EL_MX && h < 2) t += 3.0;
             if (best.splits == 0 || t < least) {
                 least = t;
                 best = TilePlan{h, (int)splits, (int)sper, part};
@@ -664,7 +750,7 @@ kq_status tile_launch_shape(const TileArgs& g, int splits, hipStream_t st, const
 // part: workspace of tile_plan(...).part floats
 template <int E, int MODE>
 kq_status tile_launch(TileArgs g, int pairs, float* part, hipStream_t st, const char* who) {
-    const TilePlan p = tile_plan<E, MODE>(g.M, g.N, g.K, pairs);
+    const TilePlan p = tile_plan<E, MODE>(g.M, g.N, g.K);
     g.pairs = pairs;
     g.sper = p.sper;
     if (p.splits > 1) {
@@ -706,14 +792,13 @@ struct FewArgs {
 constexpr int FEW_WAVES = 8, FEW_THREADS = 64 * FEW_WAVES;
 
 // Whether n tokens run here rather than as tiles. Measured on MI355X, us here / as tiles, o x i weights:
-//   E2M1  11008 x 4096: 15.3 / 17.6 at 32 tokens, 21.6 / 17.8 at 33; 4096 x 11008: 17.3 / 22.9 at 64 (every
-//         work-group of 16 rows reads the tokens again, so the bound falls with o)
+//   E2M1  11008 x 4096: 8.3 / 11.2 at 1 token, 15.4 / 16.1 at 32, 22.2 / 16.1 at 33; 4096 x 11008: 11.8 / 14.8
+//         at 32, 14.6 / 14.3 at 33
 //   bf16  gated 11008 x 4096: 34.1 / 34.7 at 8, 36.2 / 34.4 at 16; 1376 x 1000: 6.7 / 9.2 at 48
 //   fp32  gated 11008 x 4096: 104 / 135 at 32, 173 / 134 at 33; 1376 x 1000: 10.0 / 15.4 at 32, 16.6 / 15.6 at 33
 template <int E>
 bool few_tokens(int64_t n, int64_t o, int64_t i) {
-    if (E == EL_MX) return n <= 32 || (n <= 64 && n * o <= 64 * 4096);
-    if (E == EL_F32) return n <= 32;
+    if (E != EL_BF16) return n <= 32;
     return n <= 8 || (n <= 48 && o * i <= (1 << 22));
 }
 

@@ -99,9 +99,14 @@ def test_mx_product_refusals():
         for kw, st in ((dict(n=-1), ESHAPE), (dict(o=0), ESHAPE), (dict(i=0), ESHAPE), (dict(dt=7), EINVAL),
                        (dict(Ac=None), EINVAL), (dict(As=None), EINVAL), (dict(Bc=None), EINVAL), (dict(Bs=None), EINVAL),
                        (dict(Y=None), EINVAL), (dict(ldac=16), ESHAPE), (dict(ldbc=24), ESHAPE), (dict(ldbc=40), EINVAL),
-                       (dict(ldas=5), EINVAL), (dict(ldy=4), ESHAPE), (dict(ldy=9), EINVAL), (dict(ldy=12, dt=1), EINVAL),
-                       (dict(n=65), EWORKSPACE), (dict(n=65, ws=P, wb=64), EWORKSPACE)):
+                       (dict(ldas=5), EINVAL), (dict(ldy=4), ESHAPE), (dict(ldy=9), EINVAL), (dict(ldy=12, dt=1), EINVAL)):
             assert call(**kw) == st, (call.__name__, kw)
+        big = dict(n=3000, o=6000, i=2000, ldac=1008, ldas=64, ldbc=1008, ldbs=64, ldy=6000)
+        if call is gated:
+            big.update(lduc=1008, ldus=64)
+        need = K.kq_workspace_bytes("mx_gemm" if call is gemm else "mx_gated", 6000, 2000, 3000)
+        for ws, wb in ((None, 0), (P, 64), (None, need), (ctypes.c_void_p(4100), need), (P, need - 1)):
+            assert call(ws=ws, wb=wb, **big) == EWORKSPACE, (call.__name__, ws, wb)
         assert call(n=0) == 0
     for kw, st in ((dict(Uc=None), EINVAL), (dict(Us=None), EINVAL), (dict(lduc=16), ESHAPE), (dict(act=4), EINVAL),
                    (dict(act=-1), EINVAL)):
@@ -136,7 +141,7 @@ def test_gated_refusals():
 
 def test_workspace_sizes():
     for op in ("mx_gemm", "mx_gated"):
-        assert K.kq_workspace_bytes(op, 4096, 4096, 64) == 0
+        assert K.kq_workspace_bytes(op, 4096, 4096, 32) == 0
         assert K.kq_workspace_bytes(op, 4096, 11008, 8192) >= (4096 + 8192) * 344
 
 

@@ -179,9 +179,9 @@ struct TileArgs {
     int dt;                              // type of the outputs
     int act;
     int pairs;                           // TP_GRAD_W: products (2, or 1 when one gradient is wanted)
-    int sper;                            // slabs of K a work-group takes (all of them when K is not split)
-    float* part;                         // K split: sums of split s of pair p at part + (s * pairs + p) * pstride
-    int64_t pstride, pld;                // (values; gated: gate columns, then up columns from pld / 2)
+    int whole;                           // the first `whole` tiles (of each pair) take all of K, one work-group each;
+    int splits, sper;                    // the others are cut into `splits` work-groups of `sper` slabs, whose sums go
+    float* part;                         // to part + (cut tile * splits + split) * TM * TN, rows of TN
 };
 
 // Tile shapes: TM rows of A by TN rows of B (half gate, half up when gated), WM x WN wavefronts.
@@ -201,18 +201,54 @@ constexpr int TL_ROWS = 256;                     // rows of the largest tile: pa
 // Offsets inside a tile's 256 rows (or 64 K rows) are 32-bit, everything else 64-bit: rows of at most 4 MiB.
 constexpr int64_t TL_LD_MAX = 4 << 20, TL_ROWS_MAX = 1LL << 31;
 
-// Tile of a work-group. Work-groups are dealt to the 8 XCDs in turn, so the linear id is remapped to give
-// each XCD one contiguous range; inside it tiles run in groups of TL_GROUP tile rows, column by column,
-// so that a group's panels of A and B stay in that XCD's L2.
+// Work-groups are dealt to the 8 XCDs in turn, so a range of L of them is remapped to give each XCD one
+// contiguous part of it.
+__device__ __forceinline__ int xcd_range(int id, int L) {
+    const int per = L / 8, rem = L % 8, x = id % 8;
+    return x * per + (x < rem ? x : rem) + id / 8;
+}
+
+// Tile of a work-group, and its split of K. Tiles run in groups of TL_GROUP tile rows, column by column, so that a
+// group's panels of A and B stay in its XCD's L2.
 constexpr int TL_GROUP = 8;
-__device__ __forceinline__ void tile_of(int lid, int ny, int nx, int64_t& tm, int64_t& tn) {
-    const int L = nx * ny, per = L / 8, rem = L % 8, x = lid % 8;
-    lid = x * per + (x < rem ? x : rem) + lid / 8;
+struct TileAt {
+    int cut, split, pair, tm, tn;        // cut: index among the cut tiles, -1 for a whole one
+};
+// tile `lid` of a pair
+__device__ __forceinline__ void tile_place(TileAt& t, int lid, int ny, int nx) {
     const int grp = lid / (TL_GROUP * nx), r0 = grp * TL_GROUP;
     const int rows = ny - r0 < TL_GROUP ? ny - r0 : TL_GROUP;
     const int in = lid - grp * TL_GROUP * nx;
-    tm = r0 + in % rows;
-    tn = in / rows;
+    t.tm = r0 + in % rows;
+    t.tn = in / rows;
+}
+__device__ __forceinline__ void cut_place(TileAt& t, int j, int ny, int nx, int whole) {
+    const int per = nx * ny - whole;     // cut tiles of a pair
+    t.cut = j;
+    t.pair = j / per;
+    tile_place(t, whole + j % per, ny, nx);
+}
+__device__ __forceinline__ TileAt tile_of(int id, int ny, int nx, const TileArgs& g) {
+    TileAt t;
+    const int w = g.whole * g.pairs;
+    if (id < w) {
+        const int j = xcd_range(id, w);
+        t.cut = -1;
+        t.split = 0;
+        t.pair = j / g.whole;
+        tile_place(t, j % g.whole, ny, nx);
+    } else {
+        const int n = nx * ny * g.pairs - w, k = id - w;
+        t.split = k / n;
+        cut_place(t, xcd_range(k % n, n), ny, nx, g.whole);
+    }
+    // the same in every lane, but divided in vector registers
+    t.cut = __builtin_amdgcn_readfirstlane(t.cut);
+    t.split = __builtin_amdgcn_readfirstlane(t.split);
+    t.pair = __builtin_amdgcn_readfirstlane(t.pair);
+    t.tm = __builtin_amdgcn_readfirstlane(t.tm);
+    t.tn = __builtin_amdgcn_readfirstlane(t.tn);
+    return t;
 }
 
 // Rows of B go to wavefronts in groups of four fragments: 64 rows, or 32 gate rows and the same 32 up rows
@@ -243,13 +279,13 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // 16 bytes a lane from base + off straight to LDS (lds + 16 lane; base and lds are the wavefront's). HIDDEN:
 // the compiler takes a transposing LDS read to depend on every load to LDS in flight and would wait for
 // the slab just requested, so beside such reads the load is written out. It has no output register, and
-// landed_barrier waits for it.
+// landed_barrier waits for it. It leaves its LDS base in m0, which nothing else in those kernels uses.
 template <bool HIDDEN>
 __device__ __forceinline__ void dma16(const char* base, uint32_t off, char* lds) {
     if constexpr (HIDDEN) {
         const tl_i4 rsrc = {(int)(uintptr_t)base, (int)((uintptr_t)base >> 32) & 0xFFFF, -1, 0x00020000};
         asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                     :: "v"(off), "s"(rsrc), "s"((uint32_t)(uintptr_t)(lds_ptr)lds) : "memory", "m0");
+                     :: "v"(off), "s"(rsrc), "s"((uint32_t)(uintptr_t)(lds_ptr)lds) : "memory");
     } else {
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0xFFFFFFFF, 0x00020000);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)lds, 16, (int)off, 0, 0, 0);
@@ -277,13 +313,12 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int x16 = lane & 15, g4 = lane >> 4;
     const int wm = wave / C::WN, wn = wave % C::WN, grp = wn / SUB, sub = wn % SUB;
-    int64_t tm, tn;
-    tile_of((int)blockIdx.x, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), tm, tn);
-    const int64_t m0 = tm * C::TM, n0 = tn * TN_OUT;
+    const TileAt at = tile_of((int)blockIdx.x, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g);
+    const int64_t m0 = (int64_t)at.tm * C::TM, n0 = (int64_t)at.tn * TN_OUT;
     const int mlast = (int)(g.M - 1 - m0 < C::TM - 1 ? g.M - 1 - m0 : C::TM - 1);          // last row inside
     const int nlast = (int)(g.N - 1 - n0 < TN_OUT - 1 ? g.N - 1 - n0 : TN_OUT - 1);
-    const int wpair = MODE == TP_GRAD_W ? (int)blockIdx.z % g.pairs : 0;
-    const int split = MODE == TP_GRAD_W ? (int)blockIdx.z / g.pairs : (int)blockIdx.z;
+    const bool cut = at.cut >= 0;
+    const int wpair = MODE == TP_GRAD_W ? at.pair : 0;
 
     // ---- staging: loads of 16 bytes a lane; load q of a wavefront fills KiB q * W + wave of its operand
     const int r8 = lane >> 3, pos = lane & 7;
@@ -331,7 +366,8 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
     const int part = E == EL_MX ? 0 : (int)(g.K % EPC);  // values in a partial last chunk (E2M1 blocks are whole)
     const int slabsK = (int)((g.K + BK - 1) / BK);
     const int whole = (int)(g.K / BK);                   // slabs that lie inside K
-    const int s0 = split * g.sper, slabs = slabsK - s0 < g.sper ? slabsK - s0 : g.sper;    // this work-group's
+    const int s0 = cut ? at.split * g.sper : 0;          // this work-group's slabs
+    const int slabs = cut && slabsK - s0 > g.sper ? g.sper : slabsK - s0;
     int ts = 0;                                          // slab to be staged next
 
     // Stages the next slab into buffer buf. K-contiguous operands: chunks past K become zero (E2M1: a valid chunk
@@ -605,10 +641,11 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
 
     // ---- epilogue: lane holds output row x16 of fragment row i and runs of neighbouring columns
     const bool w2 = MODE == TP_GRAD_W && wpair;
-    float* pt = g.part ? g.part + (int64_t)blockIdx.z * g.pstride : nullptr;
-    void* Y = pt ? pt : w2 ? g.Y2 : g.Y;
-    const int64_t ldY = pt ? g.pld : w2 ? g.ldy2 : g.ldy;
-    const int dt = pt ? KQ_F32 : g.dt;
+    // split sums: the tile's own rows and columns, kept apart from its place in the result
+    float* pt = cut ? g.part + ((int64_t)at.cut * g.splits + at.split) * (C::TM * C::TN) - (m0 * C::TN + n0) : nullptr;
+    void* Y = cut ? pt : w2 ? g.Y2 : g.Y;
+    const int64_t ldY = cut ? C::TN : w2 ? g.ldy2 : g.ldy;
+    const int dt = cut ? KQ_F32 : g.dt;
     const int64_t nrun = n0 + grp * GW + g4 * (4 * GF) + 4 * sub * FW;
 #pragma unroll
     for (int i = 0; i < FM; i++) {
@@ -635,9 +672,9 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
                 for (int j = 0; j < FW; j++)
 #pragma unroll
                     for (int r = 0; r < 4; r++) b[4 * j + r] = acc[i][j + FW][r];
-                if (pt) {
-                    store_run<4 * FW>(pt, KQ_F32, m * g.pld + nrun, a, g.N - nrun);
-                    store_run<4 * FW>(pt, KQ_F32, m * g.pld + g.pld / 2 + nrun, b, g.N - nrun);
+                if (cut) {
+                    store_run<4 * FW>(pt, KQ_F32, m * C::TN + nrun, a, g.N - nrun);
+                    store_run<4 * FW>(pt, KQ_F32, m * C::TN + C::TN / 2 + nrun, b, g.N - nrun);
                 } else {
                     act_times(h, a, b, g.act);
                     store_run<4 * FW>(Y, dt, m * ldY + nrun, h, g.N - nrun);
@@ -649,38 +686,40 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
     }
 }
 
-// Sums of the splits, in split order, and the epilogue: 4 columns a thread.
-template <int MODE>
-__global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g, int splits) {
-    const int64_t per = (g.N + 3) / 4, total = g.M * per;
-    const int pair = blockIdx.z;
-    auto sum = [&](const float* p, float (&v)[4]) {
-        float4 s = *reinterpret_cast<const float4*>(p);
-        for (int k = 1; k < splits; k++) {
-            const float4 t = *reinterpret_cast<const float4*>(p + (int64_t)k * g.pairs * g.pstride);
+// Sums of the splits, in split order, and the epilogue: 4 columns a thread, TM * TN_OUT / 1024 work-groups a tile.
+template <int MODE, typename C>
+__global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
+    TileAt at;
+    cut_place(at, (int)(blockIdx.x / PER), (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g.whole);
+    const int e = (int)(blockIdx.x % PER) * 256 + threadIdx.x, r = e / (TN_OUT / 4), c = e % (TN_OUT / 4) * 4;
+    const int64_t m = (int64_t)at.tm * C::TM + r, n = (int64_t)at.tn * TN_OUT + c;
+    if (m >= g.M || n >= g.N) return;
+    const float* p = g.part + (int64_t)at.cut * g.splits * (C::TM * C::TN) + r * C::TN + c;
+    auto sum = [&](const float* q, float (&v)[4]) {
+        float4 s = *reinterpret_cast<const float4*>(q);
+        for (int k = 1; k < g.splits; k++) {
+            const float4 t = *reinterpret_cast<const float4*>(q + (int64_t)k * (C::TM * C::TN));
             s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
         }
         v[0] = s.x; v[1] = s.y; v[2] = s.z; v[3] = s.w;
     };
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
-        const int64_t m = e / per, n = (e - m * per) * 4;
-        const float* p = g.part + pair * g.pstride + m * g.pld + n;
-        float a[4];
-        sum(p, a);
-        if constexpr (MODE == TP_GATED) {
-            float b[4], h[4];
-            sum(p + g.pld / 2, b);
-            act_times(h, a, b, g.act);
-            store_run<4>(g.Y, g.dt, m * g.ldy + n, h, g.N - n);
-            if (g.Y2) store_run<4>(g.Y2, g.dt, m * g.ldy2 + n, a, g.N - n);
-            if (g.Y3) store_run<4>(g.Y3, g.dt, m * g.ldy3 + n, b, g.N - n);
-        } else {
-            store_run<4>(pair ? g.Y2 : g.Y, g.dt, m * (pair ? g.ldy2 : g.ldy) + n, a, g.N - n);
-        }
+    float a[4];
+    sum(p, a);
+    if constexpr (MODE == TP_GATED) {
+        float b[4], h[4];
+        sum(p + C::TN / 2, b);
+        act_times(h, a, b, g.act);
+        store_run<4>(g.Y, g.dt, m * g.ldy + n, h, g.N - n);
+        if (g.Y2) store_run<4>(g.Y2, g.dt, m * g.ldy2 + n, a, g.N - n);
+        if (g.Y3) store_run<4>(g.Y3, g.dt, m * g.ldy3 + n, b, g.N - n);
+    } else {
+        const bool w2 = MODE == TP_GRAD_W && at.pair;
+        store_run<4>(w2 ? g.Y2 : g.Y, g.dt, m * (w2 ? g.ldy2 : g.ldy) + n, a, g.N - n);
     }
 }
 
-// How a product is cut: tile shape (0 L, 1 M, 2 S) and splits of K, by the estimated time of each choice.
+// How a product is cut: tile shape (0 L, 1 M, 2 S) and the tiles whose K is split, by the estimated time of each choice.
 // A slab of a tile takes `lat` us by itself on a compute unit and `w` us of a busy one's matrix cores, a tile
 // `fix` more for its first loads and its epilogue; split sums are written and read once at 3.5 TB/s by a
 // second launch (4 us), and E2M1 scales laid out by one of 3 us. The constants are fitted to measurements of 8
@@ -690,7 +729,7 @@ __global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g, int splits
 // the fewest of them idle. Some times, us (bf16 gated block, n x o x i): 65 x 11008 x 4096 L 87, M 46, S 39; 2048 x 11008 x 4096
 // L 320, M 399, S 638; 512 x 4096 x 11008 M 122, M in two splits 93, L in four 96.
 struct TilePlan {
-    int shape, splits, sper;
+    int shape, whole, splits, sper;
     size_t part;         // floats of split sums
 };
 
@@ -702,24 +741,32 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
     constexpr int size[3] = {256, 128, 64}, occ[3] = {1, 2, 4}, cuts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
     constexpr double lat[3] = {1.4, 0.9, E == EL_MX ? 0.9 : 0.75}, fix[3] = {10.0, 4.0, 1.7};
     constexpr double w[3] = {1.55, 0.5, E == EL_F32 ? 0.2 : E == EL_MX ? 0.68 : 0.38};
-    const int64_t slabs = (K + BK - 1) / BK, cols = (N + 3) / 4 * 4 * (MODE == TP_GATED ? 2 : 1);
+    const int64_t slabs = (K + BK - 1) / BK;
     TilePlan best{};
     double least = 0.0;
     for (int h = E == EL_F32 ? 2 : 0; h < 3; h++) {
         const int64_t tn = MODE == TP_GATED ? size[h] / 2 : size[h];
-        const int64_t tiles = ((M + size[h] - 1) / size[h]) * ((N + tn - 1) / tn) * pairs;
-        for (int c = 0; c < 8; c++) {
-            const int64_t sper = (slabs + cuts[c] - 1) / cuts[c], splits = (slabs + sper - 1) / sper;
-            if (splits != cuts[c] && c > 0) continue;
-            const int64_t wgs = tiles * splits, percu = (wgs + 255) / 256, rounds = (percu + occ[h] - 1) / occ[h];
+        const int64_t tiles = ((M + size[h] - 1) / size[h]) * ((N + tn - 1) / tn) * pairs, turn = 256 * occ[h];    // turn: even
+        auto time = [&](int64_t wgs, int64_t per) {
+            const int64_t percu = (wgs + 255) / 256, rounds = (percu + occ[h] - 1) / occ[h];
             const double by_lat = (double)rounds * lat[h], by_w = (double)percu * w[h];
-            double t = (double)(sper * (MODE == TP_GRAD_X ? 2 : 1)) * (by_lat > by_w ? by_lat : by_w) + (double)rounds * fix[h];
-            const size_t part = splits > 1 ? (size_t)(splits * pairs * M * cols) : 0;
-            if (part) t += 4.0 + 8.0 * (double)part / 3.5e6;
-            if (E == EL_MX && h < 2) t += 3.0;
-            if (best.splits == 0 || t < least) {
-                least = t;
-                best = TilePlan{h, (int)splits, (int)sper, part};
+            return (double)(per * (MODE == TP_GRAD_X ? 2 : 1)) * (by_lat > by_w ? by_lat : by_w) + (double)rounds * fix[h];
+        };
+        for (int tail = 0; tail < 2; tail++) {
+            // all tiles cut alike, or only those behind the last full turn of the GPU's compute units
+            const int64_t whole = tail ? tiles / turn * turn : 0, cut = tiles - whole;
+            if (tail && (whole == 0 || cut == 0)) continue;
+            for (int c = tail; c < 8; c++) {
+                const int64_t sper = (slabs + cuts[c] - 1) / cuts[c], splits = (slabs + sper - 1) / sper;
+                if (splits != cuts[c]) continue;
+                const size_t part = splits > 1 ? (size_t)(cut * splits * size[h] * size[h]) : 0;
+                double t = (whole ? time(whole, slabs) : 0.0) + time(cut * splits, sper);
+                if (part) t += 4.0 + 8.0 * (double)part / 3.5e6;
+                if (E == EL_MX && h < 2) t += 3.0;
+                if (best.splits == 0 || t < least) {
+                    least = t;
+                    best = TilePlan{h, (int)((splits > 1 ? whole : tiles) / pairs), (int)splits, (int)sper, part};
+                }
             }
         }
     }
@@ -727,10 +774,13 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
 }
 
 template <int E, int MODE, typename C>
-kq_status tile_launch_shape(const TileArgs& g, int splits, hipStream_t st, const char* who) {
+kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const char* who) {
     constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
-    const int64_t tiles = ((g.M + C::TM - 1) / C::TM) * ((g.N + TN_OUT - 1) / TN_OUT);
-    if (tiles > (1LL << 27)) return fail(KQ_ESHAPE, "%s: too many tiles", who);     // tile_of's products stay in 31 bits
+    const int64_t tiles = ((g.M + C::TM - 1) / C::TM) * ((g.N + TN_OUT - 1) / TN_OUT);       // of a pair
+    if (tiles > (1LL << 25)) return fail(KQ_ESHAPE, "%s: too many tiles", who);     // products with TL_GROUP, pairs and splits stay in 31 bits
+    g.whole = p.whole;
+    g.splits = p.splits;
+    g.sper = p.sper;
     // the allowance for dynamic LDS belongs to a device's copy of the kernel: asked for once a device
     static std::atomic<uint64_t> allowed{0};
     int dev = 0;
@@ -742,9 +792,15 @@ kq_status tile_launch_shape(const TileArgs& g, int splits, hipStream_t st, const
         if (e != hipSuccess) return fail(KQ_EHIP, "%s: %s", who, hipGetErrorString(e));
         if (dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    hipLaunchKernelGGL((tile_kernel<E, MODE, C>), dim3((unsigned)tiles, 1, (unsigned)(splits * g.pairs)), dim3(C::THREADS),
-                       C::SMEM, st, g);
-    return check_launch(who);
+    const int64_t cut = (tiles - g.whole) * g.pairs, whole = (int64_t)g.whole * g.pairs;
+    hipLaunchKernelGGL((tile_kernel<E, MODE, C>), dim3((unsigned)(whole + cut * g.splits)), dim3(C::THREADS), C::SMEM, st, g);
+    KQ_TRY(check_launch(who));
+    if (cut) {
+        constexpr int PER = C::TM * TN_OUT / 1024;
+        hipLaunchKernelGGL((tile_reduce_kernel<MODE, C>), dim3((unsigned)(cut * PER)), dim3(256), 0, st, g);
+        KQ_TRY(check_launch(who));
+    }
+    return KQ_OK;
 }
 
 // part: workspace of tile_plan(...).part floats
@@ -752,25 +808,13 @@ template <int E, int MODE>
 kq_status tile_launch(TileArgs g, int pairs, float* part, hipStream_t st, const char* who) {
     const TilePlan p = tile_plan<E, MODE>(g.M, g.N, g.K);
     g.pairs = pairs;
-    g.sper = p.sper;
-    if (p.splits > 1) {
-        if (!part) return fail(KQ_EWORKSPACE, "%s: workspace too small", who);
-        g.part = part;
-        g.pld = (g.N + 3) / 4 * 4 * (MODE == TP_GATED ? 2 : 1);
-        g.pstride = g.M * g.pld;
-    }
+    g.part = part;
+    if (p.part && !part) return fail(KQ_EWORKSPACE, "%s: workspace too small", who);
     if constexpr (E != EL_F32) {
-        if (p.shape == 0) KQ_TRY((tile_launch_shape<E, MODE, TileL>(g, p.splits, st, who)));
-        if (p.shape == 1) KQ_TRY((tile_launch_shape<E, MODE, TileM>(g, p.splits, st, who)));
+        if (p.shape == 0) return tile_launch_shape<E, MODE, TileL>(g, p, st, who);
+        if (p.shape == 1) return tile_launch_shape<E, MODE, TileM>(g, p, st, who);
     }
-    if (p.shape == 2) KQ_TRY((tile_launch_shape<E, MODE, TileS>(g, p.splits, st, who)));
-    if (p.splits > 1) {
-        const int64_t total = g.M * ((g.N + 3) / 4), wgs = (total + 255) / 256;
-        hipLaunchKernelGGL((tile_reduce_kernel<MODE>), dim3((unsigned)(wgs < 8192 ? wgs : 8192), 1, (unsigned)pairs), dim3(256), 0,
-                           st, g, p.splits);
-        KQ_TRY(check_launch(who));
-    }
-    return KQ_OK;
+    return tile_launch_shape<E, MODE, TileS>(g, p, st, who);
 }
 
 // ------------------------------------------------------------------------------------- few tokens

@@ -76,24 +76,31 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
     }
 }
 
-// One lane expands 8 codes; the products with the scale are exact (two significant bits), so both output
+// One lane expands 8 codes (bf16) or 4 (fp32), 16 bytes of output, so that a wavefront's store is one run of
+// 1 KiB; the pass is bound by HBM writes. The products with the scale are exact (two significant bits), so both
 // types hold them exactly unless they leave the type's range.
 template <bool BF>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
                                                             const uint8_t* __restrict__ scales, int64_t lds,
                                                             int64_t rows, int64_t cols, void* __restrict__ Y, int64_t ldy) {
-    const int64_t per = (cols + 7) / 8, total = rows * per;
-    const int64_t step = (int64_t)gridDim.x * 256;
+    constexpr int V = BF ? 8 : 4;
     typedef float f2 __attribute__((ext_vector_type(2)));
+    const int64_t per = (cols + V - 1) / V, total = rows * per;
+    const int64_t step = (int64_t)gridDim.x * 256;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
-        const int64_t r = e / per, q = e - r * per, c = q * 8;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + r * ldc + q * 4);
-        const uint32_t s = scales[r * lds + (q >> 2)];
+        const int64_t r = e / per, q = e - r * per, c = q * V;
+        const uint8_t* p = codes + r * ldc + q * (V / 2);
+        const uint32_t w = BF ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+        const uint32_t s = scales[r * lds + c / 32];
         const float sc = s == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(s ? s << 23 : 0x00400000u);
+        float v[V];
         const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-        const f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-        const float v[8] = {a[0] * sc, a[1] * sc, b[0] * sc, b[1] * sc, d[0] * sc, d[1] * sc, f[0] * sc, f[1] * sc};
-        store_run<8>(Y, BF ? KQ_BF16 : KQ_F32, r * ldy + c, v, cols - c);
+        v[0] = a[0] * sc; v[1] = a[1] * sc; v[2] = b[0] * sc; v[3] = b[1] * sc;
+        if constexpr (BF) {
+            const f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+            v[4] = d[0] * sc; v[5] = d[1] * sc; v[6] = f[0] * sc; v[7] = f[1] * sc;
+        }
+        store_run<V>(Y, BF ? KQ_BF16 : KQ_F32, r * ldy + c, v, cols - c);
     }
 }
 
@@ -286,7 +293,7 @@ extern "C" kq_status kq_mx_dequantize(const uint8_t* codes, int64_t ldc, const u
     if (rows == 0) return KQ_OK;
     KQ_TRY(mx_check(who, "input", MxOperand{codes, ldc, scales, lds}, rows, cols));
     KQ_TRY(mx_out_check(who, Y, ydt, ldy, cols));
-    const int64_t total = rows * ((cols + 7) / 8);
+    const int64_t v = ydt == KQ_BF16 ? 8 : 4, total = rows * ((cols + v - 1) / v);
     const unsigned grid = (unsigned)((total + 255) / 256 < 65536 ? (total + 255) / 256 : 65536);
     if (ydt == KQ_BF16)
         hipLaunchKernelGGL((mx_dequantize_kernel<true>), dim3(grid), dim3(256), 0, hs(stream), codes, ldc, scales, lds,

@@ -72,8 +72,8 @@ __device__ __forceinline__ void store_run(void* out, int dt, int64_t off, const 
 }
 
 // ------------------------------------------------------------------------------------- activations
-// gate = act(a) / a, the factor in 0..1 that multiplies a. The logistic gates take the hardware's exp2 and
-// reciprocal (both within an ulp): the argument's rounding, |a| 2^-24 relative, is of the same order.
+// gate = act(a) / a, the factor in 0..1 that multiplies a (of max(a, 0): its derivative, 0 at 0). The logistic gates take
+// the hardware's exp2 and reciprocal (both within an ulp): the argument's rounding, |a| 2^-24 relative, is of the same order.
 __device__ __forceinline__ float logistic(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
 }
@@ -85,11 +85,18 @@ __device__ __forceinline__ float act_gate(float a) {
     else return a > 0.0f ? 1.0f : (a == a ? 0.0f : a);
 }
 
+// act(a) for its gate p: max(a, 0) by choice, since the product is not 0 at -infinity
+template <int ACT>
+__device__ __forceinline__ float act_value(float a, float p) {
+    if constexpr (ACT == KQ_ACT_RELU) return a > 0.0f ? a : p;
+    else return a * p;
+}
+
 // act(a) and act'(a)
 template <int ACT>
 __device__ __forceinline__ void act_both(float a, float& f, float& df) {
     const float p = act_gate<ACT>(a);
-    f = a * p;
+    f = act_value<ACT>(a, p);
     if constexpr (ACT == KQ_ACT_SILU) df = p * (1.0f + a * (1.0f - p));
     else if constexpr (ACT == KQ_ACT_GELU) df = p + a * __builtin_amdgcn_exp2f(-0.72134752044448170f * a * a) * 0.39894228040143268f;
     else if constexpr (ACT == KQ_ACT_GELU_TANH)
@@ -114,7 +121,7 @@ template <int N>
 __device__ __forceinline__ void act_times(float (&h)[N], const float (&a)[N], const float (&b)[N], int act) {
     with_act(act, [&](auto A) {
 #pragma unroll
-        for (int e = 0; e < N; e++) h[e] = a[e] * act_gate<A.value>(a[e]) * b[e];
+        for (int e = 0; e < N; e++) h[e] = act_value<A.value>(a[e], act_gate<A.value>(a[e])) * b[e];
     });
 }
 

@@ -388,6 +388,25 @@ def test_gated_large_arguments():
         check(get(dA), 2 * want_d, 1e-5, f"act' {kind}")
 
 
+@pytest.mark.parametrize("n", [3, 70])
+def test_gated_relu_of_infinities_and_nan(n):
+    """max(a, 0) is 0 at -infinity, and NaN stays NaN; each in its own token's row."""
+    X, x = put(np.ones((n, 8)), "f32")
+    X[1], X[2, 0] = 2.0 ** 127, float("nan")         # row 1: A overflows to -infinity, B = 128
+    Wg, _ = put(-np.ones((4, 8)), "f32")
+    Wu, _ = put(2.0 ** -120 * np.eye(8)[:4], "f32")
+    H, A, B = (mat(n, 4, "f32") for _ in range(3))
+    K.kq_gated_forward(X, Wg, Wu, "relu", H, A, B, ws_of("gated_forward", 4, 8, n, "f32"))
+    a, b, h = get(A), get(B), get(H)
+    assert (a[1] == -np.inf).all() and np.isnan(a[2]).all() and (a[3:] == -8).all() and (a[0] == -8).all()
+    assert (b[1] == 128).all() and np.isnan(h[2]).all() and (h[[0, 1]] == 0).all() and (h[3:] == 0).all()
+    B.fill_(2.0)
+    dH, dA, dB = mat(n, 4, "f32", fill=1.0), mat(n, 4, "f32"), mat(n, 4, "f32")
+    K.kq_gated_backward(dH, A, B, None, None, None, "relu", dA, dB)
+    for t in (get(dA), get(dB)):                     # act and act' of -infinity are 0
+        assert (t[1] == 0).all() and np.isnan(t[2]).all() and (t[0] == 0).all() and (t[3:] == 0).all()
+
+
 # ------------------------------------------------------------------------------------ large tiles
 # one size for each tile shape and split of K that a type and product can take
 @pytest.mark.parametrize("dt", ["f32", "bf16"])

@@ -9,7 +9,7 @@
 // bf16 operands run on the bf16 matrix cores with fp32 sums; A and B are rounded to bf16 only where the
 // caller keeps them, H is computed from the unrounded sums. dA and dB are rounded to the operands' type
 // once, as outputs and as the operands of the three gradient products: bf16 matrix cores take bf16
-// operands, and the rounding (2^-9 relative, independent from element to element) enters a sum of many
+// operands, and the rounding (2^-8 relative at most, independent from element to element) enters a sum of many
 // products below the rounding of the result. fp32 operands run on the fp32 matrix cores throughout.
 #include "tile.h"
 
@@ -129,13 +129,14 @@ static kq_status gated_forward(const char* who, const void* X, int64_t ldx, cons
 using namespace kq;
 
 size_t gated_forward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
-    if (n <= 0 || o <= 0 || i <= 0 || (dt == KQ_BF16 ? few_tokens<EL_BF16>(n, o, i) : few_tokens<EL_F32>(n, o, i))) return 0;
+    if (n <= 0 || o <= 0 || i <= 0 || !tile_sizes_ok(n, o) ||
+        (dt == KQ_BF16 ? few_tokens<EL_BF16>(n, o, i) : few_tokens<EL_F32>(n, o, i))) return 0;
     return sizeof(float) * (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GATED>(n, o, i) : tile_plan<EL_F32, TP_GATED>(n, o, i)).part;
 }
 
 // The products run one after another on the caller's stream and share the split sums' memory.
 size_t gated_backward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
-    if (n <= 0 || o <= 0 || i <= 0) return 0;
+    if (n <= 0 || o <= 0 || i <= 0 || !tile_sizes_ok(n, i) || !tile_sizes_ok(o, i)) return 0;
     const size_t w = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_W>(o, i, n) : tile_plan<EL_F32, TP_GRAD_W>(o, i, n)).part;
     const size_t x = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_X>(n, i, o) : tile_plan<EL_F32, TP_GRAD_X>(n, i, o)).part;
     return sizeof(float) * (x > w ? x : w);
@@ -150,6 +151,7 @@ extern "C" kq_status kq_gated_forward(const void* X, int64_t ldx, const void* Wg
     if (dt != KQ_F32 && dt != KQ_BF16) return fail(KQ_EINVAL, "%s: bad dtype", who);
     if (act < KQ_ACT_SILU || act > KQ_ACT_RELU) return fail(KQ_EINVAL, "%s: bad activation", who);
     if (n == 0) return KQ_OK;
+    if (!tile_sizes_ok(n, o)) return fail(KQ_ESHAPE, "%s: result too large", who);
     KQ_TRY(dense_check(who, dt, Dense{X, ldx, "X"}, n, i));
     KQ_TRY(dense_check(who, dt, Dense{Wg, ldg, "Wg"}, o, i));
     KQ_TRY(dense_check(who, dt, Dense{Wu, ldu, "Wu"}, o, i));
@@ -173,6 +175,8 @@ extern "C" kq_status kq_gated_backward(const void* dH, int64_t lddh, const void*
     if (n < 0 || o <= 0 || i <= 0) return fail(KQ_ESHAPE, "%s: bad sizes", who);
     if (dt != KQ_F32 && dt != KQ_BF16) return fail(KQ_EINVAL, "%s: bad dtype", who);
     if (act < KQ_ACT_SILU || act > KQ_ACT_RELU) return fail(KQ_EINVAL, "%s: bad activation", who);
+    if ((dX && !tile_sizes_ok(n, i)) || ((dWg || dWu) && !tile_sizes_ok(o, i)))
+        return fail(KQ_ESHAPE, "%s: gradients too large", who);
     if (dWg) KQ_TRY(dense_check(who, dt, Dense{dWg, lddg, "dWg"}, o, i));
     if (dWu) KQ_TRY(dense_check(who, dt, Dense{dWu, lddu, "dWu"}, o, i));
     const hipStream_t st = hs(stream);

@@ -205,6 +205,7 @@ static kq_status mx_out_check(const char* who, const void* Y, kq_dtype dt, int64
 static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand& B, const MxOperand* U, int64_t n,
                             int64_t o, int64_t i, int act, void* Y, kq_dtype dt, int64_t ldy, void* ws, size_t ws_bytes,
                             hipStream_t st) {
+    if (!tile_sizes_ok(n, o)) return fail(KQ_ESHAPE, "%s: result too large", who);
     if (few_tokens<EL_MX>(n, o, i)) {
         FewArgs f{};
         f.n = n; f.o = o; f.K = i;
@@ -228,6 +229,7 @@ static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand
     g.Y = Y; g.ldy = ldy; g.dt = dt; g.act = act;
     g.ksteps = mx_ksteps(i);
     const int64_t ga = mx_groups_a(n), gb = mx_groups_b(o, U != nullptr);
+    if (plan.shape < 2 && !grid_ok(ga + gb, 256)) return fail(KQ_ESHAPE, "%s: too many rows for a launch", who);
     uint32_t* la = plan.shape < 2 ? ar.take<uint32_t>((size_t)(ga * g.ksteps * 64)) : nullptr;
     uint32_t* lb = plan.shape < 2 ? ar.take<uint32_t>((size_t)(gb * g.ksteps * 64)) : nullptr;
     float* part = plan.part ? ar.take<float>(plan.part) : nullptr;
@@ -252,7 +254,7 @@ static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand
 using namespace kq;
 
 size_t mx_product_ws(int64_t o, int64_t i, int64_t n, bool gated) {
-    if (n <= 0 || o <= 0 || i <= 0 || few_tokens<EL_MX>(n, o, i)) return 0;
+    if (n <= 0 || o <= 0 || i <= 0 || !tile_sizes_ok(n, o) || few_tokens<EL_MX>(n, o, i)) return 0;
     const TilePlan plan = mx_plan(n, o, i, gated);
     Sizer s;
     if (plan.shape < 2) {

@@ -207,6 +207,10 @@ typedef TileShape<64, 64, 2, 2, 4> TileS;        // four
 constexpr int TL_ROWS = 256;                     // rows of the largest tile: padding of mx_layout's groups
 // Offsets inside a tile's 256 rows (or 64 K rows) are 32-bit, everything else 64-bit: rows of at most 4 MiB.
 constexpr int64_t TL_LD_MAX = 4 << 20, TL_ROWS_MAX = 1LL << 31;
+// Results of at most 2^44 values (dozens of times the memory), which keeps the plan's counts in 64 bits.
+inline bool tile_sizes_ok(int64_t M, int64_t N) { return M <= TL_ROWS_MAX && N <= TL_ROWS_MAX && M * N <= (1LL << 44); }
+// A launch takes fewer than 2^32 threads.
+inline bool grid_ok(int64_t groups, int64_t threads) { return groups <= 0xFFFFFFFFLL / threads; }
 
 // Work-groups are dealt to the 8 XCDs in turn, so a range of L of them is remapped to give each XCD one
 // contiguous part of it.
@@ -805,7 +809,10 @@ template <int E, int MODE, typename C>
 kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const char* who) {
     constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
     const int64_t tiles = ((g.M + C::TM - 1) / C::TM) * ((g.N + TN_OUT - 1) / TN_OUT);       // of a pair
-    if (tiles > (1LL << 25)) return fail(KQ_ESHAPE, "%s: too many tiles", who);     // products with TL_GROUP, pairs and splits stay in 31 bits
+    const int64_t cut = (tiles - p.whole) * g.pairs, whole = (int64_t)p.whole * g.pairs;
+    constexpr int PER = C::TM * TN_OUT / 1024;           // work-groups of the sums of a cut tile
+    if (!grid_ok(whole + cut * p.splits, C::THREADS) || (p.splits > 1 && !grid_ok(cut * PER, 256)))
+        return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
     g.whole = p.whole;
     g.splits = p.splits;
     g.sper = p.sper;
@@ -820,11 +827,9 @@ kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const
         if (e != hipSuccess) return fail(KQ_EHIP, "%s: %s", who, hipGetErrorString(e));
         if (dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int64_t cut = (tiles - g.whole) * g.pairs, whole = (int64_t)g.whole * g.pairs;
     hipLaunchKernelGGL((tile_kernel<E, MODE, C>), dim3((unsigned)(whole + cut * g.splits)), dim3(C::THREADS), C::SMEM, st, g);
     KQ_TRY(check_launch(who));
     if (cut) {
-        constexpr int PER = C::TM * TN_OUT / 1024;
         hipLaunchKernelGGL((tile_reduce_kernel<MODE, C>), dim3((unsigned)(cut * PER)), dim3(256), 0, st, g);
         KQ_TRY(check_launch(who));
     }
@@ -1018,7 +1023,7 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
 template <int E, bool GATED>
 kq_status few_launch(const FewArgs& g, hipStream_t st, const char* who) {
     const int64_t wgs = (g.o + 15) / 16;
-    if (wgs > 2147483647LL) return fail(KQ_ESHAPE, "%s: too many rows", who);
+    if (!grid_ok(wgs, FEW_THREADS)) return fail(KQ_ESHAPE, "%s: too many rows", who);
     const dim3 grid((unsigned)wgs);
     const size_t one = (size_t)FEW_WAVES * (GATED ? 2 : 1) * 1024;
     if (g.n <= 16) {

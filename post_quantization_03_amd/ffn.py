@@ -51,6 +51,8 @@ def calibrate_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, dH: tor
     product: H (input of the down projection), dA and dB (gradient rows of gate and up), dX, and the
     gradient covariances HG_gate and HG_up in cfg's storage form."""
     n, i = X.shape
+    if n == 0:
+        raise ValueError("calibrate_gated: no tokens, no statistics")
     o = Wg.shape[0]
     H, A, B = _rows(n, o, X), _rows(n, o, X), _rows(n, o, X)
     K.kq_gated_forward(X, Wg, Wu, act, H, A, B, _ws("gated_forward", o, i, n, X))

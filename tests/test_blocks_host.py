@@ -139,6 +139,32 @@ def test_gated_refusals():
     assert bwd(n=0, dG=None, dU=None) == 0
 
 
+def test_sizes_past_a_launch_are_refused():
+    """Results and grids that no launch can hold come back as ESHAPE, before any workspace or GPU is asked for."""
+    lib, far = K.lib(), 1 << 31
+
+    def gemm(n, o, U=False):
+        if U:
+            return lib.kq_mx_gated(P, 32, P, 4, P, 32, P, 4, P, 32, P, 4, n, o, 40, 0, P, 0, o, None, 0, None)
+        return lib.kq_mx_gemm(P, 32, P, 4, P, 32, P, 4, n, o, 40, P, 0, o, None, 0, None)
+
+    for u in (False, True):
+        for n, o in ((1, 1 << 28), (far, far), (far, 64), (far + 1, 64)):
+            assert gemm(n, o, u) == ESHAPE, (n, o, u)
+    assert K.kq_workspace_bytes("mx_gemm", far, 40, far) == 0
+    for n, o in ((far + 1, 64), (far, 1 << 20)):
+        assert lib.kq_gated_forward(P, 16, P, 16, P, 16, 1, n, o, 16, 0, P, o, None, 0, None, 0, None, 0, None) == ESHAPE
+        assert lib.kq_gated_backward(P, o, P, o, P, o, P, 1 << 20, P, 1 << 20, P, 1 << 20, 1, n, o, 1 << 20, 0, P, o, P, o,
+                                     P, 1 << 20, None, 0, None, 0, None, 0, None) == ESHAPE
+
+
+def test_calibration_needs_tokens():
+    from post_quantization_03_amd.layer import LayerCfg
+    x, w = torch.zeros(0, 64), torch.zeros(8, 64)
+    with pytest.raises(ValueError, match="no tokens"):
+        ffn.calibrate_gated(x, w, w, torch.zeros(0, 8), "silu", LayerCfg(bits=4, group=64, form="diag"))
+
+
 def test_workspace_sizes():
     for op in ("mx_gemm", "mx_gated"):
         assert K.kq_workspace_bytes(op, 4096, 4096, 32) == 0

@@ -468,6 +468,81 @@ def test_gated_block_in_every_tile_shape(n, o, i, dt):
         check(get(t), w, tol, name)
 
 
+# ------------------------------------------------------------------------------ offsets past 32 bits
+def test_mx_offsets_past_32_bits():
+    """Matrices of more than 2^31 values: the last rows are those of a call on these rows alone."""
+    torch, dev = torch_dev()
+    rows, cols, k = 262501, 8200, 5
+    torch.manual_seed(1)
+    x = mat(rows, cols, "bf16", fill=0.0)
+    x[-k:].copy_(torch.randn(k, cols, device=dev))
+    x[0].copy_(torch.randn(cols, device=dev))
+    say("mx offsets: quantise")
+    c, s = K.mx_empty(rows, cols, dev)
+    K.kq_mx_quantize(x, c, s)
+    c1, s1 = K.mx_empty(k, cols, dev)
+    K.kq_mx_quantize(x[-k:], c1, s1)
+    nblk = -(-cols // 32)
+    assert np.array_equal(host(c[-k:]), host(c1)) and np.array_equal(host(s[-k:, :nblk]), host(s1[:, :nblk]))
+    x.fill_(-77.0)
+    K.kq_mx_dequantize(c, s, x)
+    for part in (slice(rows - k, rows), slice(0, 1)):
+        assert np.array_equal(get(x[part]), ob.mx_values(host(c[part]), host(s[part]), cols))
+    say("mx offsets: products")
+    (ac, as_), a = packed(np.random.default_rng(1).standard_normal((k, 64)))
+    (bc, bs), b = packed(np.random.default_rng(2).standard_normal((cols, 64)))
+    big, bigs = K.mx_empty(rows, 64, dev)
+    big.zero_(), bigs.fill_(127)
+    big[-k:].copy_(ac), bigs[-k:].copy_(as_)
+    for gated in (False, True):
+        x.fill_(-77.0)
+        if gated:
+            K.kq_mx_gated(big, bigs, bc, bs, bc, bs, 64, "relu", x, ws_of("mx_gated", cols, 64, rows))
+        else:
+            K.kq_mx_gemm(big, bigs, bc, bs, 64, x, ws_of("mx_gemm", cols, 64, rows))
+        y = a @ b.T
+        e = 64 * E23 * (np.abs(a) @ np.abs(b).T)
+        want, err = (np.maximum(y, 0) * y, 2 * e * np.abs(y) + e * e) if gated else (y, e)
+        check(get(x[-k:]), want, err + HALF["bf16"] * (np.abs(want) + err) + 2.0 ** -126, "last rows")
+        assert bool((x[:-k] == 0).all())
+
+
+def test_gated_offsets_past_32_bits():
+    """Tokens 64 KiB apart, 4.3 GB in all, read by rows (forward) and by columns (weight gradients)."""
+    torch, dev = torch_dev()
+    n, o, i, dt = 65700, 72, 40, "bf16"
+    torch.manual_seed(2)
+
+    def wide(d):
+        t = torch.empty((n, 32768), dtype=torch.bfloat16, device=dev)[:, :d]
+        t.copy_(torch.randn(n, d, device=dev))
+        return t
+
+    X, A, B, dH = wide(i), wide(o), wide(o), wide(o)
+    (Wg, g), (Wu, u) = (put(np.random.default_rng(r).standard_normal((o, i)) * 0.2, dt) for r in (1, 2))
+    H = wide(o)
+    say("gated offsets: forward")
+    K.kq_gated_forward(X, Wg, Wu, "silu", H, ws=ws_of("gated_forward", o, i, n, dt))
+    k = 300
+    x = get(X[-k:])
+    want, a, b = ob.gated(x, g, u, "silu")
+    da, db = i * E23 * (np.abs(x) @ np.abs(g).T), i * E23 * (np.abs(x) @ np.abs(u).T)
+    check(get(H[-k:]), want, gated_tol(a, b, da, db, "silu", dt), "H")
+    say("gated offsets: backward")
+    dH[k:-k] = 0.0           # 2 k rows count: adding the others' zeros is exact
+    dA, dB, dX = wide(o), wide(o), wide(i)
+    dG, dU = mat(o, i, dt), mat(o, i, dt)
+    K.kq_gated_backward(dH, A, B, X, Wg, Wu, "silu", dA, dB, dX, dG, dU, ws_of("gated_backward", o, i, n, dt))
+    want, tols = grad_tols(get(dH[-k:]), get(A[-k:]), get(B[-k:]), x, g, u, "silu", dt)
+    for name, t, w, tol in zip(("dA", "dB", "dX"), (dA, dB, dX), want, tols):
+        check(get(t[-k:]), w, tol, name)
+    xd = X.double()
+    for name, t, m in (("dWg", dG, dA), ("dWu", dU, dB)):      # from the kernel's own dA and dB
+        md = m.double()
+        w, s = host(md.T.contiguous() @ xd), host(md.abs().T.contiguous() @ xd.abs())
+        check(get(t), w, 2 * k * E23 * s + HALF[dt] * (np.abs(w) + 2 * k * E23 * s), name)
+
+
 # --------------------------------------------------------------------- streams, graphs, two calls
 @pytest.mark.parametrize("n", [3, 300])
 def test_products_replayed_from_a_graph(n):

@@ -468,6 +468,53 @@ def test_gated_block_in_every_tile_shape(n, o, i, dt):
         check(get(t), w, tol, name)
 
 
+@pytest.mark.parametrize("n,o,i", [(3, 40, 72), (50, 40, 72), (150, 300, 520), (1500, 2000, 520)])
+def test_rows_behind_the_last_one_stay(n, o, i):
+    """Outputs that are the first rows of larger buffers: the rest is left alone; and one of each pair of
+    optional outputs gives the bits of both."""
+    torch, dev = torch_dev()
+    say(f"rows behind n={n} o={o} i={i}")
+    torch.manual_seed(n)
+
+    def rnd(rows, cols, std=1.0):
+        t = mat(rows, cols, "bf16")
+        t.copy_(torch.randn(rows, cols, device=dev) * std)
+        return t
+
+    def more(rows, cols):
+        t = mat(rows + 70, cols, "bf16", 1, -77.0)
+        kept.append((t, rows))
+        return t[:rows]
+
+    kept = []
+    X, Wg, Wu, dH = rnd(n, i), rnd(o, i, 0.1), rnd(o, i, 0.1), rnd(n, o)
+    ws = ws_of("gated_forward", o, i, n)
+    H, A, B, H1, A1, B1 = (more(n, o) for _ in range(6))
+    K.kq_gated_forward(X, Wg, Wu, "gelu_tanh", H, A, B, ws)
+    K.kq_gated_forward(X, Wg, Wu, "gelu_tanh", H1, A=A1, ws=ws)
+    assert torch.equal(H, H1) and torch.equal(A, A1)
+    K.kq_gated_forward(X, Wg, Wu, "gelu_tanh", H1, B=B1, ws=ws)
+    assert torch.equal(H, H1) and torch.equal(B, B1)
+    dA, dB, dX, dG, dU, dG1 = more(n, o), more(n, o), more(n, i), more(o, i), more(o, i), more(o, i)
+    wb = ws_of("gated_backward", o, i, n)
+    K.kq_gated_backward(dH, A, B, X, Wg, Wu, "gelu_tanh", dA, dB, dX, dG, dU, wb)
+    K.kq_gated_backward(dH, A, B, X, None, None, "gelu_tanh", dA, dB, dWg=dG1, ws=wb)
+    assert torch.equal(dG, dG1)
+    q = [K.mx_empty(m, i, dev) for m in (n + 70, o, o)]
+    for c, s in q:
+        c.fill_(0xAB), s.fill_(0xAB)
+    (xc, xs), g, u = q
+    xc, xs = xc[:n], xs[:n]
+    K.kq_mx_quantize(X, xc, xs), K.kq_mx_quantize(Wg, *g), K.kq_mx_quantize(Wu, *u)
+    assert bool((q[0][0][n:] == 0xAB).all()) and bool((q[0][1][n:] == 0xAB).all())
+    K.kq_mx_gemm(xc, xs, *g, i, more(n, o), ws_of("mx_gemm", o, i, n))
+    K.kq_mx_gated(xc, xs, *g, *u, i, "silu", more(n, o), ws_of("mx_gated", o, i, n))
+    K.kq_mx_dequantize(xc, xs, more(n, i))
+    for t, rows in kept:
+        assert bool((t[rows:] == -77).all()) and bool((t.as_strided((t.shape[0], t.stride(0)), (t.stride(0), 1))[:, t.shape[1]:] == -77).all())
+        assert not bool(torch.isnan(t).any())
+
+
 # ------------------------------------------------------------------------------ offsets past 32 bits
 def test_mx_offsets_past_32_bits():
     """Matrices of more than 2^31 values: the last rows are those of a call on these rows alone."""

@@ -306,32 +306,34 @@ _TORCH: list = []       # torch.uint8, the raw current stream of a device, the c
 def _torch() -> list:
     if not _TORCH:
         import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _TORCH.extend((torch.uint8, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), torch.cuda.current_device))
+        raw, cur = (getattr(torch._C, k, None) for k in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        _TORCH.extend((torch.uint8, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), cur or torch.cuda.current_device))
         _FLOATS.update({torch.float32: (KQ_F32, 4), torch.bfloat16: (KQ_BF16, 8)})
     return _TORCH
 
 
 def _float(name: str, what: str, t):
-    """(kq_dtype, elements in 16 bytes) of a tensor's type."""
+    """(kq_dtype, elements in 16 bytes, device) of a tensor."""
     if not _FLOATS:
         _torch()
     f = _FLOATS.get(t.dtype)
     if f is None:
         raise TypeError(f"{name}: {what} has type {t.dtype}")
-    return f
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name}: {what} is not on a GPU")
+    return f[0], f[1], d
 
 
-def _matrix(name: str, what: str, t, rows: int, cols: int, dtype, per: int, whole: bool, dev: list):
-    """Checks a row-major rows x cols matrix of `dtype` on the device of the others; returns (pointer,
-    leading dimension). whole: its rows are read in pieces of `per` elements, the last one included."""
-    if t.dtype != dtype:
+def _matrix(name: str, what: str, t, rows: int, cols: int, dtype, per: int, whole: bool, dev: int):
+    """Checks a row-major rows x cols matrix of `dtype` on device `dev`; returns (pointer, leading
+    dimension). whole: its rows are read in pieces of `per` elements, the last one included."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {what} has type {t.dtype}, not {dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {(rows, cols)}")
-    d = t.get_device()
-    if d < 0 or not dev or d != dev[0]:
-        _same_device(name, what, d, dev)
+    if t.get_device() != dev:
+        _other_device(name, what, t, dev)
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name}: {what} is not row-major")
@@ -344,27 +346,24 @@ def _matrix(name: str, what: str, t, rows: int, cols: int, dtype, per: int, whol
     return t.data_ptr(), ld
 
 
-def _same_device(name: str, what: str, d: int, dev: list) -> None:
-    if d < 0:
+def _other_device(name: str, what: str, t, dev: int) -> None:
+    if t.get_device() < 0:
         raise ValueError(f"{name}: {what} is not on a GPU")
-    if not dev:
-        dev.append(d)
-    elif d != dev[0]:
-        raise ValueError(f"{name}: operands on different devices: {what} on cuda:{d}, others on cuda:{dev[0]}")
+    raise ValueError(f"{name}: operands on different devices: {what} on {t.device}, others on cuda:{dev}")
 
 
-def _mx(name: str, what: str, codes, scales, cols: int, dev: list) -> tuple:
+def _mx(name: str, what: str, codes, scales, cols: int, dev: int) -> tuple:
     """Checks a microscaled operand of `cols` columns; returns its four C arguments."""
-    u8 = _torch()[0]
-    if codes.dtype != u8 or scales.dtype != u8:
+    u8 = _TORCH[0]
+    if codes.dtype is not u8 or scales.dtype is not u8:
         raise TypeError(f"{name}: {what} codes and scales have types {codes.dtype} and {scales.dtype}, not uint8")
     cs, ss = codes.shape, scales.shape
     if len(cs) != 2 or len(ss) != 2 or cs[0] != ss[0]:
         raise ValueError(f"{name}: {what} needs codes and scales with one row for each of the matrix")
-    d, e = codes.get_device(), scales.get_device()
-    if d < 0 or d != e or not dev or d != dev[0]:
-        _same_device(name, what + " codes", d, dev)
-        _same_device(name, what + " scales", e, dev)
+    if codes.get_device() != dev:
+        _other_device(name, what + " codes", codes, dev)
+    if scales.get_device() != dev:
+        _other_device(name, what + " scales", scales, dev)
     nblk = (cols + 31) // 32
     rows, wide, have = cs[0], (nblk + 3) // 4 * 4, ss[1]
     if cs[1] != 16 * nblk or not nblk <= have <= wide:
@@ -380,27 +379,28 @@ def _mx(name: str, what: str, codes, scales, cols: int, dev: list) -> tuple:
     return codes.data_ptr(), ldc, scales.data_ptr(), lds
 
 
-def _launch(name: str, fn, dev: list, ws, stream, *args) -> None:
-    """fn(*args [, workspace, its bytes], stream) on the operands' device."""
-    _, raw_stream, current_device = _torch()
-    d = dev[0]
-    if ws is not False:
-        if ws is None:
-            args += (None, 0)
-        else:
-            _same_device(name, "the workspace", ws.get_device(), dev)
-            args += (ws.data_ptr(), ws.numel() * ws.element_size())
+def _workspace(name: str, ws, dev: int) -> tuple:
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev:
+        _other_device(name, "the workspace", ws, dev)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _launch(name: str, fn, dev: int, stream, args: tuple) -> None:
+    """fn(*args, stream) on device `dev`."""
+    _, raw_stream, current_device = _TORCH
     if stream is None:
-        s = raw_stream(d)
-    elif stream.device.index != d:
-        raise ValueError(f"{name}: the stream is on {stream.device}, the operands on cuda:{d}")
+        s = raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the operands on cuda:{dev}")
     else:
         s = stream.cuda_stream
-    if current_device() == d:
+    if current_device() == dev:
         status = fn(*args, s)
     else:
         import torch
-        with torch.cuda.device(d):
+        with torch.cuda.device(dev):
             status = fn(*args, s)
     if status:
         raise KQError(name, status, last_error())
@@ -423,74 +423,74 @@ def mx_empty(rows: int, cols: int, device):
 
 def kq_mx_quantize(X, codes, scales, stream=None) -> None:
     """X (rows x cols, fp32 or bf16) into codes and scales of mx_empty(rows, cols)."""
-    name, dev = "kq_mx_quantize", []
+    name = "kq_mx_quantize"
     rows, cols = X.shape
-    dt, per = _float(name, "X", X)
-    p = _matrix(name, "X", X, rows, cols, X.dtype, per, False, dev)
+    dt, per, dev = _float(name, "X", X)
+    p, ld = _matrix(name, "X", X, rows, cols, X.dtype, per, False, dev)
     if codes.shape[0] != rows:
         raise ValueError(f"{name}: {codes.shape[0]} rows of codes for {rows} rows")
-    _launch(name, lib().kq_mx_quantize, dev, False, stream, p[0], dt, rows, cols, p[1],
-            *_mx(name, "the output", codes, scales, cols, dev))
+    _launch(name, lib().kq_mx_quantize, dev, stream, (p, dt, rows, cols, ld, *_mx(name, "the output", codes, scales, cols, dev)))
 
 
 def kq_mx_dequantize(codes, scales, Y, stream=None) -> None:
     """The values that codes and scales stand for, into Y (rows x cols, fp32 or bf16)."""
-    name, dev = "kq_mx_dequantize", []
+    name = "kq_mx_dequantize"
     rows, cols = Y.shape
-    dt, per = _float(name, "Y", Y)
-    p = _matrix(name, "Y", Y, rows, cols, Y.dtype, per, False, dev)
+    dt, per, dev = _float(name, "Y", Y)
+    p, ld = _matrix(name, "Y", Y, rows, cols, Y.dtype, per, False, dev)
     if codes.shape[0] != rows:
         raise ValueError(f"{name}: {codes.shape[0]} rows of codes for {rows} rows")
-    _launch(name, lib().kq_mx_dequantize, dev, False, stream, *_mx(name, "the input", codes, scales, cols, dev), rows, cols,
-            p[0], dt, p[1])
+    _launch(name, lib().kq_mx_dequantize, dev, stream,
+            (*_mx(name, "the input", codes, scales, cols, dev), rows, cols, p, dt, ld))
 
 
 def kq_mx_gemm(Ac, As, Bc, Bs, i: int, Y, ws=None, stream=None) -> None:
     """Y (n x o, fp32 or bf16) = A B^T for microscaled A (n x i) and B (o x i)."""
-    name, dev = "kq_mx_gemm", []
+    name = "kq_mx_gemm"
     n, o = Ac.shape[0], Bc.shape[0]
-    dt, per = _float(name, "Y", Y)
-    p = _matrix(name, "Y", Y, n, o, Y.dtype, per, False, dev)
-    _launch(name, lib().kq_mx_gemm, dev, ws, stream, *_mx(name, "A", Ac, As, i, dev), *_mx(name, "B", Bc, Bs, i, dev), n, o,
-            i, p[0], dt, p[1])
+    dt, per, dev = _float(name, "Y", Y)
+    p, ld = _matrix(name, "Y", Y, n, o, Y.dtype, per, False, dev)
+    _launch(name, lib().kq_mx_gemm, dev, stream,
+            (*_mx(name, "A", Ac, As, i, dev), *_mx(name, "B", Bc, Bs, i, dev), n, o, i, p, dt, ld,
+             *_workspace(name, ws, dev)))
 
 
 def kq_mx_gated(Xc, Xs, Gc, Gs, Uc, Us, i: int, act: str, H, ws=None, stream=None) -> None:
     """H (n x o, fp32 or bf16) = act(X G^T) * (X U^T) for microscaled X (n x i), G and U (o x i)."""
-    name, dev = "kq_mx_gated", []
+    name = "kq_mx_gated"
     n, o = Xc.shape[0], Gc.shape[0]
     if Uc.shape[0] != o:
         raise ValueError(f"{name}: {o} gate rows and {Uc.shape[0]} up rows")
-    dt, per = _float(name, "H", H)
-    p = _matrix(name, "H", H, n, o, H.dtype, per, False, dev)
-    _launch(name, lib().kq_mx_gated, dev, ws, stream, *_mx(name, "X", Xc, Xs, i, dev),
-            *_mx(name, "gate weights", Gc, Gs, i, dev), *_mx(name, "up weights", Uc, Us, i, dev), n, o, i, _act(name, act),
-            p[0], dt, p[1])
+    dt, per, dev = _float(name, "H", H)
+    p, ld = _matrix(name, "H", H, n, o, H.dtype, per, False, dev)
+    _launch(name, lib().kq_mx_gated, dev, stream,
+            (*_mx(name, "X", Xc, Xs, i, dev), *_mx(name, "gate weights", Gc, Gs, i, dev),
+             *_mx(name, "up weights", Uc, Us, i, dev), n, o, i, _act(name, act), p, dt, ld, *_workspace(name, ws, dev)))
 
 
 def kq_gated_forward(X, Wg, Wu, act: str, H, A=None, B=None, ws=None, stream=None) -> None:
     """H = act(X Wg^T) * (X Wu^T); A and B, where given, take the two products. One type for all."""
-    name, dev = "kq_gated_forward", []
+    name = "kq_gated_forward"
     (n, i), o, t = X.shape, Wg.shape[0], X.dtype
-    dt, per = _float(name, "X", X)
-    args = (*_matrix(name, "X", X, n, i, t, per, True, dev), *_matrix(name, "Wg", Wg, o, i, t, per, True, dev),
-            *_matrix(name, "Wu", Wu, o, i, t, per, True, dev), dt, n, o, i, _act(name, act),
-            *_matrix(name, "H", H, n, o, t, per, False, dev),
-            *((None, 0) if A is None else _matrix(name, "A", A, n, o, t, per, False, dev)),
-            *((None, 0) if B is None else _matrix(name, "B", B, n, o, t, per, False, dev)))
-    _launch(name, lib().kq_gated_forward, dev, ws, stream, *args)
+    dt, per, dev = _float(name, "X", X)
+    _launch(name, lib().kq_gated_forward, dev, stream,
+            (*_matrix(name, "X", X, n, i, t, per, True, dev), *_matrix(name, "Wg", Wg, o, i, t, per, True, dev),
+             *_matrix(name, "Wu", Wu, o, i, t, per, True, dev), dt, n, o, i, _act(name, act),
+             *_matrix(name, "H", H, n, o, t, per, False, dev),
+             *((None, 0) if A is None else _matrix(name, "A", A, n, o, t, per, False, dev)),
+             *((None, 0) if B is None else _matrix(name, "B", B, n, o, t, per, False, dev)), *_workspace(name, ws, dev)))
 
 
 def kq_gated_backward(dH, A, B, X, Wg, Wu, act: str, dA, dB, dX=None, dWg=None, dWu=None, ws=None, stream=None) -> None:
     """Gradients of kq_gated_forward from dH and the A and B that it kept: dA and dB always, dX, dWg and
     dWu where given (X may be None without weight gradients, Wg and Wu without dX)."""
-    name, dev = "kq_gated_backward", []
+    name = "kq_gated_backward"
     (n, o), t = dH.shape, dH.dtype
-    dt, per = _float(name, "dH", dH)
     if dX is not None and (Wg is None or Wu is None):
         raise ValueError(f"{name}: dX needs Wg and Wu")
     if (dWg is not None or dWu is not None) and X is None:
         raise ValueError(f"{name}: weight gradients need X")
+    dt, per, dev = _float(name, "dH", dH)
     some = next((m for m in (dX, dWg, dWu, X, Wg, Wu) if m is not None), None)
     i = 1 if some is None else some.shape[1]
 
@@ -498,8 +498,8 @@ def kq_gated_backward(dH, A, B, X, Wg, Wu, act: str, dA, dB, dX=None, dWg=None, 
         return (None, 0) if m is None else _matrix(name, what, m, rows, cols, t, per, whole, dev)
 
     # dA and dB are also operands, of the products that follow
-    args = (*take("dH", dH, n, o, False), *take("A", A, n, o, False), *take("B", B, n, o, False), *take("X", X, n, i, True),
-            *take("Wg", Wg, o, i, True), *take("Wu", Wu, o, i, True), dt, n, o, i, _act(name, act),
-            *take("dA", dA, n, o, True), *take("dB", dB, n, o, True), *take("dX", dX, n, i, False),
-            *take("dWg", dWg, o, i, False), *take("dWu", dWu, o, i, False))
-    _launch(name, lib().kq_gated_backward, dev, ws, stream, *args)
+    _launch(name, lib().kq_gated_backward, dev, stream,
+            (*take("dH", dH, n, o, False), *take("A", A, n, o, False), *take("B", B, n, o, False),
+             *take("X", X, n, i, True), *take("Wg", Wg, o, i, True), *take("Wu", Wu, o, i, True), dt, n, o, i, _act(name, act),
+             *take("dA", dA, n, o, True), *take("dB", dB, n, o, True), *take("dX", dX, n, i, False),
+             *take("dWg", dWg, o, i, False), *take("dWu", dWu, o, i, False), *_workspace(name, ws, dev)))

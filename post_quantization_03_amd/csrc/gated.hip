@@ -119,9 +119,9 @@ static kq_status gated_forward(const char* who, const void* X, int64_t ldx, cons
     g.B2 = bytes_of(Wu); g.ldb2 = ldu * es;
     g.Y = H; g.ldy = ldh; g.Y2 = A; g.ldy2 = lda; g.Y3 = B; g.ldy3 = ldb;
     g.dt = dt; g.act = act;
-    Arena ar(ws, ws_bytes);
-    const size_t np = tile_plan<E, TP_GATED>(n, o, i).part;
-    return tile_launch<E, TP_GATED>(g, 1, np ? ar.take<float>(np) : nullptr, st, who);
+    const TilePlan plan = tile_plan<E, TP_GATED>(n, o, i);
+    if (plan.part) KQ_TRY(ws_check(who, ws, ws_bytes, sizeof(float) * plan.part));
+    return tile_launch<E, TP_GATED>(g, plan, 1, static_cast<float*>(ws), st, who);
 }
 
 }  // namespace kq
@@ -134,12 +134,21 @@ size_t gated_forward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
     return sizeof(float) * (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GATED>(n, o, i) : tile_plan<EL_F32, TP_GATED>(n, o, i)).part;
 }
 
-// The products run one after another on the caller's stream and share the split sums' memory.
+struct GradPlans {
+    TilePlan w, x;
+    size_t bytes;        // the products run one after another on the caller's stream and share the split sums' memory
+};
+static GradPlans grad_plans(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
+    GradPlans p;
+    p.w = dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_W>(o, i, n) : tile_plan<EL_F32, TP_GRAD_W>(o, i, n);
+    p.x = dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_X>(n, i, o) : tile_plan<EL_F32, TP_GRAD_X>(n, i, o);
+    p.bytes = sizeof(float) * (p.x.part > p.w.part ? p.x.part : p.w.part);
+    return p;
+}
+
 size_t gated_backward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
     if (n <= 0 || o <= 0 || i <= 0 || !tile_sizes_ok(n, i) || !tile_sizes_ok(o, i)) return 0;
-    const size_t w = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_W>(o, i, n) : tile_plan<EL_F32, TP_GRAD_W>(o, i, n)).part;
-    const size_t x = (dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_X>(n, i, o) : tile_plan<EL_F32, TP_GRAD_X>(n, i, o)).part;
-    return sizeof(float) * (x > w ? x : w);
+    return grad_plans(o, i, n, dt).bytes;
 }
 
 extern "C" kq_status kq_gated_forward(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu,
@@ -158,7 +167,6 @@ extern "C" kq_status kq_gated_forward(const void* X, int64_t ldx, const void* Wg
     KQ_TRY(dense_check(who, dt, Dense{H, ldh, "H"}, n, o));
     if (A) KQ_TRY(dense_check(who, dt, Dense{A, lda, "A"}, n, o));
     if (B) KQ_TRY(dense_check(who, dt, Dense{B, ldb, "B"}, n, o));
-    if (const size_t need = gated_forward_ws(o, i, n, dt)) KQ_TRY(ws_check(who, ws, ws_bytes, need));
     if (dt == KQ_BF16)
         return gated_forward<EL_BF16>(who, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, ws, ws_bytes,
                                       hs(stream));
@@ -204,8 +212,11 @@ extern "C" kq_status kq_gated_backward(const void* dH, int64_t lddh, const void*
         KQ_TRY(dense_check(who, dt, Dense{Wu, ldu, "Wu"}, o, i));
     }
     if (dWg || dWu) KQ_TRY(dense_check(who, dt, Dense{X, ldx, "X"}, n, i));
-    if (dX || dWg || dWu)
-        if (const size_t need = gated_backward_ws(o, i, n, dt)) KQ_TRY(ws_check(who, ws, ws_bytes, need));
+    GradPlans plans{};
+    if (dX || dWg || dWu) {
+        plans = grad_plans(o, i, n, dt);
+        if (plans.bytes) KQ_TRY(ws_check(who, ws, ws_bytes, plans.bytes));
+    }
     float* part = static_cast<float*>(ws);
     {
         const int64_t total = n * ((o + 16 / es - 1) / (16 / es));
@@ -224,8 +235,8 @@ extern "C" kq_status kq_gated_backward(const void* dH, int64_t lddh, const void*
         g.A = bytes_of(dA); g.lda = ldda * es; g.B = bytes_of(Wg); g.ldb = ldg * es;
         g.A2 = bytes_of(dB); g.lda2 = lddb * es; g.B2 = bytes_of(Wu); g.ldb2 = ldu * es;
         g.Y = dX; g.ldy = lddx; g.dt = dt;
-        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_X>(g, 1, part, st, who)));
-        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_X>(g, 1, part, st, who)));
+        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_X>(g, plans.x, 1, part, st, who)));
+        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_X>(g, plans.x, 1, part, st, who)));
     }
     if (dWg || dWu) {
         TileArgs g{};
@@ -235,8 +246,8 @@ extern "C" kq_status kq_gated_backward(const void* dH, int64_t lddh, const void*
         g.B = bytes_of(X); g.ldb = ldx * es;
         g.Y = dWg ? dWg : dWu; g.ldy = dWg ? lddg : lddu; g.Y2 = dWu; g.ldy2 = lddu; g.dt = dt;
         const int pairs = dWg && dWu ? 2 : 1;
-        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_W>(g, pairs, part, st, who)));
-        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_W>(g, pairs, part, st, who)));
+        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_W>(g, plans.w, pairs, part, st, who)));
+        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_W>(g, plans.w, pairs, part, st, who)));
     }
     return KQ_OK;
 }

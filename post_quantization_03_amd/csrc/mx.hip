@@ -246,7 +246,7 @@ static kq_status mx_product(const char* who, const MxOperand& A, const MxOperand
         else hipLaunchKernelGGL((mx_layout_kernel<false>), grid, dim3(256), 0, st, a, b, nblk, (int)g.ksteps);
         KQ_TRY(check_launch(who));
     }
-    return U ? tile_launch<EL_MX, TP_GATED>(g, 1, part, st, who) : tile_launch<EL_MX, TP_PLAIN>(g, 1, part, st, who);
+    return U ? tile_launch<EL_MX, TP_GATED>(g, plan, 1, part, st, who) : tile_launch<EL_MX, TP_PLAIN>(g, plan, 1, part, st, who);
 }
 
 }  // namespace kq

@@ -836,10 +836,9 @@ kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const
     return KQ_OK;
 }
 
-// part: workspace of tile_plan(...).part floats
+// p: tile_plan<E, MODE>(M, N, K); part: workspace of p.part floats
 template <int E, int MODE>
-kq_status tile_launch(TileArgs g, int pairs, float* part, hipStream_t st, const char* who) {
-    const TilePlan p = tile_plan<E, MODE>(g.M, g.N, g.K);
+kq_status tile_launch(TileArgs g, const TilePlan& p, int pairs, float* part, hipStream_t st, const char* who) {
     g.pairs = pairs;
     g.part = part;
     if (p.part && !part) return fail(KQ_EWORKSPACE, "%s: workspace too small", who);

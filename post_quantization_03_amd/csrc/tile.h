@@ -314,7 +314,7 @@ __device__ __forceinline__ void landed_barrier() {
 // them: at 8192 tokens of 4096 x 11008 weights (MI355X) the bf16 gated block takes 1110 us (1.33 PFLOP/s; matrix cores
 // busy 66 % of the time at 1.7 GHz; a loop of bf16 matrix instructions alone reaches 1.43 PFLOP/s), dX 1045 us
 // (1.42 PFLOP/s), both weight gradients 1150 us (1.29 PFLOP/s), the 4-bit product 157 us (4.7 PFLOP/s, 60 % busy at
-// 1.9 GHz), the 4-bit gated block 350 us (4.2 PFLOP/s; its activations take as long as two slabs of a tile's 16).
+// 1.9 GHz), the 4-bit gated block 350 us (4.2 PFLOP/s, 53 %: its tiles have 16 slabs between their first loads and their activations).
 // No LDS bank conflicts in any of them. A work-group that walks over its tiles and loads the next one's first slab
 // before the epilogue changed none of these by more than 2 %.
 template <int E, int MODE, typename C>
@@ -965,8 +965,7 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
     for (int m = 0; m < MATS; m++)
 #pragma unroll
         for (int b = 0; b < NB; b++) acc[m][b] = tl_f4{0, 0, 0, 0};
-    // U slabs at a time: all their loads are in flight before the first product (dense types at two: no faster, and
-    // 64 values more in registers)
+    // U slabs at a time: all their loads are in flight before the first product (dense types with two are slower)
     auto batch = [&](int64_t s, auto UC, bool whole) {
         constexpr int U = UC.value;
         FewFrag<E> w[U][MATS], a[U][NB];

@@ -312,9 +312,9 @@ __device__ __forceinline__ void landed_barrier() {
 
 // One tile, or one split of it. Large products are bound by the matrix cores at the clock that the card's power allows
 // them: at 8192 tokens of 4096 x 11008 weights (MI355X) the bf16 gated block takes 1110 us (1.33 PFLOP/s; matrix cores
-// busy 66 % of the time at 1.7 GHz; a loop of bf16 matrix instructions alone reaches 1.43 PFLOP/s), dX 1045 us
+// busy 66 % of the time at 1.7 GHz; a loop of bf16 matrix instructions alone reaches 1.6 PFLOP/s), dX 1045 us
 // (1.42 PFLOP/s), both weight gradients 1150 us (1.29 PFLOP/s), the 4-bit product 157 us (4.7 PFLOP/s, 60 % busy at
-// 1.9 GHz), the 4-bit gated block 350 us (4.2 PFLOP/s, 53 %: its tiles have 16 slabs between their first loads and their activations).
+// 1.9 GHz; the instructions alone 6.5), the 4-bit gated block 350 us (4.2 PFLOP/s, 53 %: its tiles have 16 slabs between their first loads and their activations).
 // No LDS bank conflicts in any of them. A work-group that walks over its tiles and loads the next one's first slab
 // before the epilogue changed none of these by more than 2 %.
 template <int E, int MODE, typename C>

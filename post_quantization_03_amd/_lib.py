@@ -307,7 +307,8 @@ def _torch() -> list:
     if not _TORCH:
         import torch
         raw, cur = (getattr(torch._C, k, None) for k in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
-        _TORCH.extend((torch.uint8, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), cur or torch.cuda.current_device))
+        # in one piece: two threads may come here at once
+        _TORCH[:] = (torch.uint8, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), cur or torch.cuda.current_device)
         _FLOATS.update({torch.float32: (KQ_F32, 4), torch.bfloat16: (KQ_BF16, 8)})
     return _TORCH
 

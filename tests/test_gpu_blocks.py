@@ -739,6 +739,7 @@ def test_calibrate_quantise_and_serve():
             assert np.array_equal(host(alone[name]), host(out[k][name])), (k, name)
 
     block = ffn.MXFeedForward(Wg, Wu, Wd, "silu")
+    assert block(X[:0]).shape == (0, m)
     for rows in (n, 1, 3):
         y = get(block(X[:rows]))
         xq = ob.mx_values(*ob.mx_quantize(x[:rows]), i)

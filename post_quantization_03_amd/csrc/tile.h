@@ -738,11 +738,15 @@ __global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g) {
     if (m >= g.M || n >= g.N) return;
     const float* p = g.part + (int64_t)at.cut * g.splits * (C::TM * C::TN) + r * C::TN + c;
     auto sum = [&](const float* q, float (&v)[4]) {
-        float4 s = *reinterpret_cast<const float4*>(q);
-        for (int k = 1; k < g.splits; k++) {
-            const float4 t = *reinterpret_cast<const float4*>(q + (int64_t)k * (C::TM * C::TN));
-            s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+        auto load = [&](int k) { return *reinterpret_cast<const float4*>(q + (int64_t)k * (C::TM * C::TN)); };
+        float4 s = load(0);
+        auto add = [&](const float4& t) { s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w; };
+        int k = 1;
+        for (; k + 4 <= g.splits; k += 4) {      // four loads in flight, added in order
+            const float4 t0 = load(k), t1 = load(k + 1), t2 = load(k + 2), t3 = load(k + 3);
+            add(t0); add(t1); add(t2); add(t3);
         }
+        for (; k < g.splits; k++) add(load(k));
         v[0] = s.x; v[1] = s.y; v[2] = s.z; v[3] = s.w;
     };
     float a[4];
@@ -799,7 +803,7 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
             if (tail && (whole == 0 || cut == 0)) continue;
             for (int c = tail; c < 8; c++) {
                 const int64_t sper = (slabs + cuts[c] - 1) / cuts[c], splits = (slabs + sper - 1) / sper;
-                if (splits != cuts[c]) continue;
+                if (c && splits <= cuts[c - 1]) continue;        // another choice has these, or nearly
                 const size_t part = splits > 1 ? (size_t)(cut * splits * size[h] * size[h]) : 0;
                 double t = (whole ? time(whole, slabs) : 0.0) + time(cut * splits, sper);
                 if (part) t += 4.0 + 8.0 * (double)part / 3.5e6;

@@ -138,13 +138,13 @@ size_t gated_forward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
 
 struct GradPlans {
     TilePlan w, x;
-    size_t bytes;        // the products run one after another on the caller's stream and share the split sums' memory
+    size_t bytes;        // of split sums: shared by products that run one after another on the caller's stream
 };
 static GradPlans grad_plans(int64_t o, int64_t i, int64_t n, kq_dtype dt) {
     GradPlans p;
     p.w = dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_W>(o, i, n) : tile_plan<EL_F32, TP_GRAD_W>(o, i, n);
     p.x = dt == KQ_BF16 ? tile_plan<EL_BF16, TP_GRAD_X>(n, i, o) : tile_plan<EL_F32, TP_GRAD_X>(n, i, o);
-    p.bytes = sizeof(float) * (p.x.part > p.w.part ? p.x.part : p.w.part);
+    p.bytes = sizeof(float) * (grads_together(p.x, p.w) ? p.x.part + p.w.part : p.x.part > p.w.part ? p.x.part : p.w.part);
     return p;
 }
 
@@ -231,25 +231,30 @@ extern "C" kq_status kq_gated_backward(const void* dH, int64_t lddh, const void*
                                dA, ldda, dB, lddb);
         KQ_TRY(check_launch(who));
     }
+    TileArgs x{}, w{};
+    x.M = n; x.N = i; x.K = o;
+    x.A = bytes_of(dA); x.lda = ldda * es; x.B = bytes_of(Wg); x.ldb = ldg * es;
+    x.A2 = bytes_of(dB); x.lda2 = lddb * es; x.B2 = bytes_of(Wu); x.ldb2 = ldu * es;
+    x.Y = dX; x.ldy = lddx; x.dt = dt;
+    w.M = o; w.N = i; w.K = n;
+    w.A = bytes_of(dWg ? dA : dB); w.lda = (dWg ? ldda : lddb) * es;
+    w.A2 = bytes_of(dB); w.lda2 = lddb * es;
+    w.B = bytes_of(X); w.ldb = ldx * es;
+    w.Y = dWg ? dWg : dWu; w.ldy = dWg ? lddg : lddu; w.Y2 = dWu; w.ldy2 = lddu; w.dt = dt;
+    const int pairs = dWg && dWu ? 2 : 1;
+    if (dX && (dWg || dWu) && grads_together(plans.x, plans.w)) {
+        x.pairs = 1; x.part = part;
+        w.pairs = pairs; w.part = part + plans.x.part;
+        return dt == KQ_BF16 ? tile_launch_grads<EL_BF16>(x, plans.x, w, plans.w, st, who)
+                             : tile_launch_grads<EL_F32>(x, plans.x, w, plans.w, st, who);
+    }
     if (dX) {
-        TileArgs g{};
-        g.M = n; g.N = i; g.K = o;
-        g.A = bytes_of(dA); g.lda = ldda * es; g.B = bytes_of(Wg); g.ldb = ldg * es;
-        g.A2 = bytes_of(dB); g.lda2 = lddb * es; g.B2 = bytes_of(Wu); g.ldb2 = ldu * es;
-        g.Y = dX; g.ldy = lddx; g.dt = dt;
-        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_X>(g, plans.x, 1, part, st, who)));
-        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_X>(g, plans.x, 1, part, st, who)));
+        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_X>(x, plans.x, 1, part, st, who)));
+        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_X>(x, plans.x, 1, part, st, who)));
     }
     if (dWg || dWu) {
-        TileArgs g{};
-        g.M = o; g.N = i; g.K = n;
-        g.A = bytes_of(dWg ? dA : dB); g.lda = (dWg ? ldda : lddb) * es;
-        g.A2 = bytes_of(dB); g.lda2 = lddb * es;
-        g.B = bytes_of(X); g.ldb = ldx * es;
-        g.Y = dWg ? dWg : dWu; g.ldy = dWg ? lddg : lddu; g.Y2 = dWu; g.ldy2 = lddu; g.dt = dt;
-        const int pairs = dWg && dWu ? 2 : 1;
-        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_W>(g, plans.w, pairs, part, st, who)));
-        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_W>(g, plans.w, pairs, part, st, who)));
+        if (dt == KQ_BF16) KQ_TRY((tile_launch<EL_BF16, TP_GRAD_W>(w, plans.w, pairs, part, st, who)));
+        else KQ_TRY((tile_launch<EL_F32, TP_GRAD_W>(w, plans.w, pairs, part, st, who)));
     }
     return KQ_OK;
 }

@@ -318,7 +318,7 @@ __device__ __forceinline__ void landed_barrier() {
 // No LDS bank conflicts in any of them. A work-group that walks over its tiles and loads the next one's first slab
 // before the epilogue changed none of these by more than 2 %.
 template <int E, int MODE, typename C>
-__global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
+__device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
     extern __shared__ __align__(16) char tl_sm[];
     constexpr bool TA = MODE == TP_GRAD_W, TB = MODE == TP_GRAD_X || MODE == TP_GRAD_W, GATED = MODE == TP_GATED;
     static_assert(!TB || E != EL_MX, "blocks of E2M1 lie along K");
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int x16 = lane & 15, g4 = lane >> 4;
     const int wm = wave / C::WN, wn = wave % C::WN, grp = wn / SUB, sub = wn % SUB;
-    const TileAt at = tile_of((int)blockIdx.x, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g);
+    const TileAt at = tile_of(id, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g);
     const int64_t m0 = (int64_t)at.tm * C::TM, n0 = (int64_t)at.tn * TN_OUT;
     const int mlast = (int)(g.M - 1 - m0 < C::TM - 1 ? g.M - 1 - m0 : C::TM - 1);          // last row inside
     const int nlast = (int)(g.N - 1 - n0 < TN_OUT - 1 ? g.N - 1 - n0 : TN_OUT - 1);
@@ -725,15 +725,29 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
     }
 }
 
+template <int E, int MODE, typename C>
+__global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
+    tile_body<E, MODE, C>(g, (int)blockIdx.x);
+}
+
+// dX and the weight gradients side by side: `first` work-groups for dX, the rest for the others. For small products, which
+// leave compute units idle, and whose launches cost as much as they do (61 tokens of 1376 x 1000 fp32: 14.4 us, one
+// after the other 9.5 and 9.1 and a launch between; the whole call 22.9 -> 19.3 us).
+template <int E, typename C>
+__global__ __launch_bounds__(C::THREADS, C::EU) void tile_grads_kernel(TileArgs x, TileArgs w, int first) {
+    if ((int)blockIdx.x < first) tile_body<E, TP_GRAD_X, C>(x, (int)blockIdx.x);
+    else tile_body<E, TP_GRAD_W, C>(w, (int)blockIdx.x - first);
+}
+
 // Sums of the splits, in split order, and the epilogue: 4 columns a thread, TM * TN_OUT / 1024 work-groups a tile.
 // HBM-bound, or latency (96 L tiles in two splits, the tail of the weight gradients at 8192 tokens: 10.6 us, 5.9 TB/s;
-// 16 S tiles in eight: 4 us). Splits are not added by atomics: their order would change the sums.
+// 16 S tiles in 15: 4 us). Splits are not added by atomics: their order would change the sums.
 template <int MODE, typename C>
-__global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g) {
+__device__ __forceinline__ void tile_reduce(const TileArgs& g, int block) {
     constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
     TileAt at;
-    cut_place(at, (int)(blockIdx.x / PER), (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g.whole);
-    const int e = (int)(blockIdx.x % PER) * 256 + threadIdx.x, r = e / (TN_OUT / 4), c = e % (TN_OUT / 4) * 4;
+    cut_place(at, block / PER, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g.whole);
+    const int e = block % PER * 256 + threadIdx.x, r = e / (TN_OUT / 4), c = e % (TN_OUT / 4) * 4;
     const int64_t m = (int64_t)at.tm * C::TM + r, n = (int64_t)at.tn * TN_OUT + c;
     if (m >= g.M || n >= g.N) return;
     const float* p = g.part + (int64_t)at.cut * g.splits * (C::TM * C::TN) + r * C::TN + c;
@@ -762,6 +776,17 @@ __global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g) {
         const bool w2 = MODE == TP_GRAD_W && at.pair;
         store_run<4>(w2 ? g.Y2 : g.Y, g.dt, m * (w2 ? g.ldy2 : g.ldy) + n, a, g.N - n);
     }
+}
+
+template <int MODE, typename C>
+__global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g) {
+    tile_reduce<MODE, C>(g, (int)blockIdx.x);
+}
+
+template <typename C>
+__global__ __launch_bounds__(256) void tile_reduce_grads_kernel(TileArgs x, TileArgs w, int first) {
+    if ((int)blockIdx.x < first) tile_reduce<TP_GRAD_X, C>(x, (int)blockIdx.x);
+    else tile_reduce<TP_GRAD_W, C>(w, (int)blockIdx.x - first);
 }
 
 // How a product is cut: tile shape (0 L, 1 M, 2 S) and the tiles whose K is split, by the estimated time of each choice.
@@ -818,17 +843,28 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
     return best;
 }
 
-template <int E, int MODE, typename C>
-kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const char* who) {
-    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
+// Work-groups of a product and of its split sums, after setting the plan's fields of g.
+struct TileGrids {
+    int64_t tiles, sums;
+};
+template <int MODE, typename C>
+kq_status tile_grids(TileGrids& n, TileArgs& g, const TilePlan& p, const char* who) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
     const int64_t tiles = ((g.M + C::TM - 1) / C::TM) * ((g.N + TN_OUT - 1) / TN_OUT);       // of a pair
-    const int64_t cut = (tiles - p.whole) * g.pairs, whole = (int64_t)p.whole * g.pairs;
-    constexpr int PER = C::TM * TN_OUT / 1024;           // work-groups of the sums of a cut tile
-    if (!grid_ok(whole + cut * p.splits, C::THREADS) || (p.splits > 1 && !grid_ok(cut * PER, 256)))
-        return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
+    const int64_t cut = (tiles - p.whole) * g.pairs;
+    n.tiles = (int64_t)p.whole * g.pairs + cut * p.splits;
+    n.sums = cut * PER;
+    if (!grid_ok(n.tiles, C::THREADS) || !grid_ok(n.sums, 256)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
     g.whole = p.whole;
     g.splits = p.splits;
     g.sper = p.sper;
+    return KQ_OK;
+}
+
+template <int E, int MODE, typename C>
+kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const char* who) {
+    TileGrids n;
+    KQ_TRY((tile_grids<MODE, C>(n, g, p, who)));
     // the allowance for dynamic LDS belongs to a device's copy of the kernel: asked for once a device
     static std::atomic<uint64_t> allowed{0};
     int dev = 0;
@@ -840,10 +876,30 @@ kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const
         if (e != hipSuccess) return fail(KQ_EHIP, "%s: %s", who, hipGetErrorString(e));
         if (dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    hipLaunchKernelGGL((tile_kernel<E, MODE, C>), dim3((unsigned)(whole + cut * g.splits)), dim3(C::THREADS), C::SMEM, st, g);
+    hipLaunchKernelGGL((tile_kernel<E, MODE, C>), dim3((unsigned)n.tiles), dim3(C::THREADS), C::SMEM, st, g);
     KQ_TRY(check_launch(who));
-    if (cut) {
-        hipLaunchKernelGGL((tile_reduce_kernel<MODE, C>), dim3((unsigned)(cut * PER)), dim3(256), 0, st, g);
+    if (n.sums) {
+        hipLaunchKernelGGL((tile_reduce_kernel<MODE, C>), dim3((unsigned)n.sums), dim3(256), 0, st, g);
+        KQ_TRY(check_launch(who));
+    }
+    return KQ_OK;
+}
+
+// Both gradient products in one launch where both are cut into S tiles.
+inline bool grads_together(const TilePlan& x, const TilePlan& w) { return x.shape == 2 && w.shape == 2; }
+template <int E>
+kq_status tile_launch_grads(TileArgs x, const TilePlan& px, TileArgs w, const TilePlan& pw, hipStream_t st, const char* who) {
+    typedef TileS C;
+    TileGrids nx, nw;
+    KQ_TRY((tile_grids<TP_GRAD_X, C>(nx, x, px, who)));
+    KQ_TRY((tile_grids<TP_GRAD_W, C>(nw, w, pw, who)));
+    if (!grid_ok(nx.tiles + nw.tiles, C::THREADS) || !grid_ok(nx.sums + nw.sums, 256))
+        return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
+    hipLaunchKernelGGL((tile_grads_kernel<E, C>), dim3((unsigned)(nx.tiles + nw.tiles)), dim3(C::THREADS), C::SMEM, st, x, w,
+                       (int)nx.tiles);
+    KQ_TRY(check_launch(who));
+    if (nx.sums + nw.sums) {
+        hipLaunchKernelGGL((tile_reduce_grads_kernel<C>), dim3((unsigned)(nx.sums + nw.sums)), dim3(256), 0, st, x, w, (int)nx.sums);
         KQ_TRY(check_launch(who));
     }
     return KQ_OK;

@@ -793,8 +793,8 @@ __global__ __launch_bounds__(256) void tile_reduce_grads_kernel(TileArgs x, Tile
 // A slab of a tile takes `lat` us by itself on a compute unit and `w` us of a busy one's matrix cores, a tile
 // `fix` more for its first loads and its epilogue; split sums are written and read once at 3.5 TB/s by a
 // second launch (4 us), and E2M1 scales laid out by one of 3 us. The constants are fitted to measurements of 8
-// products at 15 sizes each, all shapes and 1 to 16 splits (MI355X); the choice is within 2 % of the
-// fastest on average and 14 % at worst.
+// products at 15 sizes each, all shapes and 1 to 16 splits (MI355X); the choice was within 2 % of
+// the fastest on average and 14 % at worst.
 // fp32 products are bound by the matrix cores in every shape and always take the small one, which leaves
 // the fewest of them idle. Some times, us (bf16 gated block, n x o x i): 65 x 11008 x 4096 L 87, M 46, S 39; 2048 x 11008 x 4096
 // L 320, M 399, S 638; 512 x 4096 x 11008 M 122, M in two splits 93, L in four 96.

@@ -310,13 +310,16 @@ __device__ __forceinline__ void landed_barrier() {
     __syncthreads();
 }
 
-// One tile, or one split of it. Large products are bound by the matrix cores at the clock that the card's power allows
-// them: at 8192 tokens of 4096 x 11008 weights (MI355X) the bf16 gated block takes 1110 us (1.33 PFLOP/s; matrix cores
-// busy 66 % of the time at 1.7 GHz; a loop of bf16 matrix instructions alone reaches 1.6 PFLOP/s), dX 1045 us
-// (1.42 PFLOP/s), both weight gradients 1150 us (1.29 PFLOP/s), the 4-bit product 157 us (4.7 PFLOP/s, 60 % busy at
-// 1.9 GHz; the instructions alone 6.5), the 4-bit gated block 350 us (4.2 PFLOP/s, 53 %: its tiles have 16 slabs between their first loads and their activations).
-// No LDS bank conflicts in any of them. A work-group that walks over its tiles and loads the next one's first slab
-// before the epilogue changed none of these by more than 2 %.
+// One tile, or one split of it. Large products are bound by feeding the matrix cores: at 8192 tokens of 4096 x 11008
+// weights (MI355X) the bf16 gated block takes 1110 us (1.33 PFLOP/s, matrix cores busy 66 % of the time at a clock of
+// 1.7 GHz), dX 1045 us (1.42 PFLOP/s), both weight gradients 1150 us (1.29 PFLOP/s), the 4-bit product 157 us (4.7
+// PFLOP/s, 60 % busy at 1.9 GHz), the 4-bit gated block 350 us (4.2 PFLOP/s, 53 %: its tiles have 16 slabs between
+// their first loads and their activations). With their operands in registers the same instructions run at 2.1 (bf16) and
+// 7.4 PFLOP/s (E2M1), all the time busy at 2.06 GHz: the LDS reads and the loads cost clock as well as time. The
+// 32 x 32 instructions, by themselves, are slower (1.9 and 6.7 PFLOP/s). No LDS bank conflicts in any of them. A
+// work-group that walks over its tiles and loads the next one's first slab before the epilogue changed none of these by
+// more than 2 %; four wavefronts of 128 x 128 instead of eight of 128 x 64 read a third less LDS but no longer fit
+// their sums and fragments into registers (4-bit product 222 -> 276 us at the time).
 template <int E, int MODE, typename C>
 __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
     extern __shared__ __align__(16) char tl_sm[];

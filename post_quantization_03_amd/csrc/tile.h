@@ -626,8 +626,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
                     if (s == 0) fx[i] = fragA(at, INPL + i, nx);
                     else fa[INPL + i] = fragA(at, INPL + i, nx);
                 }
-#pragma unroll
-                for (int j = i * FN / FM; j < (i + 1) * FN / FM; j++) fb[nx][j] = fragB(at, j, nx);
+                if (i < FN) fb[nx][i] = fragB(at, i, nx);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }

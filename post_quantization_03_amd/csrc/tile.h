@@ -312,7 +312,7 @@ __device__ __forceinline__ void landed_barrier() {
 
 // One tile, or one split of it. Large products are bound by feeding the matrix cores: at 8192 tokens of 4096 x 11008
 // weights (MI355X) the bf16 gated block takes 1110 us (1.33 PFLOP/s, matrix cores busy 66 % of the time at a clock of
-// 1.7 GHz), dX 1045 us (1.42 PFLOP/s), both weight gradients 1150 us (1.29 PFLOP/s), the 4-bit product 157 us (4.7
+// 1.7 GHz), dX 1045 us (1.42 PFLOP/s), both weight gradients 1140 us (1.30 PFLOP/s), the 4-bit product 157 us (4.7
 // PFLOP/s, 60 % busy at 1.9 GHz), the 4-bit gated block 350 us (4.2 PFLOP/s, 53 %: its tiles have 16 slabs between
 // their first loads and their activations). With their operands in registers the same instructions run at 2.1 (bf16) and
 // 7.4 PFLOP/s (E2M1), all the time busy at 2.06 GHz: the LDS reads and the loads cost clock as well as time. The
@@ -609,7 +609,9 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
     // One step: the products of A's fragment i with all of B's, then the reads that replace what they used and
     // (LOAD) loads of the slab after the next into buffer buf, spread over the step: a burst of either holds up the
     // products (8192 tokens, loads spread instead of issued at once: bf16 gated block 1165 -> 1108 us, weight
-    // gradients 1270 -> 1145 us, 4-bit product 182 -> 167 us).
+    // gradients 1270 -> 1145 us, 4-bit product 182 -> 167 us; over half the step: 1 to 8 % slower than over all of it; two
+    // of eight put off to the next step: bf16 3 to 5 % slower, they land late). The reads end two rows of products
+    // before the step does, so that the barrier finds them done (weight gradients 1157 -> 1138 us).
     auto step = [&](int s, int at, auto READ, auto LOAD, int buf) {
         const int nx = s ^ 1;            // the step whose fragments are read (slab at `at`), unless there is none
 #pragma unroll

@@ -299,25 +299,25 @@ def kq_allocate_bits(scores, sizes, budget: float = 3.0, bmin: int = 2, bmax: in
 # These wrappers also check what the C calls cannot see: types, shapes, devices and the memory behind a
 # view (rows are read in whole 16-byte pieces). A call on few tokens runs for a few microseconds on the
 # GPU, so the checks read each tensor's attributes once and no device guard is entered on the current device.
-_FLOATS: dict = {}      # torch dtype -> (kq_dtype, elements in 16 bytes)
-_TORCH: list = []       # torch.uint8, the raw current stream of a device, the current device
+_TORCH: tuple | None = None
 
 
-def _torch() -> list:
-    if not _TORCH:
+def _torch() -> tuple:
+    """torch.uint8, the raw current stream of a device, the current device, and torch dtype -> (kq_dtype,
+    elements in 16 bytes): looked up at the first call and published whole, since two threads may come here at
+    once."""
+    global _TORCH
+    if _TORCH is None:
         import torch
         raw, cur = (getattr(torch._C, k, None) for k in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
-        # in one piece: two threads may come here at once
-        _TORCH[:] = (torch.uint8, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), cur or torch.cuda.current_device)
-        _FLOATS.update({torch.float32: (KQ_F32, 4), torch.bfloat16: (KQ_BF16, 8)})
+        _TORCH = (torch.uint8, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), cur or torch.cuda.current_device,
+                  {torch.float32: (KQ_F32, 4), torch.bfloat16: (KQ_BF16, 8)})
     return _TORCH
 
 
 def _float(name: str, what: str, t):
     """(kq_dtype, elements in 16 bytes, device) of a tensor."""
-    if not _FLOATS:
-        _torch()
-    f = _FLOATS.get(t.dtype)
+    f = (_TORCH or _torch())[3].get(t.dtype)
     if f is None:
         raise TypeError(f"{name}: {what} has type {t.dtype}")
     d = t.get_device()
@@ -355,7 +355,7 @@ def _other_device(name: str, what: str, t, dev: int) -> None:
 
 def _mx(name: str, what: str, codes, scales, cols: int, dev: int) -> tuple:
     """Checks a microscaled operand of `cols` columns; returns its four C arguments."""
-    u8 = _TORCH[0]
+    u8 = (_TORCH or _torch())[0]
     if codes.dtype is not u8 or scales.dtype is not u8:
         raise TypeError(f"{name}: {what} codes and scales have types {codes.dtype} and {scales.dtype}, not uint8")
     cs, ss = codes.shape, scales.shape
@@ -390,7 +390,7 @@ def _workspace(name: str, ws, dev: int) -> tuple:
 
 def _launch(name: str, fn, dev: int, stream, args: tuple) -> None:
     """fn(*args, stream) on device `dev`."""
-    _, raw_stream, current_device = _TORCH
+    _, raw_stream, current_device, _ = _TORCH or _torch()
     if stream is None:
         s = raw_stream(dev)
     elif stream.device.index != dev:

@@ -192,3 +192,56 @@ def test_wrappers_refuse_host_tensors_and_bad_types():
         ffn.MXFeedForward(torch.zeros(8, 4), torch.zeros(8, 5), torch.zeros(4, 8))
     with pytest.raises(ValueError, match="activation"):
         ffn.MXFeedForward(torch.zeros(8, 4), torch.zeros(8, 4), torch.zeros(4, 8), "tanh")
+
+
+def test_first_calls_of_two_threads_at_any_point():
+    """A second thread's first call at every line of the first thread's gets the same answer: a fresh copy of
+    the module, whose lazy set-up is interrupted line by line."""
+    import importlib.util
+    import sys
+    import threading
+
+    spec = importlib.util.spec_from_file_location("fresh_lib", K.__file__)
+    x = torch.zeros(4, 64)
+    answers = []
+
+    def call(mod):
+        try:
+            mod._float("first", "X", x)
+        except Exception as e:      # noqa: BLE001  the answer: this tensor is refused for its device alone
+            answers.append(f"{type(e).__name__}: {e}")
+
+    def first(mod, stop):
+        seen = 0
+
+        def trace(frame, event, arg):
+            nonlocal seen
+            if frame.f_code.co_filename != K.__file__:
+                return None
+            if event == "line":
+                if seen == stop:
+                    other = threading.Thread(target=call, args=(mod,))
+                    other.start()
+                    other.join(20)
+                    assert not other.is_alive()
+                seen += 1
+            return trace
+
+        sys.settrace(trace)
+        try:
+            call(mod)
+        finally:
+            sys.settrace(None)
+        return seen
+
+    lines, stop = 1, 0
+    while stop < lines:             # as many times as the first call has lines
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        t = threading.Thread(target=lambda: counts.append(first(mod, stop)))
+        counts: list = []
+        t.start()
+        t.join(30)
+        lines, stop = counts[0], stop + 1
+    assert lines > 5
+    assert set(answers) == {"ValueError: first: X is not on a GPU"}, set(answers)

@@ -385,6 +385,8 @@ def _workspace(name: str, ws, dev: int) -> tuple:
         return None, 0
     if ws.get_device() != dev:
         _other_device(name, "the workspace", ws, dev)
+    if not ws.is_contiguous():      # its size in bytes would not be that of the memory behind it
+        raise ValueError(f"{name}: the workspace is not contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 

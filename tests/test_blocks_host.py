@@ -245,3 +245,15 @@ def test_first_calls_of_two_threads_at_any_point():
         lines, stop = counts[0], stop + 1
     assert lines > 5
     assert set(answers) == {"ValueError: first: X is not on a GPU"}, set(answers)
+
+
+def test_workspaces_whose_bytes_are_not_in_one_piece_are_refused():
+    """A view counts values that it does not own: an expanded one (stride 0) claims bytes past its storage, a
+    strided one bytes between its values."""
+    whole = torch.empty(4096, dtype=torch.uint8)
+    assert K._workspace("w", whole, -1) == (whole.data_ptr(), 4096)
+    assert K._workspace("w", whole[256:].view(15, 256), -1) == (whole.data_ptr() + 256, 3840)
+    assert K._workspace("w", whole[:1024].view(torch.float32), -1) == (whole.data_ptr(), 1024)
+    for bad in (whole[:1].expand(4096), whole[::2], whole.view(64, 64).T, whole.view(64, 64)[:, :32]):
+        with pytest.raises(ValueError, match="contiguous"):
+            K._workspace("w", bad, -1)

@@ -33,6 +33,11 @@ def _ws(op: str, o: int, i: int, n: int, like: torch.Tensor) -> torch.Tensor:
     return torch.empty(max(K.kq_workspace_bytes(op, o, i, n, xdt), 256), dtype=torch.uint8, device=like.device)
 
 
+def _on(t: torch.Tensor, name: str):
+    """t's device as the current one: the solver's calls launch on the current device and its stream."""
+    return torch.cuda.device(K._float(name, "X", t)[2])
+
+
 def _covariance(G: torch.Tensor, cfg: LayerCfg) -> torch.Tensor:
     """H_G = G^T G / n of gradient rows G (n x o) in cfg's storage form."""
     n, o = G.shape
@@ -54,11 +59,12 @@ def calibrate_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, dH: tor
     if n == 0:
         raise ValueError("calibrate_gated: no tokens, no statistics")
     o = Wg.shape[0]
-    H, A, B = _rows(n, o, X), _rows(n, o, X), _rows(n, o, X)
-    K.kq_gated_forward(X, Wg, Wu, act, H, A, B, _ws("gated_forward", o, i, n, X))
-    dA, dB, dX = _rows(n, o, X), _rows(n, o, X), _rows(n, i, X)
-    K.kq_gated_backward(dH, A, B, X, Wg, Wu, act, dA, dB, dX, ws=_ws("gated_backward", o, i, n, X))
-    return {"H": H, "dA": dA, "dB": dB, "dX": dX, "HG_gate": _covariance(dA, cfg), "HG_up": _covariance(dB, cfg)}
+    with _on(X, "calibrate_gated"):
+        H, A, B = _rows(n, o, X), _rows(n, o, X), _rows(n, o, X)
+        K.kq_gated_forward(X, Wg, Wu, act, H, A, B, _ws("gated_forward", o, i, n, X))
+        dA, dB, dX = _rows(n, o, X), _rows(n, o, X), _rows(n, i, X)
+        K.kq_gated_backward(dH, A, B, X, Wg, Wu, act, dA, dB, dX, ws=_ws("gated_backward", o, i, n, X))
+        return {"H": H, "dA": dA, "dB": dB, "dX": dX, "HG_gate": _covariance(dA, cfg), "HG_up": _covariance(dB, cfg)}
 
 
 def quantize_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, dH: torch.Tensor, act: str, s: torch.Tensor,
@@ -66,8 +72,9 @@ def quantize_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, dH: torc
     """Calibrates the block and quantises its gate and up projections with the per-layer solver:
     {"gate": ..., "up": ...} as quantize_layer returns them, and calibrate_gated's result."""
     cal = calibrate_gated(X, Wg, Wu, dH, act, cfg)
-    return {"gate": quantize_layer(X, Wg, cal["HG_gate"], s, t_gate, cfg, verify=verify),
-            "up": quantize_layer(X, Wu, cal["HG_up"], s, t_up, cfg, verify=verify), "calibration": cal}
+    with _on(X, "quantize_gated"):
+        return {"gate": quantize_layer(X, Wg, cal["HG_gate"], s, t_gate, cfg, verify=verify),
+                "up": quantize_layer(X, Wu, cal["HG_up"], s, t_up, cfg, verify=verify), "calibration": cal}
 
 
 def mx_quantize(X: torch.Tensor) -> tuple:

@@ -257,3 +257,45 @@ def test_workspaces_whose_bytes_are_not_in_one_piece_are_refused():
     for bad in (whole[:1].expand(4096), whole[::2], whole.view(64, 64).T, whole.view(64, 64)[:, :32]):
         with pytest.raises(ValueError, match="contiguous"):
             K._workspace("w", bad, -1)
+
+
+def test_calibration_runs_on_its_tensors_device(monkeypatch):
+    """Tensors on a device other than the current one: every call of the calibration, those of the older entry points
+    among them (which launch on the current device), runs with the tensors' device current."""
+    import contextlib
+
+    from post_quantization_03_amd.layer import LayerCfg
+
+    class OnOne(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    current, calls = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(d if isinstance(d, int) else 1)
+        yield
+        current.pop()
+
+    def record(name):
+        def call(*args, **kw):
+            calls.append((name, current[-1]))
+            return {}
+        return call
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for name in ("kq_gated_forward", "kq_gated_backward", "kq_hessian_accum", "kq_hg_extract"):
+        monkeypatch.setattr(K, name, record(name))
+    monkeypatch.setattr(ffn, "quantize_layer", record("quantize_layer"))
+    x, w, dh = (torch.zeros(*s).as_subclass(OnOne) for s in ((4, 64), (8, 64), (4, 8)))
+    cfg = LayerCfg(bits=4, group=64, form="diag")
+    ffn.calibrate_gated(x, w, w, dh, "silu", cfg)
+    names = ["kq_gated_forward", "kq_gated_backward"] + 2 * ["kq_hessian_accum", "kq_hg_extract"]
+    assert calls == [(n, 1) for n in names]
+    calls.clear()
+    ffn.quantize_gated(x, w, w, dh, "silu", None, None, None, cfg)
+    assert calls == [(n, 1) for n in names + 2 * ["quantize_layer"]]
+    assert current == [0]
+    with pytest.raises(ValueError, match="not on a GPU"):
+        ffn.calibrate_gated(torch.zeros(4, 64), w, w, dh, "silu", cfg)

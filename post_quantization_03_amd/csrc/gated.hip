@@ -9,8 +9,12 @@
 // bf16 operands run on the bf16 matrix cores with fp32 sums; A and B are rounded to bf16 only where the
 // caller keeps them, H is computed from the unrounded sums. dA and dB are rounded to the operands' type
 // once, as outputs and as the operands of the three gradient products: bf16 matrix cores take bf16
-// operands, and the rounding (2^-8 relative at most, independent from element to element) enters a sum of many
-// products below the rounding of the result. fp32 operands run on the fp32 matrix cores throughout.
+// operands, and a second product with what the rounding leaves would double the matrix work. The roundings (2^-8
+// relative at most, independent from element to element) add up to an error of the size of the result's own
+// rounding, not below it: at 8192 tokens of 11008 x 4096 weights dX, dWg and dWu are 0.0024 relative (norm of the
+// difference over the norm) off the products of unrounded dA and dB, of which rounding the results alone makes
+// 0.0017; elements whose terms cancel are off by more of themselves. fp32 operands run on the fp32 matrix cores throughout
+// and are not rounded.
 #include "tile.h"
 
 namespace kq {

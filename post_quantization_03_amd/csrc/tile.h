@@ -315,11 +315,17 @@ __device__ __forceinline__ void landed_barrier() {
 // 1.7 GHz), dX 1045 us (1.42 PFLOP/s), both weight gradients 1140 us (1.30 PFLOP/s), the 4-bit product 157 us (4.7
 // PFLOP/s, 60 % busy at 1.9 GHz), the 4-bit gated block 350 us (4.2 PFLOP/s, 53 %: its tiles have 16 slabs between
 // their first loads and their activations). With their operands in registers the same instructions run at 2.1 (bf16) and
-// 7.4 PFLOP/s (E2M1), all the time busy at 2.06 GHz: the LDS reads and the loads cost clock as well as time. The
+// 7.4 PFLOP/s (E2M1), all the time busy at 2.06 GHz: the LDS reads and the loads cost clock as well as time. A slab of
+// shape L moves 256 KiB through LDS (8 wavefronts read 24 KiB each, the loads write 64), 2048 clocks at 128 bytes a
+// clock, as many as its matrix instructions take (64 a wavefront, two wavefronts a SIMD, 16 clocks each): the LDS port
+// is as full as the matrix cores. The
 // 32 x 32 instructions, by themselves, are slower (1.9 and 6.7 PFLOP/s). No LDS bank conflicts in any of them. A
 // work-group that walks over its tiles and loads the next one's first slab before the epilogue changed none of these by
 // more than 2 %; four wavefronts of 128 x 128 instead of eight of 128 x 64 read a third less LDS but no longer fit
-// their sums and fragments into registers (4-bit product 222 -> 276 us at the time).
+// their sums and fragments into registers (4-bit product 222 -> 276 us at the time). Grids of about one work-group a
+// compute unit are bound by the latency of a slab instead: at 1024 tokens of 4096 x 11008 4-bit weights 256 work-groups of
+// shape M walk 43 slabs each in 34 us, 0.79 us a slab whose matrix instructions take 0.25 (32 a wavefront, one wavefront a SIMD),
+// since one slab's products are all that covers the next but one's loads.
 template <int E, int MODE, typename C>
 __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
     extern __shared__ __align__(16) char tl_sm[];
@@ -797,8 +803,9 @@ __global__ __launch_bounds__(256) void tile_reduce_grads_kernel(TileArgs x, Tile
 // A slab of a tile takes `lat` us by itself on a compute unit and `w` us of a busy one's matrix cores, a tile
 // `fix` more for its first loads and its epilogue; split sums are written and read once at 3.5 TB/s by a
 // second launch (4 us), and E2M1 scales laid out by one of 3 us. The constants are fitted to measurements of 8
-// products at 15 sizes each, all shapes and 1 to 16 splits (MI355X); the choice was within 2 % of
-// the fastest on average and 14 % at worst.
+// products at 15 sizes each, all shapes and 1 to 16 splits (MI355X); when they were, the choice was within 2 % of
+// the fastest on average and 14 % at worst. They rank choices and do not foretell times: fp32's w of 0.2 is less than half of
+// the 0.44 us that its matrix cores take for a slab of a tile.
 // fp32 products are bound by the matrix cores in every shape and always take the small one, which leaves
 // the fewest of them idle. Some times, us (bf16 gated block, n x o x i): 65 x 11008 x 4096 L 87, M 46, S 39; 2048 x 11008 x 4096
 // L 320, M 399, S 638; 512 x 4096 x 11008 M 122, M in two splits 93, L in four 96.
@@ -927,9 +934,12 @@ kq_status tile_launch(TileArgs g, const TilePlan& p, int pairs, float* part, hip
 // and that stream is what bounds the call. A work-group owns 16 rows of B (and of B2); its 8 wavefronts take
 // the 128-byte slabs of K in turn and their sums meet in LDS, in wavefront order. The rows of A (tokens)
 // are few and come from L2. All work-groups of the usual widths are resident at once, and a wavefront has all its loads
-// of one or two slabs in flight, so what is left above the stream is one launch and one latency. MI355X: 4096 x
-// 11008 E2M1, one token 6.4 us (3.7 TB/s); gated 11008 x 4096 E2M1, four tokens 12.8 us (3.7 TB/s); gated bf16, one
-// token 38.9 us (4.6 TB/s).
+// of one or two slabs in flight, so what is left above the stream is one launch and one latency. MI355X, the kernel
+// alone, on weights that the last-level cache holds from call to call and (second) on weights rotated past it: 4096 x 11008
+// E2M1, one token 6.0 and 8.5 us (4.0 and 2.8 TB/s); gated 11008 x 4096 E2M1, four tokens 13.0 and 15.7 us (3.7
+// and 3.1 TB/s); gated bf16, one token 31.4 and 38.1 us (5.7 and 4.7 TB/s, the latter the rate of a copy of 4 GiB). From 9
+// tokens on the rows of A cost as well: every work-group reads all of them for its 16 rows of B, at 32 tokens twice the
+// bytes of its weights, from L2 (4096 x 11008 E2M1: 7.8 us at 16 tokens, 10.7 at 32).
 struct FewArgs {
     int64_t n, o, K;                      // tokens, rows of B, values of K
     const char *A, *B, *B2;

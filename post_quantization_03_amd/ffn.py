@@ -11,7 +11,11 @@ from the gradient at H gives the output gradients of gate and up, whose covarian
 quantize_gated then runs the per-layer solver on gate and up with these statistics.
 
 Serving in microscaled 4-bit floating point (MXFeedForward): weights quantised once, tokens and
-activations quantised per call; kq_mx_gated and kq_mx_gemm do the products.
+activations quantised per call, all to the nearest code (the solver's results are integer codes and do not
+enter here); kq_mx_gated and kq_mx_gemm do the products.
+
+Matrices are passed on as they are, so the rows of X, dH and the weights start on 16 bytes: a contiguous matrix
+of another width is refused (KQError) and has to be copied into padded rows first.
 Torch only allocates device memory and supplies the stream.
 """
 from __future__ import annotations

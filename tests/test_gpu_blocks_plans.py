@@ -87,17 +87,18 @@ def mx_exact(rows, cols, low, spread, g):
 MX_GEMM = [("few", 1, 41, 11008), ("few", 16, 41, 1001), ("few", 17, 100, 11008), ("few", 32, 41, 1001),
            ("S", 49, 67, 35), ("S split", 50, 65, 4359), ("S split", 65, 130, 2000), ("M", 3151, 1938, 33),
            ("M split", 2731, 68, 9421), ("M split", 130, 4001, 7990), ("M mixed", 1287, 5950, 2406),
-           ("L", 1694, 6991, 1049), ("L mixed", 1765, 9349, 5379)]
+           ("L", 1694, 6991, 1049), ("L split", 17109, 136, 23215), ("L mixed", 1765, 9349, 5379)]
 MX_GATED = [("few", 1, 41, 11008), ("few", 16, 41, 1001), ("few", 17, 100, 11008), ("few", 32, 41, 1001),
             ("S", 49, 67, 35), ("S split", 50, 65, 4359), ("M", 258, 10735, 34), ("M split", 66, 1513, 9276),
-            ("M mixed", 6580, 577, 2332), ("L", 539, 9939, 1027), ("L mixed", 658, 11003, 6107)]
+            ("M mixed", 6580, 577, 2332), ("L", 539, 9939, 1027), ("L split", 136, 8250, 21747),
+            ("L mixed", 658, 11003, 6107)]
 
 
 @pytest.mark.parametrize("plan,n,o,i", MX_GEMM)
 def test_mx_gemm_exact(plan, n, o, i):
     """Values are multiples of 2^-2 (tokens) and 2^-1 (weights) of at most 6 and 12, so products are multiples of 2^-3 of
-    at most 72, and 11008 of them sum to less than 2^20 = 2^23 * 2^-3. The rows' powers multiply whole
-    results; the largest is below 2^(20 + 100), the smallest other than 0 2^(-3 - 100)."""
+    at most 72, and 23215 of them sum to less than 2^21 = 2^24 * 2^-3. The rows' powers multiply whole
+    results; the largest is below 2^(21 + 100), the smallest other than 0 2^(-3 - 100)."""
     import torch
     say(f"mx gemm exact {plan} n={n} o={o} i={i}")
     g = generator(n + o + i)

@@ -83,12 +83,21 @@ typedef enum {
     KQ_OP_MX_GEMM = 13,    /* o, i, n tokens */
     KQ_OP_MX_GATED = 14,   /* o, i, n tokens */
     KQ_OP_GATED_FORWARD = 15,  /* o, i, n tokens, xdt */
-    KQ_OP_GATED_BACKWARD = 16  /* o, i, n tokens, xdt */
+    KQ_OP_GATED_BACKWARD = 16, /* o, i, n tokens, xdt */
+    KQ_OP_I8_GEMM = 17,        /* o, i, n tokens, group = experts (0 without offsets) */
+    KQ_OP_I8_GATED = 18,       /* the same */
+    KQ_OP_GROUPED_GEMM = 19,   /* o, i, n rows, xdt, group = experts */
+    KQ_OP_GROUPED_GATED = 20,  /* the same */
+    KQ_OP_GROUPED_BACKWARD = 21,  /* the same */
+    KQ_OP_NORM_BACKWARD = 22   /* n rows, i = width, xdt */
 } kq_op;
 
 /* Activations of the gated feed-forward block: a / (1 + exp(-a)); a Phi(a) with the normal distribution's
  * Phi; the same with Phi replaced by (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2; max(a, 0). */
 typedef enum { KQ_ACT_SILU = 0, KQ_ACT_GELU = 1, KQ_ACT_GELU_TANH = 2, KQ_ACT_RELU = 3 } kq_act;
+
+/* Norms: of the differences from the row's mean, or of the values themselves. */
+typedef enum { KQ_NORM_LAYER = 0, KQ_NORM_RMS = 1 } kq_norm;
 
 /* Workspace bytes needed by `op` for a layer of o x i weights, n calibration tokens (X dtype
  * xdt), `bits`, `group` and H_G `form`/`blk`. Arguments an op does not use are ignored. */
@@ -460,6 +469,125 @@ kq_status kq_gated_backward(const void* dH, int64_t lddh, const void* A, int64_t
                             int64_t n, int64_t o, int64_t i, kq_act act, void* dA, int64_t ldda, void* dB, int64_t lddb,
                             void* dX, int64_t lddx, void* dWg, int64_t lddg, void* dWu, int64_t lddu, void* ws,
                             size_t ws_bytes, kq_stream stream);
+
+/*
+ * 8-bit integers with a scale for each row (KronQ review page, Limitations (3): the quantized weights are
+ * multiplied at inference time; Goal: low-bit weights; symmetric rounding, a scale for each token and each output
+ * channel): value = code * scale, codes -127 .. 127. codes: rows of ldc bytes, ldc a multiple of 16 and at most
+ * 4 MiB, base aligned to 16 bytes; the last 16 bytes of a row belong to it, whatever they hold past `cols`. scales:
+ * one float a row.
+ *
+ * Quantise X (rows x cols, fp32 or bf16, leading dimension ldx, a multiple of 16 bytes): with a the row's largest
+ * magnitude, scale = a / 127 and m = 127 / a, both rounded to fp32; a code is the whole number nearest to x m,
+ * ties to the even one, of the exact product. A row with a < 2^-119 gets scale 0 and zero codes, one with an infinity or
+ * a NaN scale NaN and zero codes. Bytes past cols are left alone. rows = 0 does nothing. Outputs overlap neither
+ * each other nor X.
+ */
+kq_status kq_i8_quantize(const void* X, kq_dtype xdt, int64_t rows, int64_t cols, int64_t ldx, int8_t* codes, int64_t ldc,
+                         float* scales, kq_stream stream);
+
+/*
+ * The values that codes and scales stand for (format above; KronQ review page, Limitations (3)), code * scale rounded to
+ * Y (rows x cols, fp32 or bf16, leading dimension ldy, a multiple of 16 bytes; code * scale is rounded to fp32 before it
+ * is rounded to bf16).
+ */
+kq_status kq_i8_dequantize(const int8_t* codes, int64_t ldc, const float* scales, int64_t rows, int64_t cols, void* Y,
+                           kq_dtype ydt, int64_t ldy, kq_stream stream);
+
+/*
+ * Product of 8-bit integers with scales (KronQ review page, Limitations (3): the product with the quantized weights at
+ * inference), Y_to = (sA_t sB_o) sum_k A_tk B_ok on the int8 matrix cores: A n x i tokens, B o x i weights, both in the format
+ * above (codes of -128 are allowed; i at most 131071, so that the int32 sums are exact). The product of the two
+ * scales is rounded to fp32, the sum too, and their product to Y (n x o, fp32 or bf16, ldy, a multiple of 16 bytes). A scale
+ * that is NaN makes NaN of its token's row of Y (of its weight's column). Y overlaps no input. n = 0 does nothing.
+ *
+ * offsets NULL and experts 0: one matrix of weights. Otherwise the rows of A are grouped by expert and B holds
+ * experts * o rows, with the rules of kq_grouped_gemm.
+ *
+ * Workspace: kq_workspace_bytes(KQ_OP_I8_GEMM, o, i, n, .., group = experts, ..), possibly 0; its rules and the limits of
+ * sizes are those of kq_mx_gemm.
+ */
+kq_status kq_i8_gemm(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t ldb, const float* sB,
+                     const int32_t* offsets, int64_t experts, int64_t n, int64_t o, int64_t i, void* Y, kq_dtype ydt,
+                     int64_t ldy, void* ws, size_t ws_bytes, kq_stream stream);
+
+/*
+ * Gated feed-forward block on 8-bit integers (KronQ review page, Limitations (3)), H = act(X G^T) * (X U^T): G and U o x i (or
+ * experts * o rows) gate and up weights; both products stay in fp32 until H is rounded to its type. Formats, offsets,
+ * overlap and workspace (KQ_OP_I8_GATED) as for kq_i8_gemm.
+ */
+kq_status kq_i8_gated(const int8_t* X, int64_t ldx, const float* sX, const int8_t* G, int64_t ldg, const float* sG,
+                      const int8_t* U, int64_t ldu, const float* sU, const int32_t* offsets, int64_t experts, int64_t n,
+                      int64_t o, int64_t i, kq_act act, void* H, kq_dtype hdt, int64_t ldh, void* ws, size_t ws_bytes,
+                      kq_stream stream);
+
+/*
+ * Products grouped by expert (KronQ review page, Method: layer statistics come from a calibration pass; each expert of
+ * an expert layer has its own, over the tokens sent to it): the rows of X (n x i) are sorted by expert, W holds the experts'
+ * o x i matrices one under the other (experts * o rows of leading dimension ldw), and
+ *     Y_r = X_r W_k^T,   offsets[k] <= r < offsets[k + 1]
+ * offsets: experts + 1 int32 values on the device, not decreasing, in 0 .. n; they are read when the kernels run. Any other
+ * contents are read as if each value were clamped to 0 .. n and raised to the largest before it. Experts may have no
+ * rows; rows before the first offset and from the last one on are neither read nor written. All matrices of type dt
+ * (fp32 or bf16), leading dimensions as for kq_gated_forward; sums are fp32, rounded once. Outputs overlap neither each
+ * other nor any input. 1 to 4096 experts; n below 2^31. n = 0 does nothing. Workspace: kq_workspace_bytes(KQ_OP_GROUPED_GEMM, o,
+ * i, n, dt, .., group = experts, ..), possibly 0; its rules are those of kq_mx_gemm. A row's result does not depend on the
+ * rows of other experts.
+ */
+kq_status kq_grouped_gemm(const void* X, int64_t ldx, const void* W, int64_t ldw, const int32_t* offsets, int64_t experts,
+                          kq_dtype dt, int64_t n, int64_t o, int64_t i, void* Y, int64_t ldy, void* ws, size_t ws_bytes,
+                          kq_stream stream);
+
+/*
+ * Gated feed-forward block of each expert (KronQ review page, Method), kq_gated_forward with the rows and weights of
+ * kq_grouped_gemm: A_r = X_r Wg_k^T, B_r = X_r Wu_k^T, H = act(A) * B; A and B (n x o) are written where not NULL. dA and dB
+ * come from kq_gated_backward with no other gradients (on the rows inside the offsets; it knows no experts).
+ * Workspace: KQ_OP_GROUPED_GATED.
+ */
+kq_status kq_grouped_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu,
+                           const int32_t* offsets, int64_t experts, kq_dtype dt, int64_t n, int64_t o, int64_t i, kq_act act,
+                           void* H, int64_t ldh, void* A, int64_t lda, void* B, int64_t ldb, void* ws, size_t ws_bytes,
+                           kq_stream stream);
+
+/*
+ * Gradients of grouped products (KronQ review page, Method: the gradient covariance H_G from one calibration backward pass),
+ * of one product Y = X W^T or of two that share X (gate and up):
+ *     dX_r = dY_r W_k [+ dY2_r W2_k],   dW_k = sum over expert k's rows r of dY_r^T X_r   [dW2_k likewise]
+ * dX (n x i), dW and dW2 (experts * o rows of i) are written where not NULL; dY2, W2 and dW2 are NULL for a single
+ * product, and for two dX takes both. W and W2 may be NULL without dX, X without weight gradients. dW_k of an expert
+ * without rows is zero; rows of dX outside the offsets are left alone. Each gradient has the same bits whichever others
+ * are asked for. n = 0 writes zeros to dW and dW2. Types, offsets, overlap and workspace (KQ_OP_GROUPED_BACKWARD) as for
+ * kq_grouped_gemm.
+ */
+kq_status kq_grouped_backward(const void* dY, int64_t lddy, const void* W, int64_t ldw, const void* dY2, int64_t lddy2,
+                              const void* W2, int64_t ldw2, const void* X, int64_t ldx, const int32_t* offsets, int64_t experts,
+                              kq_dtype dt, int64_t n, int64_t o, int64_t i, void* dX, int64_t lddx, void* dW, int64_t lddw,
+                              void* dW2, int64_t lddw2, void* ws, size_t ws_bytes, kq_stream stream);
+
+/*
+ * The norm in front of a block (KronQ review page, Method: X of a layer, in the calibration pass, is its norm's output), of
+ * each row x of X (n x d):
+ *     KQ_NORM_LAYER  m = mean x, r = 1 / sqrt(mean (x - m)^2 + eps)      KQ_NORM_RMS  m = 0, r = 1 / sqrt(mean x^2 + eps)
+ *     Y = (x - m) r gamma + beta
+ * X, Y, gamma and beta (d values) of type dt (fp32 or bf16), ldx and ldy multiples of 16 bytes and at most 2^20, gamma and
+ * beta aligned to 16 bytes; gamma NULL stands for ones, beta NULL for zeros. mean and rstd (n floats, m and r) are written
+ * where not NULL: kq_norm_backward takes them. eps in (0, 1]. Sums are fp32, so squares past 3.4e38 make r zero. Infinities and
+ * NaN change their own row alone. Y may be X (with ldy = ldx), else outputs overlap neither each other nor any input. n = 0 does nothing.
+ */
+kq_status kq_norm_forward(const void* X, int64_t ldx, const void* gamma, const void* beta, kq_dtype dt, int64_t n, int64_t d,
+                          kq_norm kind, float eps, void* Y, int64_t ldy, float* mean, float* rstd, kq_stream stream);
+
+/*
+ * Gradients of the norm (KronQ review page, Method: the backward pass goes through it to the sublayers before), from dY and
+ * the mean and rstd that kq_norm_forward kept (mean may be NULL for KQ_NORM_RMS). With h = (x - m) r and g = dY gamma,
+ *     dX = r (g - c - h mean(g h)), c = mean g (KQ_NORM_LAYER) or 0,  dgamma = sum over rows of dY h,  dbeta = sum over rows of dY
+ * dX (n x d) and dgamma and dbeta (d values, aligned to 4 bytes) are written where not NULL, all of type dt. n = 0 writes zeros to
+ * dgamma and dbeta. dX may be dY or X (with the same leading dimension), else outputs overlap neither each other nor any input. Workspace for
+ * dgamma or dbeta: kq_workspace_bytes(KQ_OP_NORM_BACKWARD, .., i = d, n, dt, ..); its rules are those of kq_mx_gemm.
+ */
+kq_status kq_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* gamma, const float* mean,
+                           const float* rstd, kq_dtype dt, int64_t n, int64_t d, kq_norm kind, void* dX, int64_t lddx,
+                           void* dgamma, void* dbeta, void* ws, size_t ws_bytes, kq_stream stream);
 
 /*
  * Sublayer mixed-precision bit allocation (review page, Method (2) and Comparison: the joint score

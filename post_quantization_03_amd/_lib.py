@@ -14,14 +14,18 @@ KQ_F32, KQ_BF16 = 0, 1
 HG_FORM = {"diag": 0, "block": 1, "full": 2}
 OP = {"hessian": 0, "rotate_in": 1, "hg_sqrt": 2, "rotate_out": 3, "cholinv": 4, "quantize": 5, "unrotate": 6,
       "loss": 7, "matvec": 8, "hg_lowrank": 9, "kfac_loss": 10, "cross": 11, "drift": 12, "mx_gemm": 13,
-      "mx_gated": 14, "gated_forward": 15, "gated_backward": 16}
+      "mx_gated": 14, "gated_forward": 15, "gated_backward": 16, "i8_gemm": 17, "i8_gated": 18, "grouped_gemm": 19,
+      "grouped_gated": 20, "grouped_backward": 21, "norm_backward": 22}
 ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+NORM = {"layer": 0, "rms": 1}
 EXPORTS = ("kq_workspace_bytes", "kq_hessian_accum", "kq_rotate_in", "kq_hg_sqrt", "kq_rotate_out", "kq_cholinv",
            "kq_quantize_layer", "kq_sensitivity", "kq_unrotate", "kq_layer_loss", "kq_strerror", "kq_last_error",
            "kq_hadamard_order", "kq_version", "kq_allocate_bits", "kq_matvec_quantized",
            "kq_hg_extract", "kq_hg_lowrank", "kq_kfac_loss", "kq_quantize_layer_search",
            "kq_block_order", "kq_permute_blocks", "kq_cross_accum", "kq_drift_target", "kq_matvec_quantized_static",
-           "kq_mx_quantize", "kq_mx_dequantize", "kq_mx_gemm", "kq_mx_gated", "kq_gated_forward", "kq_gated_backward")
+           "kq_mx_quantize", "kq_mx_dequantize", "kq_mx_gemm", "kq_mx_gated", "kq_gated_forward", "kq_gated_backward",
+           "kq_i8_quantize", "kq_i8_dequantize", "kq_i8_gemm", "kq_i8_gated", "kq_grouped_gemm", "kq_grouped_gated",
+           "kq_grouped_backward", "kq_norm_forward", "kq_norm_backward")
 
 
 class KQError(RuntimeError):
@@ -80,6 +84,16 @@ def lib() -> ctypes.CDLL:
         "kq_mx_gated": (_int, [_vp, _i64] * 6 + [_i64, _i64, _i64, _int, _vp, _int, _i64, _vp, _sz, _vp]),
         "kq_gated_forward": (_int, [_vp, _i64] * 3 + [_int, _i64, _i64, _i64, _int] + [_vp, _i64] * 3 + [_vp, _sz, _vp]),
         "kq_gated_backward": (_int, [_vp, _i64] * 6 + [_int, _i64, _i64, _i64, _int] + [_vp, _i64] * 5 + [_vp, _sz, _vp]),
+        "kq_i8_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+        "kq_i8_dequantize": (_int, [_vp, _i64, _vp, _i64, _i64, _vp, _int, _i64, _vp]),
+        "kq_i8_gemm": (_int, [_vp, _i64, _vp] * 2 + [_vp, _i64, _i64, _i64, _i64, _vp, _int, _i64, _vp, _sz, _vp]),
+        "kq_i8_gated": (_int, [_vp, _i64, _vp] * 3 + [_vp, _i64, _i64, _i64, _i64, _int, _vp, _int, _i64, _vp, _sz, _vp]),
+        "kq_grouped_gemm": (_int, [_vp, _i64] * 2 + [_vp, _i64, _int, _i64, _i64, _i64, _vp, _i64, _vp, _sz, _vp]),
+        "kq_grouped_gated": (_int, [_vp, _i64] * 3 + [_vp, _i64, _int, _i64, _i64, _i64, _int] + [_vp, _i64] * 3 +
+                             [_vp, _sz, _vp]),
+        "kq_grouped_backward": (_int, [_vp, _i64] * 5 + [_vp, _i64, _int, _i64, _i64, _i64] + [_vp, _i64] * 3 + [_vp, _sz, _vp]),
+        "kq_norm_forward": (_int, [_vp, _i64, _vp, _vp, _int, _i64, _i64, _int, _f32, _vp, _i64, _vp, _vp, _vp]),
+        "kq_norm_backward": (_int, [_vp, _i64] * 2 + [_vp, _vp, _vp, _int, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -506,3 +520,217 @@ def kq_gated_backward(dH, A, B, X, Wg, Wu, act: str, dA, dB, dX=None, dWg=None, 
              *take("X", X, n, i, True), *take("Wg", Wg, o, i, True), *take("Wu", Wu, o, i, True), dt, n, o, i, _act(name, act),
              *take("dA", dA, n, o, True), *take("dB", dB, n, o, True), *take("dX", dX, n, i, False),
              *take("dWg", dWg, o, i, False), *take("dWu", dWu, o, i, False), *_workspace(name, ws, dev)))
+
+
+# ------------------------------------- 8-bit integer products, products grouped by expert, norms
+_WORDS: tuple | None = None
+
+
+def _words() -> tuple:
+    """torch.int8, torch.int32 and torch.float32, published whole as _torch's."""
+    global _WORDS
+    if _WORDS is None:
+        import torch
+        _WORDS = (torch.int8, torch.int32, torch.float32)
+    return _WORDS
+
+
+def _stack(name: str, what: str, t, e: int, o: int, cols: int, dtype, per: int, whole: bool, dev: int):
+    """_matrix for e matrices o x cols one under the other; returns (pointer, leading dimension)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {what} has type {t.dtype}, not {dtype}")
+    if t.shape != (e, o, cols):
+        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {(e, o, cols)}")
+    if t.get_device() != dev:
+        _other_device(name, what, t, dev)
+    each, ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name}: {what} is not row-major")
+    if o == 1:
+        ld = each       # the stride of a single row is arbitrary
+    elif e > 1 and each != o * ld:
+        raise ValueError(f"{name}: the matrices of {what} do not lie one under the other")
+    rows = e * o
+    if rows <= 1:
+        ld = -(-cols // per) * per
+    if whole and cols % per and rows:
+        end = t.storage_offset() + (rows - 1) * ld + -(-cols // per) * per
+        if end * t.element_size() > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the last row of {what} ends inside its 16 bytes, past the storage")
+    return t.data_ptr(), ld
+
+
+def _vector(name: str, what: str, t, shape: tuple, dtype, dev: int):
+    """Checks a contiguous tensor of `shape`; returns its pointer (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {what} has type {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {shape}")
+    if t.get_device() != dev:
+        _other_device(name, what, t, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: {what} is not contiguous")
+    return t.data_ptr()
+
+
+def _offsets(name: str, t, experts: int, dev: int):
+    return _vector(name, "offsets", t, (experts + 1,), (_WORDS or _words())[1], dev)
+
+
+def _i8(name: str, what: str, codes, scales, rows: int, cols: int, dev: int) -> tuple:
+    """Checks 8-bit codes and their scales; returns their three C arguments."""
+    i8, _, f32 = _WORDS or _words()
+    return *_matrix(name, what + " codes", codes, rows, cols, i8, 16, True, dev), _vector(name, what + " scales", scales, (rows,), f32, dev)
+
+
+def _i8_weights(name: str, what: str, codes, scales, experts: int, o: int, i: int, dev: int) -> tuple:
+    if not experts:
+        return _i8(name, what, codes, scales, o, i, dev)
+    i8, _, f32 = _WORDS or _words()
+    return (*_stack(name, what + " codes", codes, experts, o, i, i8, 16, True, dev),
+            _vector(name, what + " scales", scales, (experts, o), f32, dev))
+
+
+def _experts(name: str, what: str, t, offsets) -> tuple:
+    """(experts, rows) of weights: those of a stack with offsets, of a matrix (no experts) without."""
+    if t.dim() != (2 if offsets is None else 3):
+        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}: one matrix, or with offsets a stack of them")
+    return (0, t.shape[0]) if offsets is None else (t.shape[0], t.shape[1])
+
+
+def i8_empty(rows: int, cols: int, device):
+    """Buffers for a rows x cols matrix of 8-bit integers: codes (int8, rows starting on 16 bytes) and scales (a
+    float a row), contents undefined."""
+    import torch
+    return (torch.empty((rows, -(-cols // 16) * 16), dtype=torch.int8, device=device)[:, :cols],
+            torch.empty(rows, dtype=torch.float32, device=device))
+
+
+def kq_i8_quantize(X, codes, scales, stream=None) -> None:
+    """X (rows x cols, fp32 or bf16) into codes and scales of i8_empty(rows, cols)."""
+    name = "kq_i8_quantize"
+    rows, cols = X.shape
+    dt, per, dev = _float(name, "X", X)
+    p, ld = _matrix(name, "X", X, rows, cols, X.dtype, per, False, dev)
+    _launch(name, lib().kq_i8_quantize, dev, stream, (p, dt, rows, cols, ld, *_i8(name, "output", codes, scales, rows, cols, dev)))
+
+
+def kq_i8_dequantize(codes, scales, Y, stream=None) -> None:
+    """The values that codes and scales stand for, into Y (rows x cols, fp32 or bf16)."""
+    name = "kq_i8_dequantize"
+    rows, cols = Y.shape
+    dt, per, dev = _float(name, "Y", Y)
+    p, ld = _matrix(name, "Y", Y, rows, cols, Y.dtype, per, False, dev)
+    _launch(name, lib().kq_i8_dequantize, dev, stream, (*_i8(name, "input", codes, scales, rows, cols, dev), rows, cols, p, dt, ld))
+
+
+def kq_i8_gemm(Ac, As, Bc, Bs, Y, offsets=None, ws=None, stream=None) -> None:
+    """Y (n x o, fp32 or bf16) = A B^T for 8-bit A (n x i) and B (o x i, scales o); with offsets (experts + 1 int32)
+    the rows of A are sorted by expert and B is experts x o x i, its scales experts x o."""
+    name = "kq_i8_gemm"
+    (n, i), (e, o) = Ac.shape, _experts(name, "B codes", Bc, offsets)
+    dt, per, dev = _float(name, "Y", Y)
+    p, ld = _matrix(name, "Y", Y, n, o, Y.dtype, per, False, dev)
+    _launch(name, lib().kq_i8_gemm, dev, stream,
+            (*_i8(name, "A", Ac, As, n, i, dev), *_i8_weights(name, "B", Bc, Bs, e, o, i, dev), _offsets(name, offsets, e, dev),
+             e, n, o, i, p, dt, ld, *_workspace(name, ws, dev)))
+
+
+def kq_i8_gated(Xc, Xs, Gc, Gs, Uc, Us, act: str, H, offsets=None, ws=None, stream=None) -> None:
+    """H (n x o, fp32 or bf16) = act(X G^T) * (X U^T) for 8-bit X (n x i), G and U; offsets as for kq_i8_gemm."""
+    name = "kq_i8_gated"
+    (n, i), (e, o) = Xc.shape, _experts(name, "gate codes", Gc, offsets)
+    dt, per, dev = _float(name, "H", H)
+    p, ld = _matrix(name, "H", H, n, o, H.dtype, per, False, dev)
+    _launch(name, lib().kq_i8_gated, dev, stream,
+            (*_i8(name, "X", Xc, Xs, n, i, dev), *_i8_weights(name, "gate", Gc, Gs, e, o, i, dev),
+             *_i8_weights(name, "up", Uc, Us, e, o, i, dev), _offsets(name, offsets, e, dev), e, n, o, i, _act(name, act), p, dt,
+             ld, *_workspace(name, ws, dev)))
+
+
+def kq_grouped_gemm(X, W, offsets, Y, ws=None, stream=None) -> None:
+    """Y_r = X_r W_k^T for the rows offsets[k] .. offsets[k + 1] - 1 of X (n x i); W: experts x o x i, offsets: experts + 1
+    int32. Rows outside the offsets are left alone."""
+    name = "kq_grouped_gemm"
+    (n, i), (e, o, _), t = X.shape, W.shape, X.dtype
+    dt, per, dev = _float(name, "X", X)
+    _launch(name, lib().kq_grouped_gemm, dev, stream,
+            (*_matrix(name, "X", X, n, i, t, per, True, dev), *_stack(name, "W", W, e, o, i, t, per, True, dev),
+             _offsets(name, offsets, e, dev), e, dt, n, o, i, *_matrix(name, "Y", Y, n, o, t, per, False, dev),
+             *_workspace(name, ws, dev)))
+
+
+def kq_grouped_gated(X, Wg, Wu, offsets, act: str, H, A=None, B=None, ws=None, stream=None) -> None:
+    """kq_gated_forward for each expert's rows; Wg, Wu and offsets as kq_grouped_gemm's."""
+    name = "kq_grouped_gated"
+    (n, i), (e, o, _), t = X.shape, Wg.shape, X.dtype
+    dt, per, dev = _float(name, "X", X)
+    _launch(name, lib().kq_grouped_gated, dev, stream,
+            (*_matrix(name, "X", X, n, i, t, per, True, dev), *_stack(name, "Wg", Wg, e, o, i, t, per, True, dev),
+             *_stack(name, "Wu", Wu, e, o, i, t, per, True, dev), _offsets(name, offsets, e, dev), e, dt, n, o, i,
+             _act(name, act), *_matrix(name, "H", H, n, o, t, per, False, dev),
+             *((None, 0) if A is None else _matrix(name, "A", A, n, o, t, per, False, dev)),
+             *((None, 0) if B is None else _matrix(name, "B", B, n, o, t, per, False, dev)), *_workspace(name, ws, dev)))
+
+
+def kq_grouped_backward(dY, X, W, offsets, dX=None, dW=None, dY2=None, W2=None, dW2=None, ws=None, stream=None) -> None:
+    """Gradients of kq_grouped_gemm: dX and dW where given (W may be None without dX, X without weight gradients).
+    With dY2 they are those of two products of the same X: dX the sum of both, dW2 the second's."""
+    name = "kq_grouped_backward"
+    (n, o), t = dY.shape, dY.dtype
+    if dX is not None and (W is None or (dY2 is not None and W2 is None)):
+        raise ValueError(f"{name}: dX needs the weights")
+    if (dW is not None or dW2 is not None) and X is None:
+        raise ValueError(f"{name}: weight gradients need X")
+    if dY2 is None and (W2 is not None or dW2 is not None):
+        raise ValueError(f"{name}: W2 and dW2 go with dY2")
+    dt, per, dev = _float(name, "dY", dY)
+    e = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
+    some = next((m for m in (dX, dW, dW2, X, W, W2) if m is not None), None)
+    i = 1 if some is None else some.shape[-1]
+
+    def take(what, m, rows, cols, whole):
+        return (None, 0) if m is None else _matrix(name, what, m, rows, cols, t, per, whole, dev)
+
+    def stack(what, m, whole):
+        return (None, 0) if m is None else _stack(name, what, m, e, o, i, t, per, whole, dev)
+
+    _launch(name, lib().kq_grouped_backward, dev, stream,
+            (*take("dY", dY, n, o, True), *stack("W", W, True), *take("dY2", dY2, n, o, True), *stack("W2", W2, True),
+             *take("X", X, n, i, True), _offsets(name, offsets, e, dev), e, dt, n, o, i, *take("dX", dX, n, i, False),
+             *stack("dW", dW, False), *stack("dW2", dW2, False), *_workspace(name, ws, dev)))
+
+
+def _norm(name: str, kind: str) -> int:
+    if kind not in NORM:
+        raise ValueError(f"{name}: kind {kind!r} is none of {sorted(NORM)}")
+    return NORM[kind]
+
+
+def kq_norm_forward(X, gamma, beta, kind: str, eps: float, Y, mean=None, rstd=None, stream=None) -> None:
+    """Y = norm(X) * gamma + beta over the rows of X (n x d), kind "layer" or "rms"; gamma and beta (d, X's type) may be None;
+    mean and rstd (n floats), where given, take the statistics. Y may be X."""
+    name = "kq_norm_forward"
+    (n, d), t, f32 = X.shape, X.dtype, (_WORDS or _words())[2]
+    dt, per, dev = _float(name, "X", X)
+    _launch(name, lib().kq_norm_forward, dev, stream,
+            (*_matrix(name, "X", X, n, d, t, per, False, dev), _vector(name, "gamma", gamma, (d,), t, dev),
+             _vector(name, "beta", beta, (d,), t, dev), dt, n, d, _norm(name, kind), eps,
+             *_matrix(name, "Y", Y, n, d, t, per, False, dev), _vector(name, "mean", mean, (n,), f32, dev),
+             _vector(name, "rstd", rstd, (n,), f32, dev)))
+
+
+def kq_norm_backward(dY, X, gamma, mean, rstd, kind: str, dX=None, dgamma=None, dbeta=None, ws=None, stream=None) -> None:
+    """Gradients of kq_norm_forward from dY and the mean (None will do for "rms") and rstd that it kept; dX may be dY or X."""
+    name = "kq_norm_backward"
+    (n, d), t, f32 = dY.shape, dY.dtype, (_WORDS or _words())[2]
+    dt, per, dev = _float(name, "dY", dY)
+    _launch(name, lib().kq_norm_backward, dev, stream,
+            (*_matrix(name, "dY", dY, n, d, t, per, False, dev), *_matrix(name, "X", X, n, d, t, per, False, dev),
+             _vector(name, "gamma", gamma, (d,), t, dev), _vector(name, "mean", mean, (n,), f32, dev),
+             _vector(name, "rstd", rstd, (n,), f32, dev), dt, n, d, _norm(name, kind),
+             *((None, 0) if dX is None else _matrix(name, "dX", dX, n, d, t, per, False, dev)),
+             _vector(name, "dgamma", dgamma, (d,), t, dev), _vector(name, "dbeta", dbeta, (d,), t, dev),
+             *_workspace(name, ws, dev)))

@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkq.so")
 PROBE_LIB = os.path.join(HERE, "libkqprobe.so")
-SOURCES = ("api", "dense", "gj", "syrk", "hadamard", "sweep", "dequant", "hgprep", "mx", "gated")
+SOURCES = ("api", "dense", "gj", "syrk", "hadamard", "sweep", "dequant", "hgprep", "mx", "gated", "i8", "grouped",
+           "norm")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-Wno-unused-result", "-Wno-unused-value",
          "-Wno-pass-failed", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

@@ -22,6 +22,8 @@ size_t drift_ws(int64_t o, int64_t i);
 size_t mx_product_ws(int64_t o, int64_t i, int64_t n, bool gated);
 size_t gated_forward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt);
 size_t gated_backward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt);
+size_t i8_product_ws(int64_t o, int64_t i, int64_t n, bool gated, int64_t experts);
+size_t norm_backward_ws(int64_t d, int64_t n, kq_dtype dt);
 
 namespace kq {
 
@@ -70,7 +72,6 @@ extern "C" int kq_version(void) { return 1; }
 extern "C" size_t kq_workspace_bytes(kq_op op, int64_t o, int64_t i, int64_t n, kq_dtype xdt, int bits, int group,
                                      kq_hg_form form, int64_t blk) {
     (void)bits;
-    (void)group;
     switch (op) {
         case KQ_OP_HESSIAN: return hessian_ws(n, i, xdt);
         case KQ_OP_ROTATE_IN: return rotate_in_ws(o, i);
@@ -89,6 +90,12 @@ extern "C" size_t kq_workspace_bytes(kq_op op, int64_t o, int64_t i, int64_t n, 
         case KQ_OP_MX_GATED: return mx_product_ws(o, i, n, true);
         case KQ_OP_GATED_FORWARD: return gated_forward_ws(o, i, n, xdt);
         case KQ_OP_GATED_BACKWARD: return gated_backward_ws(o, i, n, xdt);
+        case KQ_OP_I8_GEMM: return i8_product_ws(o, i, n, false, group);
+        case KQ_OP_I8_GATED: return i8_product_ws(o, i, n, true, group);
+        case KQ_OP_GROUPED_GEMM:
+        case KQ_OP_GROUPED_GATED:
+        case KQ_OP_GROUPED_BACKWARD: return 0;
+        case KQ_OP_NORM_BACKWARD: return norm_backward_ws(i, n, xdt);
     }
     return 0;
 }

@@ -1,0 +1,407 @@
+// The norm in front of a block, forward and backward (KronQ review page, Method: the activation and gradient statistics of a
+// layer come from one calibration pass, which runs through the norm on its way to the sublayers before it).
+//
+//   layer   m = mean x, r = 1 / sqrt(mean (x - m)^2 + eps)      rms   m = 0, r = 1 / sqrt(mean x^2 + eps)
+//   h = (x - m) r,  y = h gamma + beta
+//   g = dy gamma,  dx = r (g - [layer: mean g] - h mean(g h)),  dgamma = sum over rows of dy h,  dbeta = sum over rows of dy
+//
+// Both passes are bound by HBM: x is read once and y written once; dy and x are read once and dx written once. A row stays in
+// registers between its statistics and its results. All sums are fp32; the variance is taken of the differences from the
+// mean, which keeps its digits where the mean is large against the deviation.
+#include "rows.h"
+
+namespace kq {
+
+// gamma (1 where there is none) and beta (0) of the columns of piece c
+template <bool BF>
+__device__ __forceinline__ void norm_weights(const void* p, int64_t col, int64_t cols, float none, float (&v)[row_chunk<BF>()]) {
+    if (p && col < cols) row_load<BF>(p, col, cols - col, v);
+    else
+#pragma unroll
+        for (int e = 0; e < row_chunk<BF>(); e++) v[e] = none;
+}
+
+struct NormArgs {
+    const void *X, *dY, *gamma, *beta;
+    int64_t ldx, lddy, n, d;
+    float eps;
+    int layer;               // the mean is taken off
+    void *Y;                 // or dX
+    int64_t ldy;
+    float *mean, *rstd;
+    float *part;             // backward: sums of dgamma, then of dbeta, of each work-group (2 x d floats each)
+};
+
+// 1 / deviation from the sums q of the squares and of the differences from m, a first mean (0 for rms). The sum of the differences
+// is what rounding left of the mean: it corrects m, and its square comes off the variance. A row of one value then has that value
+// as its mean, where one ulp beside it would come out times up to 1 / sqrt(eps).
+__device__ __forceinline__ float norm_rstd(float& m, const float (&q)[2], float width, const NormArgs& g) {
+    float var = q[0] / width;
+    if (g.layer) {
+        const float rest = q[1] / width;
+        m += rest;
+        var = __builtin_fmaf(-rest, rest, var);      // infinite where the squares are
+        if (var < 0.0f) var = 0.0f;
+    }
+    return 1.0f / sqrtf(var + g.eps);
+}
+
+template <bool BF, int T, int CH>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormArgs g) {
+    constexpr int V = row_chunk<BF>();
+    __shared__ float sm[32];
+    const RowAt<T> at;
+    const float width = (float)g.d;
+    for (int64_t r = at.first; r < g.n; r += at.step) {
+        RowRegs<BF, T, CH> x;
+        x.load(g.X, r * g.ldx, g.d, at.lane);
+        float m = 0.0f;
+        if (g.layer) {
+            float s[1] = {0.0f};
+            x.each([&](int, float v) { s[0] += v; });
+            row_sum<T>(s, sm);
+            m = s[0] / width;
+        }
+        float q[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int64_t col = ((int64_t)c * T + at.lane) * V;
+            float v[V];
+            x.get(c, v);
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                const float t = col + e < g.d ? v[e] - m : 0.0f;
+                q[0] += t * t;
+                q[1] += t;
+            }
+        }
+        row_sum<T>(q, sm);
+        const float rs = norm_rstd(m, q, width, g);
+        if (at.lane == 0) {
+            if (g.mean) g.mean[r] = m;
+            if (g.rstd) g.rstd[r] = rs;
+        }
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int64_t col = ((int64_t)c * T + at.lane) * V;
+            if (col >= g.d) continue;
+            float v[V], w[V], b[V];
+            x.get(c, v);
+            norm_weights<BF>(g.gamma, col, g.d, 1.0f, w);
+            norm_weights<BF>(g.beta, col, g.d, 0.0f, b);
+#pragma unroll
+            for (int e = 0; e < V; e++) v[e] = (v[e] - m) * rs * w[e] + b[e];
+            store_run<V>(g.Y, BF ? KQ_BF16 : KQ_F32, r * g.ldy + col, v, g.d - col);
+        }
+    }
+}
+
+// Rows that the registers do not hold: read three times, the last two mostly from a cache.
+template <bool BF>
+__global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormArgs g) {
+    constexpr int V = row_chunk<BF>();
+    __shared__ float sm[32];
+    const float width = (float)g.d;
+    for (int64_t r = blockIdx.x; r < g.n; r += gridDim.x) {
+        auto all = [&](auto&& f) {
+            for (int64_t col = (int64_t)threadIdx.x * V; col < g.d; col += 1024 * V) {
+                float v[V];
+                row_load<BF>(g.X, r * g.ldx + col, g.d - col, v);
+                f(col, v);
+            }
+        };
+        float m = 0.0f;
+        if (g.layer) {
+            float s[1] = {0.0f};
+            all([&](int64_t, float (&v)[V]) {
+                for (int e = 0; e < V; e++) s[0] += v[e];
+            });
+            row_sum<1024>(s, sm);
+            m = s[0] / width;
+        }
+        float q[2] = {0.0f, 0.0f};
+        all([&](int64_t col, float (&v)[V]) {
+            for (int e = 0; e < V; e++) {
+                const float t = col + e < g.d ? v[e] - m : 0.0f;
+                q[0] += t * t;
+                q[1] += t;
+            }
+        });
+        row_sum<1024>(q, sm);
+        const float rs = norm_rstd(m, q, width, g);
+        if (threadIdx.x == 0) {
+            if (g.mean) g.mean[r] = m;
+            if (g.rstd) g.rstd[r] = rs;
+        }
+        all([&](int64_t col, float (&v)[V]) {
+            float w[V], b[V];
+            norm_weights<BF>(g.gamma, col, g.d, 1.0f, w);
+            norm_weights<BF>(g.beta, col, g.d, 0.0f, b);
+            for (int e = 0; e < V; e++) v[e] = (v[e] - m) * rs * w[e] + b[e];
+            store_run<V>(g.Y, BF ? KQ_BF16 : KQ_F32, r * g.ldy + col, v, g.d - col);
+        });
+    }
+}
+
+// dX of a work-group's rows and its part of dgamma and dbeta, which stay in registers over its rows.
+template <bool BF, int T, int CH>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormArgs g) {
+    constexpr int V = row_chunk<BF>(), PER = T < 256 ? 256 / T : 1;
+    __shared__ float sm[32];
+    const RowAt<T> at;
+    const float inv = 1.0f / (float)g.d;
+    float dg[CH][V], db[CH][V];
+#pragma unroll
+    for (int c = 0; c < CH; c++)
+#pragma unroll
+        for (int e = 0; e < V; e++) dg[c][e] = db[c][e] = 0.0f;
+    for (int64_t r = at.first; r < g.n; r += at.step) {
+        RowRegs<BF, T, CH> x, y;
+        x.load(g.X, r * g.ldx, g.d, at.lane);
+        y.load(g.dY, r * g.lddy, g.d, at.lane);
+        const float m = g.layer ? g.mean[r] : 0.0f, rs = g.rstd[r];
+        float s[2] = {0.0f, 0.0f};       // of g h and of g
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int64_t col = ((int64_t)c * T + at.lane) * V;
+            float v[V], dy[V], w[V];
+            x.get(c, v);
+            y.get(c, dy);
+            norm_weights<BF>(g.gamma, col, g.d, 1.0f, w);
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                const float h = col + e < g.d ? (v[e] - m) * rs : 0.0f, t = dy[e] * w[e];
+                s[0] += t * h;
+                s[1] += t;
+                dg[c][e] += dy[e] * h;
+                db[c][e] += dy[e];
+            }
+        }
+        if (!g.Y) continue;
+        row_sum<T>(s, sm);
+        const float c1 = s[0] * inv, c0 = g.layer ? s[1] * inv : 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int64_t col = ((int64_t)c * T + at.lane) * V;
+            if (col >= g.d) continue;
+            float v[V], dy[V], w[V];
+            x.get(c, v);
+            y.get(c, dy);
+            norm_weights<BF>(g.gamma, col, g.d, 1.0f, w);
+#pragma unroll
+            for (int e = 0; e < V; e++) v[e] = rs * (dy[e] * w[e] - c0 - (v[e] - m) * rs * c1);
+            store_run<V>(g.Y, BF ? KQ_BF16 : KQ_F32, r * g.ldy + col, v, g.d - col);
+        }
+    }
+    if (!g.part) return;
+    // a row of sums for each of a work-group's rows at a time
+    const int64_t mine = (int64_t)blockIdx.x * PER + (PER > 1 ? (int)threadIdx.x / T : 0);
+    float* p = g.part + mine * 2 * g.d;
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+        const int64_t col = ((int64_t)c * T + at.lane) * V;
+#pragma unroll
+        for (int e = 0; e < V; e++)
+            if (col + e < g.d) {
+                p[col + e] = dg[c][e];
+                p[g.d + col + e] = db[c][e];
+            }
+    }
+}
+
+template <bool BF>
+__global__ __launch_bounds__(1024) void norm_backward_long_kernel(NormArgs g) {
+    constexpr int V = row_chunk<BF>();
+    __shared__ float sm[32];
+    const float inv = 1.0f / (float)g.d;
+    for (int64_t r = blockIdx.x; r < g.n; r += gridDim.x) {
+        const float m = g.layer ? g.mean[r] : 0.0f, rs = g.rstd[r];
+        auto all = [&](auto&& f) {
+            for (int64_t col = (int64_t)threadIdx.x * V; col < g.d; col += 1024 * V) {
+                float h[V], t[V], w[V];
+                row_load<BF>(g.X, r * g.ldx + col, g.d - col, h);
+                row_load<BF>(g.dY, r * g.lddy + col, g.d - col, t);
+                norm_weights<BF>(g.gamma, col, g.d, 1.0f, w);
+                for (int e = 0; e < V; e++) {
+                    h[e] = col + e < g.d ? (h[e] - m) * rs : 0.0f;
+                    t[e] *= w[e];
+                }
+                f(col, h, t);
+            }
+        };
+        float s[2] = {0.0f, 0.0f};
+        all([&](int64_t, float (&h)[V], float (&t)[V]) {
+            for (int e = 0; e < V; e++) {
+                s[0] += t[e] * h[e];
+                s[1] += t[e];
+            }
+        });
+        row_sum<1024>(s, sm);
+        const float c1 = s[0] * inv, c0 = g.layer ? s[1] * inv : 0.0f;
+        all([&](int64_t col, float (&h)[V], float (&t)[V]) {
+            for (int e = 0; e < V; e++) t[e] = rs * (t[e] - c0 - h[e] * c1);
+            store_run<V>(g.Y, BF ? KQ_BF16 : KQ_F32, r * g.ldy + col, t, g.d - col);
+        });
+    }
+}
+
+// dgamma and dbeta of rows that the registers do not hold: a work-group's four wavefronts take its rows in turn, 64 pieces of
+// columns wide, and write a row of sums each.
+template <bool BF>
+__global__ __launch_bounds__(256) void norm_weights_long_kernel(NormArgs g) {
+    constexpr int V = row_chunk<BF>();
+    const int64_t col = ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63)) * V, mine = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6);
+    if (col >= g.d) return;
+    float dg[V], db[V];
+    for (int e = 0; e < V; e++) dg[e] = db[e] = 0.0f;
+    for (int64_t r = mine; r < g.n; r += (int64_t)gridDim.y * 4) {
+        const float m = g.layer ? g.mean[r] : 0.0f, rs = g.rstd[r];
+        float v[V], dy[V];
+        row_load<BF>(g.X, r * g.ldx + col, g.d - col, v);
+        row_load<BF>(g.dY, r * g.lddy + col, g.d - col, dy);
+        for (int e = 0; e < V; e++) {
+            dg[e] += dy[e] * ((v[e] - m) * rs);
+            db[e] += dy[e];
+        }
+    }
+    float* p = g.part + mine * 2 * g.d;
+    for (int e = 0; e < V; e++)
+        if (col + e < g.d) {
+            p[col + e] = dg[e];
+            p[g.d + col + e] = db[e];
+        }
+}
+
+// The rows of sums added in order: 64 columns a work-group, its four wavefronts a quarter of the rows each.
+__global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64_t rows, int64_t d, void* dgamma, void* dbeta, int dt) {
+    __shared__ float sm[4][64];
+    const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);      // of 2 d
+    const int w = threadIdx.x >> 6;
+    const int64_t per = (rows + 3) / 4, r0 = w * per, r1 = r0 + per < rows ? r0 + per : rows;
+    float s = 0.0f;
+    if (col < 2 * d)
+        for (int64_t r = r0; r < r1; r++) s += part[r * 2 * d + col];
+    sm[w][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (w || col >= 2 * d) return;
+    s = ((sm[0][threadIdx.x] + sm[1][threadIdx.x]) + sm[2][threadIdx.x]) + sm[3][threadIdx.x];
+    void* out = col < d ? dgamma : dbeta;
+    if (!out) return;
+    const int64_t c = col < d ? col : col - d;
+    if (dt == KQ_BF16) static_cast<uint16_t*>(out)[c] = to_bf16(s);
+    else static_cast<float*>(out)[c] = s;
+}
+
+// Work-groups of the backward pass: two for each compute unit at most (of 1024 threads; more of smaller ones), since each
+// leaves a row of sums.
+template <int T>
+unsigned norm_groups(int64_t n) { return row_groups<T>(n, T >= 1024 ? 512 : 1024); }
+// rows of sums
+static int64_t norm_parts(int64_t n, int64_t d, bool bf) {
+    int64_t parts = 0;
+    with_rows(bf, d, [&](auto, auto t, auto ch) {
+        constexpr int T = decltype(t)::value;
+        parts = decltype(ch)::value == 0 ? 4 * (n < 64 ? (n + 3) / 4 : 16) : (int64_t)norm_groups<T>(n) * (T < 256 ? 256 / T : 1);
+        return KQ_OK;
+    });
+    return parts;
+}
+
+struct NormMatrix {
+    const void* p;
+    int64_t ld;
+    const char* what;
+};
+static kq_status norm_check(const char* who, kq_dtype dt, const NormMatrix& m, int64_t n, int64_t d) {
+    if (!m.p) return fail(KQ_EINVAL, "%s: null %s", who, m.what);
+    if (m.ld < d) return fail(KQ_ESHAPE, "%s: leading dimension of %s too small", who, m.what);
+    if (!aligned16(m.p) || m.ld % (dt == KQ_BF16 ? 8 : 4))
+        return fail(KQ_EINVAL, "%s: rows of %s must be 16-byte aligned", who, m.what);
+    if (m.ld > TL_LD_MAX / 4 || n > TL_ROWS_MAX) return fail(KQ_ESHAPE, "%s: %s too large", who, m.what);
+    return KQ_OK;
+}
+static kq_status norm_args(const char* who, kq_dtype dt, int64_t n, int64_t d, kq_norm kind, const void* gamma, const void* beta) {
+    if (n < 0 || d <= 0) return fail(KQ_ESHAPE, "%s: bad sizes", who);
+    if (dt != KQ_F32 && dt != KQ_BF16) return fail(KQ_EINVAL, "%s: bad dtype", who);
+    if (kind != KQ_NORM_LAYER && kind != KQ_NORM_RMS) return fail(KQ_EINVAL, "%s: bad kind", who);
+    if (!aligned16(gamma) || !aligned16(beta)) return fail(KQ_EINVAL, "%s: gamma and beta must be 16-byte aligned", who);
+    return KQ_OK;
+}
+static bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+}  // namespace kq
+
+using namespace kq;
+
+size_t norm_backward_ws(int64_t d, int64_t n, kq_dtype dt) {
+    if (n <= 0 || d <= 0) return 0;
+    return sizeof(float) * (size_t)(2 * d * norm_parts(n, d, dt == KQ_BF16));
+}
+
+extern "C" kq_status kq_norm_forward(const void* X, int64_t ldx, const void* gamma, const void* beta, kq_dtype dt, int64_t n,
+                                     int64_t d, kq_norm kind, float eps, void* Y, int64_t ldy, float* mean, float* rstd,
+                                     kq_stream stream) {
+    const char* who = "kq_norm_forward";
+    KQ_TRY(norm_args(who, dt, n, d, kind, gamma, beta));
+    if (!(eps > 0.0f) || !(eps <= 1.0f)) return fail(KQ_EINVAL, "%s: eps must lie in (0, 1]", who);
+    if (n == 0) return KQ_OK;
+    KQ_TRY(norm_check(who, dt, NormMatrix{X, ldx, "X"}, n, d));
+    KQ_TRY(norm_check(who, dt, NormMatrix{Y, ldy, "Y"}, n, d));
+    if (!aligned4(mean) || !aligned4(rstd)) return fail(KQ_EINVAL, "%s: mean and rstd must be aligned to 4 bytes", who);
+    NormArgs g{};
+    g.X = X; g.ldx = ldx; g.gamma = gamma; g.beta = beta; g.n = n; g.d = d; g.eps = eps; g.layer = kind == KQ_NORM_LAYER;
+    g.Y = Y; g.ldy = ldy; g.mean = mean; g.rstd = rstd;
+    return with_rows(dt == KQ_BF16, d, [&](auto bf, auto t, auto ch) {
+        constexpr bool BF = decltype(bf)::value;
+        constexpr int T = decltype(t)::value, CH = decltype(ch)::value;
+        if constexpr (CH == 0)
+            hipLaunchKernelGGL((norm_forward_long_kernel<BF>), dim3(row_groups<1024>(n)), dim3(1024), 0, hs(stream), g);
+        else
+            hipLaunchKernelGGL((norm_forward_kernel<BF, T, CH>), dim3(row_groups<T>(n)), dim3(T < 256 ? 256 : T), 0, hs(stream), g);
+        return check_launch(who);
+    });
+}
+
+extern "C" kq_status kq_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* gamma, const float* mean,
+                                      const float* rstd, kq_dtype dt, int64_t n, int64_t d, kq_norm kind, void* dX, int64_t lddx,
+                                      void* dgamma, void* dbeta, void* ws, size_t ws_bytes, kq_stream stream) {
+    const char* who = "kq_norm_backward";
+    KQ_TRY(norm_args(who, dt, n, d, kind, gamma, nullptr));
+    if (!aligned4(dgamma) || !aligned4(dbeta)) return fail(KQ_EINVAL, "%s: dgamma and dbeta must be aligned to 4 bytes", who);
+    if (n > 0) {
+        KQ_TRY(norm_check(who, dt, NormMatrix{dY, lddy, "dY"}, n, d));
+        KQ_TRY(norm_check(who, dt, NormMatrix{X, ldx, "X"}, n, d));
+        if (dX) KQ_TRY(norm_check(who, dt, NormMatrix{dX, lddx, "dX"}, n, d));
+        if (!rstd || (kind == KQ_NORM_LAYER && !mean)) return fail(KQ_EINVAL, "%s: null statistics", who);
+        if (!aligned4(mean) || !aligned4(rstd)) return fail(KQ_EINVAL, "%s: mean and rstd must be aligned to 4 bytes", who);
+    }
+    const bool weights = dgamma || dbeta;
+    const int64_t parts = n > 0 ? norm_parts(n, d, dt == KQ_BF16) : 0;
+    if (weights && n > 0 && (!ws || !aligned16(ws) || ws_bytes < sizeof(float) * (size_t)(2 * d * parts)))
+        return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
+    NormArgs g{};
+    g.X = X; g.ldx = ldx; g.dY = dY; g.lddy = lddy; g.gamma = gamma; g.n = n; g.d = d; g.layer = kind == KQ_NORM_LAYER;
+    g.Y = dX; g.ldy = lddx; g.mean = const_cast<float*>(mean); g.rstd = const_cast<float*>(rstd);
+    g.part = weights ? static_cast<float*>(ws) : nullptr;
+    const hipStream_t st = hs(stream);
+    if (n > 0 && (dX || weights))
+        KQ_TRY(with_rows(dt == KQ_BF16, d, [&](auto bf, auto t, auto ch) {
+            constexpr bool BF = decltype(bf)::value;
+            constexpr int T = decltype(t)::value, CH = decltype(ch)::value;
+            if constexpr (CH == 0) {
+                // the weights' sums first: dX may overwrite what they read
+                constexpr int64_t wide = 64 * row_chunk<BF>();
+                if (weights)
+                    hipLaunchKernelGGL((norm_weights_long_kernel<BF>), dim3((unsigned)((d + wide - 1) / wide), (unsigned)(parts / 4)),
+                                       dim3(256), 0, st, g);
+                KQ_TRY(check_launch(who));
+                if (dX) hipLaunchKernelGGL((norm_backward_long_kernel<BF>), dim3(row_groups<1024>(n)), dim3(1024), 0, st, g);
+            } else {
+                hipLaunchKernelGGL((norm_backward_kernel<BF, T, CH>), dim3(norm_groups<T>(n)), dim3(T < 256 ? 256 : T), 0, st, g);
+            }
+            return check_launch(who);
+        }));
+    if (!weights) return KQ_OK;
+    hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((2 * d + 63) / 64)), dim3(256), 0, st, g.part, parts, d, dgamma, dbeta, (int)dt);
+    return check_launch(who);
+}

@@ -1,14 +1,15 @@
-// Matrix-core products shared by the microscaled 4-bit operators (mx.hip) and the gated feed-forward
-// block (gated.hip). Not part of the C ABI.
+// Matrix-core products shared by the microscaled 4-bit operators (mx.hip), the gated feed-forward block (gated.hip),
+// the 8-bit integer products (i8.hip) and the products grouped by expert (grouped.hip). Not part of the C ABI.
 //
-// Every operand is handled in 16-byte chunks along its rows: 4 fp32, 8 bf16 or 32 E2M1 values (one
+// Every operand is handled in 16-byte chunks along its rows: 4 fp32, 8 bf16, 16 int8 or 32 E2M1 values (one
 // microscaled block). A lane of an MFMA operand holds exactly one chunk, lane group g = lane / 16
 // owning chunk g of four, so one step of four chunks is
 //   fp32   four v_mfma_f32_16x16x4_f32          (16 columns of K; element e of every chunk pairs up)
 //   bf16   one  v_mfma_f32_16x16x32_bf16        (32 columns)
+//   int8   one  v_mfma_i32_16x16x64_i8          (64 columns, int32 sums)
 //   E2M1   one  v_mfma_scale_f32_16x16x128      (128 columns, one E8M0 scale byte per lane)
 // and one slab of 128 bytes a row is two steps whatever the type: the staging, the LDS layout and the
-// loops below are written once for the three.
+// loops below are written once for the four.
 #pragma once
 
 #include <atomic>
@@ -24,9 +25,23 @@ typedef int tl_i8 __attribute__((ext_vector_type(8)));
 typedef short tl_s4 __attribute__((ext_vector_type(4)));
 typedef __bf16 tl_b8 __attribute__((ext_vector_type(8)));
 
-enum { EL_F32 = 0, EL_BF16 = 1, EL_MX = 2 };
+enum { EL_F32 = 0, EL_BF16 = 1, EL_MX = 2, EL_I8 = 3 };
 template <int E>
-constexpr int el_chunk() { return E == EL_F32 ? 4 : E == EL_BF16 ? 8 : 32; }   // values in 16 bytes
+constexpr int el_chunk() { return E == EL_F32 ? 4 : E == EL_BF16 ? 8 : E == EL_I8 ? 16 : 32; }   // values in 16 bytes
+template <int E>
+using el_sums = std::conditional_t<E == EL_I8, tl_i4, tl_f4>;                  // four sums of a lane
+
+// A 16-byte chunk of which only the first `part` values count, the others made zero.
+template <int E>
+__device__ __forceinline__ tl_i4 chunk_head(tl_i4 v, int part) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        if constexpr (E == EL_F32) v[e] = e < part ? v[e] : 0;
+        else if constexpr (E == EL_BF16) v[e] = 2 * e + 1 < part ? v[e] : 2 * e < part ? v[e] & 0xFFFF : 0;
+        else v[e] = 4 * e + 3 < part ? v[e] : 4 * e < part ? v[e] & ((1 << 8 * (part - 4 * e)) - 1) : 0;
+    }
+    return v;
+}
 
 // ------------------------------------------------------------------------------------ conversions
 __device__ __forceinline__ uint16_t to_bf16(float v) {   // nearest even, NaN stays NaN
@@ -135,8 +150,10 @@ __device__ __forceinline__ tl_f4 mma_mx(tl_i4 a, tl_i4 b, tl_f4 c, int sa, int s
 // c += a b over one step; for E2M1 byte oa of sa and byte ob of sb are the lane's block scales
 // (oa and ob are constants after unrolling)
 template <int E>
-__device__ __forceinline__ tl_f4 mma_step(tl_i4 a, tl_i4 b, tl_f4 c, int sa, int oa, int sb, int ob) {
-    if constexpr (E == EL_BF16) {
+__device__ __forceinline__ el_sums<E> mma_step(tl_i4 a, tl_i4 b, el_sums<E> c, int sa, int oa, int sb, int ob) {
+    if constexpr (E == EL_I8) {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+    } else if constexpr (E == EL_BF16) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(tl_b8, a), __builtin_bit_cast(tl_b8, b), c, 0, 0, 0);
     } else if constexpr (E == EL_F32) {
 #pragma unroll
@@ -170,8 +187,10 @@ __device__ __forceinline__ tl_f4 mma_step(tl_i4 a, tl_i4 b, tl_f4 c, int sa, int
 //   TP_PLAIN   Y = A B^T                        A: M x K, B: N x K
 //   TP_GATED   Y = act(A B^T) * (A B2^T), optionally the two products themselves
 //   TP_GRAD_X  Y = A B + A2 B2                  A: M x K, B: K x N
+//   TP_GRAD_X1 Y = A B                          A: M x K, B: K x N
 //   TP_GRAD_W  Y = A^T B, Y2 = A2^T B           A: K x M, B: K x N
-enum { TP_PLAIN = 0, TP_GATED = 1, TP_GRAD_X = 2, TP_GRAD_W = 3 };
+enum { TP_PLAIN = 0, TP_GATED = 1, TP_GRAD_X = 2, TP_GRAD_W = 3, TP_GRAD_X1 = 4 };
+constexpr bool tp_grad_x(int mode) { return mode == TP_GRAD_X || mode == TP_GRAD_X1; }
 
 struct TileArgs {
     int64_t M, N, K;                     // K in values
@@ -188,7 +207,8 @@ struct TileArgs {
     int pairs;                           // TP_GRAD_W: products (2, or 1 when one gradient is wanted)
     int whole;                           // the first `whole` tiles (of each pair) take all of K, one work-group each;
     int splits, sper;                    // the others are cut into `splits` work-groups of `sper` slabs, whose sums go
-    float* part;                         // to part + (cut tile * splits + split) * TM * TN, rows of TN
+    float* part;                         // to part + (cut tile * splits + split) * TM * TN, rows of TN (int8: int32 sums)
+    const float *fA, *fB, *fB2;          // int8: the scales of the rows
 };
 
 // Tile shapes: TM rows of A by TN rows of B (half gate, half up when gated), WM x WN wavefronts.
@@ -327,10 +347,10 @@ __device__ __forceinline__ void landed_barrier() {
 // shape M walk 43 slabs each in 34 us, 0.79 us a slab whose matrix instructions take 0.25 (32 a wavefront, one wavefront a SIMD),
 // since one slab's products are all that covers the next but one's loads.
 template <int E, int MODE, typename C>
-__device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
+__device__ __forceinline__ void tile_body(const TileArgs& g, const TileAt& at) {
     extern __shared__ __align__(16) char tl_sm[];
-    constexpr bool TA = MODE == TP_GRAD_W, TB = MODE == TP_GRAD_X || MODE == TP_GRAD_W, GATED = MODE == TP_GATED;
-    static_assert(!TB || E != EL_MX, "blocks of E2M1 lie along K");
+    constexpr bool TA = MODE == TP_GRAD_W, TB = tp_grad_x(MODE) || MODE == TP_GRAD_W, GATED = MODE == TP_GATED;
+    static_assert(!TB || (E != EL_MX && E != EL_I8), "blocks of E2M1 lie along K; int8 has no gradients");
     constexpr bool HID = TB && E == EL_BF16;
     constexpr int EPC = el_chunk<E>(), BK = 8 * EPC, ES = 16 / (E == EL_MX ? 16 : EPC);   // ES: bytes of a dense value
     constexpr int FM = C::FM, FN = C::FN, QA = C::QA, QB = C::QB;
@@ -340,7 +360,6 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int x16 = lane & 15, g4 = lane >> 4;
     const int wm = wave / C::WN, wn = wave % C::WN, grp = wn / SUB, sub = wn % SUB;
-    const TileAt at = tile_of(id, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g);
     const int64_t m0 = (int64_t)at.tm * C::TM, n0 = (int64_t)at.tn * TN_OUT;
     const int mlast = (int)(g.M - 1 - m0 < C::TM - 1 ? g.M - 1 - m0 : C::TM - 1);          // last row inside
     const int nlast = (int)(g.N - 1 - n0 < TN_OUT - 1 ? g.N - 1 - n0 : TN_OUT - 1);
@@ -451,15 +470,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) alone
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         char* la = tl_sm + buf * C::BUF + wave * 1024 + lane * 16;
-        auto cut = [&](char* p) {
-            tl_i4 v = *reinterpret_cast<tl_i4*>(p);
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                if constexpr (E == EL_F32) v[e] = e < part ? v[e] : 0;
-                else v[e] = 2 * e + 1 < part ? v[e] : 2 * e < part ? v[e] & 0xFFFF : 0;
-            }
-            *reinterpret_cast<tl_i4*>(p) = v;
-        };
+        auto cut = [&](char* p) { *reinterpret_cast<tl_i4*>(p) = chunk_head<E>(*reinterpret_cast<tl_i4*>(p), part); };
         const int last = (int)((nch - 1) & 7);           // the chunk's place in the slab
         if (!TA && cA == last)
             for (int q = 0; q < QA; q++) cut(la + q * C::W * 1024);
@@ -467,11 +478,11 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
             for (int q = 0; q < QB; q++) cut(la + C::OPA + q * C::W * 1024);
     };
 
-    tl_f4 acc[FM][FN];
+    el_sums<E> acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; i++)
 #pragma unroll
-        for (int j = 0; j < FN; j++) acc[i][j] = tl_f4{0, 0, 0, 0};
+        for (int j = 0; j < FN; j++) acc[i][j] = el_sums<E>{0, 0, 0, 0};
 
     // Scales of a slab's two steps (E2M1). Shapes L and M take them laid out, a dword of a lane for four fragments
     // (64 rows). Shape S reads 8 bytes (a slab) of the row of each of its 4 fragments, which saves the
@@ -696,6 +707,23 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
     const int64_t ldY = cut ? C::TN : w2 ? g.ldy2 : g.ldy;
     const int dt = cut ? KQ_F32 : g.dt;
     const int64_t nrun = n0 + grp * GW + g4 * (4 * GF) + 4 * sub * FW;
+    // int8: a sum times the scales of its two rows, their product first (a token's large scale and a weight's small one
+    // cancel); a cut tile keeps the whole numbers
+    float cs[E == EL_I8 ? 4 * FW : 1], cs2[E == EL_I8 && GATED ? 4 * FW : 1];
+    if constexpr (E == EL_I8) {
+        if (!cut) {
+#pragma unroll
+            for (int e = 0; e < 4 * FW; e++) {
+                const int64_t n = nrun + e < g.N ? nrun + e : g.N - 1;
+                cs[e] = g.fB[n];
+                if constexpr (GATED) cs2[e] = g.fB2[n];
+            }
+        }
+    }
+    auto value = [&](auto sum, float sa, float sb) {
+        if constexpr (E == EL_I8) return cut ? __int_as_float(sum) : (float)sum * (sa * sb);
+        else return sum;
+    };
 #pragma unroll
     for (int i = 0; i < FM; i++) {
         const int64_t m = m0 + wm * FM * 16 + 16 * i + x16;
@@ -708,11 +736,12 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
                 store_run<4>(Y, dt, m * ldY + n, v, g.N - n);
             }
         } else {
+            const float rs = E == EL_I8 && !cut ? g.fA[m] : 0.0f;
             float a[4 * FW];
 #pragma unroll
             for (int j = 0; j < FW; j++)
 #pragma unroll
-                for (int r = 0; r < 4; r++) a[4 * j + r] = acc[i][j][r];
+                for (int r = 0; r < 4; r++) a[4 * j + r] = value(acc[i][j][r], rs, cs[E == EL_I8 ? 4 * j + r : 0]);
             if constexpr (!GATED) {
                 store_run<4 * FW>(Y, dt, m * ldY + nrun, a, g.N - nrun);
             } else {
@@ -720,7 +749,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
 #pragma unroll
                 for (int j = 0; j < FW; j++)
 #pragma unroll
-                    for (int r = 0; r < 4; r++) b[4 * j + r] = acc[i][j + FW][r];
+                    for (int r = 0; r < 4; r++) b[4 * j + r] = value(acc[i][j + FW][r], rs, cs2[E == EL_I8 && GATED ? 4 * j + r : 0]);
                 if (cut) {
                     store_run<4 * FW>(pt, KQ_F32, m * C::TN + nrun, a, g.N - nrun);
                     store_run<4 * FW>(pt, KQ_F32, m * C::TN + C::TN / 2 + nrun, b, g.N - nrun);
@@ -735,9 +764,16 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, int id) {
     }
 }
 
+// the tile of work-group `id` of a whole product
+template <int MODE, typename C>
+__device__ __forceinline__ TileAt tile_at(const TileArgs& g, int id) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
+    return tile_of(id, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g);
+}
+
 template <int E, int MODE, typename C>
 __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
-    tile_body<E, MODE, C>(g, (int)blockIdx.x);
+    tile_body<E, MODE, C>(g, tile_at<MODE, C>(g, (int)blockIdx.x));
 }
 
 // dX and the weight gradients side by side: `first` work-groups for dX, the rest for the others. For small products, which
@@ -745,14 +781,14 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_kernel(TileArgs g) {
 // after the other 9.5 and 9.1 and a launch between; the whole call 22.9 -> 19.3 us).
 template <int E, typename C>
 __global__ __launch_bounds__(C::THREADS, C::EU) void tile_grads_kernel(TileArgs x, TileArgs w, int first) {
-    if ((int)blockIdx.x < first) tile_body<E, TP_GRAD_X, C>(x, (int)blockIdx.x);
-    else tile_body<E, TP_GRAD_W, C>(w, (int)blockIdx.x - first);
+    if ((int)blockIdx.x < first) tile_body<E, TP_GRAD_X, C>(x, tile_at<TP_GRAD_X, C>(x, (int)blockIdx.x));
+    else tile_body<E, TP_GRAD_W, C>(w, tile_at<TP_GRAD_W, C>(w, (int)blockIdx.x - first));
 }
 
 // Sums of the splits, in split order, and the epilogue: 4 columns a thread, TM * TN_OUT / 1024 work-groups a tile.
 // HBM-bound, or latency (96 L tiles in two splits, the tail of the weight gradients at 8192 tokens: 10.6 us, 5.9 TB/s;
 // 16 S tiles in 15: 4 us). Splits are not added by atomics: their order would change the sums.
-template <int MODE, typename C>
+template <int MODE, typename C, int E = EL_F32>
 __device__ __forceinline__ void tile_reduce(const TileArgs& g, int block) {
     constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
     TileAt at;
@@ -761,23 +797,30 @@ __device__ __forceinline__ void tile_reduce(const TileArgs& g, int block) {
     const int64_t m = (int64_t)at.tm * C::TM + r, n = (int64_t)at.tn * TN_OUT + c;
     if (m >= g.M || n >= g.N) return;
     const float* p = g.part + (int64_t)at.cut * g.splits * (C::TM * C::TN) + r * C::TN + c;
-    auto sum = [&](const float* q, float (&v)[4]) {
-        auto load = [&](int k) { return *reinterpret_cast<const float4*>(q + (int64_t)k * (C::TM * C::TN)); };
-        float4 s = load(0);
-        auto add = [&](const float4& t) { s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w; };
+    auto sum = [&](const float* q, const float* scales, float (&v)[4]) {
+        auto load = [&](int k) { return *reinterpret_cast<const el_sums<E>*>(q + (int64_t)k * (C::TM * C::TN)); };
+        el_sums<E> s = load(0);
+        auto add = [&](const el_sums<E>& t) {
+#pragma unroll
+            for (int r = 0; r < 4; r++) s[r] += t[r];
+        };
         int k = 1;
         for (; k + 4 <= g.splits; k += 4) {      // four loads in flight, added in order
-            const float4 t0 = load(k), t1 = load(k + 1), t2 = load(k + 2), t3 = load(k + 3);
+            const el_sums<E> t0 = load(k), t1 = load(k + 1), t2 = load(k + 2), t3 = load(k + 3);
             add(t0); add(t1); add(t2); add(t3);
         }
         for (; k < g.splits; k++) add(load(k));
-        v[0] = s.x; v[1] = s.y; v[2] = s.z; v[3] = s.w;
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            if constexpr (E == EL_I8) v[r] = (float)s[r] * (g.fA[m] * scales[n + r < g.N ? n + r : g.N - 1]);
+            else v[r] = s[r];
+        }
     };
     float a[4];
-    sum(p, a);
+    sum(p, g.fB, a);
     if constexpr (MODE == TP_GATED) {
         float b[4], h[4];
-        sum(p + C::TN / 2, b);
+        sum(p + C::TN / 2, g.fB2, b);
         act_times(h, a, b, g.act);
         store_run<4>(g.Y, g.dt, m * g.ldy + n, h, g.N - n);
         if (g.Y2) store_run<4>(g.Y2, g.dt, m * g.ldy2 + n, a, g.N - n);
@@ -788,9 +831,9 @@ __device__ __forceinline__ void tile_reduce(const TileArgs& g, int block) {
     }
 }
 
-template <int MODE, typename C>
+template <int MODE, typename C, int E>
 __global__ __launch_bounds__(256) void tile_reduce_kernel(TileArgs g) {
-    tile_reduce<MODE, C>(g, (int)blockIdx.x);
+    tile_reduce<MODE, C, E>(g, (int)blockIdx.x);
 }
 
 template <typename C>
@@ -872,25 +915,29 @@ kq_status tile_grids(TileGrids& n, TileArgs& g, const TilePlan& p, const char* w
     return KQ_OK;
 }
 
-template <int E, int MODE, typename C>
-kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const char* who) {
-    TileGrids n;
-    KQ_TRY((tile_grids<MODE, C>(n, g, p, who)));
-    // the allowance for dynamic LDS belongs to a device's copy of the kernel: asked for once a device
-    static std::atomic<uint64_t> allowed{0};
+// The allowance for dynamic LDS belongs to a device's copy of a kernel: asked for once a device.
+inline kq_status allow_lds(const void* kernel, size_t bytes, std::atomic<uint64_t>& allowed, const char* who) {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) return fail(KQ_EHIP, "%s: no current device", who);
     const uint64_t bit = 1ull << (dev & 63);
     if (dev > 63 || !(allowed.load(std::memory_order_relaxed) & bit)) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_kernel<E, MODE, C>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != hipSuccess) return fail(KQ_EHIP, "%s: %s", who, hipGetErrorString(e));
         if (dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
     }
+    return KQ_OK;
+}
+
+template <int E, int MODE, typename C>
+kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const char* who) {
+    TileGrids n;
+    KQ_TRY((tile_grids<MODE, C>(n, g, p, who)));
+    static std::atomic<uint64_t> allowed{0};
+    KQ_TRY(allow_lds(reinterpret_cast<const void*>(&tile_kernel<E, MODE, C>), C::SMEM, allowed, who));
     hipLaunchKernelGGL((tile_kernel<E, MODE, C>), dim3((unsigned)n.tiles), dim3(C::THREADS), C::SMEM, st, g);
     KQ_TRY(check_launch(who));
     if (n.sums) {
-        hipLaunchKernelGGL((tile_reduce_kernel<MODE, C>), dim3((unsigned)n.sums), dim3(256), 0, st, g);
+        hipLaunchKernelGGL((tile_reduce_kernel<MODE, C, E == EL_I8 ? EL_I8 : EL_F32>), dim3((unsigned)n.sums), dim3(256), 0, st, g);
         KQ_TRY(check_launch(who));
     }
     return KQ_OK;
@@ -949,6 +996,7 @@ struct FewArgs {
     void *Y, *Y2, *Y3;
     int64_t ldy, ldy2, ldy3;
     int dt, act;
+    const float *fA, *fB, *fB2;           // int8: the scales of the rows
 };
 
 constexpr int FEW_WAVES = 8, FEW_THREADS = 64 * FEW_WAVES;
@@ -984,13 +1032,7 @@ __device__ __forceinline__ void few_load(FewFrag<E>& f, const char* row, const u
             const int64_t c = s * 8 + 4 * h + g4;
             tl_i4 v = {0, 0, 0, 0};
             if (c < nch) v = *reinterpret_cast<const tl_i4*>(p + 64 * h);
-            if (E != EL_MX && part && c == nch - 1) {
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    if constexpr (E == EL_F32) v[e] = e < part ? v[e] : 0;
-                    else v[e] = 2 * e + 1 < part ? v[e] : 2 * e < part ? v[e] & 0xFFFF : 0;
-                }
-            }
+            if (E != EL_MX && part && c == nch - 1) v = chunk_head<E>(v, part);
             f.c[h] = v;
         }
     }
@@ -1010,13 +1052,14 @@ __device__ __forceinline__ void few_load(FewFrag<E>& f, const char* row, const u
     }
 }
 
+// rows 16 block .. of B, the first 16 NB rows of A
 template <int E, bool GATED, int NB>
-__global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
+__device__ __forceinline__ void few_body(const FewArgs& g, int64_t block) {
     extern __shared__ __align__(16) float few_sm[];       // [wave][matrix][token block][lane][4]
     constexpr int EPC = el_chunk<E>(), MATS = GATED ? 2 : 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int x16 = lane & 15, g4 = lane >> 4;
-    const int64_t f0 = (int64_t)blockIdx.x * 16;
+    const int64_t f0 = block * 16;
     const int64_t row = f0 + x16 < g.o ? f0 + x16 : g.o - 1;
     const char* rB = g.B + row * g.ldb;
     const char* rB2 = GATED ? g.B2 + row * g.ldb2 : nullptr;
@@ -1034,11 +1077,12 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
     const int part = (int)(g.K % EPC);
     const int64_t full = E == EL_MX ? nch / 8 : g.K / (8 * EPC);      // slabs whose chunks are all whole
 
-    tl_f4 acc[MATS][NB];
+    typedef el_sums<E> Sums;
+    Sums acc[MATS][NB];
 #pragma unroll
     for (int m = 0; m < MATS; m++)
 #pragma unroll
-        for (int b = 0; b < NB; b++) acc[m][b] = tl_f4{0, 0, 0, 0};
+        for (int b = 0; b < NB; b++) acc[m][b] = Sums{0, 0, 0, 0};
     // U slabs at a time: all their loads are in flight before the first product (dense types with two are slower)
     auto batch = [&](int64_t s, auto UC, bool whole) {
         constexpr int U = UC.value;
@@ -1071,38 +1115,44 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
     for (int m = 0; m < MATS; m++)
 #pragma unroll
         for (int b = 0; b < NB; b++)
-            reinterpret_cast<tl_f4*>(few_sm)[((wave * MATS + m) * NB + b) * 64 + lane] = acc[m][b];
+            reinterpret_cast<Sums*>(few_sm)[((wave * MATS + m) * NB + b) * 64 + lane] = acc[m][b];
     __syncthreads();
     if (wave >= NB) return;
     // wavefront b finishes token block b: lane holds token x16 and rows f0 + 4 g4 .. + 3
-    tl_f4 sum[MATS];
+    Sums sum[MATS];
 #pragma unroll
     for (int m = 0; m < MATS; m++) {
-        sum[m] = tl_f4{0, 0, 0, 0};
+        sum[m] = Sums{0, 0, 0, 0};
         for (int w = 0; w < FEW_WAVES; w++) {
-            const tl_f4 v = reinterpret_cast<const tl_f4*>(few_sm)[((w * MATS + m) * NB + wave) * 64 + lane];
+            const Sums v = reinterpret_cast<const Sums*>(few_sm)[((w * MATS + m) * NB + wave) * 64 + lane];
 #pragma unroll
             for (int r = 0; r < 4; r++) sum[m][r] += v[r];
         }
     }
     const int64_t t = 16 * wave + x16, n = f0 + 4 * g4;
     if (t >= g.n) return;
-    float y[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
-    if constexpr (GATED) {
-        const float a[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]}, b[4] = {sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
-        act_times(y, a, b, g.act);
-    }
-    store_run<4>(g.Y, g.dt, t * g.ldy + n, y, g.o - n);
-    if constexpr (GATED) {
-        if (g.Y2) {
-            const float v[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
-            store_run<4>(g.Y2, g.dt, t * g.ldy2 + n, v, g.o - n);
+    float v[MATS][4];
+#pragma unroll
+    for (int m = 0; m < MATS; m++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            if constexpr (E == EL_I8) v[m][r] = (float)sum[m][r] * (g.fA[t] * (m ? g.fB2 : g.fB)[n + r < g.o ? n + r : g.o - 1]);
+            else v[m][r] = sum[m][r];
         }
-        if (g.Y3) {
-            const float v[4] = {sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
-            store_run<4>(g.Y3, g.dt, t * g.ldy3 + n, v, g.o - n);
-        }
+    if constexpr (GATED) {
+        float y[4];
+        act_times(y, v[0], v[1], g.act);
+        store_run<4>(g.Y, g.dt, t * g.ldy + n, y, g.o - n);
+        if (g.Y2) store_run<4>(g.Y2, g.dt, t * g.ldy2 + n, v[0], g.o - n);
+        if (g.Y3) store_run<4>(g.Y3, g.dt, t * g.ldy3 + n, v[1], g.o - n);
+    } else {
+        store_run<4>(g.Y, g.dt, t * g.ldy + n, v[0], g.o - n);
     }
+}
+
+template <int E, bool GATED, int NB>
+__global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
+    few_body<E, GATED, NB>(g, (int64_t)blockIdx.x);
 }
 
 template <int E, bool GATED>

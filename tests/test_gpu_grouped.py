@@ -1,0 +1,310 @@
+"""Products grouped by expert on the GPU. Operands are small whole numbers, so that every partial sum of a product is a whole
+number below 2^24, which fp32 holds in any order: the result is the definition's rounded once and the tolerance
+is zero. Ordinary values and the other activations: bounds of the gated block's tests."""
+import numpy as np
+import pytest
+
+from oracle import blocks as ob
+from oracle import experts as oe
+from post_quantization_03_amd import _lib as K
+from tests.gpu_util import host, say, torch_dev
+from tests.test_gpu_blocks import E23, HALF, KINDS, check, gated_tol, get, mat, put
+from tests.test_gpu_blocks_plans import generator, out, same, whole_numbers
+from tests.test_gpu_i8 import Workspace, dealt, offsets
+
+pytestmark = pytest.mark.gpu
+
+
+def stack(e, o, i, dt, top, g):
+    """e matrices of whole numbers one under the other, NaN in the padding; and as float64."""
+    t, v = whole_numbers(e * o, i, dt, top, g)
+    return t.as_strided((e, o, i), (o * t.stride(0), t.stride(0), 1)), v.view(e, o, i)
+
+
+def out_stack(e, o, i, dt):
+    t = out(e * o, i, dt)
+    return t, t.as_strided((e, o, i), (o * t.stride(0), t.stride(0), 1))
+
+
+# few rows an expert, one expert with more; tile shapes of 256, 128 and 64 rows; more experts than lanes
+FORWARD = [("bf16", 1, 1, 40, 33), ("bf16", 3, 4, 41, 100), ("bf16", 64, 16, 70, 1000), ("bf16", 90, 70, 40, 65), ("bf16", 200, 150, 30, 100),
+           ("bf16", 100, 3, 33, 400), ("bf16", 500, 7, 130, 257), ("bf16", 776, 12, 2812, 9), ("bf16", 202, 3, 5637, 10),
+           ("bf16", 3250, 1, 2435, 538), ("bf16", 3000, 5, 1100, 900), ("bf16", 4100, 130, 70, 48),
+           ("f32", 1, 1, 40, 33), ("f32", 64, 16, 70, 1000), ("f32", 517, 5, 130, 257), ("f32", 300, 70, 40, 65), ("f32", 1000, 3, 200, 72)]
+
+
+@pytest.mark.parametrize("dt,n,e,o,i", FORWARD)
+def test_grouped_forward_exact(dt, n, e, o, i):
+    """Whole numbers of at most 4: products of at most 16, 1000 of which sum to less than 2^14."""
+    import torch
+    say(f"grouped forward {dt} n={n} e={e} o={o} i={i}")
+    g = generator(n + e + o + i)
+    X, x = whole_numbers(n, i, dt, 4, g)
+    (W, w), (U, u) = stack(e, o, i, dt, 4, g), stack(e, o, i, dt, 4, g)
+    for off in (dealt(n, e, g), dealt(n, e, g, n // 4, n - n // 5), offsets([0] * e + [n])):
+        a, b = torch.zeros((n, o), dtype=torch.float64, device=X.device), torch.zeros((n, o), dtype=torch.float64, device=X.device)
+        inside = torch.zeros(n, dtype=torch.bool, device=X.device)
+        for k, p, q in oe.spans(host(off), n):
+            a[p:q], b[p:q], inside[p:q] = torch.mm(x[p:q], w[k].T), torch.mm(x[p:q], u[k].T), True
+        Y, H, A, B, H2 = (out(n, o, dt) for _ in range(5))
+        K.kq_grouped_gemm(X, W, off, Y, Workspace("grouped_gemm", o, i, n, dt, e).ws)
+        K.kq_grouped_gated(X, W, U, off, "relu", H, A, B, Workspace("grouped_gated", o, i, n, dt, e).ws)
+        K.kq_grouped_gated(X, W, U, off, "relu", H2, B=None)
+        assert torch.equal(H, H2)
+        for t, want, name in ((Y, a, "Y"), (A, a, "A"), (B, b, "B"), (H, a.float().clamp(min=0) * b.float(), "H")):
+            assert bool((t[~inside] == -77.0).all()), name + ": rows outside the offsets"
+            t[~inside] = 0.0
+            same(t, want, dt, name)
+    # NaN in a row that no expert owns stays out; in one that some expert owns it stays in its row
+    off = offsets([1] + [n] * e) if n > 1 else offsets([0] + [1] * e)
+    X[0, i - 1], X[n - 1, 0] = float("nan"), float("nan")
+    Y = out(n, o, dt)
+    K.kq_grouped_gemm(X, W, off, Y)
+    assert bool(torch.isnan(Y[n - 1]).all())
+    if n > 1:
+        assert bool((Y[0] == -77.0).all())
+        same(Y[1:n - 1], torch.mm(x[1:n - 1], w[0].T), dt, "Y beside NaN")
+
+
+@pytest.mark.parametrize("n,e,o,i", [(50, 6, 40, 64), (300, 5, 70, 130)])
+def test_any_offsets_stay_inside(n, e, o, i):
+    """Offsets that decrease, are negative or lie past the rows are read as the header says, in every entry point."""
+    import torch
+    g = generator(n)
+    X, x = whole_numbers(n, i, "bf16", 4, g)
+    W, w = stack(e, o, i, "bf16", 4, g)
+    dY, dy = whole_numbers(n, o, "bf16", 4, g)
+    big = 2 ** 31 - 1
+    for values in ([0] * (e + 1), [n] * (e + 1), [-5, n // 2, 3, n // 2 + 4, big, 7, n][:e + 1], [big] * (e + 1), [-big - 1] * e + [big],
+                   [n // 3, 0, 0, n - 1, 2 * n, 0, 0][:e + 1]):
+        off = offsets(values)
+        Y, dX, (flat, dW) = out(n, o, "bf16"), out(n, i, "bf16"), out_stack(e, o, i, "bf16")
+        K.kq_grouped_gemm(X, W, off, Y)
+        K.kq_grouped_backward(dY, X, W, off, dX, dW)
+        wy, inside = oe.grouped(host(x), host(w), values)
+        wx, ww = oe.grouped_grad(host(dy), host(x), host(w), values)
+        out_rows = torch.from_numpy(~inside).to(X.device)
+        for t, want, name in ((Y, wy, "Y"), (dX, wx, "dX")):
+            assert bool((t[out_rows] == -77.0).all()), name
+            t[out_rows] = 0.0
+            same(t, torch.from_numpy(want).to(X.device), "bf16", name)
+        same(flat, torch.from_numpy(ww).to(X.device).view(e * o, i), "bf16", "dW")
+
+
+# tile shapes of dX and dW: 256, 128 and 64 rows
+BACKWARD = [("bf16", 1, 1, 40, 33), ("bf16", 33, 3, 65, 70), ("bf16", 64, 16, 70, 200), ("bf16", 500, 70, 33, 65), ("bf16", 263, 4, 41, 8360),
+            ("bf16", 460, 1, 2002, 4121), ("bf16", 104, 30, 1097, 67), ("bf16", 2582, 2, 214, 3171), ("bf16", 3000, 5, 1100, 900),
+            ("bf16", 9000, 1, 40, 72),
+            ("f32", 1, 1, 40, 33), ("f32", 64, 16, 70, 200), ("f32", 517, 5, 130, 257), ("f32", 1000, 70, 40, 65)]
+
+
+@pytest.mark.parametrize("dt,n,e,o,i", BACKWARD)
+def test_grouped_backward_exact(dt, n, e, o, i):
+    """Whole numbers of at most 4: products of at most 16; 2 * 2002 and 9000 of them sum to less than 2^18."""
+    import torch
+    say(f"grouped backward {dt} n={n} e={e} o={o} i={i}")
+    g = generator(n + e + o + i)
+    X, x = whole_numbers(n, i, dt, 4, g)
+    (dY, dy), (dZ, dz) = whole_numbers(n, o, dt, 4, g), whole_numbers(n, o, dt, 4, g)
+    (W, w), (U, u) = stack(e, o, i, dt, 4, g), stack(e, o, i, dt, 4, g)
+    ws = Workspace("grouped_backward", o, i, n, dt, e).ws
+    for off in (dealt(n, e, g), dealt(n, e, g, n // 4, n - n // 5), offsets([0] * e + [n])):
+        d1, d2 = (torch.zeros((n, i), dtype=torch.float64, device=X.device) for _ in range(2))
+        gw, gu = (torch.zeros((e, o, i), dtype=torch.float64, device=X.device) for _ in range(2))
+        inside = torch.zeros(n, dtype=torch.bool, device=X.device)
+        for k, p, q in oe.spans(host(off), n):
+            d1[p:q], d2[p:q], inside[p:q] = torch.mm(dy[p:q], w[k]), torch.mm(dz[p:q], u[k]), True
+            gw[k], gu[k] = torch.mm(dy[p:q].T, x[p:q]), torch.mm(dz[p:q].T, x[p:q])
+        dX, dX1 = out(n, i, dt), out(n, i, dt)
+        (fW, dW), (fU, dU), (f1, dW1) = (out_stack(e, o, i, dt) for _ in range(3))
+        K.kq_grouped_backward(dY, X, W, off, dX, dW, dZ, U, dU, ws)
+        K.kq_grouped_backward(dY, X, W, off, dX1, dW1, ws=ws)
+        for t, want, name in ((dX, d1 + d2, "dX of two"), (dX1, d1, "dX")):
+            assert bool((t[~inside] == -77.0).all()), name + ": rows outside the offsets"
+            t[~inside] = 0.0
+            same(t, want, dt, name)
+        for t, want, name in ((fW, gw, "dW"), (f1, gw, "dW alone"), (fU, gu, "dW2")):
+            same(t, want.view(e * o, i), dt, name)
+        # any subset of the outputs has the same bits
+        dX2, (_, dU2) = out(n, i, dt), out_stack(e, o, i, dt)
+        K.kq_grouped_backward(dY, None, W, off, dX2, dY2=dZ, W2=U)
+        K.kq_grouped_backward(dY, X, None, off, dY2=dZ, dW2=dU2)
+        assert torch.equal(dX2[inside], dX[inside]) and torch.equal(dU2, dU)
+        assert bool((dX2[~inside] == -77.0).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [20, 400])
+def test_grouped_ordinary_values(n, dt):
+    """Products and gradients of normal values, all activations, against float64 with the bounds of sums of k products."""
+    torch, dev = torch_dev()
+    e, o, i = 4, 90, 150
+    rng = np.random.default_rng(n)
+    X, x = put(rng.standard_normal((n, i)), dt)
+    W, w = put(rng.standard_normal((e * o, i)) * 2 / np.sqrt(i), dt)
+    U, u = put(rng.standard_normal((e * o, i)) / np.sqrt(i), dt)
+    dY, dy = put(rng.standard_normal((n, o)), dt)
+    W3, U3 = (t.as_strided((e, o, i), (o * t.stride(0), t.stride(0), 1)) for t in (W, U))
+    w, u = w.reshape(e, o, i), u.reshape(e, o, i)
+    off = [0, n // 3, n // 3, n - 5, n]
+    a, b = oe.grouped(x, w, off)[0], oe.grouped(x, u, off)[0]
+    da, db = i * E23 * oe.grouped(np.abs(x), np.abs(w), off)[0], i * E23 * oe.grouped(np.abs(x), np.abs(u), off)[0]
+    for kind in KINDS:
+        H, A, B = mat(n, o, dt), mat(n, o, dt), mat(n, o, dt)
+        K.kq_grouped_gated(X, W3, U3, offsets(off), kind, H, A, B)
+        check(get(A), a, da + HALF[dt] * (np.abs(a) + da), "A")
+        check(get(B), b, db + HALF[dt] * (np.abs(b) + db), "B")
+        check(get(H), ob.act(a, kind)[0] * b, gated_tol(a, b, da, db, kind, dt), "H")
+    dX, dW = mat(n, i, dt), torch.empty((e, o, i + (-i) % 8), dtype=X.dtype, device=dev)[:, :, :i]
+    K.kq_grouped_backward(dY, X, W3, offsets(off), dX, dW)
+    wx, ww = oe.grouped_grad(dy, x, w, off)
+    sx, sw = oe.grouped_grad(np.abs(dy), np.abs(x), np.abs(w), off)
+    check(get(dX), wx, o * E23 * sx + HALF[dt] * (np.abs(wx) + o * E23 * sx), "dX")
+    check(get(dW), ww, n * E23 * sw + HALF[dt] * (np.abs(ww) + n * E23 * sw), "dW")
+    if dt == "f32":          # the kernel's gradients against differences of the product, which is linear in each operand
+        for grad, k in ((get(dX), 0), (get(dW), 1)):
+            V = rng.standard_normal(grad.shape)
+            lo, hi = ([x + (k == 0) * s * V if k == 0 else x, w + s * V if k == 1 else w] for s in (-0.5, 0.5))
+            diff = ((oe.grouped(*hi, off)[0] - oe.grouped(*lo, off)[0]) * dy).sum()
+            assert abs(diff - (grad * V).sum()) <= ((o if k == 0 else n) * E23 + 2.0 ** -23) * np.abs((sx, sw)[k] * V).sum()
+
+
+def test_no_rows():
+    torch, dev = torch_dev()
+    for dt in ("f32", "bf16"):
+        W = mat(6 * 20, 24, dt, fill=1.0).unflatten(0, (6, 20))
+        x, y = mat(0, 24, dt), mat(0, 20, dt)
+        off = offsets([0] * 7)
+        (f1, dW), (f2, dU) = out_stack(6, 20, 24, dt), out_stack(6, 20, 24, dt)
+        K.kq_grouped_gemm(x, W, off, y)
+        K.kq_grouped_gated(x, W, W, off, "silu", y)
+        K.kq_grouped_backward(y, x, W, off, x, dW, y, W, dU)
+        for f in (f1, f2):
+            same(f, torch.zeros((120, 24), device=dev), dt, "dW")
+
+
+def test_grouped_offsets_past_32_bits():
+    """Tokens 64 KiB apart (4.3 GB in all) and stacked weights and gradients past 2^31 values."""
+    torch, dev = torch_dev()
+    n, o, i, e = 65700, 72, 40, 3
+    g = generator(7)
+
+    def wide(d, fill=None):
+        t = torch.empty((n, 32768), dtype=torch.bfloat16, device=dev)[:, :d]
+        t.copy_(torch.randint(-4, 5, (n, d), generator=g, device=dev)) if fill is None else t.fill_(fill)
+        return t
+
+    X, dY, (W, w) = wide(i), wide(o), stack(e, o, i, "bf16", 4, g)
+    Y, dX, (fW, dW) = wide(o, -77.0), wide(i, -77.0), out_stack(e, o, i, "bf16")
+    cut = 65600
+    off = offsets([5, 20, cut, n])
+    say("grouped offsets: tokens")
+    K.kq_grouped_gemm(X, W, off, Y)
+    K.kq_grouped_backward(dY, X, W, off, dX, dW)
+    same(Y[cut:].contiguous(), torch.mm(X[cut:].double(), w[2].T), "bf16", "Y")
+    same(dX[cut:].contiguous(), torch.mm(dY[cut:].double(), w[2]), "bf16", "dX")
+    # up to 65580 products of at most 16: sums below 2^21
+    same(fW, torch.cat([torch.mm(dY[p:q].double().T.contiguous(), X[p:q].double()) for p, q in ((5, 20), (20, cut), (cut, n))]), "bf16", "dW")
+    assert bool((Y[:5] == -77.0).all()) and bool((dX[:5] == -77.0).all())
+    del X, dY, Y, dX
+    say("grouped offsets: weights")
+    n, o, i, e = 600, 4104, 65544, 9
+    W = torch.zeros((e, o, i), dtype=torch.bfloat16, device=dev)
+    last = torch.randint(-4, 5, (o, i), generator=g, device=dev)
+    W[e - 1].copy_(last)
+    (X, x), (dY, dy) = whole_numbers(n, i, "bf16", 4, g), whole_numbers(n, o, "bf16", 4, g)
+    Y, dX = out(n, o, "bf16"), out(n, i, "bf16")
+    off = offsets([0, 100] + [100] * (e - 2) + [n])
+    K.kq_grouped_gemm(X, W, off, Y)
+    same(Y[100:], torch.mm(x[100:], last.double().T), "bf16", "Y")
+    W[0].copy_(last)
+    K.kq_grouped_backward(dY, X, W, off, dX, W)
+    same(dX, torch.mm(dy, last.double()), "bf16", "dX")
+    assert torch.equal(W[e - 1], torch.mm(dy[100:].T.contiguous(), x[100:]).bfloat16()) and bool((W[1:e - 1] == 0).all())
+
+
+# --------------------------------------------------------------------- streams, graphs, two calls
+@pytest.mark.parametrize("n", [20, 300])
+def test_replayed_from_a_graph(n):
+    """One graph of an expert layer's calls: every replay on new inputs and new offsets gives the eager result, with eager work
+    between the replays."""
+    torch, dev = torch_dev()
+    e, o, i, dt = 5, 136, 264, "bf16"
+    g = generator(n)
+    X, dH = mat(n, i, dt, fill=0.0), mat(n, o, dt, fill=0.0)
+    (W, _), (U, _) = stack(e, o, i, dt, 4, g), stack(e, o, i, dt, 4, g)
+    gamma = torch.ones(i, dtype=X.dtype, device=dev)
+    off = offsets([0] * (e + 1))
+    wq = [K.i8_empty(e * o, i, dev) for _ in range(2)]
+    for t, q in zip((W, U), wq):
+        K.kq_i8_quantize(t.flatten(0, 1), *q)
+    gq, uq = ((c.unflatten(0, (e, o)), s.view(e, o)) for c, s in wq)
+
+    def buffers():
+        return dict(N=mat(n, i, dt, fill=0.0), stats=[torch.empty(n, device=dev) for _ in range(2)], H=mat(n, o, dt, fill=0.0), A=mat(n, o, dt, fill=0.0),
+                    B=mat(n, o, dt, fill=0.0), dA=mat(n, o, dt, fill=0.0), dB=mat(n, o, dt, fill=0.0), dN=mat(n, i, dt, fill=0.0),
+                    dW=torch.empty_like(W), dU=torch.empty_like(U), dX=mat(n, i, dt, fill=0.0), dg=torch.empty_like(gamma), q=K.i8_empty(n, i, dev),
+                    Q=mat(n, o, dt, fill=0.0), w=Workspace("norm_backward", 0, i, n, dt).ws)
+
+    def run(b):
+        K.kq_norm_forward(X, gamma, None, "rms", 1e-5, b["N"], rstd=b["stats"][1])
+        K.kq_grouped_gated(b["N"], W, U, off, "silu", b["H"], b["A"], b["B"])
+        K.kq_gated_backward(dH, b["A"], b["B"], None, None, None, "silu", b["dA"], b["dB"])
+        K.kq_grouped_backward(b["dA"], b["N"], W, off, b["dN"], b["dW"], b["dB"], U, b["dU"])
+        K.kq_norm_backward(b["dN"], X, gamma, None, b["stats"][1], "rms", b["dX"], b["dg"], ws=b["w"])
+        K.kq_i8_quantize(b["N"], *b["q"])
+        K.kq_i8_gated(*b["q"], *gq, *uq, "silu", b["Q"], off)
+
+    cap, eager = buffers(), buffers()
+    run(cap)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(cap)
+    for rep in range(3):
+        X.copy_(torch.randn(n, i, generator=g, device=dev))
+        dH.copy_(torch.randn(n, o, generator=g, device=dev))
+        off.copy_(dealt(n, e, g))
+        run(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        run(eager)
+        torch.cuda.synchronize()
+        for k in ("N", "H", "A", "B", "dA", "dB", "dN", "dW", "dU", "dX", "dg", "Q"):
+            assert torch.equal(cap[k], eager[k]), (rep, k)
+        assert torch.equal(cap["q"][0], eager["q"][0])
+
+
+def test_two_streams_at_once():
+    torch, dev = torch_dev()
+    n, e, o, i = 300, 4, 520, 512
+    g = generator(1)
+    jobs = []
+    for _ in range(2):
+        X, x = whole_numbers(n, i, "bf16", 4, g)
+        W, w = stack(e, o, i, "bf16", 4, g)
+        off = dealt(n, e, g)
+        want = torch.cat([torch.mm(x[p:q], w[k].T) for k, p, q in oe.spans(host(off), n)])
+        jobs.append((X, W, off, out(n, o, "bf16"), want, torch.cuda.Stream(dev)))
+    for _ in range(5):
+        for X, W, off, Y, _, st in jobs:
+            st.wait_stream(torch.cuda.current_stream())
+            K.kq_grouped_gemm(X, W, off, Y, stream=st)
+        torch.cuda.synchronize()
+        for _, _, _, Y, want, _ in jobs:
+            same(Y, want, "bf16", "Y")
+            Y.fill_(0.0)
+            Y.as_strided((n, Y.stride(0)), (Y.stride(0), 1))[:, o:] = -77.0
+
+
+def test_a_row_does_not_depend_on_other_experts():
+    """The same rows and weights among other experts of other sizes, in calls that are cut alike: the same bits."""
+    torch, dev = torch_dev()
+    n, e, o, i = 400, 4, 200, 300
+    torch.manual_seed(3)
+    X, W = mat(n, i, "bf16"), torch.empty((e, o, 304), dtype=torch.bfloat16, device=dev)[:, :, :i]
+    X.copy_(torch.randn(n, i, device=dev)), W.copy_(torch.randn(e, o, i, device=dev))
+    Y, Z = mat(n, o, "bf16"), mat(n, o, "bf16")
+    K.kq_grouped_gemm(X, W, offsets([0, 100, 150, 290, n]), Y)
+    K.kq_grouped_gemm(X, W, offsets([0, 20, 150, 290, 390]), Z)
+    assert torch.equal(Y[150:290], Z[150:290]) and torch.equal(Y[:20], Z[:20]) and torch.equal(Y[100:150], Z[100:150])

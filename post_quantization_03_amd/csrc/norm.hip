@@ -29,8 +29,11 @@ struct NormArgs {
     void *Y;                 // or dX
     int64_t ldy;
     float *mean, *rstd;
-    float *part;             // backward: sums of dgamma, then of dbeta, of each work-group (2 x d floats each)
+    float *part;             // backward: rows of sums of dgamma, then of dbeta
 };
+// floats of a row of sums, and of its dgamma half: whole pieces of 8 columns
+__host__ __device__ inline int64_t norm_part_half(int64_t d) { return (d + 7) / 8 * 8; }
+__host__ __device__ inline int64_t norm_part_row(int64_t d) { return 2 * norm_part_half(d); }
 
 // 1 / deviation from the sums q of the squares and of the differences from m, a first mean (0 for rms). The sum of the differences
 // is what rounding left of the mean: it corrects m, and its square comes off the variance. A row of one value then has that value
@@ -143,69 +146,102 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormArgs g) {
     }
 }
 
-// dX of a work-group's rows and its part of dgamma and dbeta, which stay in registers over its rows.
+// dX of a work-group's rows and its part of dgamma and dbeta, which stay in registers over its rows. The next row's loads are
+// in flight while one is reduced and written.
 template <bool BF, int T, int CH>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormArgs g) {
     constexpr int V = row_chunk<BF>(), PER = T < 256 ? 256 / T : 1;
     __shared__ float sm[32];
     const RowAt<T> at;
     const float inv = 1.0f / (float)g.d;
+    RowRegs<BF, T, CH> w;
+    w.load_or(g.gamma, g.d, at.lane, BF ? 0x3F803F80u : 0x3F800000u);
     float dg[CH][V], db[CH][V];
 #pragma unroll
     for (int c = 0; c < CH; c++)
 #pragma unroll
         for (int e = 0; e < V; e++) dg[c][e] = db[c][e] = 0.0f;
-    for (int64_t r = at.first; r < g.n; r += at.step) {
+    struct Row {
         RowRegs<BF, T, CH> x, y;
-        x.load(g.X, r * g.ldx, g.d, at.lane);
-        y.load(g.dY, r * g.lddy, g.d, at.lane);
-        const float m = g.layer ? g.mean[r] : 0.0f, rs = g.rstd[r];
+        float m, rs;
+    };
+    auto fetch = [&](Row& row, int64_t r) {
+        row.x.load(g.X, r * g.ldx, g.d, at.lane);
+        row.y.load(g.dY, r * g.lddy, g.d, at.lane);
+        row.m = g.layer ? g.mean[r] : 0.0f;
+        row.rs = g.rstd[r];
+    };
+    constexpr bool AHEAD = CH * V <= 24;      // with more the second row does not fit in registers
+    Row row, next;
+    if (AHEAD && at.first < g.n) fetch(row, at.first);
+    for (int64_t r = at.first; r < g.n; r += at.step) {
+        if (!AHEAD) fetch(row, r);
+        else if (r + at.step < g.n) fetch(next, r + at.step);
+        const float m = row.m, rs = row.rs;
         float s[2] = {0.0f, 0.0f};       // of g h and of g
 #pragma unroll
         for (int c = 0; c < CH; c++) {
             const int64_t col = ((int64_t)c * T + at.lane) * V;
-            float v[V], dy[V], w[V];
-            x.get(c, v);
-            y.get(c, dy);
-            norm_weights<BF>(g.gamma, col, g.d, 1.0f, w);
+            float v[V], dy[V], u[V];
+            row.x.get(c, v);
+            row.y.get(c, dy);
+            w.get(c, u);
 #pragma unroll
             for (int e = 0; e < V; e++) {
-                const float h = col + e < g.d ? (v[e] - m) * rs : 0.0f, t = dy[e] * w[e];
+                const float h = col + e < g.d ? (v[e] - m) * rs : 0.0f, t = dy[e] * u[e];
                 s[0] += t * h;
                 s[1] += t;
                 dg[c][e] += dy[e] * h;
                 db[c][e] += dy[e];
             }
         }
-        if (!g.Y) continue;
-        row_sum<T>(s, sm);
-        const float c1 = s[0] * inv, c0 = g.layer ? s[1] * inv : 0.0f;
+        if (g.Y) {
+            row_sum<T>(s, sm);
+            const float c1 = s[0] * inv, c0 = g.layer ? s[1] * inv : 0.0f;
 #pragma unroll
-        for (int c = 0; c < CH; c++) {
-            const int64_t col = ((int64_t)c * T + at.lane) * V;
-            if (col >= g.d) continue;
-            float v[V], dy[V], w[V];
-            x.get(c, v);
-            y.get(c, dy);
-            norm_weights<BF>(g.gamma, col, g.d, 1.0f, w);
+            for (int c = 0; c < CH; c++) {
+                const int64_t col = ((int64_t)c * T + at.lane) * V;
+                if (col >= g.d) continue;
+                float v[V], dy[V], u[V];
+                row.x.get(c, v);
+                row.y.get(c, dy);
+                w.get(c, u);
 #pragma unroll
-            for (int e = 0; e < V; e++) v[e] = rs * (dy[e] * w[e] - c0 - (v[e] - m) * rs * c1);
-            store_run<V>(g.Y, BF ? KQ_BF16 : KQ_F32, r * g.ldy + col, v, g.d - col);
+                for (int e = 0; e < V; e++) v[e] = rs * (dy[e] * u[e] - c0 - (v[e] - m) * rs * c1);
+                store_run<V>(g.Y, BF ? KQ_BF16 : KQ_F32, r * g.ldy + col, v, g.d - col);
+            }
         }
+        if (AHEAD) row = next;
     }
     if (!g.part) return;
-    // a row of sums for each of a work-group's rows at a time
-    const int64_t mine = (int64_t)blockIdx.x * PER + (PER > 1 ? (int)threadIdx.x / T : 0);
-    float* p = g.part + mine * 2 * g.d;
+    if constexpr (PER > 1) {
+        // the work-group's rows are those of its wavefronts: added in order, the last one writes
+        __shared__ float both[2][T * CH * V];
+        const int mine = (int)threadIdx.x / T;
+        for (int k = 0; k < PER; k++) {
+            if (mine == k)
+#pragma unroll
+                for (int c = 0; c < CH; c++)
+#pragma unroll
+                    for (int e = 0; e < V; e++) {
+                        float &a = both[0][(c * V + e) * T + at.lane], &b = both[1][(c * V + e) * T + at.lane];
+                        a = dg[c][e] = k ? a + dg[c][e] : dg[c][e];
+                        b = db[c][e] = k ? b + db[c][e] : db[c][e];
+                    }
+            __syncthreads();
+        }
+        if (mine != PER - 1) return;
+    }
+    float* p = g.part + blockIdx.x * norm_part_row(g.d);
 #pragma unroll
     for (int c = 0; c < CH; c++) {
         const int64_t col = ((int64_t)c * T + at.lane) * V;
+        if (col >= g.d) continue;        // rows of sums are padded to whole pieces
 #pragma unroll
-        for (int e = 0; e < V; e++)
-            if (col + e < g.d) {
-                p[col + e] = dg[c][e];
-                p[g.d + col + e] = db[c][e];
-            }
+        for (int e = 0; e < V; e += 4) {
+            *reinterpret_cast<float4*>(p + col + e) = make_float4(dg[c][e], dg[c][e + 1], dg[c][e + 2], dg[c][e + 3]);
+            *reinterpret_cast<float4*>(p + norm_part_half(g.d) + col + e) = make_float4(db[c][e], db[c][e + 1], db[c][e + 2], db[c][e + 3]);
+        }
     }
 }
 
@@ -264,44 +300,72 @@ __global__ __launch_bounds__(256) void norm_weights_long_kernel(NormArgs g) {
             db[e] += dy[e];
         }
     }
-    float* p = g.part + mine * 2 * g.d;
-    for (int e = 0; e < V; e++)
-        if (col + e < g.d) {
-            p[col + e] = dg[e];
-            p[g.d + col + e] = db[e];
-        }
+    float* p = g.part + mine * norm_part_row(g.d) + col;
+    for (int e = 0; e < V; e++) {
+        p[e] = dg[e];
+        p[norm_part_half(g.d) + e] = db[e];
+    }
 }
 
-// The rows of sums added in order: 64 columns a work-group, its four wavefronts a quarter of the rows each.
+// The rows of sums added: 32 columns a work-group, 8 lanes of four columns by 32 lanes of rows r, r + 32, .., whose sums are added in
+// lane order.
 __global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64_t rows, int64_t d, void* dgamma, void* dbeta, int dt) {
-    __shared__ float sm[4][64];
-    const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);      // of 2 d
-    const int w = threadIdx.x >> 6;
-    const int64_t per = (rows + 3) / 4, r0 = w * per, r1 = r0 + per < rows ? r0 + per : rows;
-    float s = 0.0f;
-    if (col < 2 * d)
-        for (int64_t r = r0; r < r1; r++) s += part[r * 2 * d + col];
-    sm[w][threadIdx.x & 63] = s;
-    __syncthreads();
-    if (w || col >= 2 * d) return;
-    s = ((sm[0][threadIdx.x] + sm[1][threadIdx.x]) + sm[2][threadIdx.x]) + sm[3][threadIdx.x];
-    void* out = col < d ? dgamma : dbeta;
+    __shared__ float sm[32][36];
+    const int64_t half = norm_part_half(d), step = norm_part_row(d);
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+    const int64_t col = (int64_t)blockIdx.x * 32 + 4 * x;       // of half, a multiple of 8
+    void* out = blockIdx.y ? dbeta : dgamma;
     if (!out) return;
-    const int64_t c = col < d ? col : col - d;
-    if (dt == KQ_BF16) static_cast<uint16_t*>(out)[c] = to_bf16(s);
-    else static_cast<float*>(out)[c] = s;
+    float4 s = make_float4(0, 0, 0, 0);
+    if (col < half) {
+        const float* p = part + blockIdx.y * half + col;
+#pragma unroll 8
+        for (int64_t r = y; r < rows; r += 32) {
+            const float4 v = *reinterpret_cast<const float4*>(p + r * step);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+    }
+    *reinterpret_cast<float4*>(&sm[y][4 * x]) = s;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    float t = sm[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < 32; k++) t += sm[k][threadIdx.x];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    if (c >= d) return;
+    if (dt == KQ_BF16) static_cast<uint16_t*>(out)[c] = to_bf16(t);
+    else static_cast<float*>(out)[c] = t;
 }
 
-// Work-groups of the backward pass: two for each compute unit at most (of 1024 threads; more of smaller ones), since each
-// leaves a row of sums.
-template <int T>
-unsigned norm_groups(int64_t n) { return row_groups<T>(n, T >= 1024 ? 512 : 1024); }
+// f(BF, T, CH, G) for the backward pass over rows of `cols` values, on G work-groups at most (each leaves a row of sums); CH = 0 as
+// for with_rows. From the same kind of sweep: a row's sums and the row ahead take registers too, so there are fewer pieces a
+// thread (8192 x 8192 bf16: 80 us on 512 threads with the row ahead, 94 without room for it, 98 on 1024; 4096 x 13824: 79, and 196
+// on 1024, which spill).
+template <typename F>
+kq_status with_grad_rows(bool bf, int64_t cols, F&& f) {
+    const int64_t pieces = (cols + (bf ? 7 : 3)) / (bf ? 8 : 4);
+    auto go = [&](auto t, auto ch, auto g) { return bf ? f(std::true_type{}, t, ch, g) : f(std::false_type{}, t, ch, g); };
+#define KQ_ROWS(T, CH, G) go(std::integral_constant<int, T>{}, std::integral_constant<int, CH>{}, std::integral_constant<int, G>{})
+    if (pieces <= 64) return KQ_ROWS(64, 1, 512);
+    if (pieces <= 128) return KQ_ROWS(64, 2, 512);
+    if (pieces <= 256) return KQ_ROWS(256, 1, 1024);
+    if (pieces <= 512) return KQ_ROWS(512, 1, 512);
+    if (pieces <= 768) return KQ_ROWS(256, 3, 512);
+    if (pieces <= 1536) return KQ_ROWS(512, 3, 256);
+    if (pieces <= 2048) return KQ_ROWS(512, 4, 256);
+    // of bf16 their sums alone would fill the registers
+    if (pieces <= 4096 && !bf)
+        return f(std::false_type{}, std::integral_constant<int, 512>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 256>{});
+    return KQ_ROWS(1024, 0, 256);
+#undef KQ_ROWS
+}
 // rows of sums
 static int64_t norm_parts(int64_t n, int64_t d, bool bf) {
     int64_t parts = 0;
-    with_rows(bf, d, [&](auto, auto t, auto ch) {
+    with_grad_rows(bf, d, [&](auto, auto t, auto ch, auto most) {
         constexpr int T = decltype(t)::value;
-        parts = decltype(ch)::value == 0 ? 4 * (n < 64 ? (n + 3) / 4 : 16) : (int64_t)norm_groups<T>(n) * (T < 256 ? 256 / T : 1);
+        parts = decltype(ch)::value == 0 ? 4 * (n < 64 ? (n + 3) / 4 : 16)
+                                         : (int64_t)row_groups<T>(n, decltype(most)::value);
         return KQ_OK;
     });
     return parts;
@@ -335,7 +399,7 @@ using namespace kq;
 
 size_t norm_backward_ws(int64_t d, int64_t n, kq_dtype dt) {
     if (n <= 0 || d <= 0) return 0;
-    return sizeof(float) * (size_t)(2 * d * norm_parts(n, d, dt == KQ_BF16));
+    return sizeof(float) * (size_t)(norm_part_row(d) * norm_parts(n, d, dt == KQ_BF16));
 }
 
 extern "C" kq_status kq_norm_forward(const void* X, int64_t ldx, const void* gamma, const void* beta, kq_dtype dt, int64_t n,
@@ -377,7 +441,7 @@ extern "C" kq_status kq_norm_backward(const void* dY, int64_t lddy, const void* 
     }
     const bool weights = dgamma || dbeta;
     const int64_t parts = n > 0 ? norm_parts(n, d, dt == KQ_BF16) : 0;
-    if (weights && n > 0 && (!ws || !aligned16(ws) || ws_bytes < sizeof(float) * (size_t)(2 * d * parts)))
+    if (weights && n > 0 && (!ws || !aligned16(ws) || ws_bytes < sizeof(float) * (size_t)(norm_part_row(d) * parts)))
         return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
     NormArgs g{};
     g.X = X; g.ldx = ldx; g.dY = dY; g.lddy = lddy; g.gamma = gamma; g.n = n; g.d = d; g.layer = kind == KQ_NORM_LAYER;
@@ -385,7 +449,7 @@ extern "C" kq_status kq_norm_backward(const void* dY, int64_t lddy, const void* 
     g.part = weights ? static_cast<float*>(ws) : nullptr;
     const hipStream_t st = hs(stream);
     if (n > 0 && (dX || weights))
-        KQ_TRY(with_rows(dt == KQ_BF16, d, [&](auto bf, auto t, auto ch) {
+        KQ_TRY(with_grad_rows(dt == KQ_BF16, d, [&](auto bf, auto t, auto ch, auto most) {
             constexpr bool BF = decltype(bf)::value;
             constexpr int T = decltype(t)::value, CH = decltype(ch)::value;
             if constexpr (CH == 0) {
@@ -397,11 +461,11 @@ extern "C" kq_status kq_norm_backward(const void* dY, int64_t lddy, const void* 
                 KQ_TRY(check_launch(who));
                 if (dX) hipLaunchKernelGGL((norm_backward_long_kernel<BF>), dim3(row_groups<1024>(n)), dim3(1024), 0, st, g);
             } else {
-                hipLaunchKernelGGL((norm_backward_kernel<BF, T, CH>), dim3(norm_groups<T>(n)), dim3(T < 256 ? 256 : T), 0, st, g);
+                hipLaunchKernelGGL((norm_backward_kernel<BF, T, CH>), dim3(row_groups<T>(n, decltype(most)::value)), dim3(T < 256 ? 256 : T), 0, st, g);
             }
             return check_launch(who);
         }));
     if (!weights) return KQ_OK;
-    hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((2 * d + 63) / 64)), dim3(256), 0, st, g.part, parts, d, dgamma, dbeta, (int)dt);
+    hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((d + 31) / 32), 2), dim3(256), 0, st, g.part, parts, d, dgamma, dbeta, (int)dt);
     return check_launch(who);
 }

@@ -73,6 +73,13 @@ struct RowRegs {
             w[c] = col < cols ? row_piece<BF>(X, off + col, cols - col) : make_uint4(0, 0, 0, 0);
         }
     }
+    // the same for one row that all share, or `none` in every word where there is no row
+    __device__ __forceinline__ void load_or(const void* P, int64_t cols, int lane, uint32_t none) {
+        if (P) load(P, 0, cols, lane);
+        else
+#pragma unroll
+            for (int c = 0; c < CH; c++) w[c] = make_uint4(none, none, none, none);
+    }
     __device__ __forceinline__ void get(int c, float (&v)[V]) const { row_unpack<BF>(w[c], v); }
     // f(piece, value) for all values, zeros behind the last column among them
     template <typename F>
@@ -120,7 +127,11 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* sm) {
     row_reduce<T>(v, sm, [](float x, float y) { return x + y; });
 }
 
-// f(BF, T, CH) for rows of `cols` values, CH = 0 for rows that the registers of 1024 threads do not hold
+// f(BF, T, CH) for rows of `cols` values, CH = 0 for rows that the registers of 512 threads do not hold. Chosen by a sweep of T and
+// CH over widths of 512 to 13824 of both types (8192 or 4096 rows, MI355X): a wavefront a row as long as four pieces hold it, then 256
+// threads, then 512; 1024 threads, of which a compute unit holds two rows, are slower (norm of 4096 x 11008 bf16: 37 us on 512 threads, 72
+// on 1024; of 8192 x 5120: 33 on 256, 38 on 1024) but for the widest rows of bf16, whose 64 values a thread of 512 take too many registers
+// (2048 x 28672: 69 us on 1024, 80 on 512).
 template <typename F>
 kq_status with_rows(bool bf, int64_t cols, F&& f) {
     const int64_t pieces = (cols + (bf ? 7 : 3)) / (bf ? 8 : 4);
@@ -128,11 +139,16 @@ kq_status with_rows(bool bf, int64_t cols, F&& f) {
 #define KQ_ROWS(T, CH) go(std::integral_constant<int, T>{}, std::integral_constant<int, CH>{})
     if (pieces <= 64) return KQ_ROWS(64, 1);
     if (pieces <= 128) return KQ_ROWS(64, 2);
-    if (pieces <= 256) return KQ_ROWS(256, 1);
+    if (pieces <= 256) return KQ_ROWS(64, 4);
     if (pieces <= 512) return KQ_ROWS(256, 2);
+    if (pieces <= 768) return KQ_ROWS(256, 3);
     if (pieces <= 1024) return KQ_ROWS(256, 4);
-    if (pieces <= 2048) return KQ_ROWS(1024, 2);
-    if (pieces <= 4096) return KQ_ROWS(1024, 4);
+    if (pieces <= 1536) return KQ_ROWS(512, 3);
+    if (pieces <= 2048) return KQ_ROWS(512, 4);
+    if (pieces <= 4096 && bf) return f(std::true_type{}, std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+    auto f32 = [&](auto ch) { return f(std::false_type{}, std::integral_constant<int, 512>{}, ch); };
+    if (pieces <= 3072) return f32(std::integral_constant<int, 6>{});
+    if (pieces <= 4096) return f32(std::integral_constant<int, 8>{});
     return KQ_ROWS(1024, 0);
 #undef KQ_ROWS
 }

@@ -23,6 +23,7 @@ size_t mx_product_ws(int64_t o, int64_t i, int64_t n, bool gated);
 size_t gated_forward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt);
 size_t gated_backward_ws(int64_t o, int64_t i, int64_t n, kq_dtype dt);
 size_t i8_product_ws(int64_t o, int64_t i, int64_t n, bool gated, int64_t experts);
+size_t grouped_ws(kq_op op, int64_t o, int64_t i, int64_t n, kq_dtype dt, int64_t experts);
 size_t norm_backward_ws(int64_t d, int64_t n, kq_dtype dt);
 
 namespace kq {
@@ -94,7 +95,7 @@ extern "C" size_t kq_workspace_bytes(kq_op op, int64_t o, int64_t i, int64_t n, 
         case KQ_OP_I8_GATED: return i8_product_ws(o, i, n, true, group);
         case KQ_OP_GROUPED_GEMM:
         case KQ_OP_GROUPED_GATED:
-        case KQ_OP_GROUPED_BACKWARD: return 0;
+        case KQ_OP_GROUPED_BACKWARD: return grouped_ws(op, o, i, n, xdt, group);
         case KQ_OP_NORM_BACKWARD: return norm_backward_ws(i, n, xdt);
     }
     return 0;

@@ -19,47 +19,66 @@ struct Group {
 };
 constexpr int64_t GROUP_MAX = 4096, GROUP_ROWS_MAX = (1LL << 31) - 1;
 
-// Expert, its rows, and the tile (of `size` rows, `nx` tiles a tile row) among its own; rows = 0 if there is none.
+__device__ __forceinline__ int clamp_row(int v, int n) { return v < 0 ? 0 : v < n ? v : n; }
+
+// 64 experts from k0 on, one a lane: their rows, and the tiles of `size` rows up to the lane's expert.
+struct GroupLanes {
+    int begin, rows;
+    unsigned own, sum;
+};
+__device__ __forceinline__ GroupLanes group_lanes(const Group& g, int k0, int before, int size) {
+    const int lane = threadIdx.x & 63, k = k0 + lane;
+    int end = k < g.experts ? clamp_row(g.off[k + 1], g.n) : 0;
+    end = end > before ? end : before;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(end, d);
+        if (lane >= d && o > end) end = o;
+    }
+    const int up = __shfl_up(end, 1);
+    GroupLanes l;
+    l.begin = lane ? up : before;
+    l.rows = end - l.begin;
+    l.own = l.sum = (unsigned)(((int64_t)l.rows + size - 1) / size);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const unsigned o = __shfl_up(l.sum, d);
+        if (lane >= d) l.sum += o;
+    }
+    return l;
+}
+__device__ __forceinline__ int group_first(const Group& g) { return clamp_row(g.off[0], g.n); }
+__device__ __forceinline__ int last_row(const GroupLanes& l) { return __builtin_amdgcn_readlane(l.begin + l.rows, 63); }
+__device__ __forceinline__ unsigned last_sum(const GroupLanes& l) { return (unsigned)__builtin_amdgcn_readlane((int)l.sum, 63); }
+
+// Tiles of `size` rows of all experts, given the lanes of the first 64.
+__device__ __forceinline__ unsigned group_tiles(const Group& g, GroupLanes l, int size) {
+    unsigned tiles = last_sum(l);
+    for (int k0 = 64; k0 < g.experts; k0 += 64) {
+        l = group_lanes(g, k0, last_row(l), size);
+        tiles += last_sum(l);
+    }
+    return tiles;
+}
+
+// Expert and rows of tile `id` (`nx` tiles a tile row), and the tile's place among the expert's own; rows = 0 if there is none.
 struct GroupAt {
     int k, begin, rows, id;
 };
-__device__ __forceinline__ int clamp_row(int v, int n) { return v < 0 ? 0 : v < n ? v : n; }
-
-__device__ __forceinline__ GroupAt group_tile(const Group& g, unsigned id, int size, unsigned nx) {
-    const int lane = threadIdx.x & 63;
-    int before = clamp_row(g.off[0], g.n);       // end of the expert before lane 0's
+__device__ __forceinline__ GroupAt group_tile(const Group& g, GroupLanes l, unsigned id, int size, unsigned nx) {
     unsigned tiles = 0;                          // of the experts before lane 0's
-    for (int k0 = 0; k0 < g.experts; k0 += 64) {
-        const int k = k0 + lane;
-        int end = k < g.experts ? clamp_row(g.off[k + 1], g.n) : 0;
-        end = end > before ? end : before;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(end, d);
-            if (lane >= d && o > end) end = o;
-        }
-        const int up = __shfl_up(end, 1), begin = lane ? up : before, rows = end - begin;
-        const unsigned own = (unsigned)(((int64_t)rows + size - 1) / size);
-        unsigned sum = own;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const unsigned o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        const uint64_t hit = __ballot((tiles + sum) * nx > id);
+    for (int k0 = 0;;) {
+        const uint64_t hit = __ballot((tiles + l.sum) * nx > id);
         if (hit) {
-            const int l = __builtin_ctzll(hit);
-            GroupAt at;
-            at.k = k0 + l;
-            at.begin = __builtin_amdgcn_readlane(begin, l);
-            at.rows = __builtin_amdgcn_readlane(rows, l);
-            at.id = (int)(id - (tiles + (unsigned)__builtin_amdgcn_readlane((int)(sum - own), l)) * nx);
-            return at;
+            const int at = __builtin_ctzll(hit);
+            return GroupAt{k0 + at, __builtin_amdgcn_readlane(l.begin, at), __builtin_amdgcn_readlane(l.rows, at),
+                           (int)(id - (tiles + (unsigned)__builtin_amdgcn_readlane((int)(l.sum - l.own), at)) * nx)};
         }
-        before = __builtin_amdgcn_readlane(end, 63);
-        tiles += (unsigned)__builtin_amdgcn_readlane((int)sum, 63);
+        k0 += 64;
+        if (k0 >= g.experts) return GroupAt{0, 0, 0, 0};
+        tiles += last_sum(l);
+        l = group_lanes(g, k0, last_row(l), size);
     }
-    return GroupAt{0, 0, 0, 0};
 }
 
 // The rows of expert k.
@@ -84,14 +103,9 @@ __device__ __forceinline__ void* rows_on(void* p, int64_t values, int dt) {
     return p ? static_cast<char*>(p) + values * (dt == KQ_BF16 ? 2 : 4) : nullptr;
 }
 
-// Products whose output rows are the tokens: Y = X W^T (plain, gated, int8) and dX = dY W. Experts take work-groups in
-// turn, each one's tiles dealt to the XCDs by themselves: experts of unequal size then load all XCDs alike.
-template <int E, int MODE, typename C>
-__global__ __launch_bounds__(C::THREADS, C::EU) void group_tile_kernel(TileArgs g, Group gr) {
-    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
-    const int nx = (int)((g.N + TN_OUT - 1) / TN_OUT);
-    const GroupAt at = group_tile(gr, blockIdx.x, C::TM, (unsigned)nx);
-    if (at.rows == 0) return;
+// A product's operands moved to those of the expert at `at`.
+template <int E, int MODE>
+__device__ __forceinline__ void group_operands(TileArgs& g, const Group& gr, const GroupAt& at) {
     const int64_t begin = at.begin, w0 = (int64_t)at.k * gr.o;
     g.M = at.rows;
     g.A += begin * g.lda;
@@ -108,14 +122,107 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void group_tile_kernel(TileArgs 
         g.Y2 = rows_on(g.Y2, begin * g.ldy2, g.dt);
         g.Y3 = rows_on(g.Y3, begin * g.ldy3, g.dt);
     }
-    TileAt t;
-    t.cut = -1;
-    t.split = t.pair = 0;
+}
+
+// Place of the expert's tile at.id: each expert's tiles are dealt to the XCDs by themselves, so that experts of unequal size load
+// all of them alike.
+template <typename C>
+__device__ __forceinline__ void group_place(TileAt& t, const GroupAt& at, int nx) {
     const int ny = (at.rows + C::TM - 1) / C::TM;
     tile_place(t, xcd_range(at.id, ny * nx), ny, nx);
     t.tm = __builtin_amdgcn_readfirstlane(t.tm);
     t.tn = __builtin_amdgcn_readfirstlane(t.tn);
+}
+
+// The largest tiles, one a compute unit at a time: those behind the last full turn of the GPU would keep it waiting a whole turn for
+// few of them, so their K is split as tile_plan splits it, with the same kind of estimate, by the count that the device
+// finds. The host makes the choice for each count of them; both kernels of a product look it up.
+constexpr int GROUP_SLOTS = 256, GROUP_SUMS = 512;       // compute units; cut tiles times splits at most
+struct GroupCuts {
+    uint32_t by_rest[GROUP_SLOTS];       // splits (1: not cut) | slabs of a split << 8
+};
+struct GroupCut {
+    unsigned whole, rest;    // tiles that take all of K, tiles that are cut
+    int splits, sper;
+};
+inline void group_cuts(GroupCuts& t, int64_t slabs, int products) {
+    for (int rest = 0; rest < GROUP_SLOTS; rest++) {
+        double least = 0.0;
+        for (int64_t s = 1; s <= 16; s++) {
+            const int64_t per = (slabs + s - 1) / s, splits = (slabs + per - 1) / per, wgs = rest * splits;
+            if (s > 1 && (wgs > GROUP_SUMS || per >= 1 << 24)) break;
+            const double turns = (double)((wgs + GROUP_SLOTS - 1) / GROUP_SLOTS);
+            const double us = turns * ((double)(per * products) * 1.5 + 10.0) + (splits > 1 ? 4.0 + 0.15 * (double)wgs : 0.0);
+            if (s == 1 || us < least) {
+                least = us;
+                t.by_rest[rest] = splits == 1 ? 1u : (uint32_t)splits | (uint32_t)per << 8;
+            }
+        }
+    }
+}
+__device__ __forceinline__ GroupCut group_cut(const GroupCuts& t, unsigned tiles) {
+    GroupCut c;
+    c.rest = tiles % GROUP_SLOTS;
+    const uint32_t v = t.by_rest[c.rest];
+    c.splits = (int)(v & 255u);
+    c.sper = (int)(v >> 8);
+    if (c.splits == 1) c.rest = 0;
+    c.whole = tiles - c.rest;
+    return c;
+}
+template <typename C>
+constexpr bool group_may_cut() { return C::TM == 256; }
+
+// Products whose output rows are the tokens: Y = X W^T (plain, gated, int8) and dX = dY W.
+template <int E, int MODE, typename C>
+__device__ __forceinline__ void group_tile_body(TileArgs g, const Group& gr, const GroupCuts& cuts, unsigned id) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
+    const int nx = (int)((g.N + TN_OUT - 1) / TN_OUT);
+    const GroupLanes l = group_lanes(gr, 0, group_first(gr), C::TM);
+    TileAt t;
+    t.cut = -1;
+    t.split = t.pair = 0;
+    if constexpr (group_may_cut<C>()) {
+        const GroupCut c = group_cut(cuts, group_tiles(gr, l, C::TM) * (unsigned)nx);
+        if (id >= c.whole) {
+            if (c.rest == 0 || id >= c.whole + c.rest * (unsigned)c.splits) return;
+            t.split = __builtin_amdgcn_readfirstlane((int)((id - c.whole) / c.rest));
+            t.cut = (int)(id - c.whole - (unsigned)t.split * c.rest);
+            id = c.whole + (unsigned)t.cut;
+            g.splits = c.splits;
+            g.sper = c.sper;
+        }
+    }
+    const GroupAt at = group_tile(gr, l, id, C::TM, (unsigned)nx);
+    if (at.rows == 0) return;
+    group_operands<E, MODE>(g, gr, at);
+    group_place<C>(t, at, nx);
     tile_body<E, MODE, C>(g, t);
+}
+template <int E, int MODE, typename C>
+__global__ __launch_bounds__(C::THREADS, C::EU) void group_tile_kernel(TileArgs g, Group gr, GroupCuts cuts) {
+    group_tile_body<E, MODE, C>(g, gr, cuts, blockIdx.x);
+}
+
+// The sums of the cut tiles' splits, in split order, and the epilogue.
+template <int E, int MODE, typename C>
+__global__ __launch_bounds__(256) void group_reduce_kernel(TileArgs g0, Group gr, GroupCuts cuts) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
+    const int nx = (int)((g0.N + TN_OUT - 1) / TN_OUT);
+    const GroupLanes l = group_lanes(gr, 0, group_first(gr), C::TM);
+    const GroupCut c = group_cut(cuts, group_tiles(gr, l, C::TM) * (unsigned)nx);
+    for (unsigned b = blockIdx.x; b < c.rest * PER; b += gridDim.x) {
+        TileArgs g = g0;
+        TileAt t;
+        t.cut = (int)(b / PER);
+        t.split = t.pair = 0;
+        const GroupAt at = group_tile(gr, l, c.whole + (unsigned)t.cut, C::TM, (unsigned)nx);
+        g.splits = c.splits;
+        g.sper = c.sper;
+        group_operands<E, MODE>(g, gr, at);
+        group_place<C>(t, at, nx);
+        tile_reduce<MODE, C, E == EL_I8 ? EL_I8 : EL_F32>(g, t, (int)(b % PER));
+    }
 }
 
 // dW = dY^T X over each expert's rows, zeros for one without any: `per` tiles an expert (of both gradients).
@@ -145,7 +252,8 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void group_grad_kernel(TileArgs 
 // from HBM the first time and from a cache after that.
 template <int E, bool GATED, int NB>
 __global__ __launch_bounds__(FEW_THREADS) void group_few_kernel(FewArgs g, Group gr, int blocks) {
-    const GroupAt at = group_tile(gr, blockIdx.x, GROUP_ROWS_MAX, (unsigned)blocks);
+    constexpr int ALL = (int)GROUP_ROWS_MAX;         // one "tile" for an expert with rows
+    const GroupAt at = group_tile(gr, group_lanes(gr, 0, group_first(gr), ALL), blockIdx.x, ALL, (unsigned)blocks);
     if (at.rows == 0) return;
     const int64_t begin = at.begin, w0 = (int64_t)at.k * gr.o;
     g.n = at.rows;
@@ -232,17 +340,38 @@ kq_status with_shape(int shape, F&& f) {
     return f(TileS{});
 }
 
+// Workspace of a product whose largest tiles may be cut: 128 MiB of split sums.
 template <int E, int MODE>
-kq_status group_launch(const TileArgs& g, const Group& gr, hipStream_t st, const char* who) {
+size_t group_ws(int64_t n, int64_t experts, int64_t N, int64_t K) {
+    if (n <= 0 || group_shape<E, MODE>(n, experts, N, K) != 0) return 0;
+    return (size_t)GROUP_SUMS * TileL::TM * TileL::TN * sizeof(float);
+}
+
+template <int E, int MODE>
+kq_status group_launch(TileArgs g, const Group& gr, void* ws, size_t ws_bytes, hipStream_t st, const char* who) {
+    const size_t need = group_ws<E, MODE>(gr.n, gr.experts, g.N, g.K);
+    if (need && (!ws || !aligned16(ws) || ws_bytes < need))
+        return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
+    g.part = static_cast<float*>(ws);
     return with_shape<E>(group_shape<E, MODE>(gr.n, gr.experts, g.N, g.K), [&](auto shape) {
         typedef decltype(shape) C;
         constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
-        const int64_t wgs = group_tiles_max(gr.n, gr.experts, C::TM) * ((g.N + TN_OUT - 1) / TN_OUT);
+        const int64_t wgs = group_tiles_max(gr.n, gr.experts, C::TM) * ((g.N + TN_OUT - 1) / TN_OUT) + (group_may_cut<C>() ? GROUP_SUMS : 0);
         if (!grid_ok(wgs, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
         static std::atomic<uint64_t> allowed{0};
         KQ_TRY(allow_lds(reinterpret_cast<const void*>(&group_tile_kernel<E, MODE, C>), C::SMEM, allowed, who));
-        hipLaunchKernelGGL((group_tile_kernel<E, MODE, C>), dim3((unsigned)wgs), dim3(C::THREADS), C::SMEM, st, g, gr);
-        return check_launch(who);
+        GroupCuts cuts;
+        if (group_may_cut<C>()) {
+            constexpr int BK = 8 * el_chunk<E>();
+            group_cuts(cuts, (g.K + BK - 1) / BK, MODE == TP_GRAD_X ? 2 : 1);
+        }
+        hipLaunchKernelGGL((group_tile_kernel<E, MODE, C>), dim3((unsigned)wgs), dim3(C::THREADS), C::SMEM, st, g, gr, cuts);
+        KQ_TRY(check_launch(who));
+        if constexpr (group_may_cut<C>()) {
+            hipLaunchKernelGGL((group_reduce_kernel<E, MODE, C>), dim3(2048), dim3(256), 0, st, g, gr, cuts);
+            KQ_TRY(check_launch(who));
+        }
+        return KQ_OK;
     });
 }
 

@@ -31,7 +31,7 @@ static const char* bytes_of(const void* p) { return static_cast<const char*>(p);
 template <int E, bool GATED>
 static kq_status forward(const char* who, const Group& gr, const void* X, int64_t ldx, const void* W, int64_t ldw, const void* W2,
                          int64_t ldw2, int64_t n, int64_t o, int64_t i, int act, kq_dtype dt, void* Y, int64_t ldy, void* A,
-                         int64_t lda, void* B, int64_t ldb, hipStream_t st) {
+                         int64_t lda, void* B, int64_t ldb, void* ws, size_t ws_bytes, hipStream_t st) {
     const int64_t es = E == EL_BF16 ? 2 : 4;
     if (group_few<E>(n, gr.experts)) {
         FewArgs f{};
@@ -50,14 +50,15 @@ static kq_status forward(const char* who, const Group& gr, const void* X, int64_
     g.B2 = bytes_of(W2); g.ldb2 = ldw2 * es;
     g.Y = Y; g.ldy = ldy; g.Y2 = A; g.ldy2 = lda; g.Y3 = B; g.ldy3 = ldb;
     g.dt = dt; g.act = act; g.pairs = 1;
-    return group_launch<E, GATED ? TP_GATED : TP_PLAIN>(g, gr, st, who);
+    return group_launch<E, GATED ? TP_GATED : TP_PLAIN>(g, gr, ws, ws_bytes, st, who);
 }
 
 template <int E>
-static kq_status backward(const char* who, const Group& gr, TileArgs x, TileArgs w, int pairs, hipStream_t st) {
+static kq_status backward(const char* who, const Group& gr, TileArgs x, TileArgs w, int pairs, void* ws, size_t ws_bytes,
+                          hipStream_t st) {
     if (x.Y) {
-        if (x.A2) KQ_TRY((group_launch<E, TP_GRAD_X>(x, gr, st, who)));
-        else KQ_TRY((group_launch<E, TP_GRAD_X1>(x, gr, st, who)));
+        if (x.A2) KQ_TRY((group_launch<E, TP_GRAD_X>(x, gr, ws, ws_bytes, st, who)));
+        else KQ_TRY((group_launch<E, TP_GRAD_X1>(x, gr, ws, ws_bytes, st, who)));
     }
     return pairs ? group_grad_launch<E>(w, gr, pairs, st, who) : KQ_OK;
 }
@@ -66,11 +67,21 @@ static kq_status backward(const char* who, const Group& gr, TileArgs x, TileArgs
 
 using namespace kq;
 
+size_t grouped_ws(kq_op op, int64_t o, int64_t i, int64_t n, kq_dtype dt, int64_t experts) {
+    if (dt != KQ_BF16 || n <= 0 || o <= 0 || i <= 0 || experts <= 0 || n > GROUP_ROWS_MAX) return 0;
+    if (op == KQ_OP_GROUPED_BACKWARD) {
+        // of one product's dX or of two's
+        const size_t a = group_ws<EL_BF16, TP_GRAD_X>(n, experts, i, o), b = group_ws<EL_BF16, TP_GRAD_X1>(n, experts, i, o);
+        return a > b ? a : b;
+    }
+    if (group_few<EL_BF16>(n, experts)) return 0;
+    return op == KQ_OP_GROUPED_GATED ? group_ws<EL_BF16, TP_GATED>(n, experts, o, i) : group_ws<EL_BF16, TP_PLAIN>(n, experts, o, i);
+}
+
 extern "C" kq_status kq_grouped_gemm(const void* X, int64_t ldx, const void* W, int64_t ldw, const int32_t* offsets,
                                      int64_t experts, kq_dtype dt, int64_t n, int64_t o, int64_t i, void* Y, int64_t ldy,
                                      void* ws, size_t ws_bytes, kq_stream stream) {
     const char* who = "kq_grouped_gemm";
-    (void)ws, (void)ws_bytes;
     if (n < 0 || o <= 0 || i <= 0) return fail(KQ_ESHAPE, "%s: bad sizes", who);
     if (dt != KQ_F32 && dt != KQ_BF16) return fail(KQ_EINVAL, "%s: bad dtype", who);
     KQ_TRY(group_check(who, offsets, experts, n, o));
@@ -80,8 +91,10 @@ extern "C" kq_status kq_grouped_gemm(const void* X, int64_t ldx, const void* W, 
     KQ_TRY(rows_check(who, dt, DenseRows{Y, ldy, "Y"}, o));
     const Group gr{offsets, (int)experts, (int)n, (int)o};
     if (dt == KQ_BF16)
-        return forward<EL_BF16, false>(who, gr, X, ldx, W, ldw, nullptr, 0, n, o, i, 0, dt, Y, ldy, nullptr, 0, nullptr, 0, hs(stream));
-    return forward<EL_F32, false>(who, gr, X, ldx, W, ldw, nullptr, 0, n, o, i, 0, dt, Y, ldy, nullptr, 0, nullptr, 0, hs(stream));
+        return forward<EL_BF16, false>(who, gr, X, ldx, W, ldw, nullptr, 0, n, o, i, 0, dt, Y, ldy, nullptr, 0, nullptr, 0, ws,
+                                      ws_bytes, hs(stream));
+    return forward<EL_F32, false>(who, gr, X, ldx, W, ldw, nullptr, 0, n, o, i, 0, dt, Y, ldy, nullptr, 0, nullptr, 0, ws,
+                                      ws_bytes, hs(stream));
 }
 
 extern "C" kq_status kq_grouped_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu,
@@ -89,7 +102,6 @@ extern "C" kq_status kq_grouped_gated(const void* X, int64_t ldx, const void* Wg
                                       kq_act act, void* H, int64_t ldh, void* A, int64_t lda, void* B, int64_t ldb, void* ws,
                                       size_t ws_bytes, kq_stream stream) {
     const char* who = "kq_grouped_gated";
-    (void)ws, (void)ws_bytes;
     if (n < 0 || o <= 0 || i <= 0) return fail(KQ_ESHAPE, "%s: bad sizes", who);
     if (dt != KQ_F32 && dt != KQ_BF16) return fail(KQ_EINVAL, "%s: bad dtype", who);
     if (act < KQ_ACT_SILU || act > KQ_ACT_RELU) return fail(KQ_EINVAL, "%s: bad activation", who);
@@ -103,8 +115,10 @@ extern "C" kq_status kq_grouped_gated(const void* X, int64_t ldx, const void* Wg
     if (B) KQ_TRY(rows_check(who, dt, DenseRows{B, ldb, "B"}, o));
     const Group gr{offsets, (int)experts, (int)n, (int)o};
     if (dt == KQ_BF16)
-        return forward<EL_BF16, true>(who, gr, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, hs(stream));
-    return forward<EL_F32, true>(who, gr, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, hs(stream));
+        return forward<EL_BF16, true>(who, gr, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, ws,
+                                      ws_bytes, hs(stream));
+    return forward<EL_F32, true>(who, gr, X, ldx, Wg, ldg, Wu, ldu, n, o, i, act, dt, H, ldh, A, lda, B, ldb, ws,
+                                      ws_bytes, hs(stream));
 }
 
 extern "C" kq_status kq_grouped_backward(const void* dY, int64_t lddy, const void* W, int64_t ldw, const void* dY2, int64_t lddy2,
@@ -113,7 +127,6 @@ extern "C" kq_status kq_grouped_backward(const void* dY, int64_t lddy, const voi
                                          void* dW, int64_t lddw, void* dW2, int64_t lddw2, void* ws, size_t ws_bytes,
                                          kq_stream stream) {
     const char* who = "kq_grouped_backward";
-    (void)ws, (void)ws_bytes;
     if (n < 0 || o <= 0 || i <= 0) return fail(KQ_ESHAPE, "%s: bad sizes", who);
     if (dt != KQ_F32 && dt != KQ_BF16) return fail(KQ_EINVAL, "%s: bad dtype", who);
     KQ_TRY(group_check(who, offsets, experts, n, o));
@@ -143,5 +156,6 @@ extern "C" kq_status kq_grouped_backward(const void* dY, int64_t lddy, const voi
     w.B = bytes_of(X); w.ldb = ldx * es;
     w.Y = dW ? dW : dW2; w.ldy = dW ? lddw : lddw2; w.Y2 = dW2; w.ldy2 = lddw2; w.dt = dt;
     const int pairs = dW && dW2 ? 2 : dW || dW2 ? 1 : 0;
-    return dt == KQ_BF16 ? backward<EL_BF16>(who, gr, x, w, pairs, hs(stream)) : backward<EL_F32>(who, gr, x, w, pairs, hs(stream));
+    return dt == KQ_BF16 ? backward<EL_BF16>(who, gr, x, w, pairs, ws, ws_bytes, hs(stream))
+                         : backward<EL_F32>(who, gr, x, w, pairs, ws, ws_bytes, hs(stream));
 }

@@ -186,7 +186,7 @@ static kq_status i8_product(const char* who, const I8Operand& A, const I8Operand
     g.B = reinterpret_cast<const char*>(B.c); g.ldb = B.ld; g.fB = B.s;
     g.B2 = reinterpret_cast<const char*>(U.c); g.ldb2 = U.ld; g.fB2 = U.s;
     g.Y = Y; g.ldy = ldy; g.dt = dt; g.act = act; g.pairs = 1;
-    if (offsets) return group_launch<EL_I8, MODE>(g, gr, st, who);
+    if (offsets) return group_launch<EL_I8, MODE>(g, gr, ws, ws_bytes, st, who);
     const TilePlan plan = i8_plan<GATED>(n, o, i);
     if (plan.part && (!ws || !aligned16(ws) || ws_bytes < sizeof(float) * plan.part))
         return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
@@ -198,7 +198,12 @@ static kq_status i8_product(const char* who, const I8Operand& A, const I8Operand
 using namespace kq;
 
 size_t i8_product_ws(int64_t o, int64_t i, int64_t n, bool gated, int64_t experts) {
-    if (experts || n <= 0 || o <= 0 || i <= 0 || !tile_sizes_ok(n, o) || few_tokens<EL_I8>(n, o, i)) return 0;
+    if (n <= 0 || o <= 0 || i <= 0 || !tile_sizes_ok(n, o) || experts < 0) return 0;
+    if (experts) {
+        if (n > GROUP_ROWS_MAX || group_few<EL_I8>(n, experts)) return 0;
+        return gated ? group_ws<EL_I8, TP_GATED>(n, experts, o, i) : group_ws<EL_I8, TP_PLAIN>(n, experts, o, i);
+    }
+    if (few_tokens<EL_I8>(n, o, i)) return 0;
     return sizeof(float) * (gated ? i8_plan<true>(n, o, i) : i8_plan<false>(n, o, i)).part;
 }
 

@@ -788,12 +788,11 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void tile_grads_kernel(TileArgs 
 // Sums of the splits, in split order, and the epilogue: 4 columns a thread, TM * TN_OUT / 1024 work-groups a tile.
 // HBM-bound, or latency (96 L tiles in two splits, the tail of the weight gradients at 8192 tokens: 10.6 us, 5.9 TB/s;
 // 16 S tiles in 15: 4 us). Splits are not added by atomics: their order would change the sums.
+// Piece `piece` of them, of the cut tile `at`:
 template <int MODE, typename C, int E = EL_F32>
-__device__ __forceinline__ void tile_reduce(const TileArgs& g, int block) {
-    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
-    TileAt at;
-    cut_place(at, block / PER, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g.whole);
-    const int e = block % PER * 256 + threadIdx.x, r = e / (TN_OUT / 4), c = e % (TN_OUT / 4) * 4;
+__device__ __forceinline__ void tile_reduce(const TileArgs& g, const TileAt& at, int piece) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
+    const int e = piece * 256 + threadIdx.x, r = e / (TN_OUT / 4), c = e % (TN_OUT / 4) * 4;
     const int64_t m = (int64_t)at.tm * C::TM + r, n = (int64_t)at.tn * TN_OUT + c;
     if (m >= g.M || n >= g.N) return;
     const float* p = g.part + (int64_t)at.cut * g.splits * (C::TM * C::TN) + r * C::TN + c;
@@ -829,6 +828,15 @@ __device__ __forceinline__ void tile_reduce(const TileArgs& g, int block) {
         const bool w2 = MODE == TP_GRAD_W && at.pair;
         store_run<4>(w2 ? g.Y2 : g.Y, g.dt, m * (w2 ? g.ldy2 : g.ldy) + n, a, g.N - n);
     }
+}
+
+// the piece of work-group `block` of a whole product
+template <int MODE, typename C, int E = EL_F32>
+__device__ __forceinline__ void tile_reduce(const TileArgs& g, int block) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
+    TileAt at;
+    cut_place(at, block / PER, (int)((g.M + C::TM - 1) / C::TM), (int)((g.N + TN_OUT - 1) / TN_OUT), g.whole);
+    tile_reduce<MODE, C, E>(g, at, block % PER);
 }
 
 template <int MODE, typename C, int E>

@@ -130,14 +130,18 @@ def test_i8_product_refusals(call):
     if call is i8_gated:
         for kw in (dict(U=None), dict(sU=None), dict(act=4), dict(act=-1), dict(U=FOUR)):
             assert call(**kw) == EINVAL, kw
+    large = dict(n=8192, o=4096, i=4096, off=P, e=4, lda=4096, ldb=4096, ldy=4096, **({"ldu": 4096} if call is i8_gated else {}))
+    for ws, wb in ((None, 0), (P, (128 << 20) - 1), (FOUR, 128 << 20)):
+        assert call(ws=ws, wb=wb, **large) == EWORKSPACE, (ws, wb)
 
 
-def gg(X=P, ldx=16, W=P, ldw=16, off=P, e=3, dt=1, n=4, o=8, i=16, Y=P, ldy=8):
-    return K.lib().kq_grouped_gemm(X, ldx, W, ldw, off, e, dt, n, o, i, Y, ldy, None, 0, None)
+def gg(X=P, ldx=16, W=P, ldw=16, off=P, e=3, dt=1, n=4, o=8, i=16, Y=P, ldy=8, ws=None, wb=0):
+    return K.lib().kq_grouped_gemm(X, ldx, W, ldw, off, e, dt, n, o, i, Y, ldy, ws, wb, None)
 
 
-def ggated(X=P, ldx=16, W=P, ldw=16, U=P, ldu=16, off=P, e=3, dt=1, n=4, o=8, i=16, act=0, Y=P, ldy=8, A=P, lda=8, B=P, ldb=8):
-    return K.lib().kq_grouped_gated(X, ldx, W, ldw, U, ldu, off, e, dt, n, o, i, act, Y, ldy, A, lda, B, ldb, None, 0, None)
+def ggated(X=P, ldx=16, W=P, ldw=16, U=P, ldu=16, off=P, e=3, dt=1, n=4, o=8, i=16, act=0, Y=P, ldy=8, A=P, lda=8, B=P, ldb=8, ws=None,
+           wb=0):
+    return K.lib().kq_grouped_gated(X, ldx, W, ldw, U, ldu, off, e, dt, n, o, i, act, Y, ldy, A, lda, B, ldb, ws, wb, None)
 
 
 @pytest.mark.parametrize("call", [gg, ggated])
@@ -151,6 +155,9 @@ def test_grouped_refusals(call):
     if call is ggated:
         for kw, st in ((dict(U=None), EINVAL), (dict(act=9), EINVAL), (dict(lda=4), ESHAPE), (dict(B=ODD), EINVAL)):
             assert call(**kw) == st, kw
+    large = dict(n=8192, o=4096, i=4096, e=4, ldx=4096, ldw=4096, ldy=4096, **({"ldu": 4096, "A": None, "B": None} if call is ggated else {}))
+    for ws, wb in ((None, 0), (P, (128 << 20) - 1), (FOUR, 128 << 20)):
+        assert call(ws=ws, wb=wb, **large) == EWORKSPACE, (ws, wb)
     assert call(n=0) == 0
 
 
@@ -199,9 +206,12 @@ def test_norm_refusals():
 def test_workspace_sizes():
     for op in ("i8_gemm", "i8_gated"):
         assert K.kq_workspace_bytes(op, 4096, 4096, 32) == 0
-        assert K.kq_workspace_bytes(op, 200, 9000, 300, group=4) == 0       # grouped products are not split
+        assert K.kq_workspace_bytes(op, 200, 9000, 300, group=4) == 0       # small grouped products are not cut
+        assert K.kq_workspace_bytes(op, 4096, 4096, 8192, group=4) == 128 << 20
     for op in ("grouped_gemm", "grouped_gated", "grouped_backward"):
-        assert K.kq_workspace_bytes(op, 4096, 4096, 8192, group=8) == 0
+        assert K.kq_workspace_bytes(op, 200, 900, 300, group=4) == 0
+        assert K.kq_workspace_bytes(op, 4096, 4096, 8192, group=4) == 128 << 20
+        assert K.kq_workspace_bytes(op, 4096, 4096, 8192, K.KQ_F32, group=4) == 0
     for d in (1, 100, 1000, 4096, 11008, 50000):
         for n in (1, 3, 333, 8192):
             for dt in (K.KQ_F32, K.KQ_BF16):

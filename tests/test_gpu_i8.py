@@ -228,9 +228,10 @@ def dealt(n, e, g, first=0, last=None):
     return off
 
 
-# few rows an expert, one expert with more than the others; tile shapes; more experts than lanes
+# few rows an expert, one expert with more than the others; tile shapes, also with K cut; more experts than lanes
 GROUPS = [(1, 1, 40, 33), (3, 4, 41, 100), (64, 16, 70, 1000), (90, 70, 40, 65), (200, 150, 30, 100), (100, 3, 33, 400), (500, 7, 130, 257),
-          (776, 12, 2812, 17), (1607, 1, 5088, 976), (3000, 5, 1100, 900), (4100, 130, 70, 48)]
+          (776, 12, 2812, 17), (1607, 1, 5088, 976), (3000, 5, 1100, 900), (4100, 130, 70, 48),
+          (8737, 2, 4325, 5866), (9224, 18, 736, 9018), (6466, 2, 2920, 5710)]
 
 
 @pytest.mark.parametrize("n,e,o,i", GROUPS)
@@ -248,9 +249,10 @@ def test_i8_grouped_exact(n, e, o, i):
             wa[p:q], wu[p:q], inside[p:q] = product(rows, (b[0][k], b[1][k])), product(rows, (u[0][k], u[1][k])), True
         for dt in ("f32", "bf16"):
             y, h = out(n, o, dt), out(n, o, dt)
-            w = Workspace("i8_gemm", o, i, n, dt, e)
-            K.kq_i8_gemm(*a, *b, y, off, w.ws)
-            K.kq_i8_gated(*a, *b, *u, "relu", h, off, Workspace("i8_gated", o, i, n, dt, e).ws)
+            w1, w2 = Workspace("i8_gemm", o, i, n, dt, e), Workspace("i8_gated", o, i, n, dt, e)
+            K.kq_i8_gemm(*a, *b, y, off, w1.ws)
+            K.kq_i8_gated(*a, *b, *u, "relu", h, off, w2.ws)
+            assert w1.kept() and w2.kept()
             for t, want, name in ((y, wa, "Y"), (h, wa.clamp(min=0) * wu, "H")):
                 assert bool((t[~inside] == -77.0).all()), name + ": rows outside the offsets"
                 t[~inside] = 0.0
@@ -267,7 +269,7 @@ def test_i8_offsets_past_32_bits():
     b[0][e - 1].copy_(last), b[1][e - 1].copy_(sl)
     y = out(n, o, "bf16")
     say("i8 offsets: grouped weights")
-    K.kq_i8_gemm(*a, *b, y, offsets([0, 10, 10, 30, n]))
+    K.kq_i8_gemm(*a, *b, y, offsets([0, 10, 10, 30, n]), Workspace("i8_gemm", o, i, n, experts=e).ws)
     assert bool((y[:30] == 0).all())
     same(y[30:], product((a[0][30:], a[1][30:]), (last, sl)), "bf16", "Y")
     del b, y

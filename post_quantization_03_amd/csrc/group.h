@@ -134,44 +134,31 @@ __device__ __forceinline__ void group_place(TileAt& t, const GroupAt& at, int nx
     t.tn = __builtin_amdgcn_readfirstlane(t.tn);
 }
 
-// The largest tiles, one a compute unit at a time: those behind the last full turn of the GPU would keep it waiting a whole turn for
-// few of them, so their K is split as tile_plan splits it, with the same kind of estimate, by the count that the device
-// finds. The host makes the choice for each count of them; both kernels of a product look it up.
-constexpr int GROUP_SLOTS = 256, GROUP_SUMS = 512;       // compute units; cut tiles times splits at most
+// The tiles behind the last full turn of the GPU would keep it waiting a whole turn for few of them, so their K is split as
+// tile_plan splits it, by the count that the device finds. The host makes the choice for the counts there can be; both
+// kernels of a product look it up.
+constexpr int GROUP_COUNTS = 256;        // entries of the table: counts up to a turn's tiles, in steps of group_step
+template <typename C>
+constexpr unsigned group_step() { return C::TM == 256 ? 1 : C::TM == 128 ? 2 : 4; }      // work-groups a compute unit
 struct GroupCuts {
-    uint32_t by_rest[GROUP_SLOTS];       // splits (1: not cut) | slabs of a split << 8
+    uint32_t at[GROUP_COUNTS + 1];       // splits (1: not cut) | slabs of a split << 8
 };
 struct GroupCut {
     unsigned whole, rest;    // tiles that take all of K, tiles that are cut
     int splits, sper;
 };
-inline void group_cuts(GroupCuts& t, int64_t slabs, int products) {
-    for (int rest = 0; rest < GROUP_SLOTS; rest++) {
-        double least = 0.0;
-        for (int64_t s = 1; s <= 16; s++) {
-            const int64_t per = (slabs + s - 1) / s, splits = (slabs + per - 1) / per, wgs = rest * splits;
-            if (s > 1 && (wgs > GROUP_SUMS || per >= 1 << 24)) break;
-            const double turns = (double)((wgs + GROUP_SLOTS - 1) / GROUP_SLOTS);
-            const double us = turns * ((double)(per * products) * 1.5 + 10.0) + (splits > 1 ? 4.0 + 0.15 * (double)wgs : 0.0);
-            if (s == 1 || us < least) {
-                least = us;
-                t.by_rest[rest] = splits == 1 ? 1u : (uint32_t)splits | (uint32_t)per << 8;
-            }
-        }
-    }
-}
+template <typename C>
 __device__ __forceinline__ GroupCut group_cut(const GroupCuts& t, unsigned tiles) {
+    constexpr unsigned STEP = group_step<C>(), TURN = GROUP_COUNTS * STEP;
     GroupCut c;
-    c.rest = tiles % GROUP_SLOTS;
-    const uint32_t v = t.by_rest[c.rest];
+    c.rest = tiles % TURN;
+    const uint32_t v = t.at[(c.rest + STEP - 1) / STEP];
     c.splits = (int)(v & 255u);
     c.sper = (int)(v >> 8);
     if (c.splits == 1) c.rest = 0;
     c.whole = tiles - c.rest;
     return c;
 }
-template <typename C>
-constexpr bool group_may_cut() { return C::TM == 256; }
 
 // Products whose output rows are the tokens: Y = X W^T (plain, gated, int8) and dX = dY W.
 template <int E, int MODE, typename C>
@@ -182,16 +169,14 @@ __device__ __forceinline__ void group_tile_body(TileArgs g, const Group& gr, con
     TileAt t;
     t.cut = -1;
     t.split = t.pair = 0;
-    if constexpr (group_may_cut<C>()) {
-        const GroupCut c = group_cut(cuts, group_tiles(gr, l, C::TM) * (unsigned)nx);
-        if (id >= c.whole) {
-            if (c.rest == 0 || id >= c.whole + c.rest * (unsigned)c.splits) return;
-            t.split = __builtin_amdgcn_readfirstlane((int)((id - c.whole) / c.rest));
-            t.cut = (int)(id - c.whole - (unsigned)t.split * c.rest);
-            id = c.whole + (unsigned)t.cut;
-            g.splits = c.splits;
-            g.sper = c.sper;
-        }
+    const GroupCut c = group_cut<C>(cuts, group_tiles(gr, l, C::TM) * (unsigned)nx);
+    if (id >= c.whole) {
+        if (c.rest == 0 || id >= c.whole + c.rest * (unsigned)c.splits) return;
+        t.split = __builtin_amdgcn_readfirstlane((int)((id - c.whole) / c.rest));
+        t.cut = (int)(id - c.whole - (unsigned)t.split * c.rest);
+        id = c.whole + (unsigned)t.cut;
+        g.splits = c.splits;
+        g.sper = c.sper;
     }
     const GroupAt at = group_tile(gr, l, id, C::TM, (unsigned)nx);
     if (at.rows == 0) return;
@@ -210,7 +195,7 @@ __global__ __launch_bounds__(256) void group_reduce_kernel(TileArgs g0, Group gr
     constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
     const int nx = (int)((g0.N + TN_OUT - 1) / TN_OUT);
     const GroupLanes l = group_lanes(gr, 0, group_first(gr), C::TM);
-    const GroupCut c = group_cut(cuts, group_tiles(gr, l, C::TM) * (unsigned)nx);
+    const GroupCut c = group_cut<C>(cuts, group_tiles(gr, l, C::TM) * (unsigned)nx);
     for (unsigned b = blockIdx.x; b < c.rest * PER; b += gridDim.x) {
         TileArgs g = g0;
         TileAt t;
@@ -299,12 +284,21 @@ bool group_few(int64_t n, int64_t experts) {
     return n <= 16 * some;
 }
 
-// Tile shape of a grouped product, from the times that tile_plan takes and rows dealt evenly.
+// Estimated time, us, of work-groups of `per` slabs of tile shape h, with the constants of tile_plan.
+template <int E>
+inline double group_time(int h, int64_t wgs, int64_t per) {
+    constexpr int occ_log2[3] = {0, 1, 2};
+    constexpr double lat[3] = {1.4, 0.9, 0.75}, fix[3] = {10.0, 4.0, 1.7}, w[3] = {1.55, 0.5, E == EL_F32 ? 0.44 : 0.38};
+    const int64_t percu = (wgs + 255) >> 8, rounds = (percu + (1 << occ_log2[h]) - 1) >> occ_log2[h];
+    const double by_lat = (double)rounds * lat[h], by_w = (double)percu * w[h];
+    return (double)per * (by_lat > by_w ? by_lat : by_w) + (double)rounds * fix[h];
+}
+
+// Tile shape of a grouped product, for rows dealt evenly.
 template <int E, int MODE>
 int group_shape(int64_t n, int64_t experts, int64_t N, int64_t K) {
     if (E == EL_F32) return 2;
-    constexpr int size[3] = {256, 128, 64}, occ[3] = {1, 2, 4}, BK = 8 * el_chunk<E>();
-    constexpr double lat[3] = {1.4, 0.9, 0.75}, fix[3] = {10.0, 4.0, 1.7}, w[3] = {1.55, 0.5, 0.38};
+    constexpr int size[3] = {256, 128, 64}, BK = 8 * el_chunk<E>();
     const int64_t some = experts < n ? experts : n;
     const int64_t each = some ? (n + some - 1) / some : 0;
     int best = 2;
@@ -319,15 +313,62 @@ int group_shape(int64_t n, int64_t experts, int64_t N, int64_t K) {
             tiles = some * ((each + size[h] - 1) / size[h]) * ((N + tn - 1) / tn);
             slabs = (K + BK - 1) / BK * (MODE == TP_GRAD_X ? 2 : 1);
         }
-        const int64_t percu = (tiles + 255) / 256, rounds = (percu + occ[h] - 1) / occ[h];
-        const double by_lat = (double)rounds * lat[h], by_w = (double)percu * w[h];
-        const double t = (double)slabs * (by_lat > by_w ? by_lat : by_w) + (double)rounds * fix[h];
+        const double t = group_time<E>(h, tiles, slabs);
         if (h == 0 || t < least) {
             least = t;
             best = h;
         }
     }
     return best;
+}
+
+// How the tiles behind the last full turn are cut, for each number of them, and the most split sums (of a tile) that can make. Split
+// sums are written and read once at 3.5 TB/s, by a second launch, which is left out (and nothing cut) where it would not pay: where
+// cutting gains less than 5 us on average over the tile counts that n rows may make.
+template <int E, int MODE, typename C>
+int64_t group_cuts(GroupCuts& t, int64_t n, int64_t experts, int64_t N, int64_t K) {
+    constexpr int h = C::TM == 256 ? 0 : C::TM == 128 ? 1 : 2, BK = 8 * el_chunk<E>(), TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
+    constexpr int64_t STEP = group_step<C>(), TURN = GROUP_COUNTS * STEP;
+    constexpr int products = MODE == TP_GRAD_X ? 2 : 1;
+    const int64_t slabs = (K + BK - 1) / BK, nx = (N + TN_OUT - 1) / TN_OUT, most = group_tiles_max(n, experts, C::TM) * nx;
+    constexpr int CUTS = 7, cuts[CUTS] = {2, 3, 4, 6, 8, 12, 16};
+    int64_t per[CUTS], splits[CUTS];
+    for (int c = 0; c < CUTS; c++) {
+        per[c] = (slabs + cuts[c] - 1) / cuts[c];
+        splits[c] = (slabs + per[c] - 1) / per[c];
+    }
+    double gain[GROUP_COUNTS + 1];
+    for (int k = 0; k <= GROUP_COUNTS; k++) {
+        t.at[k] = 1u;
+        gain[k] = 0.0;
+        const int64_t rest = k * STEP;
+        if (rest == 0 || rest >= TURN || rest >= most + STEP) continue;
+        const double whole = group_time<E>(h, rest, slabs * products);
+        double least = whole;
+        for (int c = 0; c < CUTS; c++) {
+            const int64_t wgs = rest * splits[c];
+            if (wgs > 2 * TURN || per[c] >= 1 << 24) break;
+            const double us = group_time<E>(h, wgs, per[c] * products) + 4.0 + (double)wgs * (C::TM * C::TN * 8 / 3.5e6);
+            if (us < least) {
+                least = us;
+                t.at[k] = (uint32_t)splits[c] | (uint32_t)per[c] << 8;
+            }
+        }
+        if ((t.at[k] & 255u) == 1) t.at[k] = 1u;
+        gain[k] = whole - least;
+    }
+    // tile rows: a whole one for every C::TM rows, and up to one more an expert
+    const int64_t some = experts < n ? experts : n, least = (n + C::TM - 1) / C::TM > some ? (n + C::TM - 1) / C::TM : some;
+    double sum = 0.0;
+    for (int k = 0; k <= 16; k++)
+        sum += gain[((least * nx + (most - least * nx) * k / 16) % TURN + STEP - 1) / STEP];
+    if (sum < 5.0 * 17) return 0;
+    int64_t sums = 0;
+    for (int k = 0; k <= GROUP_COUNTS && (k - 1) * STEP < most; k++) {
+        const int64_t m = (t.at[k] & 255u) > 1 ? k * STEP * (int64_t)(t.at[k] & 255u) : 0;
+        sums = m > sums ? m : sums;
+    }
+    return sums;
 }
 
 // f(tile shape) for 0 L, 1 M, 2 S; fp32 has S alone
@@ -340,35 +381,42 @@ kq_status with_shape(int shape, F&& f) {
     return f(TileS{});
 }
 
-// Workspace of a product whose largest tiles may be cut: 128 MiB of split sums.
+// Workspace of a product whose tiles may be cut.
 template <int E, int MODE>
 size_t group_ws(int64_t n, int64_t experts, int64_t N, int64_t K) {
-    if (n <= 0 || group_shape<E, MODE>(n, experts, N, K) != 0) return 0;
-    return (size_t)GROUP_SUMS * TileL::TM * TileL::TN * sizeof(float);
+    size_t bytes = 0;
+    if (n > 0)
+        with_shape<E>(group_shape<E, MODE>(n, experts, N, K), [&](auto shape) {
+            typedef decltype(shape) C;
+            GroupCuts cuts;
+            bytes = (size_t)group_cuts<E, MODE, C>(cuts, n, experts, N, K) * C::TM * C::TN * sizeof(float);
+            return KQ_OK;
+        });
+    return bytes;
 }
 
 template <int E, int MODE>
 kq_status group_launch(TileArgs g, const Group& gr, void* ws, size_t ws_bytes, hipStream_t st, const char* who) {
-    const size_t need = group_ws<E, MODE>(gr.n, gr.experts, g.N, g.K);
-    if (need && (!ws || !aligned16(ws) || ws_bytes < need))
-        return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
-    g.part = static_cast<float*>(ws);
     return with_shape<E>(group_shape<E, MODE>(gr.n, gr.experts, g.N, g.K), [&](auto shape) {
         typedef decltype(shape) C;
-        constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
-        const int64_t wgs = group_tiles_max(gr.n, gr.experts, C::TM) * ((g.N + TN_OUT - 1) / TN_OUT) + (group_may_cut<C>() ? GROUP_SUMS : 0);
+        constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
+        GroupCuts cuts;
+        const int64_t sums = group_cuts<E, MODE, C>(cuts, gr.n, gr.experts, g.N, g.K);
+        if (sums && (!ws || !aligned16(ws) || ws_bytes < (size_t)sums * C::TM * C::TN * sizeof(float)))
+            return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
+        if (!sums)
+            for (uint32_t& c : cuts.at) c = 1u;
+        g.part = static_cast<float*>(ws);
+        const int64_t wgs = group_tiles_max(gr.n, gr.experts, C::TM) * ((g.N + TN_OUT - 1) / TN_OUT) + sums;
         if (!grid_ok(wgs, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
         static std::atomic<uint64_t> allowed{0};
         KQ_TRY(allow_lds(reinterpret_cast<const void*>(&group_tile_kernel<E, MODE, C>), C::SMEM, allowed, who));
-        GroupCuts cuts;
-        if (group_may_cut<C>()) {
-            constexpr int BK = 8 * el_chunk<E>();
-            group_cuts(cuts, (g.K + BK - 1) / BK, MODE == TP_GRAD_X ? 2 : 1);
-        }
         hipLaunchKernelGGL((group_tile_kernel<E, MODE, C>), dim3((unsigned)wgs), dim3(C::THREADS), C::SMEM, st, g, gr, cuts);
         KQ_TRY(check_launch(who));
-        if constexpr (group_may_cut<C>()) {
-            hipLaunchKernelGGL((group_reduce_kernel<E, MODE, C>), dim3(2048), dim3(256), 0, st, g, gr, cuts);
+        if (sums) {
+            const int64_t pieces = sums * PER;
+            hipLaunchKernelGGL((group_reduce_kernel<E, MODE, C>), dim3((unsigned)(pieces < 2048 ? pieces : 2048)), dim3(256), 0, st, g, gr,
+                               cuts);
             KQ_TRY(check_launch(who));
         }
         return KQ_OK;

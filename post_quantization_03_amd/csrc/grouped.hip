@@ -67,15 +67,20 @@ static kq_status backward(const char* who, const Group& gr, TileArgs x, TileArgs
 
 using namespace kq;
 
-size_t grouped_ws(kq_op op, int64_t o, int64_t i, int64_t n, kq_dtype dt, int64_t experts) {
-    if (dt != KQ_BF16 || n <= 0 || o <= 0 || i <= 0 || experts <= 0 || n > GROUP_ROWS_MAX) return 0;
+template <int E>
+static size_t grouped_ws_of(kq_op op, int64_t o, int64_t i, int64_t n, int64_t experts) {
     if (op == KQ_OP_GROUPED_BACKWARD) {
         // of one product's dX or of two's
-        const size_t a = group_ws<EL_BF16, TP_GRAD_X>(n, experts, i, o), b = group_ws<EL_BF16, TP_GRAD_X1>(n, experts, i, o);
+        const size_t a = group_ws<E, TP_GRAD_X>(n, experts, i, o), b = group_ws<E, TP_GRAD_X1>(n, experts, i, o);
         return a > b ? a : b;
     }
-    if (group_few<EL_BF16>(n, experts)) return 0;
-    return op == KQ_OP_GROUPED_GATED ? group_ws<EL_BF16, TP_GATED>(n, experts, o, i) : group_ws<EL_BF16, TP_PLAIN>(n, experts, o, i);
+    if (group_few<E>(n, experts)) return 0;
+    return op == KQ_OP_GROUPED_GATED ? group_ws<E, TP_GATED>(n, experts, o, i) : group_ws<E, TP_PLAIN>(n, experts, o, i);
+}
+
+size_t grouped_ws(kq_op op, int64_t o, int64_t i, int64_t n, kq_dtype dt, int64_t experts) {
+    if (n <= 0 || o <= 0 || i <= 0 || experts <= 0 || experts > GROUP_MAX || n > GROUP_ROWS_MAX || !tile_sizes_ok(n, o > i ? o : i)) return 0;
+    return dt == KQ_BF16 ? grouped_ws_of<EL_BF16>(op, o, i, n, experts) : grouped_ws_of<EL_F32>(op, o, i, n, experts);
 }
 
 extern "C" kq_status kq_grouped_gemm(const void* X, int64_t ldx, const void* W, int64_t ldw, const int32_t* offsets,

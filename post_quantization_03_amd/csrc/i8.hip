@@ -200,7 +200,7 @@ using namespace kq;
 size_t i8_product_ws(int64_t o, int64_t i, int64_t n, bool gated, int64_t experts) {
     if (n <= 0 || o <= 0 || i <= 0 || !tile_sizes_ok(n, o) || experts < 0) return 0;
     if (experts) {
-        if (n > GROUP_ROWS_MAX || group_few<EL_I8>(n, experts)) return 0;
+        if (experts > GROUP_MAX || n > GROUP_ROWS_MAX || group_few<EL_I8>(n, experts)) return 0;
         return gated ? group_ws<EL_I8, TP_GATED>(n, experts, o, i) : group_ws<EL_I8, TP_PLAIN>(n, experts, o, i);
     }
     if (few_tokens<EL_I8>(n, o, i)) return 0;

@@ -130,8 +130,9 @@ def test_i8_product_refusals(call):
     if call is i8_gated:
         for kw in (dict(U=None), dict(sU=None), dict(act=4), dict(act=-1), dict(U=FOUR)):
             assert call(**kw) == EINVAL, kw
-    large = dict(n=8192, o=4096, i=4096, off=P, e=4, lda=4096, ldb=4096, ldy=4096, **({"ldu": 4096} if call is i8_gated else {}))
-    for ws, wb in ((None, 0), (P, (128 << 20) - 1), (FOUR, 128 << 20)):
+    large = dict(n=16384, o=4096, i=11008, off=P, e=8, lda=11008, ldb=11008, ldy=4096, **({"ldu": 11008} if call is i8_gated else {}))
+    need = K.kq_workspace_bytes("i8_gemm" if call is i8_gemm else "i8_gated", 4096, 11008, 16384, group=8)
+    for ws, wb in ((None, 0), (P, need - 1), (FOUR, need)):
         assert call(ws=ws, wb=wb, **large) == EWORKSPACE, (ws, wb)
 
 
@@ -155,8 +156,10 @@ def test_grouped_refusals(call):
     if call is ggated:
         for kw, st in ((dict(U=None), EINVAL), (dict(act=9), EINVAL), (dict(lda=4), ESHAPE), (dict(B=ODD), EINVAL)):
             assert call(**kw) == st, kw
-    large = dict(n=8192, o=4096, i=4096, e=4, ldx=4096, ldw=4096, ldy=4096, **({"ldu": 4096, "A": None, "B": None} if call is ggated else {}))
-    for ws, wb in ((None, 0), (P, (128 << 20) - 1), (FOUR, 128 << 20)):
+    large = dict(n=16384, o=4096, i=11008, e=8, ldx=11008, ldw=11008, ldy=4096,
+                 **({"ldu": 11008, "A": None, "B": None} if call is ggated else {}))
+    need = K.kq_workspace_bytes("grouped_gemm" if call is gg else "grouped_gated", 4096, 11008, 16384, group=8)
+    for ws, wb in ((None, 0), (P, need - 1), (FOUR, need)):
         assert call(ws=ws, wb=wb, **large) == EWORKSPACE, (ws, wb)
     assert call(n=0) == 0
 
@@ -206,12 +209,13 @@ def test_norm_refusals():
 def test_workspace_sizes():
     for op in ("i8_gemm", "i8_gated"):
         assert K.kq_workspace_bytes(op, 4096, 4096, 32) == 0
-        assert K.kq_workspace_bytes(op, 200, 9000, 300, group=4) == 0       # small grouped products are not cut
-        assert K.kq_workspace_bytes(op, 4096, 4096, 8192, group=4) == 128 << 20
-    for op in ("grouped_gemm", "grouped_gated", "grouped_backward"):
-        assert K.kq_workspace_bytes(op, 200, 900, 300, group=4) == 0
-        assert K.kq_workspace_bytes(op, 4096, 4096, 8192, group=4) == 128 << 20
-        assert K.kq_workspace_bytes(op, 4096, 4096, 8192, K.KQ_F32, group=4) == 0
+        assert 0 < K.kq_workspace_bytes(op, 200, 9000, 300, group=4) <= 32 << 20
+    for op in ("i8_gemm", "i8_gated", "grouped_gemm", "grouped_gated", "grouped_backward"):
+        assert K.kq_workspace_bytes(op, 200, 100, 300, group=4) == 0        # small grouped products are not cut
+        assert 0 < K.kq_workspace_bytes(op, 4096, 11008, 16384, group=8) <= 128 << 20
+        assert K.kq_workspace_bytes(op, 4096, 11008, 16384, group=0) == 0 or op.startswith("i8")
+        assert K.kq_workspace_bytes(op, 4096, 11008, 16384, group=5000) == 0
+        assert K.kq_workspace_bytes(op, 4096, 11008, 1 << 40, group=8) == 0
     for d in (1, 100, 1000, 4096, 11008, 50000):
         for n in (1, 3, 333, 8192):
             for dt in (K.KQ_F32, K.KQ_BF16):

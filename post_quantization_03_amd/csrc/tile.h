@@ -728,7 +728,32 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, const TileAt& at) {
     for (int i = 0; i < FM; i++) {
         const int64_t m = m0 + wm * FM * 16 + 16 * i + x16;
         if (m >= g.M) continue;
-        if constexpr (TB) {
+        if (TB && E == EL_BF16 && !cut) {
+            // two fragments at a time: lane groups exchange halves, so that each has 8 columns of one of them and a row is written in
+            // 64 bytes
+#pragma unroll
+            for (int j = 0; j < FN; j += 2) {
+                uint32_t p[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+#pragma unroll
+                    for (int f = 0; f < 2; f++)
+                        p[f][h] = (uint32_t)to_bf16((float)acc[i][j + f][2 * h]) | (uint32_t)to_bf16((float)acc[i][j + f][2 * h + 1]) << 16;
+                    const auto q = __builtin_amdgcn_permlane16_swap(p[0][h], p[1][h], false, false);
+                    p[0][h] = q[0];
+                    p[1][h] = q[1];
+                }
+                const int64_t n = n0 + wn * FN * 16 + 16 * (j + (g4 & 1)) + 8 * (g4 >> 1);
+                uint16_t* out = static_cast<uint16_t*>(Y) + m * ldY + n;
+                if (n + 8 <= g.N) {
+                    *reinterpret_cast<uint4*>(out) = make_uint4(p[0][0], p[0][1], p[1][0], p[1][1]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (n + e < g.N) out[e] = (uint16_t)(p[e / 4][e / 2 % 2] >> (16 * (e % 2)));
+                }
+            }
+        } else if constexpr (TB) {
 #pragma unroll
             for (int j = 0; j < FN; j++) {
                 const int64_t n = n0 + wn * FN * 16 + 16 * j + 4 * g4;

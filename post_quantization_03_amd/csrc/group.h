@@ -233,15 +233,16 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void group_grad_kernel(TileArgs 
     tile_body<E, TP_GRAD_W, C>(g, t);
 }
 
-// Few rows an expert: work-group (block of 16 rows of B, expert with rows). Its rows go 16 NB at a time, the weights
-// from HBM the first time and from a cache after that.
+// Few rows an expert: a work-group for 16 NB of them and 16 rows of B. Of an expert with more, the weights come from HBM for the
+// work-group that is first and from a cache for the others.
 template <int E, bool GATED, int NB>
 __global__ __launch_bounds__(FEW_THREADS) void group_few_kernel(FewArgs g, Group gr, int blocks) {
-    constexpr int ALL = (int)GROUP_ROWS_MAX;         // one "tile" for an expert with rows
-    const GroupAt at = group_tile(gr, group_lanes(gr, 0, group_first(gr), ALL), blockIdx.x, ALL, (unsigned)blocks);
+    constexpr int ROWS = 16 * NB;
+    const GroupAt at = group_tile(gr, group_lanes(gr, 0, group_first(gr), ROWS), blockIdx.x, ROWS, (unsigned)blocks);
     if (at.rows == 0) return;
-    const int64_t begin = at.begin, w0 = (int64_t)at.k * gr.o;
-    g.n = at.rows;
+    const int first = at.id / blocks * ROWS;
+    const int64_t begin = at.begin + first, w0 = (int64_t)at.k * gr.o;
+    g.n = at.rows - first < ROWS ? at.rows - first : ROWS;
     g.A += begin * g.lda;
     g.B += w0 * g.ldb;
     if (GATED) g.B2 += w0 * g.ldb2;
@@ -255,19 +256,7 @@ __global__ __launch_bounds__(FEW_THREADS) void group_few_kernel(FewArgs g, Group
         g.Y2 = rows_on(g.Y2, begin * g.ldy2, g.dt);
         g.Y3 = rows_on(g.Y3, begin * g.ldy3, g.dt);
     }
-    for (;;) {
-        few_body<E, GATED, NB>(g, at.id);
-        g.n -= 16 * NB;
-        if (g.n <= 0) return;
-        __syncthreads();         // the sums in LDS have been read
-        g.A += 16 * NB * g.lda;
-        if (E == EL_I8) g.fA += 16 * NB;
-        g.Y = rows_on(g.Y, 16 * NB * g.ldy, g.dt);
-        if (GATED) {
-            g.Y2 = rows_on(g.Y2, 16 * NB * g.ldy2, g.dt);
-            g.Y3 = rows_on(g.Y3, 16 * NB * g.ldy3, g.dt);
-        }
-    }
+    few_body<E, GATED, NB>(g, at.id % blocks);
 }
 
 // ------------------------------------------------------------------------------------------ launches
@@ -277,11 +266,15 @@ inline int64_t group_tiles_max(int64_t n, int64_t experts, int64_t size) {
     return (n - some) / size + some;
 }
 
-// Whether n rows of `experts` experts run as few tokens each. The counts are not known here; the rule takes their mean.
+// Whether n rows of `experts` experts run as few tokens each. The counts are not known here; the rule takes their mean. MI355X, us as
+// few tokens / as tiles, o x i weights an expert, at a mean of
+//   4   bf16 gated 16 x 1376 x 4096: 68 / 89; int8 the same: 38 / 43
+//   8   bf16 8 x 4096 x 11008: 152 / 152, gated 8 x 1376 x 4096: 44 / 53; int8 16 x 4096 x 4096: 66 / 71
+//   10  bf16 8 x 4096 x 11008: 170 / 165;  12  int8 gated 8 x 1376 x 4096: 27 / 20;  16  bf16 8 x 4096 x 11008: 205 / 165
+// and fp32 5 x 1376 x 1000, 32 rows a work-group: gated at 12 19.2 / 23.3, plain at 20 14.8 / 18.4, at 40 16.8 / 21.1.
 template <int E>
 bool group_few(int64_t n, int64_t experts) {
-    const int64_t some = experts < n ? experts : n;
-    return n <= 16 * some;
+    return n <= (E == EL_F32 ? 32 : 8) * (experts < n ? experts : n);
 }
 
 // Estimated time, us, of work-groups of `per` slabs of tile shape h, with the constants of tile_plan.
@@ -439,11 +432,19 @@ kq_status group_grad_launch(TileArgs g, const Group& gr, int pairs, hipStream_t 
 
 template <int E, bool GATED>
 kq_status group_few_launch(const FewArgs& g, const Group& gr, hipStream_t st, const char* who) {
-    const int64_t blocks = (g.o + 15) / 16, wgs = blocks * (gr.experts < gr.n ? gr.experts : gr.n);
-    if (!grid_ok(wgs, FEW_THREADS)) return fail(KQ_ESHAPE, "%s: too many rows", who);
-    const size_t sums = (size_t)FEW_WAVES * (GATED ? 2 : 1) * 1024;
-    hipLaunchKernelGGL((group_few_kernel<E, GATED, 1>), dim3((unsigned)wgs), dim3(FEW_THREADS), sums, st, g, gr, (int)blocks);
-    return check_launch(who);
+    const int64_t blocks = (g.o + 15) / 16;
+    auto run = [&](auto nb) {
+        constexpr int NB = decltype(nb)::value;          // 16 rows each
+        const int64_t wgs = blocks * group_tiles_max(gr.n, gr.experts, 16 * NB);
+        if (!grid_ok(wgs, FEW_THREADS)) return fail(KQ_ESHAPE, "%s: too many rows", who);
+        const size_t sums = (size_t)FEW_WAVES * (GATED ? 2 : 1) * NB * 1024;
+        hipLaunchKernelGGL((group_few_kernel<E, GATED, NB>), dim3((unsigned)wgs), dim3(FEW_THREADS), sums, st, g, gr, (int)blocks);
+        return check_launch(who);
+    };
+    if constexpr (E == EL_F32) {
+        if (gr.n > 8 * (int64_t)gr.experts) return run(std::integral_constant<int, 2>{});
+    }
+    return run(std::integral_constant<int, 1>{});
 }
 
 // ------------------------------------------------------------------------------------------- checks

@@ -212,8 +212,8 @@ __global__ __launch_bounds__(256) void group_reduce_kernel(TileArgs g0, Group gr
 
 // dW = dY^T X over each expert's rows, zeros for one without any: `per` tiles an expert (of both gradients).
 template <int E, typename C>
-__global__ __launch_bounds__(C::THREADS, C::EU) void group_grad_kernel(TileArgs g, Group gr, int per) {
-    const int k = (int)(blockIdx.x / (unsigned)per), id = (int)(blockIdx.x - (unsigned)k * (unsigned)per);
+__device__ __forceinline__ void group_grad_body(TileArgs g, const Group& gr, int per, unsigned block) {
+    const int k = (int)(block / (unsigned)per), id = (int)(block - (unsigned)k * (unsigned)per);
     int begin, rows;
     group_rows(gr, k, begin, rows);
     g.K = rows;
@@ -231,6 +231,18 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void group_grad_kernel(TileArgs 
     t.tm = __builtin_amdgcn_readfirstlane(t.tm);
     t.tn = __builtin_amdgcn_readfirstlane(t.tn);
     tile_body<E, TP_GRAD_W, C>(g, t);
+}
+template <int E, typename C>
+__global__ __launch_bounds__(C::THREADS, C::EU) void group_grad_kernel(TileArgs g, Group gr, int per) {
+    group_grad_body<E, C>(g, gr, per, blockIdx.x);
+}
+
+// dX and dW side by side, `first` work-groups for dX, for small products: each leaves compute units idle that the other fills
+// (517 rows of 5 experts 1376 x 1000 fp32: one after the other 24 and 26 us, together and with the launch between 50 -> 44 us a call).
+template <int E, int MODE, typename C>
+__global__ __launch_bounds__(C::THREADS, C::EU) void group_grads_kernel(TileArgs x, TileArgs w, Group gr, GroupCuts cuts, int per, unsigned first) {
+    if (blockIdx.x < first) group_tile_body<E, MODE, C>(x, gr, cuts, blockIdx.x);
+    else group_grad_body<E, C>(w, gr, per, blockIdx.x - first);
 }
 
 // Few rows an expert: a work-group for 16 NB of them and 16 rows of B. Of an expert with more, the weights come from HBM for the
@@ -388,31 +400,40 @@ size_t group_ws(int64_t n, int64_t experts, int64_t N, int64_t K) {
     return bytes;
 }
 
+// Work-groups of a product, after its cuts are chosen and its workspace checked.
+template <int E, int MODE, typename C>
+kq_status group_prepare(GroupCuts& cuts, int64_t& wgs, int64_t& sums, TileArgs& g, const Group& gr, void* ws, size_t ws_bytes, const char* who) {
+    constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
+    sums = group_cuts<E, MODE, C>(cuts, gr.n, gr.experts, g.N, g.K);
+    if (sums && (!ws || !aligned16(ws) || ws_bytes < (size_t)sums * C::TM * C::TN * sizeof(float)))
+        return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
+    if (!sums)
+        for (uint32_t& c : cuts.at) c = 1u;
+    g.part = static_cast<float*>(ws);
+    wgs = group_tiles_max(gr.n, gr.experts, C::TM) * ((g.N + TN_OUT - 1) / TN_OUT) + sums;
+    return grid_ok(wgs, C::THREADS) ? KQ_OK : fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
+}
+template <int E, int MODE, typename C>
+kq_status group_sums_launch(const TileArgs& g, const Group& gr, const GroupCuts& cuts, int64_t sums, hipStream_t st, const char* who) {
+    constexpr int PER = C::TM * (MODE == TP_GATED ? C::TN / 2 : C::TN) / 1024;
+    if (!sums) return KQ_OK;
+    const int64_t pieces = sums * PER;
+    hipLaunchKernelGGL((group_reduce_kernel<E, MODE, C>), dim3((unsigned)(pieces < 2048 ? pieces : 2048)), dim3(256), 0, st, g, gr, cuts);
+    return check_launch(who);
+}
+
 template <int E, int MODE>
 kq_status group_launch(TileArgs g, const Group& gr, void* ws, size_t ws_bytes, hipStream_t st, const char* who) {
     return with_shape<E>(group_shape<E, MODE>(gr.n, gr.experts, g.N, g.K), [&](auto shape) {
         typedef decltype(shape) C;
-        constexpr int TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN, PER = C::TM * TN_OUT / 1024;
         GroupCuts cuts;
-        const int64_t sums = group_cuts<E, MODE, C>(cuts, gr.n, gr.experts, g.N, g.K);
-        if (sums && (!ws || !aligned16(ws) || ws_bytes < (size_t)sums * C::TM * C::TN * sizeof(float)))
-            return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
-        if (!sums)
-            for (uint32_t& c : cuts.at) c = 1u;
-        g.part = static_cast<float*>(ws);
-        const int64_t wgs = group_tiles_max(gr.n, gr.experts, C::TM) * ((g.N + TN_OUT - 1) / TN_OUT) + sums;
-        if (!grid_ok(wgs, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
+        int64_t wgs, sums;
+        KQ_TRY((group_prepare<E, MODE, C>(cuts, wgs, sums, g, gr, ws, ws_bytes, who)));
         static std::atomic<uint64_t> allowed{0};
         KQ_TRY(allow_lds(reinterpret_cast<const void*>(&group_tile_kernel<E, MODE, C>), C::SMEM, allowed, who));
         hipLaunchKernelGGL((group_tile_kernel<E, MODE, C>), dim3((unsigned)wgs), dim3(C::THREADS), C::SMEM, st, g, gr, cuts);
         KQ_TRY(check_launch(who));
-        if (sums) {
-            const int64_t pieces = sums * PER;
-            hipLaunchKernelGGL((group_reduce_kernel<E, MODE, C>), dim3((unsigned)(pieces < 2048 ? pieces : 2048)), dim3(256), 0, st, g, gr,
-                               cuts);
-            KQ_TRY(check_launch(who));
-        }
-        return KQ_OK;
+        return group_sums_launch<E, MODE, C>(g, gr, cuts, sums, st, who);
     });
 }
 
@@ -428,6 +449,26 @@ kq_status group_grad_launch(TileArgs g, const Group& gr, int pairs, hipStream_t 
                            (int)per);
         return check_launch(who);
     });
+}
+
+// Both gradients where both are cut into the smallest tiles.
+template <int E, int MODE>
+bool group_grads_together(const TileArgs& x, const TileArgs& w, const Group& gr) {
+    return gr.n > 0 && group_shape<E, MODE>(gr.n, gr.experts, x.N, x.K) == 2 && group_shape<E, TP_GRAD_W>(gr.n, gr.experts, w.M, w.N) == 2;
+}
+template <int E, int MODE>
+kq_status group_grads_launch(TileArgs x, const TileArgs& w, const Group& gr, int pairs, void* ws, size_t ws_bytes, hipStream_t st,
+                             const char* who) {
+    typedef TileS C;
+    GroupCuts cuts;
+    int64_t wgs, sums;
+    KQ_TRY((group_prepare<E, MODE, C>(cuts, wgs, sums, x, gr, ws, ws_bytes, who)));
+    const int64_t per = ((w.M + C::TM - 1) / C::TM) * ((w.N + C::TN - 1) / C::TN) * pairs;
+    if (!grid_ok(wgs + per * gr.experts, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
+    hipLaunchKernelGGL((group_grads_kernel<E, MODE, C>), dim3((unsigned)(wgs + per * gr.experts)), dim3(C::THREADS), C::SMEM, st, x, w, gr,
+                       cuts, (int)per, (unsigned)wgs);
+    KQ_TRY(check_launch(who));
+    return group_sums_launch<E, MODE, C>(x, gr, cuts, sums, st, who);
 }
 
 template <int E, bool GATED>

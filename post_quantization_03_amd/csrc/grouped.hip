@@ -53,14 +53,18 @@ static kq_status forward(const char* who, const Group& gr, const void* X, int64_
     return group_launch<E, GATED ? TP_GATED : TP_PLAIN>(g, gr, ws, ws_bytes, st, who);
 }
 
-template <int E>
-static kq_status backward(const char* who, const Group& gr, TileArgs x, TileArgs w, int pairs, void* ws, size_t ws_bytes,
+template <int E, int MODE>
+static kq_status backward(const char* who, const Group& gr, const TileArgs& x, const TileArgs& w, int pairs, void* ws, size_t ws_bytes,
                           hipStream_t st) {
-    if (x.Y) {
-        if (x.A2) KQ_TRY((group_launch<E, TP_GRAD_X>(x, gr, ws, ws_bytes, st, who)));
-        else KQ_TRY((group_launch<E, TP_GRAD_X1>(x, gr, ws, ws_bytes, st, who)));
-    }
+    if (x.Y && pairs && group_grads_together<E, MODE>(x, w, gr)) return group_grads_launch<E, MODE>(x, w, gr, pairs, ws, ws_bytes, st, who);
+    if (x.Y) KQ_TRY((group_launch<E, MODE>(x, gr, ws, ws_bytes, st, who)));
     return pairs ? group_grad_launch<E>(w, gr, pairs, st, who) : KQ_OK;
+}
+template <int E>
+static kq_status backward(const char* who, const Group& gr, const TileArgs& x, const TileArgs& w, int pairs, void* ws, size_t ws_bytes,
+                          hipStream_t st) {
+    return x.A2 ? backward<E, TP_GRAD_X>(who, gr, x, w, pairs, ws, ws_bytes, st)
+                : backward<E, TP_GRAD_X1>(who, gr, x, w, pairs, ws, ws_bytes, st);
 }
 
 }  // namespace kq

@@ -9,6 +9,7 @@ import torch
 
 from oracle import experts as oe
 from post_quantization_03_amd import _lib as K
+from post_quantization_03_amd import ffn
 
 EINVAL, ESHAPE, EWORKSPACE = 1, 2, 6
 P = ctypes.c_void_p(4096)        # a stand-in: refused calls never dereference it
@@ -281,3 +282,67 @@ def test_stacks_and_vectors():
         K._act("a", "tanh")
     with pytest.raises(ValueError, match="kind"):
         K._norm("n", "batch")
+
+
+# ----------------------------------------------------------------------------------------- drivers
+def test_driver_refusals():
+    from post_quantization_03_amd.layer import LayerCfg
+    z = torch.zeros
+    for shapes in (((8, 4), (8, 5), (4, 8)), ((8, 4), (8, 4), (4, 7)), ((3, 8, 4), (3, 8, 4), (4, 8)), ((3, 8, 4), (3, 8, 4), (2, 4, 8)),
+                   ((8,), (8,), (8,))):
+        with pytest.raises(ValueError, match="shapes"):
+            ffn.Int8FeedForward(*(z(*s) for s in shapes))
+    with pytest.raises(ValueError, match="activation"):
+        ffn.Int8FeedForward(z(8, 4), z(8, 4), z(4, 8), "tanh")
+    for bad in ([0, 5, 4], [-1, 2, 4], [0, 2, 11]):
+        with pytest.raises(ValueError, match="ascend"):
+            ffn._spans(torch.tensor(bad, dtype=torch.int32), 10)
+    assert ffn._spans(torch.tensor([2, 2, 10], dtype=torch.int32), 10) == [(2, 2), (2, 10)]
+    cfg = LayerCfg(bits=4, group=64, form="diag")
+    with pytest.raises(ValueError, match="GPU"):
+        ffn.calibrate_experts(z(4, 64), z(2, 8, 64), z(2, 8, 64), torch.tensor([0, 2, 4], dtype=torch.int32), z(4, 8), "silu", cfg)
+    with pytest.raises(ValueError, match="GPU"):
+        ffn.calibrate_norm_gated(z(4, 64), z(64), None, "layer", 1e-5, z(8, 64), z(8, 64), z(4, 8), "silu", cfg)
+
+
+def test_drivers_run_on_their_tensors_device(monkeypatch):
+    """Tensors on a device other than the current one: every call of the drivers runs with the tensors' device current."""
+    import contextlib
+
+    from post_quantization_03_amd.layer import LayerCfg
+
+    class OnOne(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    current, calls = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(d if isinstance(d, int) else 1)
+        yield
+        current.pop()
+
+    def record(name):
+        def call(*args, **kw):
+            calls.append((name, current[-1]))
+            return {}
+        return call
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for name in ("kq_gated_forward", "kq_gated_backward", "kq_hessian_accum", "kq_hg_extract", "kq_norm_forward", "kq_norm_backward",
+                 "kq_grouped_gated", "kq_grouped_backward"):
+        monkeypatch.setattr(K, name, record(name))
+    monkeypatch.setattr(ffn, "quantize_layer", record("quantize_layer"))
+    rows = ffn._rows
+    monkeypatch.setattr(ffn, "_rows", lambda n, d, like: rows(n, d, like).as_subclass(OnOne))
+    x, w, dh, gamma, ws = (torch.zeros(*s).as_subclass(OnOne) for s in ((4, 64), (8, 64), (4, 8), (64,), (3, 8, 64)))
+    cfg = LayerCfg(bits=4, group=64, form="diag")
+    ffn.calibrate_norm_gated(x, gamma, None, "rms", 1e-5, w, w, dh, "silu", cfg)
+    assert calls == [(n, 1) for n in ["kq_norm_forward", "kq_gated_forward", "kq_gated_backward"] +
+                     2 * ["kq_hessian_accum", "kq_hg_extract"] + ["kq_norm_backward"]]
+    calls.clear()
+    out = ffn.quantize_experts(x, ws, ws, torch.tensor([0, 1, 1, 4], dtype=torch.int32), dh, "silu", None, None, None, cfg)
+    assert calls == [(n, 1) for n in ["kq_grouped_gated", "kq_gated_backward", "kq_grouped_backward"] +
+                     4 * ["kq_hessian_accum", "kq_hg_extract"] + 4 * ["quantize_layer"]]
+    assert out["gate"][1] is None and out["up"][1] is None and current == [0]

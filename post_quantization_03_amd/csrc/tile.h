@@ -1037,10 +1037,13 @@ constexpr int FEW_WAVES = 8, FEW_THREADS = 64 * FEW_WAVES;
 // Whether n tokens run here rather than as tiles. Measured on MI355X, us here / as tiles, o x i weights:
 //   E2M1  11008 x 4096: 8.3 / 11.2 at 1 token, 15.4 / 16.1 at 32, 22.2 / 16.1 at 33; 4096 x 11008: 11.8 / 14.8
 //         at 32, 14.6 / 14.3 at 33
+//   int8  4096 x 11008: 9.6 / 12.7 at 1, 12.0 / 13.9 at 16, 16.4 / 14.3 at 20; 4096 x 4096: 8.5 / 10.8 at 24; gated 11008 x 4096:
+//         17.7 / 17.7 at 1, 19.6 / 17.8 at 16; gated 1376 x 4096: 9.7 / 12.3 at 16
 //   bf16  gated 11008 x 4096: 34.1 / 34.7 at 8, 36.2 / 34.4 at 16; 1376 x 1000: 6.7 / 9.2 at 48
 //   fp32  gated 11008 x 4096: 104 / 135 at 32, 173 / 134 at 33; 1376 x 1000: 10.0 / 15.4 at 32, 16.6 / 15.6 at 33
 template <int E>
 bool few_tokens(int64_t n, int64_t o, int64_t i) {
+    if (E == EL_I8) return n <= 16 || (n <= 32 && o * i <= (1 << 24));
     if (E != EL_BF16) return n <= 32;
     return n <= 8 || (n <= 48 && o * i <= (1 << 22));
 }

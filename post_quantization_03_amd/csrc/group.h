@@ -238,7 +238,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void group_grad_kernel(TileArgs 
 }
 
 // dX and dW side by side, `first` work-groups for dX, for small products: each leaves compute units idle that the other fills
-// (517 rows of 5 experts 1376 x 1000 fp32: one after the other 24 and 26 us, together and with the launch between 50 -> 44 us a call).
+// (517 rows of 5 experts 1376 x 1000 fp32: a call of 50 us one after the other, 41 together).
 template <int E, int MODE, typename C>
 __global__ __launch_bounds__(C::THREADS, C::EU) void group_grads_kernel(TileArgs x, TileArgs w, Group gr, GroupCuts cuts, int per, unsigned first) {
     if (blockIdx.x < first) group_tile_body<E, MODE, C>(x, gr, cuts, blockIdx.x);
@@ -361,6 +361,15 @@ int64_t group_cuts(GroupCuts& t, int64_t n, int64_t experts, int64_t N, int64_t 
         }
         if ((t.at[k] & 255u) == 1) t.at[k] = 1u;
         gain[k] = whole - least;
+    }
+    if constexpr (tp_grad_x(MODE) && C::TM == 64) {
+        // dX of small products runs beside dW, which fills what a long K leaves idle: nothing is cut unless K is much longer than both
+        // take together (517 rows of 5 experts 1376 x 1000 fp32, us with dX cut / whole: 43.8 / 41.0; 100 rows, two products: 42 / 61; 300
+        // rows of 8 experts bf16, two products: 34.6 / 28.9). Also where dX is asked for alone, so that it has the same bits.
+        const int64_t each = (n + experts - 1) / experts;
+        const int64_t dw = experts * ((K + 63) / 64) * ((N + 63) / 64) * products * ((each + BK - 1) / BK);
+        const double both = (double)(most * slabs * products + dw) * (E == EL_F32 ? 0.44 : 0.38) / 256.0;
+        if ((double)(slabs * products) * 0.75 < 1.5 * both + 10.0) return 0;
     }
     // tile rows: a whole one for every C::TM rows, and up to one more an expert
     const int64_t some = experts < n ? experts : n, least = (n + C::TM - 1) / C::TM > some ? (n + C::TM - 1) / C::TM : some;

@@ -124,12 +124,10 @@ __device__ __forceinline__ void group_operands(TileArgs& g, const Group& gr, con
     }
 }
 
-// Place of the expert's tile at.id: each expert's tiles are dealt to the XCDs by themselves, so that experts of unequal size load
-// all of them alike.
+// Place of the expert's tile at.id.
 template <typename C>
 __device__ __forceinline__ void group_place(TileAt& t, const GroupAt& at, int nx) {
-    const int ny = (at.rows + C::TM - 1) / C::TM;
-    tile_place(t, xcd_range(at.id, ny * nx), ny, nx);
+    tile_place(t, at.id, (at.rows + C::TM - 1) / C::TM, nx);
     t.tm = __builtin_amdgcn_readfirstlane(t.tm);
     t.tn = __builtin_amdgcn_readfirstlane(t.tn);
 }
@@ -170,7 +168,12 @@ __device__ __forceinline__ void group_tile_body(TileArgs g, const Group& gr, con
     t.cut = -1;
     t.split = t.pair = 0;
     const GroupCut c = group_cut<C>(cuts, group_tiles(gr, l, C::TM) * (unsigned)nx);
-    if (id >= c.whole) {
+    if (id < c.whole) {
+        // each turn's work-groups, dealt to the 8 XCDs one by one, take tiles XCD by XCD: neighbours in one L2 share their panels
+        constexpr unsigned TURN = GROUP_COUNTS * group_step<C>();
+        const unsigned first = id / TURN * TURN, left = c.whole - first;
+        id = first + (unsigned)xcd_range((int)(id - first), (int)(left < TURN ? left : TURN));
+    } else {
         if (c.rest == 0 || id >= c.whole + c.rest * (unsigned)c.splits) return;
         t.split = __builtin_amdgcn_readfirstlane((int)((id - c.whole) / c.rest));
         t.cut = (int)(id - c.whole - (unsigned)t.split * c.rest);

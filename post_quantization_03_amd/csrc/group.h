@@ -213,31 +213,58 @@ __global__ __launch_bounds__(256) void group_reduce_kernel(TileArgs g0, Group gr
     }
 }
 
-// dW = dY^T X over each expert's rows, zeros for one without any: `per` tiles an expert (of both gradients).
+// dW = dY^T X over each expert's rows, zeros for one without any: `per` tiles an expert (of both gradients), g.splits work-groups a
+// tile, each a part of the expert's rows (whose number the device finds: a split may be left without any).
 template <int E, typename C>
-__device__ __forceinline__ void group_grad_body(TileArgs g, const Group& gr, int per, unsigned block) {
-    const int k = (int)(block / (unsigned)per), id = (int)(block - (unsigned)k * (unsigned)per);
+__device__ __forceinline__ void group_grad_operands(TileArgs& g, const Group& gr, int k) {
     int begin, rows;
     group_rows(gr, k, begin, rows);
+    constexpr int BK = 8 * el_chunk<E>();
     g.K = rows;
+    g.sper = ((rows + BK - 1) / BK + g.splits - 1) / g.splits;
     g.A += begin * g.lda;
     g.A2 += begin * g.lda2;
     g.B += begin * g.ldb;
     g.Y = rows_on(g.Y, (int64_t)k * gr.o * g.ldy, g.dt);
     g.Y2 = rows_on(g.Y2, (int64_t)k * gr.o * g.ldy2, g.dt);
-    TileAt t;
-    t.cut = -1;
-    t.split = 0;
+}
+template <typename C>
+__device__ __forceinline__ void group_grad_place(TileAt& t, const TileArgs& g, int id, int per) {
     const int ny = (int)((g.M + C::TM - 1) / C::TM), nx = (int)((g.N + C::TN - 1) / C::TN), j = xcd_range(id, per);
     t.pair = __builtin_amdgcn_readfirstlane(j / (ny * nx));
     tile_place(t, j % (ny * nx), ny, nx);
     t.tm = __builtin_amdgcn_readfirstlane(t.tm);
     t.tn = __builtin_amdgcn_readfirstlane(t.tn);
+}
+template <int E, typename C>
+__device__ __forceinline__ void group_grad_body(TileArgs g, const Group& gr, int per, unsigned block) {
+    const unsigned each = (unsigned)per * (unsigned)g.splits;
+    const int k = (int)(block / each), in = (int)(block - (unsigned)k * each), id = in % per;
+    group_grad_operands<E, C>(g, gr, k);
+    TileAt t;
+    t.split = __builtin_amdgcn_readfirstlane(in / per);
+    t.cut = g.splits > 1 ? __builtin_amdgcn_readfirstlane(k * per + id) : -1;
+    group_grad_place<C>(t, g, id, per);
     tile_body<E, TP_GRAD_W, C>(g, t);
 }
 template <int E, typename C>
 __global__ __launch_bounds__(C::THREADS, C::EU) void group_grad_kernel(TileArgs g, Group gr, int per) {
     group_grad_body<E, C>(g, gr, per, blockIdx.x);
+}
+// the sums of the splits
+template <int E, typename C>
+__global__ __launch_bounds__(256) void group_grad_reduce_kernel(TileArgs g0, Group gr, int per) {
+    constexpr int PER = C::TM * C::TN / 1024;
+    const unsigned pieces = (unsigned)per * (unsigned)gr.experts * PER;
+    for (unsigned b = blockIdx.x; b < pieces; b += gridDim.x) {
+        TileArgs g = g0;
+        TileAt t;
+        t.cut = (int)(b / PER);
+        t.split = 0;
+        group_grad_operands<E, C>(g, gr, t.cut / per);
+        group_grad_place<C>(t, g, t.cut % per, per);
+        tile_reduce<TP_GRAD_W, C>(g, t, (int)(b % PER));
+    }
 }
 
 // dX and dW side by side, `first` work-groups for dX, for small products: each leaves compute units idle that the other fills
@@ -314,17 +341,39 @@ int group_shape(int64_t n, int64_t experts, int64_t N, int64_t K) {
     for (int h = 0; h < 3; h++) {
         const int64_t tn = MODE == TP_GATED ? size[h] / 2 : size[h];
         int64_t tiles, slabs;
-        if (MODE == TP_GRAD_W) {         // N: rows of dW, K: its columns
-            tiles = experts * ((N + size[h] - 1) / size[h]) * ((K + size[h] - 1) / size[h]);
-            slabs = (each + BK - 1) / BK;
-        } else {
-            tiles = some * ((each + size[h] - 1) / size[h]) * ((N + tn - 1) / tn);
-            slabs = (K + BK - 1) / BK * (MODE == TP_GRAD_X ? 2 : 1);
-        }
+        tiles = some * ((each + size[h] - 1) / size[h]) * ((N + tn - 1) / tn);
+        slabs = (K + BK - 1) / BK * (MODE == TP_GRAD_X ? 2 : 1);
         const double t = group_time<E>(h, tiles, slabs);
         if (h == 0 || t < least) {
             least = t;
             best = h;
+        }
+    }
+    return best;
+}
+
+// How the weight gradients (o x i, an expert) are cut: tile shape and splits of an expert's rows, for rows dealt evenly. One plan for one
+// gradient and for two, so that each has the same bits either way.
+struct GradPlan {
+    int shape, splits;
+};
+template <int E>
+GradPlan group_grad_plan(int64_t n, int64_t experts, int64_t o, int64_t i) {
+    constexpr int size[3] = {256, 128, 64}, BK = 8 * el_chunk<E>(), CUTS = 8, cuts[CUTS] = {1, 2, 3, 4, 6, 8, 12, 16};
+    const int64_t slabs = ((n + experts - 1) / experts + BK - 1) / BK;
+    GradPlan best{2, 1};
+    double least = 0.0;
+    for (int h = E == EL_F32 ? 2 : 0; h < 3; h++) {
+        const int64_t tiles = experts * ((o + size[h] - 1) / size[h]) * ((i + size[h] - 1) / size[h]);
+        for (int c = 0; c < CUTS; c++) {
+            const int64_t wgs = tiles * cuts[c], per = (slabs + cuts[c] - 1) / cuts[c];
+            if (c && (wgs > 512 << h || per * (cuts[c] - 1) >= slabs)) break;    // two turns at most, and no split empty
+            double t = group_time<E>(h, wgs, per);
+            if (c) t += 4.0 + (double)wgs * (size[h] * size[h] * 8 / 3.5e6);
+            if (least == 0.0 || t < least) {
+                least = t;
+                best = GradPlan{h, cuts[c]};
+            }
         }
     }
     return best;
@@ -450,31 +499,53 @@ kq_status group_launch(TileArgs g, const Group& gr, void* ws, size_t ws_bytes, h
 }
 
 template <int E>
-kq_status group_grad_launch(TileArgs g, const Group& gr, int pairs, hipStream_t st, const char* who) {
-    return with_shape<E>(group_shape<E, TP_GRAD_W>(gr.n, gr.experts, g.M, g.N), [&](auto shape) {
+size_t group_grad_ws(int64_t n, int64_t experts, int64_t o, int64_t i, int pairs) {
+    if (n <= 0) return 0;
+    const GradPlan p = group_grad_plan<E>(n, experts, o, i);
+    const int64_t size = 256 >> p.shape, tiles = experts * ((o + size - 1) / size) * ((i + size - 1) / size) * pairs;
+    return p.splits > 1 ? sizeof(float) * (size_t)(tiles * p.splits * size * size) : 0;
+}
+
+template <int E>
+kq_status group_grad_launch(TileArgs g, const Group& gr, int pairs, void* ws, size_t ws_bytes, hipStream_t st, const char* who) {
+    const GradPlan plan = group_grad_plan<E>(gr.n, gr.experts, g.M, g.N);
+    const size_t need = group_grad_ws<E>(gr.n, gr.experts, g.M, g.N, pairs);
+    if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
+    g.part = static_cast<float*>(ws);
+    g.splits = plan.splits;
+    return with_shape<E>(plan.shape, [&](auto shape) {
         typedef decltype(shape) C;
-        const int64_t per = ((g.M + C::TM - 1) / C::TM) * ((g.N + C::TN - 1) / C::TN) * pairs;
-        if (!grid_ok(per * gr.experts, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
+        const int64_t per = ((g.M + C::TM - 1) / C::TM) * ((g.N + C::TN - 1) / C::TN) * pairs, wgs = per * gr.experts * plan.splits;
+        if (!grid_ok(wgs, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
         static std::atomic<uint64_t> allowed{0};
         KQ_TRY(allow_lds(reinterpret_cast<const void*>(&group_grad_kernel<E, C>), C::SMEM, allowed, who));
-        hipLaunchKernelGGL((group_grad_kernel<E, C>), dim3((unsigned)(per * gr.experts)), dim3(C::THREADS), C::SMEM, st, g, gr,
-                           (int)per);
-        return check_launch(who);
+        hipLaunchKernelGGL((group_grad_kernel<E, C>), dim3((unsigned)wgs), dim3(C::THREADS), C::SMEM, st, g, gr, (int)per);
+        KQ_TRY(check_launch(who));
+        if (plan.splits > 1) {
+            const int64_t pieces = per * gr.experts * (C::TM * C::TN / 1024);
+            hipLaunchKernelGGL((group_grad_reduce_kernel<E, C>), dim3((unsigned)(pieces < 4096 ? pieces : 4096)), dim3(256), 0, st, g, gr,
+                               (int)per);
+            KQ_TRY(check_launch(who));
+        }
+        return KQ_OK;
     });
 }
 
 // Both gradients where both are cut into the smallest tiles.
 template <int E, int MODE>
 bool group_grads_together(const TileArgs& x, const TileArgs& w, const Group& gr) {
-    return gr.n > 0 && group_shape<E, MODE>(gr.n, gr.experts, x.N, x.K) == 2 && group_shape<E, TP_GRAD_W>(gr.n, gr.experts, w.M, w.N) == 2;
+    if (gr.n == 0 || group_shape<E, MODE>(gr.n, gr.experts, x.N, x.K) != 2) return false;
+    const GradPlan p = group_grad_plan<E>(gr.n, gr.experts, w.M, w.N);
+    return p.shape == 2 && p.splits == 1;
 }
 template <int E, int MODE>
-kq_status group_grads_launch(TileArgs x, const TileArgs& w, const Group& gr, int pairs, void* ws, size_t ws_bytes, hipStream_t st,
+kq_status group_grads_launch(TileArgs x, TileArgs w, const Group& gr, int pairs, void* ws, size_t ws_bytes, hipStream_t st,
                              const char* who) {
     typedef TileS C;
     GroupCuts cuts;
     int64_t wgs, sums;
     KQ_TRY((group_prepare<E, MODE, C>(cuts, wgs, sums, x, gr, ws, ws_bytes, who)));
+    w.splits = 1;
     const int64_t per = ((w.M + C::TM - 1) / C::TM) * ((w.N + C::TN - 1) / C::TN) * pairs;
     if (!grid_ok(wgs + per * gr.experts, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
     hipLaunchKernelGGL((group_grads_kernel<E, MODE, C>), dim3((unsigned)(wgs + per * gr.experts)), dim3(C::THREADS), C::SMEM, st, x, w, gr,

@@ -58,7 +58,7 @@ static kq_status backward(const char* who, const Group& gr, const TileArgs& x, c
                           hipStream_t st) {
     if (x.Y && pairs && group_grads_together<E, MODE>(x, w, gr)) return group_grads_launch<E, MODE>(x, w, gr, pairs, ws, ws_bytes, st, who);
     if (x.Y) KQ_TRY((group_launch<E, MODE>(x, gr, ws, ws_bytes, st, who)));
-    return pairs ? group_grad_launch<E>(w, gr, pairs, st, who) : KQ_OK;
+    return pairs ? group_grad_launch<E>(w, gr, pairs, ws, ws_bytes, st, who) : KQ_OK;
 }
 template <int E>
 static kq_status backward(const char* who, const Group& gr, const TileArgs& x, const TileArgs& w, int pairs, void* ws, size_t ws_bytes,
@@ -74,9 +74,10 @@ using namespace kq;
 template <int E>
 static size_t grouped_ws_of(kq_op op, int64_t o, int64_t i, int64_t n, int64_t experts) {
     if (op == KQ_OP_GROUPED_BACKWARD) {
-        // of one product's dX or of two's
+        // the most that any call of these sizes takes: dX of one product or of two, one weight gradient or two
         const size_t a = group_ws<E, TP_GRAD_X>(n, experts, i, o), b = group_ws<E, TP_GRAD_X1>(n, experts, i, o);
-        return a > b ? a : b;
+        const size_t w = group_grad_ws<E>(n, experts, o, i, 2);
+        return a > b ? (a > w ? a : w) : b > w ? b : w;
     }
     if (group_few<E>(n, experts)) return 0;
     return op == KQ_OP_GROUPED_GATED ? group_ws<E, TP_GATED>(n, experts, o, i) : group_ws<E, TP_PLAIN>(n, experts, o, i);

@@ -31,20 +31,25 @@ def out_stack(e, o, i, dt):
     return t, t.as_strided((e, o, i), (o * t.stride(0), t.stride(0), 1))
 
 
-# few rows an expert, one expert with more; tile shapes of 256, 128 and 64 rows, with K whole, split for all tiles or for those
-# behind the last full turn; more experts than lanes
-FORWARD = [("bf16", 1, 1, 40, 33), ("bf16", 3, 4, 41, 100), ("bf16", 64, 16, 70, 1000), ("bf16", 90, 70, 40, 65), ("bf16", 200, 150, 30, 100),
-           ("bf16", 100, 3, 33, 400), ("bf16", 500, 7, 130, 257), ("bf16", 776, 12, 2812, 9), ("bf16", 202, 3, 5637, 10),
-           ("bf16", 3250, 1, 2435, 538), ("bf16", 3000, 5, 1100, 900), ("bf16", 7652, 2, 4948, 3515), ("bf16", 4331, 3, 1795, 11052),
-           ("bf16", 5109, 2, 3754, 3346), ("bf16", 4509, 2, 913, 10687), ("bf16", 4100, 130, 70, 48),
-           ("f32", 1, 1, 40, 33), ("f32", 64, 16, 70, 1000), ("f32", 517, 5, 130, 257), ("f32", 300, 70, 40, 65), ("f32", 1000, 3, 200, 72)]
+# few rows an expert, one expert with more, more experts than lanes; then tile shapes of 256, 128 and 64 rows (L, M, S) with K whole,
+# split for all tiles, or for those behind the last full turn (mixed), of the plain or the gated product
+FORWARD = [("few", "bf16", 1, 1, 40, 33), ("few", "bf16", 3, 4, 41, 100), ("few", "bf16", 64, 16, 70, 1000), ("few", "bf16", 90, 70, 40, 65),
+           ("few", "bf16", 200, 150, 30, 100), ("few", "f32", 1, 1, 40, 33), ("few", "f32", 64, 16, 70, 1000), ("few", "f32", 300, 70, 40, 65),
+           ("S", "bf16", 100, 3, 33, 400), ("S", "bf16", 500, 7, 130, 257), ("S", "bf16", 4100, 130, 70, 48), ("S", "bf16", 3000, 5, 1100, 900),
+           ("S split", "bf16", 25, 2, 1, 876), ("S mixed", "bf16", 110, 9, 7674, 1792), ("S mixed gated", "bf16", 51, 5, 7228, 1593),
+           ("M", "bf16", 776, 12, 2812, 9), ("M", "bf16", 655, 10, 3306, 3), ("M split", "bf16", 4277, 2, 464, 3085),
+           ("M split gated", "bf16", 1479, 2, 752, 3154), ("M mixed", "bf16", 5500, 3, 3126, 2463), ("M mixed gated", "bf16", 4873, 2, 1664, 1853),
+           ("L", "bf16", 4011, 3, 2059, 548), ("L", "bf16", 2313, 3, 1609, 594), ("L split", "bf16", 5840, 2, 1483, 10880),
+           ("L split gated", "bf16", 1539, 2, 2539, 11720), ("L mixed", "bf16", 8505, 2, 4325, 5866), ("L mixed gated", "bf16", 4273, 3, 4150, 4753),
+           ("S", "f32", 517, 5, 130, 257), ("S", "f32", 1000, 3, 200, 72), ("S split", "f32", 92, 2, 2, 437), ("S mixed", "f32", 3637, 2, 1191, 755),
+           ("S mixed gated", "f32", 3517, 3, 597, 633)]
 
 
-@pytest.mark.parametrize("dt,n,e,o,i", FORWARD)
-def test_grouped_forward_exact(dt, n, e, o, i):
-    """Whole numbers of at most 4: products of at most 16, 11052 of which sum to less than 2^18."""
+@pytest.mark.parametrize("plan,dt,n,e,o,i", FORWARD)
+def test_grouped_forward_exact(plan, dt, n, e, o, i):
+    """Whole numbers of at most 4: products of at most 16, 11720 of which sum to less than 2^18."""
     import torch
-    say(f"grouped forward {dt} n={n} e={e} o={o} i={i}")
+    say(f"grouped forward {plan} {dt} n={n} e={e} o={o} i={i}")
     g = generator(n + e + o + i)
     X, x = whole_numbers(n, i, dt, 4, g)
     (W, w), (U, u) = stack(e, o, i, dt, 4, g), stack(e, o, i, dt, 4, g)
@@ -100,24 +105,31 @@ def test_any_offsets_stay_inside(n, e, o, i):
         same(flat, torch.from_numpy(ww).to(X.device).view(e * o, i), "bf16", "dW")
 
 
-# tile shapes of dX and dW: 256, 128 and 64 rows; dX with K whole and split
-BACKWARD = [("bf16", 1, 1, 40, 33), ("bf16", 33, 3, 65, 70), ("bf16", 64, 16, 70, 200), ("bf16", 500, 70, 33, 65), ("bf16", 263, 4, 41, 8360),
-            ("bf16", 460, 1, 2002, 4121), ("bf16", 104, 30, 1097, 67), ("bf16", 2582, 2, 214, 3171), ("bf16", 3000, 5, 1100, 900),
-            ("bf16", 10910, 2, 1584, 3338), ("bf16", 5602, 2, 5068, 1467), ("bf16", 8610, 2, 2529, 4308),
-            ("bf16", 9000, 1, 40, 72),
-            ("f32", 1, 1, 40, 33), ("f32", 64, 16, 70, 200), ("f32", 517, 5, 130, 257), ("f32", 1000, 70, 40, 65)]
+# what each is there for: tile shapes and cuts of dX (of one product, of two) and of dW; two uncut S plans run in one launch
+BACKWARD = [("one launch", "bf16", 1, 1, 40, 33), ("one launch", "bf16", 33, 3, 65, 70), ("one launch", "bf16", 64, 16, 70, 200),
+            ("one launch", "bf16", 500, 70, 33, 65), ("one launch, dX cut", "bf16", 21, 2, 477, 1), ("one launch, dX cut", "bf16", 21, 7, 914, 1),
+            ("dX M", "bf16", 263, 4, 41, 8360), ("dX M", "bf16", 643, 10, 2, 3470), ("dX2 M split", "bf16", 1564, 2, 1616, 1459),
+            ("dX2 M mixed", "bf16", 1838, 2, 740, 8681), ("dX M split", "bf16", 1003, 2, 2830, 2059), ("dX M mixed", "bf16", 4747, 2, 1491, 3430),
+            ("dX2 L split", "bf16", 2764, 2, 6048, 3195), ("dX2 L mixed", "bf16", 7189, 2, 1656, 6962), ("dX L mixed", "bf16", 10782, 2, 3298, 3479),
+            ("dW L", "bf16", 915, 2, 935, 4375), ("dW L split", "bf16", 11824, 2, 941, 2069), ("dW M", "bf16", 66, 19, 66, 1748),
+            ("dW M split", "bf16", 5001, 2, 371, 971), ("dW S split", "bf16", 907, 2, 1, 1), ("dW S split", "bf16", 9000, 1, 40, 72),
+            ("some", "bf16", 104, 30, 1097, 67), ("some", "bf16", 3000, 5, 1100, 900),
+            ("one launch", "f32", 1, 1, 40, 33), ("one launch", "f32", 64, 16, 70, 200), ("one launch", "f32", 517, 5, 130, 257),
+            ("one launch, dX cut", "f32", 21, 2, 235, 1), ("dW split", "f32", 478, 2, 1, 1), ("some", "f32", 1000, 70, 40, 65),
+            ("some", "f32", 3000, 2, 200, 100)]
 
 
-@pytest.mark.parametrize("dt,n,e,o,i", BACKWARD)
-def test_grouped_backward_exact(dt, n, e, o, i):
-    """Whole numbers of at most 4: products of at most 16; 2 * 5068 and 10910 of them sum to less than 2^18."""
+@pytest.mark.parametrize("plan,dt,n,e,o,i", BACKWARD)
+def test_grouped_backward_exact(plan, dt, n, e, o, i):
+    """Whole numbers of at most 4: products of at most 16; 2 * 6048 and 11824 of them sum to less than 2^18."""
     import torch
-    say(f"grouped backward {dt} n={n} e={e} o={o} i={i}")
+    say(f"grouped backward {plan} {dt} n={n} e={e} o={o} i={i}")
     g = generator(n + e + o + i)
     X, x = whole_numbers(n, i, dt, 4, g)
     (dY, dy), (dZ, dz) = whole_numbers(n, o, dt, 4, g), whole_numbers(n, o, dt, 4, g)
     (W, w), (U, u) = stack(e, o, i, dt, 4, g), stack(e, o, i, dt, 4, g)
-    ws = Workspace("grouped_backward", o, i, n, dt, e).ws
+    space_ = Workspace("grouped_backward", o, i, n, dt, e)
+    ws = space_.ws
     for off in (dealt(n, e, g), dealt(n, e, g, n // 4, n - n // 5), offsets([0] * e + [n])):
         d1, d2 = (torch.zeros((n, i), dtype=torch.float64, device=X.device) for _ in range(2))
         gw, gu = (torch.zeros((e, o, i), dtype=torch.float64, device=X.device) for _ in range(2))
@@ -140,7 +152,7 @@ def test_grouped_backward_exact(dt, n, e, o, i):
         K.kq_grouped_backward(dY, None, W, off, dX2, dY2=dZ, W2=U, ws=ws)
         K.kq_grouped_backward(dY, X, None, off, dY2=dZ, dW2=dU2, ws=ws)
         assert torch.equal(dX2[inside], dX[inside]) and torch.equal(dU2, dU)
-        assert bool((dX2[~inside] == -77.0).all())
+        assert bool((dX2[~inside] == -77.0).all()) and space_.kept()
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])

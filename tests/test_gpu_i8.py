@@ -228,10 +228,12 @@ def dealt(n, e, g, first=0, last=None):
     return off
 
 
-# few rows an expert, one expert with more than the others; tile shapes, also with K cut; more experts than lanes
+# few rows an expert, one expert with more than the others, more experts than lanes; then tile shapes with K whole, split, or split
+# for the tiles behind the last full turn, of the plain or the gated product
 GROUPS = [(1, 1, 40, 33), (3, 4, 41, 100), (64, 16, 70, 1000), (90, 70, 40, 65), (200, 150, 30, 100), (100, 3, 33, 400), (500, 7, 130, 257),
-          (776, 12, 2812, 17), (1607, 1, 5088, 976), (3000, 5, 1100, 900), (4100, 130, 70, 48),
-          (8737, 2, 4325, 5866), (9224, 18, 736, 9018), (6466, 2, 2920, 5710)]
+          (776, 12, 2812, 17), (3000, 5, 1100, 900), (4100, 130, 70, 48), (20, 2, 1, 2488), (300, 28, 2330, 3184), (163, 15, 2386, 5039),
+          (655, 10, 3306, 3), (1738, 2, 1176, 6420), (843, 3, 1123, 6029), (4046, 2, 4429, 5540), (2866, 2, 2926, 4064), (3652, 2, 2320, 1370),
+          (5633, 3, 724, 901), (8505, 2, 4325, 5866), (9239, 2, 2685, 5103), (9224, 18, 736, 9018)]
 
 
 @pytest.mark.parametrize("n,e,o,i", GROUPS)

@@ -535,6 +535,30 @@ def _words() -> tuple:
     return _WORDS
 
 
+def _lead(name: str, what: str, t, whole: bool) -> tuple:
+    """The operand that sets a call's type, device and two of its sizes, its attributes read once: (kq_dtype, torch dtype, elements in 16
+    bytes, device, rows, cols, pointer, leading dimension), checked as _matrix does."""
+    dtype = t.dtype
+    f = (_TORCH or _torch())[3].get(dtype)
+    if f is None:
+        raise TypeError(f"{name}: {what} has type {dtype}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: {what} is not on a GPU")
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name}: {what} is not row-major")
+    dt, per = f
+    if rows <= 1:
+        ld = -(-cols // per) * per
+    if whole and cols % per and rows:
+        end = t.storage_offset() + (rows - 1) * ld + -(-cols // per) * per
+        if end * t.element_size() > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}: the last row of {what} ends inside its 16 bytes, past the storage")
+    return dt, dtype, per, dev, rows, cols, t.data_ptr(), ld
+
+
 def _stack(name: str, what: str, t, e: int, o: int, cols: int, dtype, per: int, whole: bool, dev: int):
     """_matrix for e matrices o x cols one under the other; returns (pointer, leading dimension)."""
     if t.dtype is not dtype:
@@ -593,11 +617,10 @@ def _i8_weights(name: str, what: str, codes, scales, experts: int, o: int, i: in
             _vector(name, what + " scales", scales, (experts, o), f32, dev))
 
 
-def _experts(name: str, what: str, t, offsets) -> tuple:
-    """(experts, rows) of weights: those of a stack with offsets, of a matrix (no experts) without."""
-    if t.dim() != (2 if offsets is None else 3):
-        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}: one matrix, or with offsets a stack of them")
-    return (0, t.shape[0]) if offsets is None else (t.shape[0], t.shape[1])
+def _experts(name: str, what: str, t) -> int:
+    if t.dim() != 3:
+        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}: with offsets it is a stack of matrices")
+    return t.shape[0]
 
 
 def i8_empty(rows: int, cols: int, device):
@@ -611,18 +634,14 @@ def i8_empty(rows: int, cols: int, device):
 def kq_i8_quantize(X, codes, scales, stream=None) -> None:
     """X (rows x cols, fp32 or bf16) into codes and scales of i8_empty(rows, cols)."""
     name = "kq_i8_quantize"
-    rows, cols = X.shape
-    dt, per, dev = _float(name, "X", X)
-    p, ld = _matrix(name, "X", X, rows, cols, X.dtype, per, False, dev)
+    dt, _, _, dev, rows, cols, p, ld = _lead(name, "X", X, False)
     _launch(name, lib().kq_i8_quantize, dev, stream, (p, dt, rows, cols, ld, *_i8(name, "output", codes, scales, rows, cols, dev)))
 
 
 def kq_i8_dequantize(codes, scales, Y, stream=None) -> None:
     """The values that codes and scales stand for, into Y (rows x cols, fp32 or bf16)."""
     name = "kq_i8_dequantize"
-    rows, cols = Y.shape
-    dt, per, dev = _float(name, "Y", Y)
-    p, ld = _matrix(name, "Y", Y, rows, cols, Y.dtype, per, False, dev)
+    dt, _, _, dev, rows, cols, p, ld = _lead(name, "Y", Y, False)
     _launch(name, lib().kq_i8_dequantize, dev, stream, (*_i8(name, "input", codes, scales, rows, cols, dev), rows, cols, p, dt, ld))
 
 
@@ -630,9 +649,8 @@ def kq_i8_gemm(Ac, As, Bc, Bs, Y, offsets=None, ws=None, stream=None) -> None:
     """Y (n x o, fp32 or bf16) = A B^T for 8-bit A (n x i) and B (o x i, scales o); with offsets (experts + 1 int32)
     the rows of A are sorted by expert and B is experts x o x i, its scales experts x o."""
     name = "kq_i8_gemm"
-    (n, i), (e, o) = Ac.shape, _experts(name, "B codes", Bc, offsets)
-    dt, per, dev = _float(name, "Y", Y)
-    p, ld = _matrix(name, "Y", Y, n, o, Y.dtype, per, False, dev)
+    dt, _, _, dev, n, o, p, ld = _lead(name, "Y", Y, False)
+    i, e = Ac.shape[1], 0 if offsets is None else _experts(name, "B codes", Bc)
     _launch(name, lib().kq_i8_gemm, dev, stream,
             (*_i8(name, "A", Ac, As, n, i, dev), *_i8_weights(name, "B", Bc, Bs, e, o, i, dev), _offsets(name, offsets, e, dev),
              e, n, o, i, p, dt, ld, *_workspace(name, ws, dev)))
@@ -641,9 +659,8 @@ def kq_i8_gemm(Ac, As, Bc, Bs, Y, offsets=None, ws=None, stream=None) -> None:
 def kq_i8_gated(Xc, Xs, Gc, Gs, Uc, Us, act: str, H, offsets=None, ws=None, stream=None) -> None:
     """H (n x o, fp32 or bf16) = act(X G^T) * (X U^T) for 8-bit X (n x i), G and U; offsets as for kq_i8_gemm."""
     name = "kq_i8_gated"
-    (n, i), (e, o) = Xc.shape, _experts(name, "gate codes", Gc, offsets)
-    dt, per, dev = _float(name, "H", H)
-    p, ld = _matrix(name, "H", H, n, o, H.dtype, per, False, dev)
+    dt, _, _, dev, n, o, p, ld = _lead(name, "H", H, False)
+    i, e = Xc.shape[1], 0 if offsets is None else _experts(name, "gate codes", Gc)
     _launch(name, lib().kq_i8_gated, dev, stream,
             (*_i8(name, "X", Xc, Xs, n, i, dev), *_i8_weights(name, "gate", Gc, Gs, e, o, i, dev),
              *_i8_weights(name, "up", Uc, Us, e, o, i, dev), _offsets(name, offsets, e, dev), e, n, o, i, _act(name, act), p, dt,
@@ -654,10 +671,10 @@ def kq_grouped_gemm(X, W, offsets, Y, ws=None, stream=None) -> None:
     """Y_r = X_r W_k^T for the rows offsets[k] .. offsets[k + 1] - 1 of X (n x i); W: experts x o x i, offsets: experts + 1
     int32. Rows outside the offsets are left alone."""
     name = "kq_grouped_gemm"
-    (n, i), (e, o, _), t = X.shape, W.shape, X.dtype
-    dt, per, dev = _float(name, "X", X)
+    dt, t, per, dev, n, i, p, ld = _lead(name, "X", X, True)
+    e, o, _ = W.shape
     _launch(name, lib().kq_grouped_gemm, dev, stream,
-            (*_matrix(name, "X", X, n, i, t, per, True, dev), *_stack(name, "W", W, e, o, i, t, per, True, dev),
+            (p, ld, *_stack(name, "W", W, e, o, i, t, per, True, dev),
              _offsets(name, offsets, e, dev), e, dt, n, o, i, *_matrix(name, "Y", Y, n, o, t, per, False, dev),
              *_workspace(name, ws, dev)))
 
@@ -665,10 +682,10 @@ def kq_grouped_gemm(X, W, offsets, Y, ws=None, stream=None) -> None:
 def kq_grouped_gated(X, Wg, Wu, offsets, act: str, H, A=None, B=None, ws=None, stream=None) -> None:
     """kq_gated_forward for each expert's rows; Wg, Wu and offsets as kq_grouped_gemm's."""
     name = "kq_grouped_gated"
-    (n, i), (e, o, _), t = X.shape, Wg.shape, X.dtype
-    dt, per, dev = _float(name, "X", X)
+    dt, t, per, dev, n, i, p, ld = _lead(name, "X", X, True)
+    e, o, _ = Wg.shape
     _launch(name, lib().kq_grouped_gated, dev, stream,
-            (*_matrix(name, "X", X, n, i, t, per, True, dev), *_stack(name, "Wg", Wg, e, o, i, t, per, True, dev),
+            (p, ld, *_stack(name, "Wg", Wg, e, o, i, t, per, True, dev),
              *_stack(name, "Wu", Wu, e, o, i, t, per, True, dev), _offsets(name, offsets, e, dev), e, dt, n, o, i,
              _act(name, act), *_matrix(name, "H", H, n, o, t, per, False, dev),
              *((None, 0) if A is None else _matrix(name, "A", A, n, o, t, per, False, dev)),
@@ -679,14 +696,13 @@ def kq_grouped_backward(dY, X, W, offsets, dX=None, dW=None, dY2=None, W2=None, 
     """Gradients of kq_grouped_gemm: dX and dW where given (W may be None without dX, X without weight gradients).
     With dY2 they are those of two products of the same X: dX the sum of both, dW2 the second's."""
     name = "kq_grouped_backward"
-    (n, o), t = dY.shape, dY.dtype
     if dX is not None and (W is None or (dY2 is not None and W2 is None)):
         raise ValueError(f"{name}: dX needs the weights")
     if (dW is not None or dW2 is not None) and X is None:
         raise ValueError(f"{name}: weight gradients need X")
     if dY2 is None and (W2 is not None or dW2 is not None):
         raise ValueError(f"{name}: W2 and dW2 go with dY2")
-    dt, per, dev = _float(name, "dY", dY)
+    dt, t, per, dev, n, o, p, ld = _lead(name, "dY", dY, True)
     e = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
     some = next((m for m in (dX, dW, dW2, X, W, W2) if m is not None), None)
     i = 1 if some is None else some.shape[-1]
@@ -698,7 +714,7 @@ def kq_grouped_backward(dY, X, W, offsets, dX=None, dW=None, dY2=None, W2=None, 
         return (None, 0) if m is None else _stack(name, what, m, e, o, i, t, per, whole, dev)
 
     _launch(name, lib().kq_grouped_backward, dev, stream,
-            (*take("dY", dY, n, o, True), *stack("W", W, True), *take("dY2", dY2, n, o, True), *stack("W2", W2, True),
+            (p, ld, *stack("W", W, True), *take("dY2", dY2, n, o, True), *stack("W2", W2, True),
              *take("X", X, n, i, True), _offsets(name, offsets, e, dev), e, dt, n, o, i, *take("dX", dX, n, i, False),
              *stack("dW", dW, False), *stack("dW2", dW2, False), *_workspace(name, ws, dev)))
 
@@ -713,10 +729,10 @@ def kq_norm_forward(X, gamma, beta, kind: str, eps: float, Y, mean=None, rstd=No
     """Y = norm(X) * gamma + beta over the rows of X (n x d), kind "layer" or "rms"; gamma and beta (d, X's type) may be None;
     mean and rstd (n floats), where given, take the statistics. Y may be X."""
     name = "kq_norm_forward"
-    (n, d), t, f32 = X.shape, X.dtype, (_WORDS or _words())[2]
-    dt, per, dev = _float(name, "X", X)
+    f32 = (_WORDS or _words())[2]
+    dt, t, per, dev, n, d, p, ld = _lead(name, "X", X, False)
     _launch(name, lib().kq_norm_forward, dev, stream,
-            (*_matrix(name, "X", X, n, d, t, per, False, dev), _vector(name, "gamma", gamma, (d,), t, dev),
+            (p, ld, _vector(name, "gamma", gamma, (d,), t, dev),
              _vector(name, "beta", beta, (d,), t, dev), dt, n, d, _norm(name, kind), eps,
              *_matrix(name, "Y", Y, n, d, t, per, False, dev), _vector(name, "mean", mean, (n,), f32, dev),
              _vector(name, "rstd", rstd, (n,), f32, dev)))
@@ -725,10 +741,10 @@ def kq_norm_forward(X, gamma, beta, kind: str, eps: float, Y, mean=None, rstd=No
 def kq_norm_backward(dY, X, gamma, mean, rstd, kind: str, dX=None, dgamma=None, dbeta=None, ws=None, stream=None) -> None:
     """Gradients of kq_norm_forward from dY and the mean (None will do for "rms") and rstd that it kept; dX may be dY or X."""
     name = "kq_norm_backward"
-    (n, d), t, f32 = dY.shape, dY.dtype, (_WORDS or _words())[2]
-    dt, per, dev = _float(name, "dY", dY)
+    f32 = (_WORDS or _words())[2]
+    dt, t, per, dev, n, d, p, ld = _lead(name, "dY", dY, False)
     _launch(name, lib().kq_norm_backward, dev, stream,
-            (*_matrix(name, "dY", dY, n, d, t, per, False, dev), *_matrix(name, "X", X, n, d, t, per, False, dev),
+            (p, ld, *_matrix(name, "X", X, n, d, t, per, False, dev),
              _vector(name, "gamma", gamma, (d,), t, dev), _vector(name, "mean", mean, (n,), f32, dev),
              _vector(name, "rstd", rstd, (n,), f32, dev), dt, n, d, _norm(name, kind),
              *((None, 0) if dX is None else _matrix(name, "dX", dX, n, d, t, per, False, dev)),

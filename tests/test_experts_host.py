@@ -240,10 +240,12 @@ def test_wrappers_refuse_host_tensors_shapes_and_types():
         K.kq_i8_quantize(x.double(), c, s)
     with pytest.raises(TypeError, match="type"):
         K.kq_grouped_gemm(x.half(), w, off, x)
-    with pytest.raises(ValueError, match="one matrix"):
-        K.kq_i8_gemm(c, s, c, s, x, off)
-    with pytest.raises(ValueError, match="one matrix"):
-        K.kq_i8_gemm(c, s, c.view(1, 4, 60), s, x)
+    with pytest.raises(ValueError, match="stack of matrices"):
+        K._experts("e", "B codes", c)
+    assert K._experts("e", "B codes", c.unflatten(0, (2, 2))) == 2
+    for bad, match in ((x.T, "GPU"), (x.double(), "type"), (x.to(torch.int32), "type")):
+        with pytest.raises((TypeError, ValueError), match=match):
+            K._lead("l", "X", bad, True)
     with pytest.raises(ValueError, match="needs the weights"):
         K.kq_grouped_backward(x, x, None, off, dX=x)
     with pytest.raises(ValueError, match="needs the weights"):

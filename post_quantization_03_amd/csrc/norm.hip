@@ -5,7 +5,8 @@
 //   h = (x - m) r,  y = h gamma + beta
 //   g = dy gamma,  dx = r (g - [layer: mean g] - h mean(g h)),  dgamma = sum over rows of dy h,  dbeta = sum over rows of dy
 //
-// Both passes are bound by HBM: x is read once and y written once; dy and x are read once and dx written once. A row stays in
+// Both passes are bound by HBM: x is read once and y written once (8192 x 4096 bf16 27.7 us, 4.8 TB/s); dy and x are read once and dx written
+// once (37 us, 5.4 TB/s, and 4.6 us for the sums of 512 work-groups' 17 MB); a copy of 4 GiB runs at 4.7 TB/s. A row stays in
 // registers between its statistics and its results. All sums are fp32; the variance is taken of the differences from the
 // mean, which keeps its digits where the mean is large against the deviation.
 #include "rows.h"
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormArg
     }
 }
 
-// Rows that the registers do not hold: read three times, the last two mostly from a cache.
+// Rows that the registers do not hold: read three times, the last two mostly from a cache (2048 x 28672 fp32: 136 us).
 template <bool BF>
 __global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormArgs g) {
     constexpr int V = row_chunk<BF>();
@@ -245,6 +246,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormAr
     }
 }
 
+// dX of rows that the registers do not hold: read twice (2048 x 28672 fp32: 275 us with the weights' gradients, 181 without).
 template <bool BF>
 __global__ __launch_bounds__(1024) void norm_backward_long_kernel(NormArgs g) {
     constexpr int V = row_chunk<BF>();

@@ -336,9 +336,11 @@ __device__ __forceinline__ void landed_barrier() {
 // PFLOP/s, 60 % busy at 1.9 GHz), the 4-bit gated block 350 us (4.2 PFLOP/s, 53 %: its tiles have 16 slabs between
 // their first loads and their activations). With their operands in registers the same instructions run at 2.1 (bf16) and
 // 7.4 PFLOP/s (E2M1), all the time busy at 2.06 GHz: the LDS reads and the loads cost clock as well as time. A slab of
-// shape L moves 256 KiB through LDS (8 wavefronts read 24 KiB each, the loads write 64), 2048 clocks at 128 bytes a
-// clock, as many as its matrix instructions take (64 a wavefront, two wavefronts a SIMD, 16 clocks each): the LDS port
-// is as full as the matrix cores. The
+// shape L has 192 KiB read from LDS, 771 clocks by its counter (255 bytes a clock), beside the 2048 of its matrix instructions (64 a
+// wavefront, two wavefronts a SIMD, 16 clocks each): LDS is not the bound. With every load a hit in L2 (all of them of one and the same
+// slab) bf16 products take 12 % less and int8 ones 7 %: the loads' latency, of which half a slab's products to a whole one's cover what
+// they can. Neither bringing later slabs' lines into L2 by loads of 4 bytes a line (28 to 40 % slower: 64 requests a load) nor four wavefronts of
+// 128 x 128 with their sums pinned in accumulation registers (weight gradients 14 % slower: nothing runs beside a barrier) helped. The
 // 32 x 32 instructions, by themselves, are slower (1.9 and 6.7 PFLOP/s). No LDS bank conflicts in any of them. A
 // work-group that walks over its tiles and loads the next one's first slab before the epilogue changed none of these by
 // more than 2 %; four wavefronts of 128 x 128 instead of eight of 128 x 64 read a third less LDS but no longer fit

@@ -530,7 +530,7 @@ kq_status kq_i8_gated(const int8_t* X, int64_t ldx, const float* sX, const int8_
  * contents are read as if each value were clamped to 0 .. n and raised to the largest before it. Experts may have no
  * rows; rows before the first offset and from the last one on are neither read nor written. All matrices of type dt
  * (fp32 or bf16), leading dimensions as for kq_gated_forward; sums are fp32, rounded once. Outputs overlap neither each
- * other nor any input. 1 to 4096 experts; n below 2^31. n = 0 does nothing. Workspace: kq_workspace_bytes(KQ_OP_GROUPED_GEMM, o,
+ * other nor any input. 1 to 4096 experts; n at most 2^31 - 512. n = 0 does nothing. Workspace: kq_workspace_bytes(KQ_OP_GROUPED_GEMM, o,
  * i, n, dt, .., group = experts, ..), possibly 0; its rules are those of kq_mx_gemm. The order of a sum depends on the
  * offsets (the device cuts the last tiles of large products), never on anything else: the same call gives the same bits.
  */

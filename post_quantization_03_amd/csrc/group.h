@@ -17,7 +17,7 @@ struct Group {
     int n;                   // rows of A: offsets are clamped to 0 .. n
     int o;                   // rows of B an expert
 };
-constexpr int64_t GROUP_MAX = 4096, GROUP_ROWS_MAX = (1LL << 31) - 1;
+constexpr int64_t GROUP_MAX = 4096, GROUP_ROWS_MAX = (1LL << 31) - 512;    // rows and a tile's more fit in 32 bits
 
 __device__ __forceinline__ int clamp_row(int v, int n) { return v < 0 ? 0 : v < n ? v : n; }
 

@@ -152,7 +152,7 @@ def test_grouped_refusals(call):
                    (dict(W=None), EINVAL), (dict(Y=None), EINVAL), (dict(off=None), EINVAL), (dict(off=ODD), EINVAL),
                    (dict(e=0), ESHAPE), (dict(e=-1), ESHAPE), (dict(e=4097), ESHAPE), (dict(ldx=8), ESHAPE), (dict(ldw=20), EINVAL),
                    (dict(ldy=12), EINVAL), (dict(ldx=1 << 22), ESHAPE), (dict(n=1 << 31), ESHAPE), (dict(e=4096, o=1 << 20), ESHAPE),
-                   (dict(n=(1 << 31) - 1, o=1 << 16, ldy=1 << 16), ESHAPE)):
+                   (dict(n=(1 << 31) - 511), ESHAPE), (dict(n=(1 << 31) - 512, o=1 << 16, ldy=1 << 16), ESHAPE)):
         assert call(**kw) == st, kw
     if call is ggated:
         for kw, st in ((dict(U=None), EINVAL), (dict(act=9), EINVAL), (dict(lda=4), ESHAPE), (dict(B=ODD), EINVAL)):

@@ -347,9 +347,8 @@ int group_shape(int64_t n, int64_t experts, int64_t N, int64_t K) {
     double least = 0.0;
     for (int h = 0; h < 3; h++) {
         const int64_t tn = MODE == TP_GATED ? size[h] / 2 : size[h];
-        int64_t tiles, slabs;
-        tiles = some * ((each + size[h] - 1) / size[h]) * ((N + tn - 1) / tn);
-        slabs = (K + BK - 1) / BK * (MODE == TP_GRAD_X ? 2 : 1);
+        const int64_t tiles = some * ((each + size[h] - 1) / size[h]) * ((N + tn - 1) / tn);
+        const int64_t slabs = (K + BK - 1) / BK * (MODE == TP_GRAD_X ? 2 : 1);
         const double t = group_time<E>(h, tiles, slabs);
         if (h == 0 || t < least) {
             least = t;
@@ -401,12 +400,11 @@ int64_t group_cuts(GroupCuts& t, int64_t n, int64_t experts, int64_t N, int64_t 
         per[c] = (slabs + cuts[c] - 1) / cuts[c];
         splits[c] = (slabs + per[c] - 1) / per[c];
     }
-    double gain[GROUP_COUNTS + 1];
-    for (int k = 0; k <= GROUP_COUNTS; k++) {
+    // the cut for k * STEP tiles, and what it gains
+    auto choose = [&](int k) {
         t.at[k] = 1u;
-        gain[k] = 0.0;
         const int64_t rest = k * STEP;
-        if (rest == 0 || rest >= TURN || rest >= most + STEP) continue;
+        if (rest == 0 || rest >= TURN || rest >= most + STEP) return 0.0;
         const double whole = group_time<E>(h, rest, slabs * products);
         double least = whole;
         for (int c = 0; c < CUTS; c++) {
@@ -415,12 +413,11 @@ int64_t group_cuts(GroupCuts& t, int64_t n, int64_t experts, int64_t N, int64_t 
             const double us = group_time<E>(h, wgs, per[c] * products) + 4.0 + (double)wgs * (C::TM * C::TN * 8 / 3.5e6);
             if (us < least) {
                 least = us;
-                t.at[k] = (uint32_t)splits[c] | (uint32_t)per[c] << 8;
+                t.at[k] = splits[c] > 1 ? (uint32_t)splits[c] | (uint32_t)per[c] << 8 : 1u;
             }
         }
-        if ((t.at[k] & 255u) == 1) t.at[k] = 1u;
-        gain[k] = whole - least;
-    }
+        return whole - least;
+    };
     if constexpr (tp_grad_x(MODE) && C::TM == 64) {
         // dX of small products runs beside dW, which fills what a long K leaves idle: nothing is cut unless K is much longer than both
         // take together (517 rows of 5 experts 1376 x 1000 fp32, us with dX cut / whole: 43.8 / 41.0; 100 rows, two products: 42 / 61; 300
@@ -434,8 +431,9 @@ int64_t group_cuts(GroupCuts& t, int64_t n, int64_t experts, int64_t N, int64_t 
     const int64_t some = experts < n ? experts : n, least = (n + C::TM - 1) / C::TM > some ? (n + C::TM - 1) / C::TM : some;
     double sum = 0.0;
     for (int k = 0; k <= 16; k++)
-        sum += gain[((least * nx + (most - least * nx) * k / 16) % TURN + STEP - 1) / STEP];
+        sum += choose((int)(((least * nx + (most - least * nx) * k / 16) % TURN + STEP - 1) / STEP));
     if (sum < 5.0 * 17) return 0;
+    for (int k = 0; k <= GROUP_COUNTS; k++) choose(k);
     int64_t sums = 0;
     for (int k = 0; k <= GROUP_COUNTS && (k - 1) * STEP < most; k++) {
         const int64_t m = (t.at[k] & 255u) > 1 ? k * STEP * (int64_t)(t.at[k] & 255u) : 0;

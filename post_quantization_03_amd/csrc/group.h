@@ -137,7 +137,7 @@ __device__ __forceinline__ void group_place(TileAt& t, const GroupAt& at, int nx
 // kernels of a product look it up.
 constexpr int GROUP_COUNTS = 256;        // entries of the table: counts up to a turn's tiles, in steps of group_step
 template <typename C>
-constexpr unsigned group_step() { return C::TM == 256 ? 1 : C::TM == 128 ? 2 : 4; }      // work-groups a compute unit
+constexpr unsigned group_step() { return 512 / (C::TM * C::DEEP); }      // work-groups a compute unit
 struct GroupCuts {
     uint32_t at[GROUP_COUNTS + 1];       // splits (1: not cut) | slabs of a split << 8
 };
@@ -329,33 +329,11 @@ bool group_few(int64_t n, int64_t experts) {
 // Estimated time, us, of work-groups of `per` slabs of tile shape h, with the constants of tile_plan.
 template <int E>
 inline double group_time(int h, int64_t wgs, int64_t per) {
-    constexpr int occ_log2[3] = {0, 1, 2};
-    constexpr double lat[3] = {1.4, 0.9, 0.75}, fix[3] = {10.0, 4.0, 1.7}, w[3] = {1.55, 0.5, E == EL_F32 ? 0.44 : 0.38};
+    constexpr int occ_log2[5] = {0, 1, 2, 0, 1};
+    constexpr double lat[5] = {1.4, 0.9, 0.75, 0.45, 0.2}, fix[5] = {10.0, 4.0, 1.7, 5.5, 3.0}, w[5] = {1.55, 0.5, E == EL_F32 ? 0.44 : 0.38, 0.45, 0.19};
     const int64_t percu = (wgs + 255) >> 8, rounds = (percu + (1 << occ_log2[h]) - 1) >> occ_log2[h];
     const double by_lat = (double)rounds * lat[h], by_w = (double)percu * w[h];
     return (double)per * (by_lat > by_w ? by_lat : by_w) + (double)rounds * fix[h];
-}
-
-// Tile shape of a grouped product, for rows dealt evenly.
-template <int E, int MODE>
-int group_shape(int64_t n, int64_t experts, int64_t N, int64_t K) {
-    if (E == EL_F32) return 2;
-    constexpr int size[3] = {256, 128, 64}, BK = 8 * el_chunk<E>();
-    const int64_t some = experts < n ? experts : n;
-    const int64_t each = some ? (n + some - 1) / some : 0;
-    int best = 2;
-    double least = 0.0;
-    for (int h = 0; h < 3; h++) {
-        const int64_t tn = MODE == TP_GATED ? size[h] / 2 : size[h];
-        const int64_t tiles = some * ((each + size[h] - 1) / size[h]) * ((N + tn - 1) / tn);
-        const int64_t slabs = (K + BK - 1) / BK * (MODE == TP_GRAD_X ? 2 : 1);
-        const double t = group_time<E>(h, tiles, slabs);
-        if (h == 0 || t < least) {
-            least = t;
-            best = h;
-        }
-    }
-    return best;
 }
 
 // How the weight gradients (o x i, an expert) are cut: tile shape and splits of an expert's rows, for rows dealt evenly. One plan for one
@@ -385,12 +363,62 @@ GradPlan group_grad_plan(int64_t n, int64_t experts, int64_t o, int64_t i) {
     return best;
 }
 
+// Whether the weight gradients run beside dX where its tiles are S.
+template <int E>
+bool group_grad_side(int64_t n, int64_t experts, int64_t o, int64_t i) {
+    const GradPlan p = group_grad_plan<E>(n, experts, o, i);
+    return p.shape == 2 && p.splits == 1;
+}
+
+// Whether a product may take tiles with more slabs in LDS. MI355X, us without / with them, bf16: 500 rows of 4 experts 1376 x 4096 30.6 / 17.6,
+// 2000 of 8 64 / 33.7, 300 of 2 4096 x 11008 104 / 75; dX and dW, 2222 rows of 3 experts 5263 x 1251 109 / 91. Slower by up to 7 % where
+// few rows leave the weights' stream to bound it: 100 rows of 2 experts 4096 x 11008 52.4 / 55.9. Weight gradients have short sums.
+template <int E, int MODE>
+constexpr bool group_deep() { return E != EL_F32 && MODE != TP_GRAD_W; }
+
+// Tile shape of a grouped product, for rows dealt evenly (and cut, if that pays: 300 rows of 2 experts 4096 x 11008 bf16 98.7 -> 75.3 us).
+template <int E, int MODE>
+int group_shape(int64_t n, int64_t experts, int64_t N, int64_t K) {
+    if (E == EL_F32) return 2;
+    constexpr int size[5] = {256, 128, 64, 128, 64}, BK = 8 * el_chunk<E>();
+    const int64_t some = experts < n ? experts : n;
+    const int64_t each = some ? (n + some - 1) / some : 0;
+    int best = 2;
+    double least = 0.0;
+    for (int h = 0; h < (group_deep<E, MODE>() ? 5 : 3); h++) {
+        const int64_t tn = MODE == TP_GATED ? size[h] / 2 : size[h];
+        // small products run side by side, in S tiles (300 rows of 8 experts 1376 x 1000, two products: 28.4 / 41.4 apart, with SD for dX)
+        if (h == 3 && tp_grad_x(MODE) && best == 2 && group_grad_side<E>(n, experts, K, N)) break;
+        // MD and SD: one turn, however the rows are dealt
+        if (h > 2 && group_tiles_max(n, experts, size[h]) * ((N + tn - 1) / tn) > (h == 3 ? 256 : 512)) continue;
+        const int64_t tiles = some * ((each + size[h] - 1) / size[h]) * ((N + tn - 1) / tn);
+        const int64_t slabs = (K + BK - 1) / BK * (MODE == TP_GRAD_X ? 2 : 1);
+        double t = group_time<E>(h, tiles, slabs);
+        if constexpr (!tp_grad_x(MODE)) {
+            // what the cuts of group_cuts would gain
+            const int64_t turn = h > 2 ? 512 >> (4 - h) : 256 << h;
+            double cut = t;
+            for (int c : {2, 3, 4, 6, 8, 12, 16}) {
+                if (tiles >= turn || c > slabs || tiles * c > (h > 2 ? turn : 2 * turn)) break;
+                const double us = group_time<E>(h, tiles * c, (slabs + c - 1) / c) + 4.0 + (double)(tiles * c) * (size[h] * size[h] * 8 / 3.5e6);
+                cut = us < cut ? us : cut;
+            }
+            if (cut < t - 5.0) t = cut;
+        }
+        if (h == 0 || t < least) {
+            least = t;
+            best = h;
+        }
+    }
+    return best;
+}
+
 // How the tiles behind the last full turn are cut, for each number of them, and the most split sums (of a tile) that can make. Split
 // sums are written and read once at 3.5 TB/s, by a second launch, which is left out (and nothing cut) where it would not pay: where
 // cutting gains less than 5 us on average over the tile counts that n rows may make.
 template <int E, int MODE, typename C>
 int64_t group_cuts(GroupCuts& t, int64_t n, int64_t experts, int64_t N, int64_t K) {
-    constexpr int h = C::TM == 256 ? 0 : C::TM == 128 ? 1 : 2, BK = 8 * el_chunk<E>(), TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
+    constexpr int h = (C::TM == 256 ? 0 : C::TM == 128 ? 1 : 2) + (C::DEEP > 2 ? 2 : 0), BK = 8 * el_chunk<E>(), TN_OUT = MODE == TP_GATED ? C::TN / 2 : C::TN;
     constexpr int64_t STEP = group_step<C>(), TURN = GROUP_COUNTS * STEP;
     constexpr int products = MODE == TP_GRAD_X ? 2 : 1;
     const int64_t slabs = (K + BK - 1) / BK, nx = (N + TN_OUT - 1) / TN_OUT, most = group_tiles_max(n, experts, C::TM) * nx;
@@ -409,7 +437,7 @@ int64_t group_cuts(GroupCuts& t, int64_t n, int64_t experts, int64_t N, int64_t 
         double least = whole;
         for (int c = 0; c < CUTS; c++) {
             const int64_t wgs = rest * splits[c];
-            if (wgs > 2 * TURN || per[c] >= 1 << 24) break;
+            if (wgs > (C::DEEP > 2 ? 1 : 2) * TURN || per[c] >= 1 << 24) break;
             const double us = group_time<E>(h, wgs, per[c] * products) + 4.0 + (double)wgs * (C::TM * C::TN * 8 / 3.5e6);
             if (us < least) {
                 least = us;
@@ -442,12 +470,16 @@ int64_t group_cuts(GroupCuts& t, int64_t n, int64_t experts, int64_t N, int64_t 
     return sums;
 }
 
-// f(tile shape) for 0 L, 1 M, 2 S; fp32 has S alone
-template <int E, typename F>
+// f(tile shape) for 0 L, 1 M, 2 S, 3 MD, 4 SD; fp32 has S alone
+template <int E, int MODE, typename F>
 kq_status with_shape(int shape, F&& f) {
     if constexpr (E != EL_F32) {
         if (shape == 0) return f(TileL{});
         if (shape == 1) return f(TileM{});
+    }
+    if constexpr (group_deep<E, MODE>()) {
+        if (shape == 3) return f(TileMD{});
+        if (shape == 4) return f(TileSD{});
     }
     return f(TileS{});
 }
@@ -457,7 +489,7 @@ template <int E, int MODE>
 size_t group_ws(int64_t n, int64_t experts, int64_t N, int64_t K) {
     size_t bytes = 0;
     if (n > 0)
-        with_shape<E>(group_shape<E, MODE>(n, experts, N, K), [&](auto shape) {
+        with_shape<E, MODE>(group_shape<E, MODE>(n, experts, N, K), [&](auto shape) {
             typedef decltype(shape) C;
             GroupCuts cuts;
             bytes = (size_t)group_cuts<E, MODE, C>(cuts, n, experts, N, K) * C::TM * C::TN * sizeof(float);
@@ -490,7 +522,7 @@ kq_status group_sums_launch(const TileArgs& g, const Group& gr, const GroupCuts&
 
 template <int E, int MODE>
 kq_status group_launch(TileArgs g, const Group& gr, void* ws, size_t ws_bytes, hipStream_t st, const char* who) {
-    return with_shape<E>(group_shape<E, MODE>(gr.n, gr.experts, g.N, g.K), [&](auto shape) {
+    return with_shape<E, MODE>(group_shape<E, MODE>(gr.n, gr.experts, g.N, g.K), [&](auto shape) {
         typedef decltype(shape) C;
         GroupCuts cuts;
         int64_t wgs, sums;
@@ -518,7 +550,7 @@ kq_status group_grad_launch(TileArgs g, const Group& gr, int pairs, void* ws, si
     if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
     g.part = static_cast<float*>(ws);
     g.splits = plan.splits;
-    return with_shape<E>(plan.shape, [&](auto shape) {
+    return with_shape<E, TP_GRAD_W>(plan.shape, [&](auto shape) {
         typedef decltype(shape) C;
         const int64_t per = ((g.M + C::TM - 1) / C::TM) * ((g.N + C::TN - 1) / C::TN) * pairs, wgs = per * gr.experts * plan.splits;
         if (!grid_ok(wgs, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
@@ -539,9 +571,7 @@ kq_status group_grad_launch(TileArgs g, const Group& gr, int pairs, void* ws, si
 // Both gradients where both are cut into the smallest tiles.
 template <int E, int MODE>
 bool group_grads_together(const TileArgs& x, const TileArgs& w, const Group& gr) {
-    if (gr.n == 0 || group_shape<E, MODE>(gr.n, gr.experts, x.N, x.K) != 2) return false;
-    const GradPlan p = group_grad_plan<E>(gr.n, gr.experts, w.M, w.N);
-    return p.shape == 2 && p.splits == 1;
+    return gr.n && group_shape<E, MODE>(gr.n, gr.experts, x.N, x.K) == 2 && group_grad_side<E>(gr.n, gr.experts, w.M, w.N);
 }
 template <int E, int MODE>
 kq_status group_grads_launch(TileArgs x, TileArgs w, const Group& gr, int pairs, void* ws, size_t ws_bytes, hipStream_t st,

@@ -212,18 +212,29 @@ struct TileArgs {
 };
 
 // Tile shapes: TM rows of A by TN rows of B (half gate, half up when gated), WM x WN wavefronts.
-template <int TM_, int TN_, int WM_, int WN_, int OCC>
+// DEEP: slabs in LDS, a power of two. Two as a rule: while one is multiplied the next arrives.
+template <int TM_, int TN_, int WM_, int WN_, int OCC, int DEEP_ = 2>
 struct TileShape {
+    typedef TileShape<TM_, TN_, WM_, WN_, OCC> Shallow;
+    static constexpr int DEEP = DEEP_;
     static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, W = WM_ * WN_, THREADS = 64 * W, EU = OCC;
     static constexpr int FM = TM / WM / 16, FN = TN / WN / 16;           // 16 x 16 fragments of a wavefront
     static constexpr int OPA = TM * 128, BUF = (TM + TN) * 128;          // bytes of A's slab, of both
     static constexpr int QA = TM / 8 / W, QB = TN / 8 / W;               // loads of 1 KiB a wavefront and slab
-    static constexpr size_t SMEM = 2 * BUF;
+    static constexpr size_t SMEM = DEEP * BUF;
     static constexpr bool LAID = TM >= 128;                              // E2M1: scales laid out ahead
 };
 typedef TileShape<256, 256, 2, 4, 2> TileL;      // one work-group a compute unit
 typedef TileShape<128, 128, 2, 2, 2> TileM;      // two
 typedef TileShape<64, 64, 2, 2, 4> TileS;        // four
+// The same tiles for grids that leave a compute unit with one work-group (MD) or two (SD). Such a grid waits for its loads: with one slab
+// in flight a slab takes as long as its load (0.4 to 0.9 us), its products a quarter of that. The LDS of the work-groups that are not there
+// holds two more slabs; sums are the same, in the same order. MI355X, int8, us with two slabs / with four, each with its best cut: 64 tokens 4096 x 11008
+// 16.0 / 14.6, 256 27.4 / 21.6, 1024 59.8 / 46.9; 700 tokens 1376 x 4096 16.8 / 10.4. Of more than one turn they are slower, since fewer
+// are resident: 2000 tokens 4096 x 4096 M 34.3, MD 43.2. Taken by the int8 products and by grouped products and dX in bf16; fp32 is
+// bound by its matrix cores (300 rows of 5 experts gated 1376 x 1000: 37.9 / 38.9).
+typedef TileShape<128, 128, 2, 2, 2, 4> TileMD;
+typedef TileShape<64, 64, 2, 2, 4, 4> TileSD;
 constexpr int TL_ROWS = 256;                     // rows of the largest tile: padding of mx_layout's groups
 // Offsets inside a tile's 256 rows (or 64 K rows) are 32-bit, everything else 64-bit: rows of at most 4 MiB.
 constexpr int64_t TL_LD_MAX = 4 << 20, TL_ROWS_MAX = 1LL << 31;
@@ -309,8 +320,8 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 
 // 16 bytes a lane from base + off straight to LDS (lds + 16 lane; base and lds are the wavefront's). HIDDEN:
 // the compiler takes a transposing LDS read to depend on every load to LDS in flight and would wait for
-// the slab just requested, so beside such reads the load is written out. It has no output register, and
-// landed_barrier waits for it. It leaves its LDS base in m0, which nothing else in those kernels uses.
+// the slab just requested, so beside such reads the load is written out, and where more slabs are in flight than one. It has
+// no output register, and landed waits for it. It leaves its LDS base in m0, which nothing else in those kernels uses.
 template <bool HIDDEN>
 __device__ __forceinline__ void dma16(const char* base, uint32_t off, char* lds) {
     if constexpr (HIDDEN) {
@@ -323,10 +334,16 @@ __device__ __forceinline__ void dma16(const char* base, uint32_t off, char* lds)
     }
 }
 
+// Waits for a wavefront's loads to LDS, but for the last LATER of them.
+template <int LATER = 0>
+__device__ __forceinline__ void landed() {
+    static_assert(LATER < 64, "the counter's six bits");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (LATER & 15) | (LATER >> 4) << 14);      // vmcnt(LATER) alone
+}
 // Barrier at which every wavefront's loads to LDS have landed. The wait is written out: a barrier by itself
 // orders ordinary LDS and global accesses, not the loads that write LDS.
 __device__ __forceinline__ void landed_barrier() {
-    __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0) alone
+    landed();
     __syncthreads();
 }
 
@@ -353,7 +370,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, const TileAt& at) {
     extern __shared__ __align__(16) char tl_sm[];
     constexpr bool TA = MODE == TP_GRAD_W, TB = tp_grad_x(MODE) || MODE == TP_GRAD_W, GATED = MODE == TP_GATED;
     static_assert(!TB || (E != EL_MX && E != EL_I8), "blocks of E2M1 lie along K; int8 has no gradients");
-    constexpr bool HID = TB && E == EL_BF16;
+    constexpr bool HID = (TB && E == EL_BF16) || C::DEEP > 2;
+    static_assert(C::DEEP == 2 || E != EL_MX, "the scales' loads would be waited for with the slabs behind them");
     constexpr int EPC = el_chunk<E>(), BK = 8 * EPC, ES = 16 / (E == EL_MX ? 16 : EPC);   // ES: bytes of a dense value
     constexpr int FM = C::FM, FN = C::FN, QA = C::QA, QB = C::QB;
     constexpr int GF = GATED ? 2 : 4, GW = GATED ? 32 : 64;              // a group's fragments and columns (of a half)
@@ -612,7 +630,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, const TileAt& at) {
     // step's (fx), whose loads would otherwise be waited for at the barrier.
     constexpr int KEEP = FM / 4, INPL = FM - KEEP;
     tl_i4 fa[FM], fx[KEEP ? KEEP : 1], fb[2][FN];
-    auto slab_at = [&](int t) { return (t & 1) * C::BUF; };
+    auto slab_at = [&](int t) { return (t & (C::DEEP - 1)) * C::BUF; };
     auto products = [&](int i, int s, tl_i4 a) {
 #pragma unroll
         for (int j = 0; j < FN; j++) {
@@ -659,17 +677,36 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, const TileAt& at) {
         pA += s0 * stepA;
         pB += s0 * stepB;
         if (GATED) pB2 += s0 * 128;
+        const int inside = E == EL_MX || whole - s0 > slabs ? slabs : whole - s0;
+        // With four slabs in LDS: the barrier in slab t leaves those behind t + 1 in flight, of whole slabs alone (whose loads are always
+        // the same in number; the loads of the slab that K ends in, if they are there, are the last ones and only make the wait longer).
+        auto deep_barrier = [&](int t) {
+            const int last = t + C::DEEP - 1 < inside - 1 ? t + C::DEEP - 1 : inside - 1, later = last - (t + 1);
+            if (later >= 2) landed<2 * LOADS>();
+            else if (later == 1) landed<LOADS>();
+            else landed();
+            __syncthreads();
+        };
         stage(0);
-        if (part && (!TA || !TB)) clear_part(0, 0);
-        if constexpr (E == EL_MX && LAID) load_laid(0);
-        if constexpr (E == EL_MX && !LAID) load_raw(0);
-        landed_barrier();
-        if (slabs > 1) stage(1);
+        if constexpr (C::DEEP == 2) {
+            if (part && (!TA || !TB)) clear_part(0, 0);
+            if constexpr (E == EL_MX && LAID) load_laid(0);
+            if constexpr (E == EL_MX && !LAID) load_raw(0);
+            landed_barrier();
+            if (slabs > 1) stage(1);
+        } else {
+            static_assert(C::DEEP == 4, "waits are written for four slabs");
+#pragma unroll
+            for (int b = 1; b < C::DEEP; b++)
+                if (b < slabs) stage(b);
+            if (part && (!TA || !TB)) clear_part(0, 0);
+            deep_barrier(-1);
+        }
 #pragma unroll
         for (int j = 0; j < FN; j++) fb[0][j] = fragB(0, j, 0);
 #pragma unroll
         for (int i = 0; i < FM; i++) fa[i] = fragA(0, i, 0);
-        // LOAD: slab t + 2 exists and lies inside K; TAIL: it exists and K ends in it; NEXT: slab t + 1 exists. Constants, so
+        // LOAD: slab t + 2 (t + DEEP) exists and lies inside K; TAIL: it exists and K ends in it; NEXT: slab t + 1 exists. Constants, so
         // that the loads of a turn of the main loop are always the same in number and the wait for the
         // scales leaves the slab's loads in flight.
         typedef std::true_type Y1;
@@ -679,23 +716,28 @@ __device__ __forceinline__ void tile_body(const TileArgs& g, const TileAt& at) {
             if constexpr (E == EL_MX && !LAID) take_raw();
             step(0, slab_at(t), Y1{}, N0{}, 0);
             if constexpr (NEXT.value) {
-                if (part && (!TA || !TB)) clear_part(t + 1, (t + 1) & 1);
-                landed_barrier();     // slab t + 1 has landed, and every wavefront holds the rest of slab t
+                if (part && (!TA || !TB)) clear_part(t + 1, (t + 1) & (C::DEEP - 1));
+                // slab t + 1 has landed, and every wavefront holds the rest of slab t
+                if constexpr (C::DEEP == 2) landed_barrier();
+                else deep_barrier(t);
                 if constexpr (E == EL_MX && LAID) load_laid(0);      // ahead of the slab's loads
                 if constexpr (E == EL_MX && !LAID) load_raw(t + 1);
-                if constexpr (TAIL.value) stage(t & 1);
+                if constexpr (TAIL.value) stage(t & (C::DEEP - 1));
             }
             __builtin_amdgcn_sched_barrier(0);
-            step(1, slab_at(t + 1), NEXT, LOAD, t & 1);
+            step(1, slab_at(t + 1), NEXT, LOAD, t & (C::DEEP - 1));
             if constexpr (LOAD.value) staged();
         };
         int t = 0;
-        const int inside = E == EL_MX || whole - s0 > slabs ? slabs : whole - s0;
-        for (; t + 2 < inside; t++) turn(t, Y1{}, N0{}, Y1{});
+        for (; t + C::DEEP < inside; t++) turn(t, Y1{}, N0{}, Y1{});
         if constexpr (E != EL_MX) {
-            if (t + 2 < slabs) turn(t++, N0{}, Y1{}, Y1{});
+            if (t + C::DEEP < slabs) turn(t++, N0{}, Y1{}, Y1{});
         }
-        if (t + 1 < slabs) turn(t++, N0{}, N0{}, Y1{});
+        if constexpr (C::DEEP == 2) {
+            if (t + 1 < slabs) turn(t++, N0{}, N0{}, Y1{});
+        } else {
+            while (t + 1 < slabs) turn(t++, N0{}, N0{}, Y1{});
+        }
         turn(t, N0{}, N0{}, N0{});
         // the next pair's first slab overwrites the buffers only once every wavefront has read its last fragments
         if (MODE == TP_GRAD_X && pair == 0) __syncthreads();
@@ -877,7 +919,7 @@ __global__ __launch_bounds__(256) void tile_reduce_grads_kernel(TileArgs x, Tile
     else tile_reduce<TP_GRAD_W, C>(w, (int)blockIdx.x - first);
 }
 
-// How a product is cut: tile shape (0 L, 1 M, 2 S) and the tiles whose K is split, by the estimated time of each choice.
+// How a product is cut: tile shape (0 L, 1 M, 2 S, 3 MD, 4 SD) and the tiles whose K is split, by the estimated time of each choice.
 // A slab of a tile takes `lat` us by itself on a compute unit and `w` us of a busy one's matrix cores, a tile
 // `fix` more for its first loads and its epilogue; split sums are written and read once at 3.5 TB/s by a
 // second launch (4 us), and E2M1 scales laid out by one of 3 us. The constants are fitted to measurements of 8
@@ -885,7 +927,8 @@ __global__ __launch_bounds__(256) void tile_reduce_grads_kernel(TileArgs x, Tile
 // the fastest on average and 14 % at worst. They rank choices and do not foretell times: fp32's w of 0.2 is less than half of
 // the 0.44 us that its matrix cores take for a slab of a tile.
 // fp32 products are bound by the matrix cores in every shape and always take the small one, which leaves
-// the fewest of them idle. Some times, us (bf16 gated block, n x o x i): 65 x 11008 x 4096 L 87, M 46, S 39; 2048 x 11008 x 4096
+// the fewest of them idle. MD and SD (int8 only) are fitted to 21 int8 products, all shapes and cuts: 8 % from the fastest at worst, with
+// one turn of work-groups at most. Some times, us (bf16 gated block, n x o x i): 65 x 11008 x 4096 L 87, M 46, S 39; 2048 x 11008 x 4096
 // L 320, M 399, S 638; 512 x 4096 x 11008 M 122, M in two splits 93, L in four 96.
 struct TilePlan {
     int shape, whole, splits, sper;
@@ -897,13 +940,13 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
     // both weight gradients' plan also where one is wanted, so that it is the same bits either way
     constexpr int pairs = MODE == TP_GRAD_W ? 2 : 1;
     constexpr int BK = 8 * el_chunk<E>();
-    constexpr int size[3] = {256, 128, 64}, occ[3] = {1, 2, 4}, cuts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
-    constexpr double lat[3] = {1.4, 0.9, E == EL_MX ? 0.9 : 0.75}, fix[3] = {10.0, 4.0, 1.7};
-    constexpr double w[3] = {1.55, 0.5, E == EL_F32 ? 0.2 : E == EL_MX ? 0.68 : 0.38};
+    constexpr int size[5] = {256, 128, 64, 128, 64}, occ[5] = {1, 2, 4, 1, 2}, cuts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
+    constexpr double lat[5] = {1.4, 0.9, E == EL_MX ? 0.9 : 0.75, 0.45, 0.2}, fix[5] = {10.0, 4.0, 1.7, 5.5, 3.0};
+    constexpr double w[5] = {1.55, 0.5, E == EL_F32 ? 0.2 : E == EL_MX ? 0.68 : 0.38, 0.45, 0.19};
     const int64_t slabs = (K + BK - 1) / BK;
     TilePlan best{};
     double least = 0.0;
-    for (int h = E == EL_F32 ? 2 : 0; h < 3; h++) {
+    for (int h = E == EL_F32 ? 2 : 0; h < (E == EL_I8 ? 5 : 3); h++) {
         const int64_t tn = MODE == TP_GATED ? size[h] / 2 : size[h];
         const int64_t tiles = ((M + size[h] - 1) / size[h]) * ((N + tn - 1) / tn) * pairs, turn = 256 * occ[h];    // turn: even
         auto time = [&](int64_t wgs, int64_t per) {
@@ -918,6 +961,7 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
             for (int c = tail; c < 8; c++) {
                 const int64_t sper = (slabs + cuts[c] - 1) / cuts[c], splits = (slabs + sper - 1) / sper;
                 if (c && splits <= cuts[c - 1]) continue;        // another choice has these, or nearly
+                if (h > 2 && tiles * splits > turn) break;       // MD and SD: one turn
                 const size_t part = splits > 1 ? (size_t)(cut * splits * size[h] * size[h]) : 0;
                 double t = (whole ? time(whole, slabs) : 0.0) + time(cut * splits, sper);
                 if (part) t += 4.0 + 8.0 * (double)part / 3.5e6;
@@ -972,7 +1016,7 @@ kq_status tile_launch_shape(TileArgs g, const TilePlan& p, hipStream_t st, const
     hipLaunchKernelGGL((tile_kernel<E, MODE, C>), dim3((unsigned)n.tiles), dim3(C::THREADS), C::SMEM, st, g);
     KQ_TRY(check_launch(who));
     if (n.sums) {
-        hipLaunchKernelGGL((tile_reduce_kernel<MODE, C, E == EL_I8 ? EL_I8 : EL_F32>), dim3((unsigned)n.sums), dim3(256), 0, st, g);
+        hipLaunchKernelGGL((tile_reduce_kernel<MODE, typename C::Shallow, E == EL_I8 ? EL_I8 : EL_F32>), dim3((unsigned)n.sums), dim3(256), 0, st, g);
         KQ_TRY(check_launch(who));
     }
     return KQ_OK;
@@ -1007,6 +1051,10 @@ kq_status tile_launch(TileArgs g, const TilePlan& p, int pairs, float* part, hip
     if constexpr (E != EL_F32) {
         if (p.shape == 0) return tile_launch_shape<E, MODE, TileL>(g, p, st, who);
         if (p.shape == 1) return tile_launch_shape<E, MODE, TileM>(g, p, st, who);
+    }
+    if constexpr (E == EL_I8) {
+        if (p.shape == 3) return tile_launch_shape<E, MODE, TileMD>(g, p, st, who);
+        if (p.shape == 4) return tile_launch_shape<E, MODE, TileSD>(g, p, st, who);
     }
     return tile_launch_shape<E, MODE, TileS>(g, p, st, who);
 }

@@ -35,14 +35,21 @@ def out_stack(e, o, i, dt):
 # split for all tiles, or for those behind the last full turn (mixed), of the plain or the gated product
 FORWARD = [("few", "bf16", 1, 1, 40, 33), ("few", "bf16", 3, 4, 41, 100), ("few", "bf16", 64, 16, 70, 1000), ("few", "bf16", 90, 70, 40, 65),
            ("few", "bf16", 200, 150, 30, 100), ("few", "f32", 1, 1, 40, 33), ("few", "f32", 64, 16, 70, 1000), ("few", "f32", 300, 70, 40, 65),
-           ("S", "bf16", 100, 3, 33, 400), ("S", "bf16", 500, 7, 130, 257), ("S", "bf16", 4100, 130, 70, 48), ("S", "bf16", 3000, 5, 1100, 900),
-           ("S split", "bf16", 25, 2, 1, 876), ("S mixed", "bf16", 110, 9, 7674, 1792), ("S mixed gated", "bf16", 51, 5, 7228, 1593),
-           ("M", "bf16", 776, 12, 2812, 9), ("M", "bf16", 655, 10, 3306, 3), ("M split", "bf16", 4277, 2, 464, 3085),
-           ("M split gated", "bf16", 1479, 2, 752, 3154), ("M mixed", "bf16", 5500, 3, 3126, 2463), ("M mixed gated", "bf16", 4873, 2, 1664, 1853),
+           ("SD", "bf16", 100, 3, 33, 400), ("SD", "bf16", 500, 7, 130, 257), ("S", "bf16", 4100, 130, 70, 48), ("MD", "bf16", 3000, 5, 1100, 900),
+           ("SD", "bf16", 25, 2, 1, 876), ("S mixed", "bf16", 110, 9, 7674, 1792), ("S mixed gated", "bf16", 51, 5, 7228, 1593),
+           ("M", "bf16", 776, 12, 2812, 9), ("M", "bf16", 655, 10, 3306, 3), ("MD", "bf16", 4277, 2, 464, 3085),
+           ("MD gated", "bf16", 1479, 2, 752, 3154), ("M mixed", "bf16", 5500, 3, 3126, 2463), ("M mixed gated", "bf16", 4873, 2, 1664, 1853),
            ("L", "bf16", 4011, 3, 2059, 548), ("L", "bf16", 2313, 3, 1609, 594), ("L split", "bf16", 5840, 2, 1483, 10880),
            ("L split gated", "bf16", 1539, 2, 2539, 11720), ("L mixed", "bf16", 8505, 2, 4325, 5866), ("L mixed gated", "bf16", 4273, 3, 4150, 4753),
            ("S", "f32", 517, 5, 130, 257), ("S", "f32", 1000, 3, 200, 72), ("S split", "f32", 92, 2, 2, 437), ("S mixed", "f32", 3637, 2, 1191, 755),
            ("S mixed gated", "f32", 3517, 3, 597, 633)]
+# tiles with four slabs in LDS (MD, SD), whole and split, and lengths of K that end anywhere in the four; (may): cut for some row counts
+FORWARD += [("L (may)", "bf16", 7077, 2, 2182, 1015), ("M (may)", "bf16", 5797, 2, 1282, 2045), ("M split", "bf16", 3493, 2, 635, 10706),
+            ("MD (may)", "bf16", 2049, 4, 208, 8814), ("MD", "bf16", 5004, 2, 628, 228), ("MD split", "bf16", 1556, 2, 762, 4803),
+            ("S (may)", "bf16", 194, 3, 289, 3165), ("S split", "bf16", 24, 2, 1, 1540), ("SD (may)", "bf16", 645, 10, 150, 6321),
+            ("SD split", "bf16", 17, 2, 1, 3734), ("MD gated", "bf16", 1278, 2, 1259, 200), ("MD split gated", "bf16", 922, 2, 177, 6388),
+            ("MD (may) gated", "bf16", 3331, 13, 134, 8278), ("SD (may) gated", "bf16", 257, 2, 62, 7247), ("S (may)", "f32", 129, 2, 211, 524)]
+FORWARD += [("SD", "bf16", 300, 3, 200, i) for i in (129, 150, 192, 193, 256, 257, 319, 320, 321, 384, 449, 513)]
 
 
 @pytest.mark.parametrize("plan,dt,n,e,o,i", FORWARD)
@@ -117,11 +124,20 @@ BACKWARD = [("one launch", "bf16", 1, 1, 40, 33), ("one launch", "bf16", 33, 3, 
             ("one launch", "f32", 1, 1, 40, 33), ("one launch", "f32", 64, 16, 70, 200), ("one launch", "f32", 517, 5, 130, 257),
             ("one launch, dX cut", "f32", 21, 2, 235, 1), ("dW split", "f32", 478, 2, 1, 1), ("some", "f32", 1000, 70, 40, 65),
             ("some", "f32", 3000, 2, 200, 100)]
+# tiles with four slabs in LDS for dX (of one product, of two), whole and split, of K that ends anywhere in the four
+BACKWARD += [("dX MD (may)", "bf16", 602, 4, 8716, 2763), ("dX MD", "bf16", 3211, 2, 466, 649), ("dX MD", "bf16", 2811, 2, 268, 1119),
+             ("dX MD", "bf16", 544, 4, 328, 2694), ("dX MD", "bf16", 609, 2, 419, 3844), ("dX MD", "bf16", 1378, 2, 199, 2346),
+             ("dX MD split", "bf16", 741, 2, 7885, 2530), ("dX SD (may)", "bf16", 257, 4, 5146, 409), ("dX SD", "bf16", 1091, 2, 452, 3),
+             ("dX SD", "bf16", 920, 2, 265, 1), ("dX SD", "bf16", 948, 2, 333, 10), ("dX SD", "bf16", 1091, 2, 412, 1),
+             ("dX SD", "bf16", 937, 2, 141, 4), ("dX SD split", "bf16", 80, 8, 4531, 66), ("dX2 MD (may)", "bf16", 2117, 11, 3496, 734),
+             ("dX2 MD", "bf16", 1547, 2, 257, 1443), ("dX2 MD", "bf16", 1965, 2, 327, 1203), ("dX2 MD", "bf16", 959, 2, 397, 2050),
+             ("dX2 MD", "bf16", 2468, 2, 129, 835), ("dX2 MD split", "bf16", 3924, 4, 4537, 491), ("dX2 SD (may)", "bf16", 129, 2, 4390, 951),
+             ("dX2 SD", "bf16", 904, 2, 65, 4)]
 
 
 @pytest.mark.parametrize("plan,dt,n,e,o,i", BACKWARD)
 def test_grouped_backward_exact(plan, dt, n, e, o, i):
-    """Whole numbers of at most 4: products of at most 16; 2 * 6048 and 11824 of them sum to less than 2^18."""
+    """Whole numbers of at most 4: products of at most 16; 2 * 8716 and 11824 of them sum to less than 2^19."""
     import torch
     say(f"grouped backward {plan} {dt} n={n} e={e} o={o} i={i}")
     g = generator(n + e + o + i)

@@ -147,9 +147,14 @@ def product(a, b):
 GEMM = [(1, 1, 1), (1, 41, 11008), (5, 100, 255), (16, 64, 256), (17, 130, 257), (32, 48, 1000), (33, 1, 1), (33, 1, 783),
         (65, 255, 100), (66, 256, 64), (255, 129, 511), (11182, 321, 2), (753, 976, 4977), (1444, 5455, 903),
         (2444, 3256, 953), (2553, 1613, 11112), (3209, 5104, 3210), (40, 50, 131071), (3, 20, 131071)]
+# tiles with four slabs in LDS (MD, SD), whole and split, of long and short K; lengths of K that end anywhere in the four; S split
+GEMM += [(961, 2080, 750), (2715, 1101, 392), (1131, 901, 8895), (33, 1, 3137), (33, 1, 4391), (200, 300, 8000)]
+GEMM += [(70, 200, i) for i in (257, 300, 384, 385, 500, 512, 513, 639, 640, 641, 767, 768, 769, 896, 1025)]
+GEMM += [(1100, 2100, i) for i in (512, 513, 640, 700, 768, 769, 897, 1024, 1151)]
 GATED = [(1, 1, 1), (1, 41, 11008), (5, 100, 255), (16, 64, 256), (17, 130, 257), (32, 48, 1000), (33, 1, 1), (33, 1, 783),
          (65, 255, 100), (255, 129, 511), (197, 8230, 5), (489, 749, 5038), (1032, 3644, 801), (2638, 1597, 943),
          (1256, 1688, 11153), (3232, 2521, 3230)]
+GATED += [(1045, 1049, 773), (545, 2867, 393), (862, 585, 8107), (33, 1, 3137), (34, 1, 8495), (33, 1, 4391), (70, 200, 640)]
 
 
 @pytest.mark.parametrize("n,o,i", GEMM)
@@ -234,6 +239,9 @@ GROUPS = [(1, 1, 40, 33), (3, 4, 41, 100), (64, 16, 70, 1000), (90, 70, 40, 65),
           (776, 12, 2812, 17), (3000, 5, 1100, 900), (4100, 130, 70, 48), (20, 2, 1, 2488), (300, 28, 2330, 3184), (163, 15, 2386, 5039),
           (655, 10, 3306, 3), (1738, 2, 1176, 6420), (843, 3, 1123, 6029), (4046, 2, 4429, 5540), (2866, 2, 2926, 4064), (3652, 2, 2320, 1370),
           (5633, 3, 724, 901), (8505, 2, 4325, 5866), (9239, 2, 2685, 5103), (9224, 18, 736, 9018)]
+# plans that came with the tiles of four slabs, and what is left of the others
+GROUPS += [(2531, 4, 3096, 2704), (4288, 19, 593, 8976), (4963, 4, 587, 467), (1442, 2, 675, 9089), (645, 37, 1713, 5097), (17, 2, 1, 3734),
+           (18, 2, 3, 7229), (6972, 2, 1120, 2033), (1322, 7, 1092, 10533), (858, 2, 1770, 427), (2065, 2, 259, 11894), (257, 2, 62, 7247)]
 
 
 @pytest.mark.parametrize("n,e,o,i", GROUPS)

@@ -305,7 +305,7 @@ __global__ __launch_bounds__(FEW_THREADS) void group_few_kernel(FewArgs g, Group
         g.Y2 = rows_on(g.Y2, begin * g.ldy2, g.dt);
         g.Y3 = rows_on(g.Y3, begin * g.ldy3, g.dt);
     }
-    few_body<E, GATED, NB>(g, at.id % blocks);
+    few_body<E, GATED, NB, true>(g, at.id % blocks);
 }
 
 // ------------------------------------------------------------------------------------------ launches
@@ -317,13 +317,13 @@ inline int64_t group_tiles_max(int64_t n, int64_t experts, int64_t size) {
 
 // Whether n rows of `experts` experts run as few tokens each. The counts are not known here; the rule takes their mean. MI355X, us as
 // few tokens / as tiles, o x i weights an expert, at a mean of
-//   4   bf16 gated 16 x 1376 x 4096: 68 / 89; int8 the same: 38 / 43
-//   8   bf16 8 x 4096 x 11008: 152 / 152, gated 8 x 1376 x 4096: 44 / 53; int8 16 x 4096 x 4096: 66 / 71
-//   10  bf16 8 x 4096 x 11008: 170 / 165;  12  int8 gated 8 x 1376 x 4096: 27 / 20;  16  bf16 8 x 4096 x 11008: 205 / 165
+//   4   bf16 8 x 4096 x 11008: 111 / 113, gated 16 x 1376 x 4096: 67 / 70, 4 x 4096 x 4096: 26 / 29; int8 8 x 4096 x 11008: 58 / 64
+//   8   the same: 142 / 132, 81 / 74, 31 / 31; 74 / 73, int8 gated 16 x 1376 x 4096 44 / 41, 12 x 2500 x 4096 31 / 33
+//   12  178 / 146, 92 / 78, 36 / 31; 93 / 81
 // and fp32 5 x 1376 x 1000, 32 rows a work-group: gated at 12 19.2 / 23.3, plain at 20 14.8 / 18.4, at 40 16.8 / 21.1.
 template <int E>
 bool group_few(int64_t n, int64_t experts) {
-    return n <= (E == EL_F32 ? 32 : 8) * (experts < n ? experts : n);
+    return n <= (E == EL_F32 ? 32 : 6) * (experts < n ? experts : n);
 }
 
 // Estimated time, us, of work-groups of `per` slabs of tile shape h, with the constants of tile_plan.

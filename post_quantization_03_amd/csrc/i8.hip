@@ -175,7 +175,7 @@ static kq_status i8_product(const char* who, const I8Operand& A, const I8Operand
     if (GATED) KQ_TRY(i8_check(who, "up weights", U, orows, i));
     KQ_TRY(i8_float_check(who, "the output", Y, dt, ldy, o));
     const Group gr{offsets, (int)experts, (int)(n <= GROUP_ROWS_MAX ? n : 0), (int)o};
-    if (offsets ? group_few<EL_I8>(n, experts) : few_tokens<EL_I8>(n, o, i)) {
+    if (offsets ? group_few<EL_I8>(n, experts) : few_tokens<EL_I8>(n, GATED ? 2 * o : o, i)) {
         FewArgs f{};
         f.n = n; f.o = o; f.K = i;
         f.A = reinterpret_cast<const char*>(A.c); f.lda = A.ld; f.fA = A.s;
@@ -208,7 +208,7 @@ size_t i8_product_ws(int64_t o, int64_t i, int64_t n, bool gated, int64_t expert
         if (experts > GROUP_MAX || n > GROUP_ROWS_MAX || group_few<EL_I8>(n, experts)) return 0;
         return gated ? group_ws<EL_I8, TP_GATED>(n, experts, o, i) : group_ws<EL_I8, TP_PLAIN>(n, experts, o, i);
     }
-    if (few_tokens<EL_I8>(n, o, i)) return 0;
+    if (few_tokens<EL_I8>(n, gated ? 2 * o : o, i)) return 0;
     return sizeof(float) * (gated ? i8_plan<true>(n, o, i) : i8_plan<false>(n, o, i)).part;
 }
 

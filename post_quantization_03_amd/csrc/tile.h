@@ -1087,13 +1087,14 @@ constexpr int FEW_WAVES = 8, FEW_THREADS = 64 * FEW_WAVES;
 // Whether n tokens run here rather than as tiles. Measured on MI355X, us here / as tiles, o x i weights:
 //   E2M1  11008 x 4096: 8.3 / 11.2 at 1 token, 15.4 / 16.1 at 32, 22.2 / 16.1 at 33; 4096 x 11008: 11.8 / 14.8
 //         at 32, 14.6 / 14.3 at 33
-//   int8  4096 x 11008: 9.6 / 12.7 at 1, 12.0 / 13.9 at 16, 16.4 / 14.3 at 20; 4096 x 4096: 8.5 / 10.8 at 24; gated 11008 x 4096:
-//         17.7 / 17.7 at 1, 19.6 / 17.8 at 16; gated 1376 x 4096: 9.7 / 12.3 at 16
+//   int8  weights from HBM; 4096 x 11008: 11.2 / 14.1 at 1, 13.0 / 14.7 at 16, 20.6 / 15.0 at 24; 16384 x 4096: 15.7 / 17.2 at 8, 19.4 / 17.5
+//         at 16; 4096 x 4096: 10.1 / 11.8 at 32; gated (o is then 2 x 11008) 11008 x 4096: 20.5 / 23.2 at 1, 24.1 / 21.8 at 16; gated 1376 x
+//         4096: 11.5 / 11.8 at 32; gated 5504 x 8192 is better as tiles from one token on, 23.7 / 21.8
 //   bf16  gated 11008 x 4096: 34.1 / 34.7 at 8, 36.2 / 34.4 at 16; 1376 x 1000: 6.7 / 9.2 at 48
 //   fp32  gated 11008 x 4096: 104 / 135 at 32, 173 / 134 at 33; 1376 x 1000: 10.0 / 15.4 at 32, 16.6 / 15.6 at 33
 template <int E>
 bool few_tokens(int64_t n, int64_t o, int64_t i) {
-    if (E == EL_I8) return n <= 16 || (n <= 32 && o * i <= (1 << 24));
+    if (E == EL_I8) return n <= 8 || (n <= 16 && o <= 8192) || (n <= 32 && o * i <= (1 << 24));
     if (E != EL_BF16) return n <= 32;
     return n <= 8 || (n <= 48 && o * i <= (1 << 22));
 }
@@ -1138,8 +1139,13 @@ __device__ __forceinline__ void few_load(FewFrag<E>& f, const char* row, const u
     }
 }
 
-// rows 16 block .. of B, the first 16 NB rows of A
-template <int E, bool GATED, int NB>
+// rows 16 block .. of B, the first 16 NB rows of A. SPREAD: where rows begin at multiples of 128 bytes, a wavefront takes neighbouring slabs of
+// K, from a place that differs from block to block. In turns, all work-groups walk along K together and their reads meet in the same memory
+// channels, most of all where rows lie a multiple of 4 KiB apart. MI355X, us in turns / spread, weights from HBM: int8, one token 4096 x 11008 13.3 / 11.2, 16384 x 4096 16.2 /
+// 14.0; 8 rows of 8 experts 4096 x 11008 bf16 89 / 78, int8 50 / 40. Other rows' slabs share a cache line with the next wavefront's (16 rows of
+// 8 experts gated 2000 x 2000 bf16 18.7 / 21.4), and from two blocks of tokens on it costs more reads of A (24 tokens gated 1376 x 4096 int8
+// 10.8 / 12.3). Not for the other products of one matrix, which keep the order of their sums; int8's are exact in any.
+template <int E, bool GATED, int NB, bool SPREAD>
 __device__ __forceinline__ void few_body(const FewArgs& g, int64_t block) {
     extern __shared__ __align__(16) float few_sm[];       // [wave][matrix][token block][lane][4]
     constexpr int EPC = el_chunk<E>(), MATS = GATED ? 2 : 1;
@@ -1193,6 +1199,16 @@ __device__ __forceinline__ void few_body(const FewArgs& g, int64_t block) {
     };
     constexpr int U = E == EL_MX && NB < 4 ? 2 : 1;
     int64_t s = wave;
+    if constexpr (SPREAD && NB == 1) {
+        static_assert(U == 1, "one slab at a time");
+        if (g.ldb % 128 == 0) {
+            const int64_t first = full * wave / FEW_WAVES, last = full * (wave + 1) / FEW_WAVES;
+            const int64_t from = last > first ? first + (unsigned)block % (unsigned)(last - first) : first;
+            for (int64_t t = from; t < last; t++) batch(t, std::integral_constant<int, 1>{}, true);
+            for (int64_t t = first; t < from; t++) batch(t, std::integral_constant<int, 1>{}, true);
+            s = full;
+        }
+    }
     for (; s + (U - 1) * FEW_WAVES < full; s += U * FEW_WAVES) batch(s, std::integral_constant<int, U>{}, true);
     if (U > 1 && s < full) batch(s, std::integral_constant<int, 1>{}, true);
     if (full < slabs && wave == (int)(full % FEW_WAVES)) batch(full, std::integral_constant<int, 1>{}, false);
@@ -1238,7 +1254,7 @@ __device__ __forceinline__ void few_body(const FewArgs& g, int64_t block) {
 
 template <int E, bool GATED, int NB>
 __global__ __launch_bounds__(FEW_THREADS) void few_kernel(FewArgs g) {
-    few_body<E, GATED, NB>(g, (int64_t)blockIdx.x);
+    few_body<E, GATED, NB, E == EL_I8>(g, (int64_t)blockIdx.x);
 }
 
 template <int E, bool GATED>
@@ -1251,7 +1267,7 @@ kq_status few_launch(const FewArgs& g, hipStream_t st, const char* who) {
         hipLaunchKernelGGL((few_kernel<E, GATED, 1>), grid, dim3(FEW_THREADS), one, st, g);
     } else if (g.n <= 32) {
         hipLaunchKernelGGL((few_kernel<E, GATED, 2>), grid, dim3(FEW_THREADS), 2 * one, st, g);
-    } else {
+    } else if constexpr (E == EL_BF16) {                 // the others have 32 tokens at most
         hipLaunchKernelGGL((few_kernel<E, GATED, 4>), grid, dim3(FEW_THREADS), 4 * one, st, g);
     }
     return check_launch(who);

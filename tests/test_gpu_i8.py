@@ -154,6 +154,10 @@ GEMM += [(1100, 2100, i) for i in (512, 513, 640, 700, 768, 769, 897, 1024, 1151
 GATED = [(1, 1, 1), (1, 41, 11008), (5, 100, 255), (16, 64, 256), (17, 130, 257), (32, 48, 1000), (33, 1, 1), (33, 1, 783),
          (65, 255, 100), (255, 129, 511), (197, 8230, 5), (489, 749, 5038), (1032, 3644, 801), (2638, 1597, 943),
          (1256, 1688, 11153), (3232, 2521, 3230)]
+# few rows that begin at multiples of 128 bytes: wavefronts without a slab, with one, with several; the ends of the choice
+SPREAD = [113, 128, 245, 896, 1017, 1024, 1152, 2160, 4090, 11008]
+GEMM += [(n, 100, i) for n in (1, 7) for i in SPREAD] + [(16, 8192, 200), (16, 8193, 200), (8, 8193, 200), (9, 8193, 200)]
+GATED += [(n, 100, i) for n in (1, 7) for i in SPREAD] + [(16, 4096, 200), (16, 4097, 200), (8, 4097, 200), (9, 4097, 200)]
 GATED += [(1045, 1049, 773), (545, 2867, 393), (862, 585, 8107), (33, 1, 3137), (34, 1, 8495), (33, 1, 4391), (70, 200, 640)]
 
 
@@ -241,7 +245,7 @@ GROUPS = [(1, 1, 40, 33), (3, 4, 41, 100), (64, 16, 70, 1000), (90, 70, 40, 65),
           (5633, 3, 724, 901), (8505, 2, 4325, 5866), (9239, 2, 2685, 5103), (9224, 18, 736, 9018)]
 # plans that came with the tiles of four slabs, and what is left of the others
 GROUPS += [(2531, 4, 3096, 2704), (4288, 19, 593, 8976), (4963, 4, 587, 467), (1442, 2, 675, 9089), (645, 37, 1713, 5097), (17, 2, 1, 3734),
-           (18, 2, 3, 7229), (6972, 2, 1120, 2033), (1322, 7, 1092, 10533), (858, 2, 1770, 427), (2065, 2, 259, 11894), (257, 2, 62, 7247)]
+           *((n, 7, 100, i) for n in (1, 40) for i in SPREAD), (18, 2, 3, 7229), (6972, 2, 1120, 2033), (1322, 7, 1092, 10533), (858, 2, 1770, 427), (2065, 2, 259, 11894), (257, 2, 62, 7247)]
 
 
 @pytest.mark.parametrize("n,e,o,i", GROUPS)

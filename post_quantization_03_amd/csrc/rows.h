@@ -147,8 +147,8 @@ kq_status with_rows(bool bf, int64_t cols, F&& f) {
     if (pieces <= 2048) return KQ_ROWS(512, 4);
     if (pieces <= 4096 && bf) return f(std::true_type{}, std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
     auto f32 = [&](auto ch) { return f(std::false_type{}, std::integral_constant<int, 512>{}, ch); };
-    if (pieces <= 3072) return f32(std::integral_constant<int, 6>{});
-    if (pieces <= 4096) return f32(std::integral_constant<int, 8>{});
+    if (pieces <= 6 * 512) return f32(std::integral_constant<int, 6>{});
+    if (pieces <= 8 * 512) return f32(std::integral_constant<int, 8>{});
     return KQ_ROWS(1024, 0);
 #undef KQ_ROWS
 }

@@ -48,7 +48,8 @@ FORWARD += [("L (may)", "bf16", 7077, 2, 2182, 1015), ("M (may)", "bf16", 5797, 
             ("MD (may)", "bf16", 2049, 4, 208, 8814), ("MD", "bf16", 5004, 2, 628, 228), ("MD split", "bf16", 1556, 2, 762, 4803),
             ("S (may)", "bf16", 194, 3, 289, 3165), ("S split", "bf16", 24, 2, 1, 1540), ("SD (may)", "bf16", 645, 10, 150, 6321),
             ("SD split", "bf16", 17, 2, 1, 3734), ("MD gated", "bf16", 1278, 2, 1259, 200), ("MD split gated", "bf16", 922, 2, 177, 6388),
-            ("MD (may) gated", "bf16", 3331, 13, 134, 8278), ("SD (may) gated", "bf16", 257, 2, 62, 7247), ("S (may)", "f32", 129, 2, 211, 524)]
+            ("MD (may) gated", "bf16", 3331, 13, 134, 8278), ("SD (may) gated", "bf16", 257, 2, 62, 7247), ("M (may) gated", "bf16", 2655, 3, 1503, 2008),
+            ("M split gated", "bf16", 3561, 2, 574, 5400), ("S (may) gated", "bf16", 129, 2, 146, 2513), ("S (may)", "f32", 129, 2, 211, 524)]
 # few rows an expert, rows that begin at multiples of 128 bytes (their padding counted): wavefronts without a slab, with one, with several
 FORWARD += [("few, spread", "bf16", n, 7, 100, i) for n in (1, 40) for i in (56, 120, 497, 504, 568, 1009, 1080, 4085)]
 FORWARD += [("few, spread", "f32", n, 7, 100, i) for n in (1, 40) for i in (28, 57, 249, 252, 284, 1017, 2044)]

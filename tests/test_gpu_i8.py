@@ -245,7 +245,8 @@ GROUPS = [(1, 1, 40, 33), (3, 4, 41, 100), (64, 16, 70, 1000), (90, 70, 40, 65),
           (5633, 3, 724, 901), (8505, 2, 4325, 5866), (9239, 2, 2685, 5103), (9224, 18, 736, 9018)]
 # plans that came with the tiles of four slabs, and what is left of the others
 GROUPS += [(2531, 4, 3096, 2704), (4288, 19, 593, 8976), (4963, 4, 587, 467), (1442, 2, 675, 9089), (645, 37, 1713, 5097), (17, 2, 1, 3734),
-           *((n, 7, 100, i) for n in (1, 40) for i in SPREAD), (18, 2, 3, 7229), (6972, 2, 1120, 2033), (1322, 7, 1092, 10533), (858, 2, 1770, 427), (2065, 2, 259, 11894), (257, 2, 62, 7247)]
+           *((n, 7, 100, i) for n in (1, 40) for i in SPREAD), (18, 2, 3, 7229), (6972, 2, 1120, 2033), (1322, 7, 1092, 10533), (858, 2, 1770, 427),
+           (2065, 2, 259, 11894), (257, 2, 62, 7247), (8798, 2, 208, 11469), (242, 28, 2330, 3184)]
 
 
 @pytest.mark.parametrize("n,e,o,i", GROUPS)

@@ -535,25 +535,36 @@ kq_status group_launch(TileArgs g, const Group& gr, void* ws, size_t ws_bytes, h
     });
 }
 
+// Floats of the weight gradients' split sums.
+inline size_t group_grad_sums(const GradPlan& p, int64_t experts, int64_t o, int64_t i, int pairs) {
+    const int64_t size = 256 >> p.shape, tiles = experts * ((o + size - 1) / size) * ((i + size - 1) / size) * pairs;
+    return p.splits > 1 ? (size_t)(tiles * p.splits * size * size) : 0;
+}
 template <int E>
 size_t group_grad_ws(int64_t n, int64_t experts, int64_t o, int64_t i, int pairs) {
     if (n <= 0) return 0;
-    const GradPlan p = group_grad_plan<E>(n, experts, o, i);
-    const int64_t size = 256 >> p.shape, tiles = experts * ((o + size - 1) / size) * ((i + size - 1) / size) * pairs;
-    return p.splits > 1 ? sizeof(float) * (size_t)(tiles * p.splits * size * size) : 0;
+    return sizeof(float) * group_grad_sums(group_grad_plan<E>(n, experts, o, i), experts, o, i, pairs);
 }
 
+// The plan of the weight gradients, its workspace and launch checked: before anything of the call is enqueued.
 template <int E>
-kq_status group_grad_launch(TileArgs g, const Group& gr, int pairs, void* ws, size_t ws_bytes, hipStream_t st, const char* who) {
-    const GradPlan plan = group_grad_plan<E>(gr.n, gr.experts, g.M, g.N);
-    const size_t need = group_grad_ws<E>(gr.n, gr.experts, g.M, g.N, pairs);
+kq_status group_grad_prepare(GradPlan& plan, const TileArgs& g, const Group& gr, int pairs, const void* ws, size_t ws_bytes, const char* who) {
+    plan = group_grad_plan<E>(gr.n, gr.experts, g.M, g.N);
+    const size_t need = gr.n ? sizeof(float) * group_grad_sums(plan, gr.experts, g.M, g.N, pairs) : 0;
     if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return fail(KQ_EWORKSPACE, "%s: workspace too small or not aligned to 16 bytes", who);
+    return with_shape<E, TP_GRAD_W>(plan.shape, [&](auto shape) {
+        typedef decltype(shape) C;
+        const int64_t per = ((g.M + C::TM - 1) / C::TM) * ((g.N + C::TN - 1) / C::TN) * pairs;
+        return grid_ok(per * gr.experts * plan.splits, C::THREADS) ? KQ_OK : fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
+    });
+}
+template <int E>
+kq_status group_grad_launch(TileArgs g, const GradPlan& plan, const Group& gr, int pairs, void* ws, hipStream_t st, const char* who) {
     g.part = static_cast<float*>(ws);
     g.splits = plan.splits;
     return with_shape<E, TP_GRAD_W>(plan.shape, [&](auto shape) {
         typedef decltype(shape) C;
         const int64_t per = ((g.M + C::TM - 1) / C::TM) * ((g.N + C::TN - 1) / C::TN) * pairs, wgs = per * gr.experts * plan.splits;
-        if (!grid_ok(wgs, C::THREADS)) return fail(KQ_ESHAPE, "%s: too many tiles for a launch", who);
         static std::atomic<uint64_t> allowed{0};
         KQ_TRY(allow_lds(reinterpret_cast<const void*>(&group_grad_kernel<E, C>), C::SMEM, allowed, who));
         hipLaunchKernelGGL((group_grad_kernel<E, C>), dim3((unsigned)wgs), dim3(C::THREADS), C::SMEM, st, g, gr, (int)per);

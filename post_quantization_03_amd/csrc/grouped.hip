@@ -57,8 +57,11 @@ template <int E, int MODE>
 static kq_status backward(const char* who, const Group& gr, const TileArgs& x, const TileArgs& w, int pairs, void* ws, size_t ws_bytes,
                           hipStream_t st) {
     if (x.Y && pairs && group_grads_together<E, MODE>(x, w, gr)) return group_grads_launch<E, MODE>(x, w, gr, pairs, ws, ws_bytes, st, who);
+    // a refused call leaves dX alone too: the weight gradients are checked first, dX by its own launch before it enqueues anything
+    GradPlan plan{};
+    if (pairs) KQ_TRY((group_grad_prepare<E>(plan, w, gr, pairs, ws, ws_bytes, who)));
     if (x.Y) KQ_TRY((group_launch<E, MODE>(x, gr, ws, ws_bytes, st, who)));
-    return pairs ? group_grad_launch<E>(w, gr, pairs, ws, ws_bytes, st, who) : KQ_OK;
+    return pairs ? group_grad_launch<E>(w, plan, gr, pairs, ws, st, who) : KQ_OK;
 }
 template <int E>
 static kq_status backward(const char* who, const Group& gr, const TileArgs& x, const TileArgs& w, int pairs, void* ws, size_t ws_bytes,

@@ -182,6 +182,25 @@ def test_grouped_backward_refusals():
     assert bwd(dX=None, dW=None, dW2=None, dY2=None, W2=None) == 0
 
 
+@pytest.mark.parametrize("two", [False, True])
+def test_grouped_backward_checks_all_before_it_launches(two):
+    """A call whose weight gradients are refused (workspace, grid) enqueues nothing, dX neither: without a GPU a launch would come back as
+    a HIP error instead of the refusal."""
+    def bwd(n, e, o, i, ws, wb, dt=1):
+        lo, li = -(-o // 8) * 8, -(-i // 8) * 8
+        more = (P, lo, P, li) if two else (None, 0, None, 0)
+        return K.lib().kq_grouped_backward(P, lo, P, li, *more, P, li, P, e, dt, n, o, i, P, li, P, li, P if two else None, li, ws, wb, None)
+
+    # what the sizes are for: more split sums of dW than of dX; split sums of dW alone; of both, fp32
+    for n, e, o, i, dt in ((6034, 2, 805, 1587, 1), (5001, 2, 371, 971, 1), (9000, 1, 40, 72, 1), (9000, 1, 40, 72, 0)):
+        need = K.kq_workspace_bytes("grouped_backward", o, i, n, dt, group=e)
+        assert need > 0
+        for ws, wb in ((None, 0), (None, need), (FOUR, need), (P, need // 2 - 1)):
+            assert bwd(n, e, o, i, ws, wb, dt) == EWORKSPACE, (n, e, o, i, dt, ws, wb)
+    # 4 rows: few tiles of dX, 4096 experts' weight gradients past a launch
+    assert bwd(4, 4096, 1 << 18, 1 << 18, P, 1 << 40) == ESHAPE
+
+
 def test_norm_refusals():
     def fwd(X=P, ldx=16, g=P, b=P, dt=1, n=4, d=16, kind=0, eps=1e-5, Y=P, ldy=16, m=P, r=P):
         return K.lib().kq_norm_forward(X, ldx, g, b, dt, n, d, kind, eps, Y, ldy, m, r, None)

@@ -88,18 +88,19 @@ def quantize_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, dH: torc
                 "up": quantize_layer(X, Wu, cal["HG_up"], s, t_up, cfg, verify=verify), "calibration": cal}
 
 
-def calibrate_norm_gated(X: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor | None, kind: str, eps: float, Wg: torch.Tensor,
-                         Wu: torch.Tensor, dH: torch.Tensor, act: str, cfg: LayerCfg) -> dict:
+def calibrate_norm_gated(X: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tensor | None, kind: str, eps: float,
+                         Wg: torch.Tensor, Wu: torch.Tensor, dH: torch.Tensor, act: str, cfg: LayerCfg) -> dict:
     """calibrate_gated of the block behind a norm, from the hidden states X (n x i): its result, the norm's output N (the input
     of gate and up, which the solver takes as X), and the gradients through the norm: dX at the hidden states (in place
-    of the block's own, which is dN), dgamma and dbeta (None without beta)."""
+    of the block's own, which is dN), dgamma (None without gamma) and dbeta (None without beta)."""
     n, i = X.shape
     with _on(X, "calibrate_norm_gated"):
         N = _rows(n, i, X)
         mean, rstd = (torch.empty(n, dtype=torch.float32, device=X.device) for _ in range(2))
         K.kq_norm_forward(X, gamma, beta, kind, eps, N, mean, rstd)
         cal = calibrate_gated(N, Wg, Wu, dH, act, cfg)
-        dX, dgamma, dbeta = _rows(n, i, X), torch.empty_like(gamma), None if beta is None else torch.empty_like(beta)
+        dX = _rows(n, i, X)
+        dgamma, dbeta = (None if p is None else torch.empty_like(p) for p in (gamma, beta))
         K.kq_norm_backward(cal["dX"], X, gamma, mean, rstd, kind, dX, dgamma, dbeta, _ws("norm_backward", 0, i, n, X))
         return {**cal, "N": N, "dN": cal["dX"], "dX": dX, "dgamma": dgamma, "dbeta": dbeta}
 

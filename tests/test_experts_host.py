@@ -326,6 +326,27 @@ def test_driver_refusals():
         ffn.calibrate_norm_gated(z(4, 64), z(64), None, "layer", 1e-5, z(8, 64), z(8, 64), z(4, 8), "silu", cfg)
 
 
+@pytest.mark.parametrize("have", [(False, False), (False, True), (True, False), (True, True)])
+def test_norm_driver_without_weights(monkeypatch, have):
+    """calibrate_norm_gated of a norm without gamma or beta: the norm's calls get None for them and for their gradients."""
+    import contextlib
+
+    from post_quantization_03_amd.layer import LayerCfg
+    seen = {}
+    monkeypatch.setattr(ffn, "_on", lambda t, name: contextlib.nullcontext())
+    monkeypatch.setattr(ffn, "calibrate_gated", lambda N, *a: {"H": None, "dX": N})
+    monkeypatch.setattr(K, "kq_norm_forward", lambda X, gamma, beta, *a: seen.update(gamma=gamma, beta=beta))
+    monkeypatch.setattr(K, "kq_norm_backward", lambda dY, X, gamma, mean, rstd, kind, dX, dgamma, dbeta, ws: seen.update(
+        gamma2=gamma, dgamma=dgamma, dbeta=dbeta))
+    x, w, dh = torch.zeros(4, 64), torch.zeros(8, 64), torch.zeros(4, 8)
+    gamma, beta = (torch.ones(64) if h else None for h in have)
+    out = ffn.calibrate_norm_gated(x, gamma, beta, "rms", 1e-5, w, w, dh, "silu", LayerCfg(bits=4, group=64, form="diag"))
+    assert seen["gamma"] is gamma and seen["gamma2"] is gamma and seen["beta"] is beta
+    for key, p in (("dgamma", gamma), ("dbeta", beta)):
+        assert out[key] is seen[key] and (out[key] is None) == (p is None)
+        assert p is None or out[key].shape == p.shape
+
+
 def test_drivers_run_on_their_tensors_device(monkeypatch):
     """Tensors on a device other than the current one: every call of the drivers runs with the tensors' device current."""
     import contextlib

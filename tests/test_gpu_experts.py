@@ -55,6 +55,27 @@ def test_block_behind_its_norm(kind, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_block_behind_a_norm_without_weights(kind, dt):
+    """No gamma is a gamma of ones and no beta one of zeros, bit for bit: factors of one and sums with zero round nothing."""
+    torch, dev = torch_dev()
+    n, o, i = 50, 24, 72
+    rng = np.random.default_rng(6)
+    X, _ = put(rng.standard_normal((n, i)) * 2 + 0.5, dt)
+    Wg, Wu = (put(rng.standard_normal((o, i)) / np.sqrt(i), dt)[0] for _ in range(2))
+    dH, _ = put(rng.standard_normal((n, o)), dt)
+    cfg = LayerCfg(bits=4, group=0, form="diag")
+    ones, zeros = torch.ones(i, dtype=X.dtype, device=dev), torch.zeros(i, dtype=X.dtype, device=dev)
+    full = ffn.calibrate_norm_gated(X, ones, zeros, kind, EPS, Wg, Wu, dH, "silu", cfg)
+    for gamma, beta in ((None, None), (None, zeros), (ones, None)):
+        cal = ffn.calibrate_norm_gated(X, gamma, beta, kind, EPS, Wg, Wu, dH, "silu", cfg)
+        for key in ("N", "H", "dA", "dB", "dN", "dX", "HG_gate", "HG_up"):
+            assert torch.equal(cal[key], full[key]), key
+        for key, p in (("dgamma", gamma), ("dbeta", beta)):
+            assert cal[key] is None if p is None else torch.equal(cal[key], full[key]), key
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_experts_calibrated_and_quantised(dt):
     torch, dev = torch_dev()
     n, e, o, i = 700, 4, 128, 128

@@ -571,8 +571,8 @@ kq_status kq_grouped_backward(const void* dY, int64_t lddy, const void* W, int64
  *     Y = (x - m) r gamma + beta
  * X, Y, gamma and beta (d values) of type dt (fp32 or bf16), ldx and ldy multiples of 16 bytes and at most 2^20, gamma and
  * beta aligned to 16 bytes; gamma NULL stands for ones, beta NULL for zeros. mean and rstd (n floats, m and r) are written
- * where not NULL: kq_norm_backward takes them. eps in (0, 1]. Sums are fp32, so squares past 3.4e38 make r zero. Infinities and
- * NaN change their own row alone. Y may be X (with ldy = ldx), else outputs overlap neither each other nor any input. n = 0 does nothing.
+ * where not NULL: kq_norm_backward takes them. eps in (0, 1]. Sums are fp32: squares of finite differences past 3.4e38 make r
+ * zero, Y beta and dX zero; the sum for m passes no limit. Infinities and NaN change their own row alone. Y may be X (with ldy = ldx), else outputs overlap neither each other nor any input. n = 0 does nothing.
  */
 kq_status kq_norm_forward(const void* X, int64_t ldx, const void* gamma, const void* beta, kq_dtype dt, int64_t n, int64_t d,
                           kq_norm kind, float eps, void* Y, int64_t ldy, float* mean, float* rstd, kq_stream stream);

@@ -36,19 +36,33 @@ struct NormArgs {
 __host__ __device__ inline int64_t norm_part_half(int64_t d) { return (d + 7) / 8 * 8; }
 __host__ __device__ inline int64_t norm_part_row(int64_t d) { return 2 * norm_part_half(d); }
 
+// A row's sum is taken at 2^-21 of its size, which 2^20 finite values cannot pass the largest number at: a power of two in a fused multiply-add
+// changes neither the bits nor the cost of a plain sum (below 2^-81 values lose digits, 2^-129 of the mean at most).
+constexpr float NORM_SCALE = 0x1p-21f;
+__device__ __forceinline__ bool is_finite(float v) { return fabsf(v) < __builtin_inff(); }
+// The mean from that sum; of values next to the largest number rounding may lead past it.
+__device__ __forceinline__ float norm_mean(float s, float width) {
+    const float m = s / (width * NORM_SCALE);
+    return is_finite(s) ? fminf(fmaxf(m, -__FLT_MAX__), __FLT_MAX__) : m;
+}
 // 1 / deviation from the sums q of the squares and of the differences from m, a first mean (0 for rms). The sum of the differences
 // is what rounding left of the mean: it corrects m, and its square comes off the variance. A row of one value then has that value
-// as its mean, where one ulp beside it would come out times up to 1 / sqrt(eps).
+// as its mean, where one ulp beside it would come out times up to 1 / sqrt(eps). Finite values whose differences are not (their squares
+// then are infinite, and not NaN as those of a row with an infinity) leave m as it is.
 __device__ __forceinline__ float norm_rstd(float& m, const float (&q)[2], float width, const NormArgs& g) {
     float var = q[0] / width;
     if (g.layer) {
         const float rest = q[1] / width;
-        m += rest;
-        var = __builtin_fmaf(-rest, rest, var);      // infinite where the squares are
-        if (var < 0.0f) var = 0.0f;
+        if (is_finite(rest) || var != __builtin_inff()) {
+            m += rest;
+            var = __builtin_fmaf(-rest, rest, var);      // infinite where the squares are
+            if (var < 0.0f) var = 0.0f;
+        }
     }
     return 1.0f / sqrtf(var + g.eps);
 }
+// What a value's difference is taken from: a row of r = 0 has h = 0, also where the difference is not finite.
+__device__ __forceinline__ float norm_from(float m, float rs) { return rs == 0.0f ? 0.0f : m; }
 
 template <bool BF, int T, int CH>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormArgs g) {
@@ -62,9 +76,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormArg
         float m = 0.0f;
         if (g.layer) {
             float s[1] = {0.0f};
-            x.each([&](int, float v) { s[0] += v; });
+            x.each([&](int, float v) { s[0] = __builtin_fmaf(v, NORM_SCALE, s[0]); });
             row_sum<T>(s, sm);
-            m = s[0] / width;
+            m = norm_mean(s[0], width);
         }
         float q[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -85,6 +99,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_forward_kernel(NormArg
             if (g.mean) g.mean[r] = m;
             if (g.rstd) g.rstd[r] = rs;
         }
+        m = norm_from(m, rs);
 #pragma unroll
         for (int c = 0; c < CH; c++) {
             const int64_t col = ((int64_t)c * T + at.lane) * V;
@@ -118,10 +133,10 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormArgs g) {
         if (g.layer) {
             float s[1] = {0.0f};
             all([&](int64_t, float (&v)[V]) {
-                for (int e = 0; e < V; e++) s[0] += v[e];
+                for (int e = 0; e < V; e++) s[0] = __builtin_fmaf(v[e], NORM_SCALE, s[0]);
             });
             row_sum<1024>(s, sm);
-            m = s[0] / width;
+            m = norm_mean(s[0], width);
         }
         float q[2] = {0.0f, 0.0f};
         all([&](int64_t col, float (&v)[V]) {
@@ -137,6 +152,7 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(NormArgs g) {
             if (g.mean) g.mean[r] = m;
             if (g.rstd) g.rstd[r] = rs;
         }
+        m = norm_from(m, rs);
         all([&](int64_t col, float (&v)[V]) {
             float w[V], b[V];
             norm_weights<BF>(g.gamma, col, g.d, 1.0f, w);
@@ -178,7 +194,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_backward_kernel(NormAr
     for (int64_t r = at.first; r < g.n; r += at.step) {
         if (!AHEAD) fetch(row, r);
         else if (r + at.step < g.n) fetch(next, r + at.step);
-        const float m = row.m, rs = row.rs;
+        const float rs = row.rs, m = norm_from(row.m, rs);
         float s[2] = {0.0f, 0.0f};       // of g h and of g
 #pragma unroll
         for (int c = 0; c < CH; c++) {
@@ -253,7 +269,8 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(NormArgs g) {
     __shared__ float sm[32];
     const float inv = 1.0f / (float)g.d;
     for (int64_t r = blockIdx.x; r < g.n; r += gridDim.x) {
-        const float m = g.layer ? g.mean[r] : 0.0f, rs = g.rstd[r];
+        const float rs = g.rstd[r];
+        float m = g.layer ? g.mean[r] : 0.0f;
         auto all = [&](auto&& f) {
             for (int64_t col = (int64_t)threadIdx.x * V; col < g.d; col += 1024 * V) {
                 float h[V], t[V], w[V];
@@ -275,7 +292,9 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(NormArgs g) {
             }
         });
         row_sum<1024>(s, sm);
-        const float c1 = s[0] * inv, c0 = g.layer ? s[1] * inv : 0.0f;
+        // norm_from here and not before the first loop, whose loads would wait for r (2048 x 40000 bf16: 132 -> 135 us)
+        m = norm_from(m, rs);
+        const float c1 = g.layer && rs == 0.0f ? 0.0f : s[0] * inv, c0 = g.layer ? s[1] * inv : 0.0f;
         all([&](int64_t col, float (&h)[V], float (&t)[V]) {
             for (int e = 0; e < V; e++) t[e] = rs * (t[e] - c0 - h[e] * c1);
             store_run<V>(g.Y, BF ? KQ_BF16 : KQ_F32, r * g.ldy + col, t, g.d - col);
@@ -293,10 +312,11 @@ __global__ __launch_bounds__(256) void norm_weights_long_kernel(NormArgs g) {
     float dg[V], db[V];
     for (int e = 0; e < V; e++) dg[e] = db[e] = 0.0f;
     for (int64_t r = mine; r < g.n; r += (int64_t)gridDim.y * 4) {
-        const float m = g.layer ? g.mean[r] : 0.0f, rs = g.rstd[r];
+        const float rs = g.rstd[r], mean = g.layer ? g.mean[r] : 0.0f;
         float v[V], dy[V];
         row_load<BF>(g.X, r * g.ldx + col, g.d - col, v);
         row_load<BF>(g.dY, r * g.lddy + col, g.d - col, dy);
+        const float m = norm_from(mean, rs);
         for (int e = 0; e < V; e++) {
             dg[e] += dy[e] * ((v[e] - m) * rs);
             db[e] += dy[e];

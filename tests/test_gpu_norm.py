@@ -160,6 +160,56 @@ def test_large_mean_constant_and_special_rows(d):
     assert np.array_equal(get(Y)[1:3], np.tile(bv, (2, 1)))
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 250, 1000, 4096, 8200, 20000, 40000])
+def test_rows_whose_sums_pass_the_largest_number(d, dt):
+    """Finite rows whose sum, or whose differences from the mean, pass 3.4e38: the mean keeps the bound of any other; r is zero where the
+    squares pass, so that Y is beta and dX zero. A constant row's mean is that constant: differences t = c - m of a first mean m, off by at
+    most (k + 3) E c, are exact, and their mean is t off by (k + 2) E t, less than E c / 2: m and it add up to c. Its r is a zero row's, or
+    zero: t is zero, or at least an ulp of c, whose square passes."""
+    torch, dev = torch_dev()
+    say(f"norm of large values d={d} {dt}")
+    rng = np.random.default_rng(d)
+    x = rng.standard_normal((9, d))
+    x[0] = 1e37
+    x[1] = 10.0 ** rng.uniform(36, 38.4, d)
+    x[2] = np.where(np.arange(d) % 2, 3e38, -3e38)
+    x[3] = -3e38
+    x[3, d // 3] = 3e38
+    x[4] = 0.0
+    x[5] = np.where(np.arange(d) < d // 2, 3e38, -3e38)
+    x[6] = -3.3e38
+    x[7] = 1e37
+    x[7, d - 1] = np.inf
+    X, x = put(x, dt)
+    (gamma, gv), (beta, bv) = vector(1 + 0.3 * rng.standard_normal(d), dt), vector(rng.standard_normal(d), dt)
+    dY, dy = put(rng.standard_normal((9, d)), dt)
+    finite = [k for k in range(9) if k != 7]
+    for kind in ("layer", "rms"):
+        Y, mean, rstd = mat(9, d, dt), torch.empty(9, device=dev), torch.empty(9, device=dev)
+        K.kq_norm_forward(X, gamma, beta, kind, EPS, Y, mean, rstd)
+        want, tols = forward_tols(x[finite], gv, bv, kind, dt)
+        check(get(mean)[finite], want[1], tols[1], "mean")
+        check(get(Y)[[8]], want[0][-1:], tols[0][-1:], "Y of an ordinary row")
+        zero, one = [1, 2, 3, 5], [0, 6]
+        assert (get(rstd)[zero] == 0).all()
+        if kind == "layer":
+            assert np.array_equal(get(mean)[one], x[one, 0]) and np.isin(get(rstd)[one], [0, get(rstd)[4]]).all() and get(rstd)[4] > 300
+            assert np.isnan(get(Y)[7]).all()
+        else:
+            assert (get(rstd)[one] == 0).all() and np.isnan(get(Y)[7, d - 1])
+        assert np.array_equal(get(Y)[zero + one + [4]], np.tile(bv, (7, 1)))
+        # gradients of the finite rows, whose values these are
+        Xf, dYf, mf, rf = X[finite].contiguous(), dY[finite].contiguous(), mean[finite].contiguous(), rstd[finite].contiguous()
+        a, b = mat(8, d, dt), mat(8, d, dt)
+        a.copy_(Xf), b.copy_(dYf)
+        dX, dg, db = mat(8, d, dt), torch.empty_like(gamma), torch.empty_like(gamma)
+        K.kq_norm_backward(b, a, gamma, mf, rf, kind, dX, dg, db, Workspace("norm_backward", 0, d, 8, dt).ws)
+        want, tols = backward_tols(dy[finite], x[finite], gv, get(mf), get(rf), kind, dt)
+        for name, t, w, tol in zip(("dX", "dgamma", "dbeta"), (dX, dg, db), want, tols):
+            check(get(t), w, tol, name)
+
+
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_gradient_against_differences(kind):
     """The fp32 kernel's gradients against central differences of the float64 forward pass along random directions: h^2 times a third

@@ -85,24 +85,25 @@ def algorithmic_work(sp, plan: tuple) -> dict:
     }
 
 
-def sources_digest() -> str:
-    """sha256 over the library's HIP sources, to tie a committed counter measurement to a build."""
+# What a phase's kernels are built from (csrc/), where a committed counter measurement belongs to it: other operators' sources do not age it.
+PHASE_SOURCES = {"hg_sqrt": ("dense.hip", "gj.hip", "kq_internal.h")}
+
+
+def sources_digest(phase: str) -> str:
+    """sha256 over the HIP sources of a phase's kernels, to tie a committed counter measurement to them."""
     import hashlib
-    import glob
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "post_quantization_03_amd", "csrc", "*"))):
-        if os.path.basename(f) == "probe.hip":   # the throughput probes are not part of the library
-            continue
-        with open(f, "rb") as fh:
-            h.update(os.path.basename(f).encode() + b"\0" + fh.read())
+    for f in PHASE_SOURCES[phase]:
+        with open(os.path.join(ROOT, "post_quantization_03_amd", "csrc", f), "rb") as fh:
+            h.update(f.encode() + b"\0" + fh.read())
     return h.hexdigest()
 
 
 def measured_traffic(phase: str):
     """HBM bytes per call of a phase from the committed rocprofv3 --pmc FETCH_SIZE / WRITE_SIZE
-    summary (profiles/<phase>_c2_traffic.md), or None when the sources changed since it was taken."""
+    summary (profiles/<phase>_c2_traffic.md), or None when the phase's sources changed since it was taken."""
     path = os.path.join(ROOT, "profiles", f"{phase}_c2_traffic.md")
-    if not os.path.exists(path):
+    if phase not in PHASE_SOURCES or not os.path.exists(path):
         return None
     vals = {}
     with open(path) as fh:
@@ -110,7 +111,7 @@ def measured_traffic(phase: str):
             if ":" in line and line.split(":", 1)[0].strip() in ("sources-sha256", "bytes-per-call"):
                 k, v = line.split(":", 1)
                 vals[k.strip()] = v.strip().strip("`")
-    if vals.get("sources-sha256") != sources_digest() or "bytes-per-call" not in vals:
+    if vals.get("sources-sha256") != sources_digest(phase) or "bytes-per-call" not in vals:
         return None
     return int(vals["bytes-per-call"])
 

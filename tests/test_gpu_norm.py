@@ -120,6 +120,16 @@ def test_forward_and_backward(n, d, dt, kind):
         assert torch.equal((a, b)[over], dX) and torch.equal(dg2, dg[:d]) and torch.equal(db2, db[:d])
 
 
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,d", [(2053, 100), (2053, 500), (2053, 1000), (1100, 2000), (700, 2900), (700, 6000), (300, 11008), (300, 13824),
+                                 (300, 16001), (300, 20000)])
+def test_more_rows_than_work_groups_take_at_once(n, d, dt, kind):
+    """Rows past the work-groups of the backward pass, not a multiple of them: the weights' sums go on from row to row, in every number of
+    threads and pieces, with the next row loaded ahead and without room for it."""
+    test_forward_and_backward(n, d, dt, kind)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [100, 3000, 33000])
 def test_without_weights(d, dt):

@@ -320,10 +320,13 @@ inline int64_t group_tiles_max(int64_t n, int64_t experts, int64_t size) {
 //   4   bf16 8 x 4096 x 11008: 111 / 113, gated 16 x 1376 x 4096: 67 / 70, 4 x 4096 x 4096: 26 / 29; int8 8 x 4096 x 11008: 58 / 64
 //   8   the same: 142 / 132, 81 / 74, 31 / 31; 74 / 73, int8 gated 16 x 1376 x 4096 44 / 41, 12 x 2500 x 4096 31 / 33
 //   12  178 / 146, 92 / 78, 36 / 31; 93 / 81
-// and fp32 5 x 1376 x 1000, 32 rows a work-group: gated at 12 19.2 / 23.3, plain at 20 14.8 / 18.4, at 40 16.8 / 21.1.
+// and fp32 (32 rows a work-group from a mean of 9 on, so that experts of more read their weights twice), plain, and gated after the comma:
+//   16  5 x 1376 x 1000: 11.9 / 17.9, 18.7 / 23.2; 8 x 1376 x 4096: 54 / 58, 102 / 112; 8 x 4096 x 11008: 413 / 413, 715 / 782
+//   24  the same: 12.5 / 18.2, 19.2 / 23.1; 61 / 58, 107 / 113; 477 / 421, 766 / 787
+//   32  15.8 / 18.6, 25.5 / 23.1; 89 / 59, 140 / 116; 627 / 426, 1036 / 793
 template <int E>
 bool group_few(int64_t n, int64_t experts) {
-    return n <= (E == EL_F32 ? 32 : 6) * (experts < n ? experts : n);
+    return n <= (E == EL_F32 ? 24 : 6) * (experts < n ? experts : n);
 }
 
 // Estimated time, us, of work-groups of `per` slabs of tile shape h, with the constants of tile_plan.

@@ -92,9 +92,9 @@ def test_grouped_forward_exact(plan, dt, n, e, o, i):
 
 
 @pytest.mark.parametrize("n,e,o,i", [(9, 1, 40, 33), (17, 1, 17, 130), (31, 1, 33, 257), (32, 1, 100, 64), (60, 3, 70, 1001), (200, 7, 41, 514),
-                                     (90, 3, 16, 2047)])
+                                     (90, 3, 16, 2047), (23, 1, 33, 257), (24, 1, 100, 64), (160, 7, 41, 514), (70, 3, 16, 2047)])
 def test_grouped_few_rows_in_two_blocks_exact(n, e, o, i):
-    """Few rows of fp32 in work-groups of 32 rows, two blocks of 16: means of 8 to 32 rows an expert."""
+    """Few rows of fp32 in work-groups of 32 rows, two blocks of 16: means of 8 to 24 rows an expert; and just above, in tiles."""
     assert 8 * e < n <= 32 * e
     test_grouped_forward_exact("few, two blocks", "f32", n, e, o, i)
 

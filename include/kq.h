@@ -531,8 +531,9 @@ kq_status kq_i8_gated(const int8_t* X, int64_t ldx, const float* sX, const int8_
  * rows; rows before the first offset and from the last one on are neither read nor written. All matrices of type dt
  * (fp32 or bf16), leading dimensions as for kq_gated_forward; sums are fp32, rounded once. Outputs overlap neither each
  * other nor any input. 1 to 4096 experts; n at most 2^31 - 512. n = 0 does nothing. Workspace: kq_workspace_bytes(KQ_OP_GROUPED_GEMM, o,
- * i, n, dt, .., group = experts, ..), possibly 0; its rules are those of kq_mx_gemm. The order of a sum depends on the
- * offsets (the device cuts the last tiles of large products), never on anything else: the same call gives the same bits.
+ * i, n, dt, .., group = experts, ..), possibly 0; its rules are those of kq_mx_gemm. The order of a sum depends on the sizes, the
+ * leading dimension of W and the offsets (the device cuts the last tiles of large products), on nothing else: the same call gives the
+ * same bits.
  */
 kq_status kq_grouped_gemm(const void* X, int64_t ldx, const void* W, int64_t ldw, const int32_t* offsets, int64_t experts,
                           kq_dtype dt, int64_t n, int64_t o, int64_t i, void* Y, int64_t ldy, void* ws, size_t ws_bytes,
@@ -572,7 +573,8 @@ kq_status kq_grouped_backward(const void* dY, int64_t lddy, const void* W, int64
  * X, Y, gamma and beta (d values) of type dt (fp32 or bf16), ldx and ldy multiples of 16 bytes and at most 2^20, gamma and
  * beta aligned to 16 bytes; gamma NULL stands for ones, beta NULL for zeros. mean and rstd (n floats, m and r) are written
  * where not NULL: kq_norm_backward takes them. eps in (0, 1]. Sums are fp32: squares of finite differences past 3.4e38 make r
- * zero, Y beta and dX zero; the sum for m passes no limit. Infinities and NaN change their own row alone. Y may be X (with ldy = ldx), else outputs overlap neither each other nor any input. n = 0 does nothing.
+ * zero, Y beta and dX zero; the sum for m passes no limit. Infinities and NaN change their own row alone. Y may be X (with ldy =
+ * ldx), else outputs overlap neither each other nor any input. n = 0 does nothing.
  */
 kq_status kq_norm_forward(const void* X, int64_t ldx, const void* gamma, const void* beta, kq_dtype dt, int64_t n, int64_t d,
                           kq_norm kind, float eps, void* Y, int64_t ldy, float* mean, float* rstd, kq_stream stream);

@@ -329,7 +329,8 @@ bool group_few(int64_t n, int64_t experts) {
     return n <= (E == EL_F32 ? 24 : 6) * (experts < n ? experts : n);
 }
 
-// Estimated time, us, of work-groups of `per` slabs of tile shape h, with the constants of tile_plan.
+// Estimated time, us, of work-groups of `per` slabs of tile shape h, with the constants of tile_plan but for fp32's w: 0.44 is what its matrix cores
+// take, and what side by side launches of dX and dW are weighed by; tile_plan's 0.2 ranks the cuts of one product.
 template <int E>
 inline double group_time(int h, int64_t wgs, int64_t per) {
     constexpr int occ_log2[5] = {0, 1, 2, 0, 1};

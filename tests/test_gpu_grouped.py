@@ -99,6 +99,32 @@ def test_grouped_few_rows_in_two_blocks_exact(n, e, o, i):
     test_grouped_forward_exact("few, two blocks", "f32", n, e, o, i)
 
 
+@pytest.mark.parametrize("dt,n", [("bf16", 1), ("bf16", 5000), ("bf16", 30000), ("f32", 5000), ("f32", 40000), ("f32", 120000)])
+def test_the_most_experts(dt, n):
+    """4096 experts, most of them empty, of few rows and of tiles: products, gated products and both gradients, exact."""
+    torch, dev = torch_dev()
+    e, o, i = 4096, 20, 40
+    say(f"grouped, 4096 experts {dt} n={n}")
+    g = generator(n)
+    (X, x), (dY, dy) = whole_numbers(n, i, dt, 4, g), whole_numbers(n, o, dt, 4, g)
+    (W, w), (U, u) = stack(e, o, i, dt, 4, g), stack(e, o, i, dt, 4, g)
+    for off in (dealt(n, e, g), offsets([0] * 4000 + [n // 3] * 96 + [n])):
+        k = torch.bucketize(torch.arange(n, device=dev), off[1:].long(), right=True)     # each row's expert
+        a, b, dx = (torch.empty((n, d), dtype=torch.float64, device=dev) for d in (o, o, i))
+        dw = torch.zeros((e, o, i), dtype=torch.float64, device=dev)
+        for p in range(0, n, 2000):
+            r = slice(p, min(p + 2000, n))
+            a[r], b[r] = (x[r, None, :] * w[k[r]]).sum(2), (x[r, None, :] * u[k[r]]).sum(2)
+            dx[r] = (dy[r, :, None] * w[k[r]]).sum(1)
+            dw.index_add_(0, k[r], dy[r, :, None] * x[r, None, :])       # whole numbers below 2^53: the order does not matter
+        Y, H, dX, (flat, dW) = out(n, o, dt), out(n, o, dt), out(n, i, dt), out_stack(e, o, i, dt)
+        K.kq_grouped_gemm(X, W, off, Y, space("grouped_gemm", o, i, n, dt, e))
+        K.kq_grouped_gated(X, W, U, off, "relu", H, ws=space("grouped_gated", o, i, n, dt, e))
+        K.kq_grouped_backward(dY, X, W, off, dX, dW, ws=space("grouped_backward", o, i, n, dt, e))
+        for t, want, name in ((Y, a, "Y"), (H, a.float().clamp(min=0) * b.float(), "H"), (dX, dx, "dX"), (flat, dw.view(e * o, i), "dW")):
+            same(t, want, dt, name)
+
+
 @pytest.mark.parametrize("n,e,o,i", [(50, 6, 40, 64), (300, 5, 70, 130)])
 def test_any_offsets_stay_inside(n, e, o, i):
     """Offsets that decrease, are negative or lie past the rows are read as the header says, in every entry point."""

@@ -219,6 +219,46 @@ def test_i8_gated_activations(n, kind, dt):
     check(get(h), want, gated_tol(a, b, da, db, kind, dt), "H")
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [1 << 22, (1 << 22) - 5])
+def test_quantise_the_widest_rows(cols, dt):
+    """Rows of 4 MiB of codes, the most that there are."""
+    torch, dev = torch_dev()
+    say(f"i8 quantise cols={cols} {dt}")
+    torch.manual_seed(cols)
+    x = mat(2, cols, dt)
+    x.copy_(torch.randn(2, cols, device=dev))
+    c, s = K.i8_empty(2, cols, dev)
+    K.kq_i8_quantize(x, c, s)
+    codes, scales = oe.i8_quantize(get(x))
+    assert np.array_equal(host(c), codes) and np.array_equal(host(s), scales)
+    y = mat(2, cols, dt)
+    K.kq_i8_dequantize(c, s, y)
+    assert torch.equal(y, torch.from_numpy(oe.i8_values(codes, scales)).to(dev).to(y.dtype))
+
+
+@pytest.mark.parametrize("n", [3, 9000, 30000])
+def test_i8_the_most_experts(n):
+    """4096 experts, most of them empty, of few rows and of tiles."""
+    torch, dev = torch_dev()
+    e, o, i = 4096, 20, 100
+    say(f"i8, 4096 experts n={n}")
+    g = generator(n)
+    a, b, u = operand(n, i, g), operand(o, i, g, e), operand(o, i, g, e)
+    for off in (dealt(n, e, g), offsets([0] * 4000 + [n // 3] * 96 + [n])):
+        k = torch.bucketize(torch.arange(n, device=dev), off[1:].long(), right=True)
+        wa, wu = (torch.empty((n, o), device=dev) for _ in range(2))
+        for p in range(0, n, 2000):
+            r = slice(p, min(p + 2000, n))
+            for t, m in ((wa, b), (wu, u)):
+                t[r] = (a[0][r, None, :].double() * m[0][k[r]].double()).sum(2).float() * (a[1][r, None] * m[1][k[r]])
+        y, h = out(n, o, "f32"), out(n, o, "f32")
+        K.kq_i8_gemm(*a, *b, y, off, Workspace("i8_gemm", o, i, n, "f32", e).ws)
+        K.kq_i8_gated(*a, *b, *u, "relu", h, off, Workspace("i8_gated", o, i, n, "f32", e).ws)
+        same(y, wa, "f32", "Y")
+        same(h, wa.clamp(min=0) * wu, "f32", "H")
+
+
 # ---------------------------------------------------------------------------------- grouped products
 def offsets(values):
     torch, dev = torch_dev()

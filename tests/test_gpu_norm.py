@@ -131,6 +131,29 @@ def test_more_rows_than_work_groups_take_at_once(n, d, dt, kind):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [1 << 20, (1 << 20) - 11])
+def test_the_widest_rows(d, dt):
+    """Rows of up to 2^20 values. Padding would take a row past the limit of leading dimensions, so it has none."""
+    torch, dev = torch_dev()
+    say(f"norm d={d} {dt}")
+    rng = np.random.default_rng(d)
+    X, x = put(rng.standard_normal((3, d)) * 2 + 0.5, dt)
+    dY, dy = put(rng.standard_normal((3, d)), dt)
+    (gamma, gv), (beta, bv) = vector(1 + 0.3 * rng.standard_normal(d), dt), vector(rng.standard_normal(d), dt)
+    for kind in ("layer", "rms"):
+        Y, mean, rstd = mat(3, d, dt), torch.empty(3, device=dev), torch.empty(3, device=dev)
+        K.kq_norm_forward(X, gamma, beta, kind, EPS, Y, mean, rstd)
+        want, tols = forward_tols(x, gv, bv, kind, dt)
+        for name, t, w, tol in zip(("Y", "mean", "rstd"), (Y, mean, rstd), want, tols):
+            check(get(t), w, tol, name)
+        dX, dg, db = mat(3, d, dt), torch.empty_like(gamma), torch.empty_like(beta)
+        K.kq_norm_backward(dY, X, gamma, mean, rstd, kind, dX, dg, db, Workspace("norm_backward", 0, d, 3, dt).ws)
+        want, tols = backward_tols(dy, x, gv, get(mean), get(rstd), kind, dt)
+        for name, t, w, tol in zip(("dX", "dgamma", "dbeta"), (dX, dg, db), want, tols):
+            check(get(t), w, tol, name)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [100, 3000, 33000])
 def test_without_weights(d, dt):
     (X, x), (dY, dy), _, _ = case(6, d, dt, 1)
